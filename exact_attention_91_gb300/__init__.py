@@ -10,8 +10,10 @@ missing this module raises instead of computing anything elsewhere.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import typing
 
 from .build import LIB_PATH
 
@@ -19,16 +21,34 @@ __all__ = ["FaError", "load_library", "fa_fwd", "fa_fwd_noalloc", "fa_strerror",
            "fa_set_wait_limit_ns", "fa_abi_version", "fa_selftest_wait_timeout", "fa_fwd_varlen",
            "fa_varlen_num_splits", "fa_selftest_exp2", "fa_selftest_ex2_rate", "EX2_RATE_THREADS",
            "EX2_RATE_CHAINS", "attention_forward", "attention_forward_varlen",
-           "head_shards", "attention_forward_heads", "EXPORTED_SYMBOLS"]
+           "head_shards", "attention_forward_heads", "EXPORTED_SYMBOLS", "CACHE_BF16", "CACHE_E4M3",
+           "FaPagedCache", "fa_decode_paged", "fa_decode_paged_workspace", "fa_rotary", "fa_cache_append",
+           "fa_page_maps", "attention_decode_paged", "rotary", "rotary_inv_freq", "cache_append", "page_maps",
+           "PageMaps"]
 
 EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_noalloc", "fa_fwd_varlen", "fa_strerror", "fa_device_status",
                     "fa_set_wait_limit_ns", "fa_abi_version", "fa_selftest_wait_timeout", "fa_varlen_num_splits",
-                    "fa_selftest_exp2", "fa_selftest_ex2_rate")
+                    "fa_selftest_exp2", "fa_selftest_ex2_rate", "fa_decode_paged", "fa_decode_paged_workspace",
+                    "fa_rotary", "fa_cache_append", "fa_page_maps")
 
 FA_OK = 0
 FA_ERR_DEVICE_TIMEOUT = -8
 
+# element types of a paged cache
+CACHE_BF16 = 0
+CACHE_E4M3 = 1
+
 _lib = None
+
+
+class FaPagedCache(ctypes.Structure):
+    """The C ``fa_paged_cache``: one layer's keys and values in pages (device
+    pointers, strides in elements)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_block", ctypes.c_longlong), ("k_token", ctypes.c_longlong),
+                ("k_head", ctypes.c_longlong), ("v_block", ctypes.c_longlong), ("v_token", ctypes.c_longlong),
+                ("v_head", ctypes.c_longlong), ("type", ctypes.c_int), ("num_blocks", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("d", ctypes.c_int)]
 
 
 class FaError(RuntimeError):
@@ -70,6 +90,17 @@ def load_library(path: str | None = None):
     lib.fa_selftest_exp2.restype = i
     lib.fa_selftest_ex2_rate.argtypes = [vp, vp, i, i, vp]
     lib.fa_selftest_ex2_rate.restype = i
+    ll, pc = ctypes.c_longlong, ctypes.POINTER(FaPagedCache)
+    lib.fa_decode_paged.argtypes = [vp, pc, vp, vp, vp, vp, i, i, i, ll, f, vp, ctypes.c_size_t, vp]
+    lib.fa_decode_paged.restype = i
+    lib.fa_decode_paged_workspace.argtypes = [i] * 8
+    lib.fa_decode_paged_workspace.restype = ll
+    lib.fa_rotary.argtypes = [vp, vp, vp, vp, i, i, i, i, vp, vp, ll, i, i, i, f, vp]
+    lib.fa_rotary.restype = i
+    lib.fa_cache_append.argtypes = [vp, vp, vp, ll, ll, ll, vp, vp, vp, pc, vp, vp, ll, ll, i, i, i, i, f, vp]
+    lib.fa_cache_append.restype = i
+    lib.fa_page_maps.argtypes = [vp] * 9 + [i, i, ll, i, i, i, vp]
+    lib.fa_page_maps.restype = i
     if path is None:
         _lib = lib
     return lib
@@ -151,6 +182,51 @@ def fa_selftest_ex2_rate(cycles: int, sink: int, blocks: int, iters: int, stream
     in SM clocks, ``sink`` (device fp32 [blocks * EX2_RATE_THREADS]) the
     chains' last values. Returns the status code."""
     return load_library().fa_selftest_ex2_rate(cycles, sink, blocks, iters, stream or None)
+
+
+def fa_decode_paged(q: int, cache: FaPagedCache, block_table: int, seq_lens: int, o: int, lse: int | None, B: int,
+                    Hq: int, table_width: int, table_stride: int, scale: float, workspace: int, workspace_bytes: int,
+                    stream: int | None) -> int:
+    """The C ``fa_decode_paged``: device pointers as ints, returns the status code."""
+    return load_library().fa_decode_paged(q, cache, block_table, seq_lens, o, lse or None, B, Hq, table_width,
+                                          table_stride, scale, workspace or None, workspace_bytes, stream or None)
+
+
+def fa_decode_paged_workspace(B: int, Hq: int, Hkv: int, d: int, cache_type: int, page_size: int, table_width: int,
+                              sm_count: int) -> int:
+    """The C ``fa_decode_paged_workspace`` (host only): workspace bytes of
+    ``fa_decode_paged`` for these sizes, or a negative status."""
+    return load_library().fa_decode_paged_workspace(B, Hq, Hkv, d, cache_type, page_size, table_width, sm_count)
+
+
+def fa_rotary(x: int, y: int, positions: int, inv_freq: int | None, B: int, H: int, N: int, d: int, x_strides,
+              y_strides, position_stride: int, rotary_dim: int, interleaved: bool, inverse: bool, factor: float,
+              stream: int | None) -> int:
+    """The C ``fa_rotary``: device pointers as ints, ``x_strides`` and
+    ``y_strides`` of three elements (b, h, n). Returns the status code."""
+    three = ctypes.c_longlong * 3
+    return load_library().fa_rotary(x, y, positions, inv_freq or None, B, H, N, d, three(*x_strides),
+                                    three(*y_strides), position_stride, rotary_dim, int(bool(interleaved)),
+                                    int(bool(inverse)), factor, stream or None)
+
+
+def fa_cache_append(q: int, k: int, v: int, q_stride: int, k_stride: int, v_stride: int, positions: int, slots: int,
+                    inv_freq: int | None, cache: FaPagedCache, q_out: int, k_out: int | None, q_out_stride: int,
+                    k_out_stride: int, T: int, Hq: int, rotary_dim: int, interleaved: bool, factor: float,
+                    stream: int | None) -> int:
+    """The C ``fa_cache_append``: device pointers as ints, returns the status code."""
+    return load_library().fa_cache_append(q, k, v, q_stride, k_stride, v_stride, positions, slots, inv_freq or None,
+                                          cache, q_out, k_out or None, q_out_stride, k_out_stride, T, Hq, rotary_dim,
+                                          int(bool(interleaved)), factor, stream or None)
+
+
+def fa_page_maps(context_lens: int, new_lens: int, block_table: int, unused_blocks: int, slots: int, positions: int,
+                 cu_seqlens: int, seq_lens: int, counts: int, B: int, table_width: int, table_stride: int,
+                 num_unused: int, page_size: int, T: int, stream: int | None) -> int:
+    """The C ``fa_page_maps``: device pointers as ints, returns the status code."""
+    return load_library().fa_page_maps(context_lens, new_lens, block_table, unused_blocks, slots, positions,
+                                       cu_seqlens, seq_lens, counts, B, table_width, table_stride, num_unused,
+                                       page_size, T, stream or None)
 
 
 def _current_stream_handle(torch, device) -> int:
@@ -288,3 +364,349 @@ def attention_forward_heads(q, k, v, head_start: int, head_count: int, causal: b
     if rc != FA_OK:
         raise FaError(rc)
     return out, lse
+
+
+# ---- serving from a paged cache, rotary positions ---------------------------
+
+
+def _serve_launch(torch, device, stream, call, made, what):
+    """Runs ``call(stream handle)`` with ``device`` current. Tensors that were
+    made for the call belong to the current stream's part of the allocator;
+    when another ``stream`` uses them it is told so, so that none is handed out
+    again while that stream's kernels may still run."""
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
+        handle = stream.cuda_stream
+    else:
+        handle = _current_stream_handle(torch, device)
+    if device.index == torch.cuda.current_device():
+        rc = call(handle or None)
+    else:
+        with torch.cuda.device(device):
+            rc = call(handle or None)
+    if rc != FA_OK:
+        raise FaError(rc, what)
+
+
+def _check_on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, the device of the first tensor")
+
+
+def _check_int32(torch, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+
+
+def _paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale) -> FaPagedCache:
+    """The C description of caches indexed [block, token, head, d]."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, page_size, heads, d]")
+    if v_cache.dtype != k_cache.dtype or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError("k_cache and v_cache must both be bf16 or both float8_e4m3fn")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the d values of a cache row must be contiguous")
+    _check_on(device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    nb, page, heads, d = k_cache.shape
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (heads,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous fp32 tensor of one value per key head")
+    return FaPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+                        v_scale.data_ptr() if v_scale is not None else None, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                        CACHE_E4M3 if k_cache.dtype == torch.float8_e4m3fn else CACHE_BF16, nb, page, heads, d)
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_workspace_bytes(B, Hq, Hkv, d, cache_type, page_size, table_width, device_index):
+    import torch
+    sms = torch.cuda.get_device_properties(device_index).multi_processor_count
+    n = fa_decode_paged_workspace(B, Hq, Hkv, d, cache_type, page_size, table_width, sms)
+    if n < 0:
+        raise FaError(n, "fa_decode_paged_workspace")
+    return n
+
+
+def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None, k_scale=None,
+                           v_scale=None, out=None, lse=None, return_lse: bool = True, workspace=None, stream=None):
+    """O [B, Hq, d] (bf16) and LSE [B, Hq] (fp32) of one new token per request
+    over its pages: q [B, Hq, d] (bf16), ``k_cache`` / ``v_cache`` indexed
+    [num_blocks, page_size, heads, d] (bf16 or float8_e4m3fn, any order in
+    memory with d innermost: a permuted or sliced view will do), int32
+    ``block_table`` [B, width] and ``seq_lens`` [B] (keys of each request, the
+    new token's among them). Hq is a multiple of heads. A value of the cache is
+    its element times ``k_scale`` / ``v_scale`` [heads] (fp32), where given.
+    A request without keys gets O = 0, LSE = -inf.
+
+    ``workspace`` (uint8, at least ``fa_decode_paged_workspace`` bytes) may be
+    given to keep allocation out of the call; calls that may overlap in time
+    need one each."""
+    import torch
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bf16")
+    if q.dim() != 3 or block_table.dim() != 2 or seq_lens.dim() != 1:
+        raise ValueError("q must be [B, Hq, d], block_table [B, width] and seq_lens [B]")
+    B, Hq, d = q.shape
+    if not q.is_cuda:
+        raise ValueError("all inputs must be CUDA tensors")
+    if k_cache.dim() != 4 or k_cache.shape[3] != d or block_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("q, the caches, block_table and seq_lens do not fit together")
+    if not q.is_contiguous() or not seq_lens.is_contiguous() or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("q, seq_lens and the rows of block_table must be contiguous")
+    _check_int32(torch, block_table=block_table, seq_lens=seq_lens)
+    device = q.device
+    _check_on(device, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse, workspace=workspace)
+    cache = _paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    made = []
+    if out is None:
+        out = torch.empty_like(q)
+        made.append(out)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+            made.append(lse)
+    elif lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq]")
+    if workspace is None:
+        n = _decode_workspace_bytes(B, Hq, cache.heads, d, cache.type, cache.page_size, block_table.shape[1],
+                                    device.index)
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        made.append(workspace)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    lib = _lib or load_library()
+    _serve_launch(torch, device, stream,
+                  lambda s: lib.fa_decode_paged(q.data_ptr(), cache, block_table.data_ptr(), seq_lens.data_ptr(),
+                                                out.data_ptr(), lse.data_ptr() if lse is not None else None, B, Hq,
+                                                block_table.shape[1], block_table.stride(0), scale,
+                                                workspace.data_ptr(), workspace.numel(), s),
+                  made, "fa_decode_paged")
+    return (out, lse) if return_lse else out
+
+
+def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None, device=None):
+    """(inv_freq, factor) for ``rotary`` and ``cache_append``: fp64 [rotary_dim
+    / 2] frequencies base^(-2i / rotary_dim) on ``device`` and the factor of cos
+    and sin, laid out once per model. ``scaling`` stretches them for contexts
+    longer than the trained one, by ``{"type": ...}``:
+
+    * ``"linear"``, ``factor``: every frequency divided by factor.
+    * ``"ntk"``, ``factor``: base raised by factor^(r / (r - 2)), so that the
+      slowest frequency is divided by factor and the fastest is kept.
+    * ``"bands"``, ``factor``, ``original`` (trained context), ``low`` = 1,
+      ``high`` = 4: frequencies that turn less than ``low`` times over the
+      trained context are divided by factor, those that turn more than
+      ``high`` times are kept, linear in the number of turns between.
+    * ``"yarn"``, ``factor``, ``original``, ``low`` = 1, ``high`` = 32,
+      ``attention_factor`` = 0.1 ln(factor) + 1: the same, linear in the
+      frequency's index between, and cos and sin times attention_factor.
+    """
+    import torch
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and >= 0")
+    if not (math.isfinite(base) and base > 0):
+        raise ValueError("base must be finite and > 0")
+    r = rotary_dim
+    index = torch.arange(0, r, 2, dtype=torch.float64)
+    freq, out_factor = float(base) ** (-index / r) if r else index, 1.0
+    if scaling is not None:
+        kind, factor = scaling.get("type"), float(scaling.get("factor", 1.0))
+        if not (math.isfinite(factor) and factor > 0):
+            raise ValueError("scaling factor must be finite and > 0")
+        if kind == "linear":
+            freq = freq / factor
+        elif kind == "ntk":
+            if r > 2:
+                freq = (base * factor ** (r / (r - 2))) ** (-index / r)
+        elif kind in ("bands", "yarn"):
+            original = float(scaling["original"])
+            low, high = float(scaling.get("low", 1.0)), float(scaling.get("high", 4.0 if kind == "bands" else 32.0))
+            if not (original > 0 and 0 < low < high):
+                raise ValueError("scaling needs original > 0 and 0 < low < high")
+            if kind == "bands":
+                keep = ((original * freq / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+            else:
+                # the (fractional) indexes whose frequencies turn `high` and `low` times over the trained context
+                i_high, i_low = (r * math.log(original / (2 * math.pi * n)) / (2 * math.log(base)) for n in (high, low))
+                first, last = max(math.floor(i_high), 0), min(math.ceil(i_low), r - 1)
+                keep = 1 - ((index / 2 - first) / max(last - first, 1e-3)).clamp(0, 1)
+                out_factor = float(scaling.get("attention_factor", 0.1 * math.log(factor) + 1 if factor > 1 else 1.0))
+            freq = freq * keep + freq / factor * (1 - keep)
+        else:
+            raise ValueError(f"unknown rotary scaling {kind!r}")
+    return (freq.to(device) if device is not None else freq), out_factor
+
+
+def _rotary_dim(torch, device, inv_freq):
+    """(rotary_dim, pointer) of the frequencies; none: (0, None)."""
+    if inv_freq is None:
+        return 0, None
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous fp64 tensor [rotary_dim / 2]")
+    _check_on(device, inv_freq=inv_freq)
+    return 2 * inv_freq.shape[0], inv_freq.data_ptr() or None
+
+
+def rotary(x, positions, inv_freq, interleaved: bool = False, inverse: bool = False, factor: float = 1.0, out=None,
+           stream=None):
+    """Rotary positions of x (bf16, CUDA): [B, H, N, d] with int32 ``positions``
+    [N] or [B, N], or token-major [T, H, d] with positions [T]. Any strides with
+    d contiguous. ``inv_freq`` (fp64 [rotary_dim / 2]) and ``factor`` are those of
+    ``rotary_inv_freq``; pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+    ``interleaved``. ``inverse`` turns back by the same angles (times factor):
+    the gradient with respect to x. ``out`` may be x. Not differentiable by
+    itself: ``torch.ops.fa91.rotary`` is."""
+    import torch
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bf16")
+    _check_int32(torch, positions=positions)
+    if x.dim() == 4:
+        B, H, N, d = x.shape
+        if positions.shape not in ((N,), (B, N)):
+            raise ValueError("positions must be [N] or [B, N]")
+        xs = x.stride()[:3]
+        pos_stride = positions.stride(0) if positions.dim() == 2 else 0
+    elif x.dim() == 3:
+        N, H, d = x.shape
+        B = 1
+        if positions.shape != (N,):
+            raise ValueError("positions must be [T]")
+        xs = (0, x.stride(1), x.stride(0))
+        pos_stride = 0
+    else:
+        raise ValueError("x must be [B, H, N, d] or [T, H, d]")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.stride(-1) != 1 or (N > 1 and positions.stride(-1) != 1):
+        raise ValueError("d of x and the rows of positions must be contiguous")
+    device = x.device
+    _check_on(device, positions=positions, out=out)
+    r, freq = _rotary_dim(torch, device, inv_freq)
+    made = []
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        made.append(out)
+    elif out.dtype != torch.bfloat16 or out.shape != x.shape or out.stride(-1) != 1:
+        raise ValueError("out must be a bf16 tensor of x's shape with d contiguous")
+    ys = out.stride()[:3] if x.dim() == 4 else (0, out.stride(1), out.stride(0))
+    lib = _lib or load_library()
+    three = ctypes.c_longlong * 3
+    _serve_launch(torch, device, stream,
+                  lambda s: lib.fa_rotary(x.data_ptr(), out.data_ptr(), positions.data_ptr(), freq, B, H, N, d,
+                                          three(*xs), three(*ys), pos_stride, r, 1 if interleaved else 0,
+                                          1 if inverse else 0, factor, s),
+                  made, "fa_rotary")
+    return out
+
+
+def cache_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved: bool = False,
+                 factor: float = 1.0, k_scale=None, v_scale=None, q_out=None, k_out=None, stream=None):
+    """One step's tokens into a paged cache: q [T, Hq, d] and k [T, heads, d]
+    (bf16, CUDA) turned by their rotary positions (``inv_freq`` None: not
+    turned), k and v [T, heads, d] written to their ``slots`` (int32 [T]; slot s
+    is token s % page_size of block s // page_size) of ``k_cache`` /
+    ``v_cache`` [num_blocks, page_size, heads, d], q returned turned (in
+    ``q_out`` where given; it may be q). ``k_out`` [T, heads, d] also receives
+    the turned k (for a prompt's own attention; it may be k). A token with a
+    negative slot is padding: nothing of it is written anywhere. q, k and v may
+    be slices of one projection's output. float8_e4m3fn caches hold value /
+    scale, with ``k_scale`` / ``v_scale`` fp32 [heads] (None: 1)."""
+    import torch
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16:
+            raise TypeError("q, k, v must be bf16")
+        if t.dim() != 3 or t.shape[0] != q.shape[0] or t.shape[2] != q.shape[2]:
+            raise ValueError("q must be [T, Hq, d] and k, v [T, heads, d]")
+        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError(f"the heads of a token of {name} must be contiguous")
+    T, Hq, d = q.shape
+    if not q.is_cuda:
+        raise ValueError("all inputs must be CUDA tensors")
+    if k_cache.dim() != 4 or k.shape != v.shape or k_cache.shape[2:] != k.shape[1:]:
+        raise ValueError("k, v and the caches do not fit together")
+    _check_int32(torch, positions=positions, slots=slots)
+    if positions.shape != (T,) or slots.shape != (T,) or not positions.is_contiguous() or not slots.is_contiguous():
+        raise ValueError("positions and slots must be contiguous [T]")
+    device = q.device
+    _check_on(device, k=k, v=v, positions=positions, slots=slots, q_out=q_out, k_out=k_out)
+    cache = _paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale)
+    r, freq = _rotary_dim(torch, device, inv_freq)
+    made = []
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
+        made.append(q_out)
+    for t, like in ((q_out, q), (k_out, k)):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape != like.shape or t.stride(2) != 1 or
+                              (t.shape[1] > 1 and t.stride(1) != d)):
+            raise ValueError("q_out and k_out must be bf16, of q's and k's shape, a token's heads contiguous")
+    lib = _lib or load_library()
+    _serve_launch(torch, device, stream,
+                  lambda s: lib.fa_cache_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), k.stride(0),
+                                                v.stride(0), positions.data_ptr(), slots.data_ptr(), freq, cache,
+                                                q_out.data_ptr(), k_out.data_ptr() if k_out is not None else None,
+                                                q_out.stride(0), k_out.stride(0) if k_out is not None else 0, T, Hq, r,
+                                                1 if interleaved else 0, factor, s),
+                  made, "fa_cache_append")
+    return q_out
+
+
+class PageMaps(typing.NamedTuple):
+    """What ``page_maps`` gives for a step (int32 CUDA tensors)."""
+    slots: "torch.Tensor"        # [T] where each new token goes (cache_append)
+    positions: "torch.Tensor"    # [T] its position in its request
+    cu_seqlens: "torch.Tensor"   # [B + 1] offsets of the requests' new tokens (attention_forward_varlen)
+    seq_lens: "torch.Tensor"     # [B] keys of each request after the step (attention_decode_paged)
+    counts: "torch.Tensor"       # [4] pages taken, pages missing, new tokens, requests past the table's width
+
+
+def page_maps(context_lens, new_lens, block_table, unused_blocks, page_size: int, num_tokens: int,
+              out: PageMaps | None = None, stream=None) -> PageMaps:
+    """Block tables and slot maps of one step, made on the GPU from request
+    lengths (int32 CUDA tensors): request b holds ``context_lens``[b] tokens and
+    gets ``new_lens``[b] more. ``block_table`` [B, width] is completed in place
+    with the blocks that the new tokens need, taken from ``unused_blocks`` in
+    order (the caller then drops the first ``counts[0]``); ``num_tokens`` is the
+    length of the token maps, which may be more than the step's tokens (the
+    rest are padding: slot -1). See ``fa_page_maps`` in include/fa.h."""
+    import torch
+    _check_int32(torch, context_lens=context_lens, new_lens=new_lens, block_table=block_table,
+                 unused_blocks=unused_blocks)
+    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [B, width] with contiguous rows")
+    B, width = block_table.shape
+    if not block_table.is_cuda:
+        raise ValueError("all inputs must be CUDA tensors")
+    if context_lens.shape != (B,) or new_lens.shape != (B,) or unused_blocks.dim() != 1:
+        raise ValueError("context_lens and new_lens must be [B], unused_blocks one list")
+    if not (context_lens.is_contiguous() and new_lens.is_contiguous() and unused_blocks.is_contiguous()):
+        raise ValueError("lengths and unused_blocks must be contiguous")
+    device = block_table.device
+    _check_on(device, context_lens=context_lens, new_lens=new_lens, unused_blocks=unused_blocks)
+    T = int(num_tokens)
+    if T < 0:
+        raise ValueError("num_tokens must be >= 0")
+    made = []
+    if out is None:
+        whole = torch.empty(2 * T + 2 * B + 5, dtype=torch.int32, device=device)
+        out = PageMaps(*whole.split((T, T, B + 1, B, 4)))
+        made.append(whole)
+    else:
+        for t, n in zip(out, (T, T, B + 1, B, 4)):
+            if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.device != device:
+                raise ValueError("out must be int32 tensors [T], [T], [B + 1], [B] and [4] on the same device")
+    lib = _lib or load_library()
+    _serve_launch(torch, device, stream,
+                  lambda s: lib.fa_page_maps(context_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+                                             unused_blocks.data_ptr() or None, out[0].data_ptr() or None,
+                                             out[1].data_ptr() or None, out[2].data_ptr(), out[3].data_ptr(),
+                                             out[4].data_ptr(), B, width, block_table.stride(0),
+                                             unused_blocks.shape[0], page_size, T, s),
+                  made, "fa_page_maps")
+    return out

@@ -1,8 +1,10 @@
 """Builds libfa.so in-tree with nvcc for sm_103a.
 
-The library is one translation unit (``csrc/fa_api.cu``) that includes the
-kernels; it links the CUDA runtime statically and resolves the driver's
-tensor-map encoder at run time, so it needs no libcuda at link time.
+The library is two translation units that include their kernels, compiled at
+once: ``csrc/fa_api.cu`` (attention forward) and ``csrc/fa_serve.cu`` (paged
+cache and rotary positions). It links the CUDA runtime statically and resolves
+the driver's tensor-map encoder at run time, so it needs no libcuda at link
+time.
 """
 from __future__ import annotations
 
@@ -30,7 +32,7 @@ def nvcc_path() -> str:
 def sources() -> list[str]:
     out = []
     for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".cu", ".cuh")):
+        if name.endswith((".cu", ".cuh", ".h")):
             out.append(os.path.join(CSRC, name))
     out.append(os.path.join(INCLUDE, "fa.h"))
     return out
@@ -38,8 +40,8 @@ def sources() -> list[str]:
 
 def nvcc_cmd(out_path: str, extra: list[str] | None = None) -> list[str]:
     return [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
-            "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC,
-            *(extra or []), os.path.join(CSRC, "fa_api.cu"), "-o", out_path]
+            "-Xcompiler", "-fPIC", "-shared", "--threads", "2", "-I", INCLUDE, "-I", CSRC,
+            *(extra or []), os.path.join(CSRC, "fa_api.cu"), os.path.join(CSRC, "fa_serve.cu"), "-o", out_path]
 
 
 def up_to_date() -> bool:

@@ -13,11 +13,12 @@
 
 #include "fa.h"
 #include "fa_fwd_kernel.cuh"
+#include "fa_host.h"
 
 namespace {
 
 constexpr unsigned long long kDefaultWaitLimitNs = 2000000000ull;
-constexpr int kMaxDevices = 64;
+constexpr int kMaxDevices = fa::kHostMaxDevices;
 
 std::mutex g_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -422,6 +423,19 @@ int run_dense(const void* q, const void* k, const void* v, void* o, float* lse, 
 
 }  // namespace
 
+namespace fa {
+
+int host_probe(int* device, int* sm_count) {
+    DeviceState* st = nullptr;
+    const int rc = probe_device(device, &st);
+    if (rc == FA_OK) *sm_count = st->sm_count;
+    return rc;
+}
+
+int host_capturing(cudaStream_t stream) { return capturing(stream); }
+
+}  // namespace fa
+
 extern "C" {
 
 int fa_abi_version(void) { return FA_ABI_VERSION; }
@@ -484,6 +498,8 @@ const char* fa_strerror(int status) {
         case FA_ERR_DEVICE_TIMEOUT: return "a kernel gave up waiting on an mbarrier";
         case FA_ERR_BAD_SCALE: return "scale must be finite and > 0";
         case FA_ERR_ALIAS: return "an output buffer overlaps an input buffer or the other output";
+        case FA_ERR_WORKSPACE: return "the workspace is missing or smaller than the call needs";
+        case FA_ERR_BAD_TYPE: return "the cache's element type must be FA_CACHE_BF16 or FA_CACHE_E4M3";
         default: return "unknown fa status";
     }
 }

@@ -1,0 +1,640 @@
+// Attention of one new token per request over a paged key-value cache.
+//
+// For request b, key head h and the G query heads that share it:
+//   s_ij = scale · ks_h · q_i·k_j (j < len_b),  O_i = vs_h · softmax_j(s_ij) v_j,
+//   LSE_i = ln Σ_j exp s_ij;  no key: O = 0, LSE = -inf
+// in one pass with the online softmax, in base 2 (log2 e folded into the scale).
+//
+// The keys and values are read once, 2·D·len bytes per key head, and meet
+// 4·G flops per value: the kernel is bound by HBM, so everything serves a
+// steady stream of loads.
+//  * A tile is one warp's step: 8 KB of cache (kKeys keys, K and V). Each warp
+//    owns a ring of kStages tiles in shared memory, filled with 16-byte
+//    cp.async and read back by itself alone, so the loop has no block barrier
+//    and about 130 KB per SM stay in flight.
+//  * The tiles of the whole batch, in the order (request, key head, tile), are
+//    cut into equal runs, one per worker (block), whatever the lengths are:
+//    the lengths are read on the GPU. A worker's loads run on across the
+//    requests and heads of its run. A unit (request, key head) that one
+//    worker holds whole is written at once; a unit that is cut leaves one
+//    fp32 partial (O, reference maximum, sum) per worker in the workspace and
+//    fa_decode_join_kernel adds them up. A worker's run has at most two cut
+//    units, its first and its last: two slots each.
+//  * One warp-level mma.sync m16n8k16 tile holds up to 16 query heads; tcgen05
+//    would want 128 rows (heads) or a softmax across TMEM lanes, for flops that
+//    are not the bound. With at most 8 heads the tile's rows 8-15 carry the
+//    rounding remainder of P: p = hi + lo, both 16 bits, so P·V keeps about
+//    16 (bf16) or 22 (fp16) bits of p at no extra instruction.
+//  * e4m3 caches are widened to fp16 (exact) in registers; q is scaled by a
+//    power of two per head into fp16's range (exact but for values 2^-14
+//    below the head's largest, whose low bits are below 2^-24 of it).
+#pragma once
+
+#include "fa_common.cuh"
+
+namespace fa {
+
+struct DecodeParams {
+    const void* q;          // bf16 [B, Hq, D]
+    const uint8_t* k;       // caches: byte strides below, D contiguous
+    const uint8_t* v;
+    void* o;                // bf16 [B, Hq, D]
+    float* lse;             // [B, Hq] or null
+    const int* table;       // [B][table_stride], `width` entries used
+    const int* lens;        // [B]
+    const float* k_scale;   // [Hkv] or null
+    const float* v_scale;
+    float* part_o;          // workspace: [2 * workers][rows][D]
+    float2* part_ml;        // [2 * workers][rows]: (reference maximum, sum)
+    int4* meta;             // [workers]: the cut unit that continues into this worker
+    long long k_block, k_token, k_head, v_block, v_token, v_head;
+    long long table_stride;
+    float scale_log2;
+    int B, Hkv, G, row_groups, num_blocks, page_shift, width;
+};
+
+template <int D, bool E4M3, bool WIDE>
+struct DecodeCfg {
+    static constexpr int kWarps = 4, kThreads = kWarps * 32;
+    static constexpr int kRows = WIDE ? 16 : 8;               // query heads of a unit
+    static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);      // one key's K (or V)
+    static constexpr int kHalfBytes = 4096;                   // a tile's K (or V)
+    static constexpr int kTileBytes = 2 * kHalfBytes;
+    static constexpr int kKeys = kHalfBytes / kRowBytes;      // 16, 32 or 64
+    static constexpr int kGroups = kKeys / 16;                // 16-key groups (a group lies in one page)
+    static constexpr int kStages = 3;
+    static constexpr int kRowLanes = kRowBytes / 16;          // lanes that copy one row
+    static constexpr int kRowsPerCopy = 32 / kRowLanes;
+    static constexpr int kCopiesPerGroup = 16 / kRowsPerCopy;
+    static constexpr int kOffMerge = kWarps * kStages * kTileBytes;  // fp32 [warp][8][D]
+    static constexpr int kOffStat = kOffMerge + kWarps * 8 * D * 4;  // float2 [warp][16]
+    static constexpr int kSmemBytes = kOffStat + kWarps * 16 * 8 + 64;
+    // P is kept in 16 bits: fp16's range is used up to 2^15 (kBias + kLazy), so
+    // that what falls below its smallest step, 2^-24, is below 2^-31 of the
+    // largest weight.
+    static constexpr float kBias = E4M3 ? 7.f : 0.f;
+    // O and the sum are rescaled only when the row maximum rises by more.
+    static constexpr float kLazy = 8.f;
+};
+
+// Position in a worker's run: tiles [t0, t1) of unit (b, hh), then `rem` more.
+struct DecodeSeg {
+    int b, hh, t0, t1, nt, len;
+    long long rem;
+};
+
+__device__ __forceinline__ int decode_len(const DecodeParams& p, int b) {
+    const long long cap = static_cast<long long>(p.width) << p.page_shift;
+    const int n = max(p.lens[b], 0);
+    return n > cap ? static_cast<int>(cap) : n;
+}
+
+template <int KEYS>
+__device__ __forceinline__ int decode_tiles(int len) {
+    return len <= KEYS ? 1 : (len - 1) / KEYS + 1;  // a request without keys still has its output to write
+}
+
+template <int KEYS>
+__device__ __forceinline__ void decode_next(DecodeSeg& s, const DecodeParams& p) {
+    if (++s.hh == p.Hkv * p.row_groups) {
+        s.hh = 0;
+        ++s.b;
+        s.len = decode_len(p, s.b);
+        s.nt = decode_tiles<KEYS>(s.len);
+    }
+    s.t0 = 0;
+    s.t1 = static_cast<int>(s.rem < s.nt ? s.rem : s.nt);
+    s.rem -= s.t1;
+}
+
+// First tile of worker c when `total` tiles are cut for `workers`; the worker
+// of a tile.
+__device__ __forceinline__ long long decode_start(long long total, int workers, int c) { return total * c / workers; }
+__device__ __forceinline__ int decode_worker_of(long long total, int workers, long long tile) {
+    return static_cast<int>(((tile + 1) * workers - 1) / total);
+}
+
+// Byte offset, inside a tile's K (or V), of 16-byte chunk c of row r: rows
+// follow one another and the chunk index is XORed with a function of the row,
+// so that the reads below touch every bank once.
+template <int D, bool E4M3>
+__device__ __forceinline__ uint32_t decode_chunk(int r, int c) {
+    constexpr int RB = D * (E4M3 ? 1 : 2);
+    if constexpr (RB == 64) {  // two rows to a 128-byte line
+        const int line = r >> 1, slot = ((r & 1) << 2) | c;
+        return line * 128 + ((slot ^ ((line & 3) << 1)) << 4);
+    } else if constexpr (E4M3) {
+        return r * RB + ((c ^ (((r >> 1) & 3) << 1) ^ ((r & 1) << 2)) << 4);
+    } else {
+        return r * RB + ((c ^ (r & 7)) << 4);
+    }
+}
+
+// Starts the copies of tile t of the segment's unit into ring slot `dst` and
+// returns which of its 16-key groups lie in a page of the cache (bit g).
+template <int D, bool E4M3, bool WIDE>
+__device__ __forceinline__ uint32_t decode_load(const DecodeParams& p, const DecodeSeg& s, int t, int page_entry,
+                                                uint32_t dst, int lane) {
+    using C = DecodeCfg<D, E4M3, WIDE>;
+    const int lr = lane / C::kRowLanes, lc = lane % C::kRowLanes;
+    const int h = s.hh / p.row_groups;
+    uint32_t ok_mask = 0;
+#pragma unroll
+    for (int g = 0; g < C::kGroups; ++g) {
+        const int page = __shfl_sync(0xffffffffu, page_entry, g);
+        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
+        ok_mask |= (ok ? 1u : 0u) << g;
+        const int key0 = t * C::kKeys + g * 16;
+        const int tok = (key0 & ((1 << p.page_shift) - 1)) + lr;
+        const long long pg = ok ? page : 0;
+        const uint8_t* ks = p.k + pg * p.k_block + h * p.k_head + tok * p.k_token + lc * 16;
+        const uint8_t* vs = p.v + pg * p.v_block + h * p.v_head + tok * p.v_token + lc * 16;
+        const int left = ok ? s.len - key0 - lr : 0;  // rows of this lane's column of rows that hold keys
+#pragma unroll
+        for (int i = 0; i < C::kCopiesPerGroup; ++i) {
+            const uint32_t bytes = i * C::kRowsPerCopy < left ? 16u : 0u;
+            const uint32_t off = decode_chunk<D, E4M3>(g * 16 + i * C::kRowsPerCopy + lr, lc);
+            ptx::cp_async16(dst + off, ks, bytes);
+            ptx::cp_async16(dst + C::kHalfBytes + off, vs, bytes);
+            ks += C::kRowsPerCopy * p.k_token;
+            vs += C::kRowsPerCopy * p.v_token;
+        }
+    }
+    return ok_mask;
+}
+
+// The page of this lane's 16-key group of tile t (lanes 0 .. kGroups-1; -1
+// past the end of the keys: never read).
+template <int D, bool E4M3, bool WIDE>
+__device__ __forceinline__ int decode_page(const DecodeParams& p, const DecodeSeg& s, int t, int lane) {
+    using C = DecodeCfg<D, E4M3, WIDE>;
+    const int key = t * C::kKeys + (lane % C::kGroups) * 16;
+    return key < s.len ? __ldg(p.table + s.b * p.table_stride + (key >> p.page_shift)) : -1;
+}
+
+template <int D, bool E4M3, bool WIDE>
+__global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p) {
+    using C = DecodeCfg<D, E4M3, WIDE>;
+    constexpr int NT = C::kKeys / 8;  // score columns, 8 keys each
+    constexpr int ND = D / 8;         // output columns, 8 values each
+    constexpr int KS = D / 16;        // steps of 16 of q·k
+    constexpr int R = WIDE ? 2 : 1;   // query rows of a lane: g (and g + 8)
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long sh_warp[C::kWarps];
+    __shared__ long long sh_begin;
+    __shared__ int sh_b;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int HH = p.Hkv * p.row_groups;
+    ptx::griddep_launch_dependents();
+
+    // ---- this worker's run of tiles
+    const int per = (p.B + C::kThreads - 1) / C::kThreads;
+    const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b))) * HH;
+    long long incl = mine;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, i);
+        if (lane >= i) incl += x;
+    }
+    if (lane == 31) sh_warp[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+        if (w < warp) before += sh_warp[w];
+        total += sh_warp[w];
+    }
+    const int worker = blockIdx.x;
+    // (a worker has a tile for every warp, as long as there are that many)
+    const long long most = (total + C::kWarps - 1) / C::kWarps;
+    const int workers = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+    if (worker >= workers) {
+        if (tid == 0) p.meta[worker] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    const long long begin = decode_start(total, workers, worker), end = decode_start(total, workers, worker + 1);
+    {
+        long long at = before + incl - mine;  // first tile of request b_lo
+        if (begin >= at && begin < at + mine) {
+            int b = b_lo;
+            for (;; ++b) {
+                const long long n = static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b))) * HH;
+                if (begin < at + n) break;
+                at += n;
+            }
+            sh_b = b;
+            sh_begin = at;
+        }
+    }
+    __syncthreads();
+    DecodeSeg seg;
+    seg.b = sh_b;
+    seg.len = decode_len(p, seg.b);
+    seg.nt = decode_tiles<C::kKeys>(seg.len);
+    seg.hh = static_cast<int>((begin - sh_begin) / seg.nt);
+    seg.t0 = static_cast<int>((begin - sh_begin) % seg.nt);
+    seg.rem = end - begin;
+    seg.t1 = static_cast<int>(seg.rem < seg.nt - seg.t0 ? seg.t0 + seg.rem : seg.nt);
+    seg.rem -= seg.t1 - seg.t0;
+    if (tid == 0) {
+        // the join of a cut unit is done at the first cut: by the block of the worker after the unit's first
+        int4 m = make_int4(-1, 0, 0, 0);
+        if (seg.t0 > 0) {
+            const long long u0 = begin - seg.t0;
+            const int first = decode_worker_of(total, workers, u0);
+            if (first == worker - 1) {
+                m.x = seg.b;
+                m.y = seg.hh;
+                m.z = decode_start(total, workers, first) == u0 ? 2 * first : 2 * first + 1;
+                m.w = decode_worker_of(total, workers, u0 + seg.nt - 1);
+            }
+        }
+        p.meta[worker] = m;
+    }
+
+    // ---- the ring: the next tiles to copy run ahead of the ones in use, across segments
+    const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kTileBytes;
+    DecodeSeg ahead = seg;
+    int at = ahead.t0 + warp;  // next tile of this warp to copy
+    bool more = true;
+    auto seek = [&]() {
+        while (at >= ahead.t1) {
+            if (ahead.rem == 0) {
+                more = false;
+                return;
+            }
+            decode_next<C::kKeys>(ahead, p);
+            at = ahead.t0 + warp;
+        }
+    };
+    seek();
+    int entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
+    uint32_t slot_in = 0, slot_out = 0, ok_bits = 0;
+    auto load = [&]() {
+        if (more) {
+            const uint32_t ok = decode_load<D, E4M3, WIDE>(p, ahead, at, entry, ring + slot_in * C::kTileBytes, lane);
+            ok_bits = (ok_bits & ~(((1u << C::kGroups) - 1) << (slot_in * C::kGroups))) | ok << (slot_in * C::kGroups);
+            at += C::kWarps;
+            seek();
+            entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
+        }
+        slot_in = slot_in + 1 == C::kStages ? 0 : slot_in + 1;
+        ptx::cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) load();
+
+    for (bool first_seg = true;; first_seg = false) {
+        const int h = seg.hh / p.row_groups, rg = seg.hh - h * p.row_groups;
+        const int rows = min(p.G - rg * C::kRows, C::kRows);  // query heads of this unit
+        const long long row0 = static_cast<long long>(seg.b) * p.Hkv * p.G + h * p.G + rg * C::kRows;
+
+        // ---- q fragments, and each row's factor from q·k to base-2 scores
+        uint32_t qa[KS][2 * R];
+        float cs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool have = g + 8 * r < rows;
+            const uint32_t* qrow = reinterpret_cast<const uint32_t*>(p.q) + (row0 + (have ? g + 8 * r : 0)) * (D / 2);
+            cs[r] = p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.f);
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // which pair of values meets the j-th register of the cache's fragment of step s
+                    const int pair = E4M3 ? ((t4 + 4 * (s / 4)) * 16 + 4 * (s % 4) + 2 * j) / 2 : s * 8 + t4 + 4 * j;
+                    qa[s][R * j + r] = have ? __ldg(qrow + pair) : 0u;
+                }
+            if constexpr (E4M3) {
+                float top = 0.f;
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 x = ptx::unpack_bf16x2(qa[s][R * j + r]);
+                        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+                e = top > 0.f ? max(-120, min(120, e)) : 0;
+                const float down = __int_as_float((127 - e) << 23);
+                cs[r] *= __int_as_float((127 + e) << 23);
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 x = ptx::unpack_bf16x2(qa[s][R * j + r]);
+                        qa[s][R * j + r] = ptx::pack_f16x2(x.x * down, x.y * down);
+                    }
+            }
+        }
+
+        float acc[ND][4];
+#pragma unroll
+        for (int n = 0; n < ND; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+        float m_ref[R], m_use[R], sum[R];  // reference maximum (-inf: no key yet), the one subtracted, row sum
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m_ref[r] = -INFINITY;
+            m_use[r] = 0.f;
+            sum[r] = 0.f;
+        }
+
+        for (int t = seg.t0 + warp; t < seg.t1; t += C::kWarps) {
+            ptx::cp_async_wait<C::kStages - 2>();
+            __syncwarp();
+            load();  // into the slot read in the previous step
+            const uint32_t kt = ring + slot_out * C::kTileBytes, vt = kt + C::kHalfBytes;
+            const uint32_t ok = ok_bits >> (slot_out * C::kGroups) & ((1u << C::kGroups) - 1);
+            slot_out = slot_out + 1 == C::kStages ? 0 : slot_out + 1;
+
+            // ---- scores: columns 2·t4, 2·t4+1 of each 8-key column block
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int n = 0; n < NT; n += 2)
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        uint32_t b[4];
+                        ptx::ldmatrix_x4(b, kt + decode_chunk<D, E4M3>(n * 8 + (lane & 7) + (lane >> 4) * 8,
+                                                                       2 * k + (lane >> 3 & 1)));
+                        const uint32_t a1 = WIDE ? qa[k][1] : 0u, a2 = qa[k][R], a3 = WIDE ? qa[k][R + R - 1] : 0u;
+                        ptx::mma_16816<false>(s[n], qa[k][0], a1, a2, a3, b[0], b[1]);
+                        ptx::mma_16816<false>(s[n + 1], qa[k][0], a1, a2, a3, b[2], b[3]);
+                    }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint4 w = ptx::lds128(kt + decode_chunk<D, E4M3>(n * 8 + g, t4 + 4 * c));
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int k = 4 * c + j;
+                            const uint32_t a1 = WIDE ? qa[k][1] : 0u, a2 = qa[k][R], a3 = WIDE ? qa[k][R + R - 1] : 0u;
+                            ptx::mma_16816<true>(s[n], qa[k][0], a1, a2, a3,
+                                                 ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(ws[j])),
+                                                 ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(ws[j] >> 16)));
+                        }
+                    }
+            }
+
+            // ---- mask, maximum, exponentials
+            const int key0 = t * C::kKeys;
+            const bool ragged = key0 + C::kKeys > seg.len || ok != (1u << C::kGroups) - 1;
+            float top[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float x = s[n][2 * r + j] * cs[r];
+                        if (ragged && (key0 + n * 8 + 2 * t4 + j >= seg.len || !(ok >> (n / 2) & 1))) x = -INFINITY;
+                        s[n][2 * r + j] = x;
+                    }
+                top[r] = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
+#pragma unroll
+                for (int n = 1; n < NT; ++n) top[r] = ptx::fmax3(top[r], s[n][2 * r], s[n][2 * r + 1]);
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+            }
+            bool rise = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) rise = rise || top[r] > m_ref[r] + C::kLazy;
+            if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float alpha = 1.f;
+                    if (top[r] > m_ref[r] + C::kLazy) {
+                        alpha = ptx::ex2_approx(m_ref[r] - top[r]);
+                        m_ref[r] = top[r];
+                        m_use[r] = top[r] - C::kBias;
+                    }
+                    sum[r] *= alpha;
+#pragma unroll
+                    for (int n = 0; n < ND; ++n) {
+                        acc[n][2 * r] *= alpha;
+                        acc[n][2 * r + 1] *= alpha;
+                        if constexpr (!WIDE) {
+                            acc[n][2] *= alpha;
+                            acc[n][3] *= alpha;
+                        }
+                    }
+                }
+            }
+
+            // ---- P = hi + lo in 16 bits, O += P V, 16 keys at a time
+#pragma unroll
+            for (int kg = 0; kg < C::kGroups; ++kg) {
+                uint32_t hi[2 * R], lo[2 * R];  // [16-bit pairs of keys 2t4.. | 2t4+8..][row]
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float p0 = ptx::ex2_approx(s[2 * kg + j][2 * r] - m_use[r]);
+                        const float p1 = ptx::ex2_approx(s[2 * kg + j][2 * r + 1] - m_use[r]);
+                        sum[r] += p0 + p1;
+                        if constexpr (E4M3) {
+                            hi[R * j + r] = ptx::pack_f16x2(p0, p1);
+                            const float2 w = ptx::unpack_f16x2(hi[R * j + r]);
+                            lo[R * j + r] = ptx::pack_f16x2(p0 - w.x, p1 - w.y);
+                        } else {
+                            hi[R * j + r] = ptx::pack_bf16x2(p0, p1);
+                            const float2 w = ptx::unpack_bf16x2(hi[R * j + r]);
+                            lo[R * j + r] = ptx::pack_bf16x2(p0 - w.x, p1 - w.y);
+                        }
+                    }
+                auto pv = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
+                    if constexpr (WIDE) {
+                        ptx::mma_16816<E4M3>(c, hi[0], hi[1], hi[2], hi[3], b0, b1);
+                        ptx::mma_16816<E4M3>(c, lo[0], lo[1], lo[2], lo[3], b0, b1);
+                    } else {
+                        ptx::mma_16816<E4M3>(c, hi[0], lo[0], hi[1], lo[1], b0, b1);
+                    }
+                };
+                if constexpr (!E4M3) {
+#pragma unroll
+                    for (int n = 0; n < ND; n += 2) {
+                        uint32_t b[4];
+                        ptx::ldmatrix_x4_trans(
+                            b, vt + decode_chunk<D, E4M3>(kg * 16 + (lane & 7) + (lane >> 3 & 1) * 8, n + (lane >> 4)));
+                        pv(acc[n], b[0], b[1]);
+                        pv(acc[n + 1], b[2], b[3]);
+                    }
+                } else {
+                    // lane (g, t4) reads D/8 values, from column g·D/8 on, of keys 2t4, 2t4+1, 2t4+8, 2t4+9
+                    uint32_t w[4][D / 32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = kg * 16 + 2 * t4 + (i & 1) + (i >> 1) * 8;
+                        if constexpr (D == 128) {
+                            const uint4 x = ptx::lds128(vt + decode_chunk<D, E4M3>(r, g));
+                            w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                        } else {
+                            const uint2 x = ptx::lds64(vt + decode_chunk<D, E4M3>(r, g >> 1) + (g & 1) * 8);
+                            w[i][0] = x.x, w[i][1] = x.y;
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < ND; n += 2) {
+                        // bytes (key a, key b) of values n, n + 1
+                        const uint32_t sel = n % 4 == 0 ? 0x5140u : 0x7362u;
+                        const uint32_t x = __byte_perm(w[0][n / 4], w[1][n / 4], sel);
+                        const uint32_t y = __byte_perm(w[2][n / 4], w[3][n / 4], sel);
+                        pv(acc[n], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x)),
+                           ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(y)));
+                        pv(acc[n + 1], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16)),
+                           ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(y >> 16)));
+                    }
+                }
+            }
+        }
+
+        // ---- the warps' results of this segment, added up: 8 rows at a time
+        float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat);
+        float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+        if constexpr (!WIDE) {
+#pragma unroll
+            for (int n = 0; n < ND; ++n) {
+                acc[n][0] += acc[n][2];
+                acc[n][1] += acc[n][3];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+            if (t4 == 0)
+                // (a sum of zero: no key, or scores of -inf alone; NaN is no zero and is passed on)
+                stat[warp * 16 + g + 8 * r] = make_float2(sum[r] == 0.f ? -INFINITY : m_use[r], sum[r]);
+        }
+        const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
+        const long long slot = 2LL * worker + (first_seg ? 0 : 1);
+        const float vs = p.v_scale ? p.v_scale[h] : 1.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            __syncthreads();
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < C::kWarps; ++w) m = fmaxf(m, stat[w * 16 + g + 8 * r].x);
+            const float mine_m = stat[warp * 16 + g + 8 * r].x;
+            const float f = mine_m == -INFINITY ? 0.f : ptx::ex2_approx(mine_m - m);
+            float* mrow = merge + (warp * 8 + g) * D;
+            if constexpr (E4M3) {
+                // value n of columns 2t4, 2t4+1 is value (column · D/8 + n)
+#pragma unroll
+                for (int n = 0; n < ND; ++n) {
+                    mrow[(2 * t4) * ND + n] = acc[n][2 * r] * f;
+                    mrow[(2 * t4 + 1) * ND + n] = acc[n][2 * r + 1] * f;
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < ND; ++n)
+                    *reinterpret_cast<float2*>(mrow + n * 8 + 2 * t4) =
+                        make_float2(acc[n][2 * r] * f, acc[n][2 * r + 1] * f);
+            }
+            __syncthreads();
+            for (int i = tid; i < 8 * D / 4; i += C::kThreads) {
+                const int row = i / (D / 4), col = i % (D / 4) * 4;
+                if (row + 8 * r >= rows) continue;
+                float ms[C::kWarps], mm = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int w = 0; w < C::kWarps; ++w) {
+                    ms[w] = stat[w * 16 + row + 8 * r].x;
+                    mm = fmaxf(mm, ms[w]);
+                }
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < C::kWarps; ++w) {
+                    if (ms[w] != -INFINITY) l += stat[w * 16 + row + 8 * r].y * ptx::ex2_approx(ms[w] - mm);
+                    const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * D + col);
+                    o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+                }
+                if (whole) {
+                    const float inv = l == 0.f ? 0.f : vs / l;
+                    const long long out = row0 + row + 8 * r;
+                    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.o) + out * D + col) =
+                        make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+                    if (col == 0 && p.lse)
+                        p.lse[out] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+                } else {
+                    *reinterpret_cast<float4*>(p.part_o + ((slot * C::kRows) + row + 8 * r) * D + col) = o;
+                    if (col == 0) p.part_ml[slot * C::kRows + row + 8 * r] = make_float2(mm, l);
+                }
+            }
+        }
+        if (seg.rem == 0) break;
+        decode_next<C::kKeys>(seg, p);
+        __syncthreads();  // stat and merge are written again
+    }
+}
+
+// Adds up the partial results of the cut units. Block (c, row) does row `row`
+// of the unit whose first cut lies between workers c - 1 and c, if there is
+// one: the threads share out the workers, then add across in shared memory.
+// Bound by latency: a few KB per block.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128) fa_decode_join_kernel(const DecodeParams p) {
+    constexpr int kCols = D / 4, kParts = 128 / kCols;
+    __shared__ float4 sh_o[128];
+    __shared__ float2 sh_ml[kParts];
+    ptx::griddep_wait();
+    const int4 meta = p.meta[blockIdx.x];
+    const int row = blockIdx.y;
+    if (meta.x < 0) return;
+    const int h = meta.y / p.row_groups, rg = meta.y - h * p.row_groups;
+    if (row >= p.G - rg * ROWS) return;
+    const int tid = threadIdx.x, part = tid / kCols, col = tid % kCols;
+    const int n = meta.w - static_cast<int>(blockIdx.x) + 2;  // partials: the first worker's, then one per worker
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = part; i < n; i += kParts) {
+        const long long slot = i == 0 ? meta.z : 2LL * (blockIdx.x + i - 1);
+        const float2 ml = p.part_ml[slot * ROWS + row];
+        const float4 x = *reinterpret_cast<const float4*>(p.part_o + (slot * ROWS + row) * D + col * 4);
+        const float mm = fmaxf(m, ml.x);
+        const float fa_ = m == -INFINITY ? 0.f : ptx::ex2_approx(m - mm);
+        const float fb = ml.x == -INFINITY ? 0.f : ptx::ex2_approx(ml.x - mm);
+        l = l * fa_ + ml.y * fb;
+        o.x = o.x * fa_ + x.x * fb;
+        o.y = o.y * fa_ + x.y * fb;
+        o.z = o.z * fa_ + x.z * fb;
+        o.w = o.w * fa_ + x.w * fb;
+        m = mm;
+    }
+    sh_o[tid] = o;
+    if (col == 0) sh_ml[part] = make_float2(m, l);
+    __syncthreads();
+    if (part != 0) return;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) mm = fmaxf(mm, sh_ml[i].x);
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        if (sh_ml[i].x == -INFINITY) continue;
+        const float f = ptx::ex2_approx(sh_ml[i].x - mm);
+        const float4 x = sh_o[i * kCols + col];
+        l += sh_ml[i].y * f;
+        o.x += x.x * f;
+        o.y += x.y * f;
+        o.z += x.z * f;
+        o.w += x.w * f;
+    }
+    const float inv = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[h] : 1.f) / l;
+    const long long out = static_cast<long long>(meta.x) * p.Hkv * p.G + h * p.G + rg * ROWS + row;
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.o) + out * D + col * 4) =
+        make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+    if (col == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+}
+
+}  // namespace fa

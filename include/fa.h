@@ -31,6 +31,8 @@
 #ifndef FA_H_
 #define FA_H_
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -48,7 +50,9 @@ typedef enum fa_status {
                                          captured into a CUDA graph before the device's first ordinary call */
     FA_ERR_DEVICE_TIMEOUT = -8,       /* a kernel gave up waiting on an mbarrier (see fa_device_status) */
     FA_ERR_BAD_SCALE = -9,            /* scale is not finite, or not > 0 */
-    FA_ERR_ALIAS = -10                /* o or lse overlaps q, k or v, or lse overlaps o */
+    FA_ERR_ALIAS = -10,               /* o or lse overlaps q, k or v, or lse overlaps o */
+    FA_ERR_WORKSPACE = -11,           /* workspace NULL or smaller than the call needs */
+    FA_ERR_BAD_TYPE = -12             /* cache element type is not one of FA_CACHE_* */
 } fa_status;
 
 /*
@@ -186,6 +190,169 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
  * sm_count < 1.
  */
 int fa_varlen_num_splits(int B, int H, int total_k, int max_seqlen_q, int sm_count);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Serving from a paged key-value cache.
+ *
+ * A step of a server: fa_page_maps gives the step's new tokens their pages,
+ * slots and positions; fa_cache_append turns q and k by their rotary positions
+ * and writes k and v to their slots; fa_decode_paged attends one new token per
+ * request over its pages (prompts: fa_fwd_varlen on the rotated q, k and v).
+ * fa_rotary is the rotary step alone, for training, with its gradient.
+ * (The source pages have no counterpart to any of these.)
+ *
+ * All are asynchronous on `stream`, allocate nothing, keep no pointer and
+ * check their arguments on the host before anything is queued, as fa_fwd does;
+ * they may be captured into CUDA graphs once the device has had one ordinary
+ * call of any of them (a captured call before then returns FA_ERR_LAUNCH).
+ * They keep no state on the device either: calls on different streams and
+ * replays of different graphs share nothing but the buffers given to them.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element types of a cache. */
+#define FA_CACHE_BF16 0
+#define FA_CACHE_E4M3 1 /* 8-bit floats; a value is code * scale[head] */
+
+/*
+ * fa_paged_cache — one layer's keys and values in pages ("blocks") of
+ * page_size tokens. Value x of head h of token t of block b is at
+ * k[b*k_block + t*k_token + h*k_head + x] (strides in elements), so token-major
+ * blocks [page_size, heads, d], head-major blocks [heads, page_size, d] and
+ * keys and values side by side in one tensor are all covered.
+ *
+ * page_size is a power of two, 16 to 65536; d is 64 or 128, its values
+ * contiguous. k and v are 16-byte aligned; strides are multiples of 16 bytes
+ * and at least d (that of a dimension of size 1 is not used).
+ * k_scale, v_scale: device fp32 [heads], or NULL for 1. They apply to caches
+ * of either type when reading, and to FA_CACHE_E4M3 when writing.
+ */
+typedef struct fa_paged_cache {
+    void* k;
+    void* v;
+    const float* k_scale;
+    const float* v_scale;
+    long long k_block, k_token, k_head;
+    long long v_block, v_token, v_head;
+    int type; /* FA_CACHE_BF16 or FA_CACHE_E4M3 */
+    int num_blocks, page_size, heads, d;
+} fa_paged_cache;
+
+/*
+ * fa_decode_paged — attention of one new token per request over its pages:
+ *   O = softmax(scale · q Kᵀ) V over the first seq_lens[b] keys of request b,
+ *   LSE = ln Σ exp of the scaled scores.
+ *
+ *   q, o         bf16 [B, Hq, d], device, contiguous, 16-byte aligned
+ *   lse          fp32 [B, Hq], device, or NULL
+ *   cache        see above; Hq is a multiple of cache->heads, and query head i
+ *                reads key head i / (Hq / heads)
+ *   block_table  int32 [B][table_stride], device; entry i < table_width of row b
+ *                is the block of keys i*page_size .. of request b
+ *   seq_lens     int32 [B], device: keys of each request, the new token's own
+ *                among them (append it first). 0 or less: O = 0, LSE = -inf.
+ *                More than table_width*page_size counts as that many
+ *                (at most 2^31 - 65536).
+ *   workspace    device, 16-byte aligned, at least fa_decode_paged_workspace()
+ *                bytes; needs no initial value, holds nothing after the call's
+ *                kernels. Calls (or graph replays) that may overlap in time
+ *                need workspaces of their own.
+ *
+ * Keys whose block is outside [0, num_blocks) are hidden, as if they were not
+ * there; table entries past a request's last key are not read. Values in
+ * hidden and unfilled places of a page (NaN included) have no effect.
+ * The result does not depend on what else runs; which partial sums are joined
+ * depends on the batch, so the same request may differ in the last bits
+ * between batches.
+ */
+int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block_table, const int* seq_lens, void* o,
+                    float* lse, int B, int Hq, int table_width, long long table_stride, float scale, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * fa_decode_paged_workspace — host-only: workspace bytes of fa_decode_paged
+ * for these sizes on a GPU with sm_count SMs (a few MB at most), or a negative
+ * status under the call's own rules.
+ */
+long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_type, int page_size, int table_width,
+                                    int sm_count);
+
+/*
+ * fa_rotary — rotary positions of x [B, H, N, d] (bf16, device), into y.
+ * Pair i < rotary_dim/2 of each head is turned by a = position · inv_freq[i]:
+ *   (y1, y2) = factor · (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
+ * where the pair is values (i, i + rotary_dim/2), or (2i, 2i+1) when
+ * `interleaved`; values from rotary_dim on are copied. `inverse` uses -a: the
+ * transposed map, which is the gradient of y with respect to x.
+ *
+ *   positions   int32, device: that of (b, n) is positions[b*position_stride + n]
+ *               (0: shared by the batch). Any int32 value.
+ *   inv_freq    fp64 [rotary_dim/2], device, finite, in radians per position.
+ *               The angle is off by |position|·2^-51 + 2^-29 radians at most
+ *               (frequencies up to 1).
+ *   x_strides, y_strides  host arrays: elements from one b, h, n to the next
+ *               (multiples of 8; x's may be 0; those of a dimension of size 1
+ *               are not used); d's values are contiguous. y may be x itself
+ *               with the same strides, or overlap nothing of it.
+ *   rotary_dim  a multiple of 16, 0 to d.  factor finite (1: a pure rotation).
+ *
+ * Sums and products are fp32, rounded to bf16 once.
+ */
+int fa_rotary(const void* x, void* y, const int* positions, const double* inv_freq, int B, int H, int N, int d,
+              const long long* x_strides, const long long* y_strides, long long position_stride, int rotary_dim,
+              int interleaved, int inverse, float factor, void* stream);
+
+/*
+ * fa_cache_append — one step's tokens: q and k turned as by fa_rotary, q into
+ * q_out, k (and v as it is) into the cache at their slots.
+ *
+ *   q, q_out    bf16 [T, Hq, d]; k, v, k_out  bf16 [T, heads, d], device: a
+ *               token's heads contiguous, tokens *_stride elements apart (a
+ *               multiple of 8), so that slices of one projection's output can
+ *               be given. k_out may be NULL. q_out may be q and k_out may be k,
+ *               with the same stride; apart from that outputs overlap nothing.
+ *   positions, slots  int32 [T], device. Slot s is token s % page_size of block
+ *               s / page_size. A token whose slot is negative or past the cache
+ *               is padding: nothing of it is written, in no output.
+ *               Slots of one call are distinct (of two tokens with the same
+ *               slot, either's values are kept, in pieces of 8 or 16 values).
+ *
+ * FA_CACHE_E4M3: code = e4m3(x / scale[head]) from the fp32 value, by the
+ * scale's fp32 reciprocal, round to nearest even, past ±448 to ±448, NaN kept.
+ */
+int fa_cache_append(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                    long long v_stride, const int* positions, const int* slots, const double* inv_freq,
+                    const fa_paged_cache* cache, void* q_out, void* k_out, long long q_out_stride,
+                    long long k_out_stride, int T, int Hq, int rotary_dim, int interleaved, float factor,
+                    void* stream);
+
+/*
+ * fa_page_maps — block tables and slot maps of one step, from request lengths.
+ * Request b < B (1 to 8192) holds context_lens[b] tokens and gets new_lens[b]
+ * more (negative counts as 0). All arrays int32, device.
+ *
+ *   block_table   [B][table_stride], in and out: the entries of the pages that
+ *                 the context holds are kept; those of pages that the new tokens
+ *                 need beyond them are written, from unused_blocks in order,
+ *                 request by request (-1 once it has run out). Others are kept.
+ *   unused_blocks [num_unused], read only: the caller drops the first counts[0].
+ *   cu_seqlens    [B + 1]: exclusive sums of the new lengths (fa_fwd_varlen's
+ *                 cu_seqlens_q)
+ *   seq_lens      [B]: context + new (fa_decode_paged's seq_lens)
+ *   slots, positions  [T]: of token t, the (t - cu_seqlens[b])-th new one of its
+ *                 request b; slot -1 where its page is missing (none left, past
+ *                 table_width, or a negative entry). Tokens past the last
+ *                 request's get slot -1, position 0 (a padded batch); tokens past
+ *                 T are not written.
+ *   counts        [4]: pages taken, pages missing, new tokens in all, requests
+ *                 longer than table_width*page_size
+ *
+ * Sums past 2^31 - 1 stay there. The arrays written overlap no other.
+ */
+int fa_page_maps(const int* context_lens, const int* new_lens, int* block_table, const int* unused_blocks, int* slots,
+                 int* positions, int* cu_seqlens, int* seq_lens, int* counts, int B, int table_width,
+                 long long table_stride, int num_unused, int page_size, int T, void* stream);
 
 /* Static English text for a return code (never NULL). */
 const char* fa_strerror(int status);
