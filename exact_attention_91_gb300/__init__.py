@@ -13,6 +13,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 import typing
 
 from .build import LIB_PATH
@@ -90,14 +91,14 @@ def load_library(path: str | None = None):
     lib.fa_selftest_exp2.restype = i
     lib.fa_selftest_ex2_rate.argtypes = [vp, vp, i, i, vp]
     lib.fa_selftest_ex2_rate.restype = i
-    ll, pc = ctypes.c_longlong, ctypes.POINTER(FaPagedCache)
-    lib.fa_decode_paged.argtypes = [vp, pc, vp, vp, vp, vp, i, i, i, ll, f, vp, ctypes.c_size_t, vp]
+    ll = ctypes.c_longlong
+    lib.fa_decode_paged.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, ll, f, vp, ctypes.c_size_t, vp]
     lib.fa_decode_paged.restype = i
     lib.fa_decode_paged_workspace.argtypes = [i] * 8
     lib.fa_decode_paged_workspace.restype = ll
     lib.fa_rotary.argtypes = [vp, vp, vp, vp, i, i, i, i, vp, vp, ll, i, i, i, f, vp]
     lib.fa_rotary.restype = i
-    lib.fa_cache_append.argtypes = [vp, vp, vp, ll, ll, ll, vp, vp, vp, pc, vp, vp, ll, ll, i, i, i, i, f, vp]
+    lib.fa_cache_append.argtypes = [vp, vp, vp, ll, ll, ll, vp, vp, vp, vp, vp, vp, ll, ll, i, i, i, i, f, vp]
     lib.fa_cache_append.restype = i
     lib.fa_page_maps.argtypes = [vp] * 9 + [i, i, ll, i, i, i, vp]
     lib.fa_page_maps.restype = i
@@ -188,8 +189,9 @@ def fa_decode_paged(q: int, cache: FaPagedCache, block_table: int, seq_lens: int
                     Hq: int, table_width: int, table_stride: int, scale: float, workspace: int, workspace_bytes: int,
                     stream: int | None) -> int:
     """The C ``fa_decode_paged``: device pointers as ints, returns the status code."""
-    return load_library().fa_decode_paged(q, cache, block_table, seq_lens, o, lse or None, B, Hq, table_width,
-                                          table_stride, scale, workspace or None, workspace_bytes, stream or None)
+    return load_library().fa_decode_paged(q, ctypes.byref(cache), block_table, seq_lens, o, lse or None, B, Hq,
+                                          table_width, table_stride, scale, workspace or None, workspace_bytes,
+                                          stream or None)
 
 
 def fa_decode_paged_workspace(B: int, Hq: int, Hkv: int, d: int, cache_type: int, page_size: int, table_width: int,
@@ -216,8 +218,8 @@ def fa_cache_append(q: int, k: int, v: int, q_stride: int, k_stride: int, v_stri
                     stream: int | None) -> int:
     """The C ``fa_cache_append``: device pointers as ints, returns the status code."""
     return load_library().fa_cache_append(q, k, v, q_stride, k_stride, v_stride, positions, slots, inv_freq or None,
-                                          cache, q_out, k_out or None, q_out_stride, k_out_stride, T, Hq, rotary_dim,
-                                          int(bool(interleaved)), factor, stream or None)
+                                          ctypes.byref(cache), q_out, k_out or None, q_out_stride, k_out_stride, T,
+                                          Hq, rotary_dim, int(bool(interleaved)), factor, stream or None)
 
 
 def fa_page_maps(context_lens: int, new_lens: int, block_table: int, unused_blocks: int, slots: int, positions: int,
@@ -369,55 +371,69 @@ def attention_forward_heads(q, k, v, head_start: int, head_count: int, causal: b
 # ---- serving from a paged cache, rotary positions ---------------------------
 
 
-def _serve_launch(torch, device, stream, call, made, what):
-    """Runs ``call(stream handle)`` with ``device`` current. Tensors that were
-    made for the call belong to the current stream's part of the allocator;
-    when another ``stream`` uses them it is told so, so that none is handed out
-    again while that stream's kernels may still run."""
-    if stream is not None:
+# struct fa_paged_cache as bytes (laid out as FaPagedCache), which a call takes in
+# a tenth of the time that building the ctypes structure does
+_pack_cache = struct.Struct("PPPPqqqqqqiiiii4x").pack
+
+
+def _launch(torch, fn, args, device, stream, made, what):
+    """``fn(*args, stream handle)`` with CUDA device number ``device`` current.
+    Tensors that were made for the call belong to the current stream's part of
+    the allocator; when another ``stream`` uses them it is told so, so that none
+    is handed out again while that stream's kernels may still run."""
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+    else:
+        handle = stream.cuda_stream
         for t in made:
             t.record_stream(stream)
-        handle = stream.cuda_stream
-    else:
-        handle = _current_stream_handle(torch, device)
-    if device.index == torch.cuda.current_device():
-        rc = call(handle or None)
+    if device == torch.cuda.current_device():
+        rc = fn(*args, handle or None)
     else:
         with torch.cuda.device(device):
-            rc = call(handle or None)
+            rc = fn(*args, handle or None)
     if rc != FA_OK:
         raise FaError(rc, what)
 
 
-def _check_on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, the device of the first tensor")
+def _elsewhere(device, tensors):
+    """Raises for the tensors (of those that are not None) that are not on CUDA
+    device number ``device``; -1 is the CPU."""
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("all tensors must be on the same CUDA device")
 
 
-def _check_int32(torch, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32")
-
-
-def _paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale) -> FaPagedCache:
-    """The C description of caches indexed [block, token, head, d]."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must both be [num_blocks, page_size, heads, d]")
-    if v_cache.dtype != k_cache.dtype or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+def _pack_paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale):
+    """(struct fa_paged_cache as bytes, its type) of caches indexed [block,
+    token, head, d]."""
+    t = k_cache.dtype
+    if t is torch.bfloat16:
+        kind = CACHE_BF16
+    elif t is torch.float8_e4m3fn:
+        kind = CACHE_E4M3
+    else:
         raise TypeError("k_cache and v_cache must both be bf16 or both float8_e4m3fn")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[3] != 1 or vs[3] != 1:
+    if v_cache.dtype is not t:
+        raise TypeError("k_cache and v_cache must both be bf16 or both float8_e4m3fn")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, page_size, heads, d]")
+    kb, kt, kh, kd = k_cache.stride()
+    vb, vt, vh, vd = v_cache.stride()
+    if kd != 1 or vd != 1:
         raise ValueError("the d values of a cache row must be contiguous")
-    _check_on(device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
-    nb, page, heads, d = k_cache.shape
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is not None and (t.dtype != torch.float32 or t.shape != (heads,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous fp32 tensor of one value per key head")
-    return FaPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
-                        v_scale.data_ptr() if v_scale is not None else None, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                        CACHE_E4M3 if k_cache.dtype == torch.float8_e4m3fn else CACHE_BF16, nb, page, heads, d)
+    if k_cache.get_device() != device or v_cache.get_device() != device:
+        _elsewhere(device, (k_cache, v_cache))
+    scales = [0, 0]
+    for i, x in enumerate((k_scale, v_scale)):
+        if x is not None:
+            if x.dtype is not torch.float32 or x.shape != (shape[2],) or not x.is_contiguous():
+                raise ValueError("k_scale and v_scale must be contiguous fp32 tensors of one value per key head")
+            _elsewhere(device, (x,))
+            scales[i] = x.data_ptr()
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), *scales, kb, kt, kh, vb, vt, vh, kind, *shape), kind
 
 
 @functools.lru_cache(maxsize=256)
@@ -445,49 +461,51 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: fl
     given to keep allocation out of the call; calls that may overlap in time
     need one each."""
     import torch
-    if q.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16:
         raise TypeError("q must be bf16")
-    if q.dim() != 3 or block_table.dim() != 2 or seq_lens.dim() != 1:
+    if block_table.dtype is not torch.int32 or seq_lens.dtype is not torch.int32:
+        raise TypeError("block_table and seq_lens must be int32")
+    if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [B, Hq, d], block_table [B, width] and seq_lens [B]")
-    B, Hq, d = q.shape
-    if not q.is_cuda:
+    device = q.get_device()
+    if device < 0:
         raise ValueError("all inputs must be CUDA tensors")
-    if k_cache.dim() != 4 or k_cache.shape[3] != d or block_table.shape[0] != B or seq_lens.shape[0] != B:
-        raise ValueError("q, the caches, block_table and seq_lens do not fit together")
-    if not q.is_contiguous() or not seq_lens.is_contiguous() or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    B, Hq, d = q.shape
+    rows, width = block_table.shape
+    if rows != B or seq_lens.shape != (B,):
+        raise ValueError("q must be [B, Hq, d], block_table [B, width] and seq_lens [B]")
+    row_stride, step = block_table.stride()
+    if (step != 1 and width > 1) or not q.is_contiguous() or not seq_lens.is_contiguous():
         raise ValueError("q, seq_lens and the rows of block_table must be contiguous")
-    _check_int32(torch, block_table=block_table, seq_lens=seq_lens)
-    device = q.device
-    _check_on(device, block_table=block_table, seq_lens=seq_lens, out=out, lse=lse, workspace=workspace)
-    cache = _paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    made = []
+    _elsewhere(device, (block_table, seq_lens, out, lse, workspace))
+    cache, kind = _pack_paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale)
+    _, page, heads, cache_d = k_cache.shape
+    if cache_d != d:
+        raise ValueError("q and the caches must have the same d")
+    made = ()
     if out is None:
         out = torch.empty_like(q)
-        made.append(out)
-    elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+        made = (out,)
+    elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor of q's shape")
     if lse is None:
         if return_lse:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
-            made.append(lse)
-    elif lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous():
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+            made += (lse,)
+    elif lse.dtype is not torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [B, Hq]")
     if workspace is None:
-        n = _decode_workspace_bytes(B, Hq, cache.heads, d, cache.type, cache.page_size, block_table.shape[1],
-                                    device.index)
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
-        made.append(workspace)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        room = _decode_workspace_bytes(B, Hq, heads, d, kind, page, width, device)
+        workspace = torch.empty(room, dtype=torch.uint8, device=q.device)
+        made += (workspace,)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    lib = _lib or load_library()
-    _serve_launch(torch, device, stream,
-                  lambda s: lib.fa_decode_paged(q.data_ptr(), cache, block_table.data_ptr(), seq_lens.data_ptr(),
-                                                out.data_ptr(), lse.data_ptr() if lse is not None else None, B, Hq,
-                                                block_table.shape[1], block_table.stride(0), scale,
-                                                workspace.data_ptr(), workspace.numel(), s),
-                  made, "fa_decode_paged")
+    else:
+        room = workspace.numel()
+    _launch(torch, (_lib or load_library()).fa_decode_paged,
+            (q.data_ptr(), cache, block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+             lse.data_ptr() if lse is not None else None, B, Hq, width, row_stride, 1.0 / math.sqrt(d) if scale is None
+             else scale, workspace.data_ptr(), room), device, stream, made, "fa_decode_paged")
     return (out, lse) if return_lse else out
 
 
@@ -544,14 +562,18 @@ def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: dict | None
     return (freq.to(device) if device is not None else freq), out_factor
 
 
-def _rotary_dim(torch, device, inv_freq):
+def _frequencies(torch, device, inv_freq):
     """(rotary_dim, pointer) of the frequencies; none: (0, None)."""
     if inv_freq is None:
         return 0, None
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous fp64 tensor [rotary_dim / 2]")
-    _check_on(device, inv_freq=inv_freq)
+    if inv_freq.get_device() != device:
+        _elsewhere(device, (inv_freq,))
     return 2 * inv_freq.shape[0], inv_freq.data_ptr() or None
+
+
+_three = struct.Struct("qqq").pack  # strides, as the C call reads them
 
 
 def rotary(x, positions, inv_freq, interleaved: bool = False, inverse: bool = False, factor: float = 1.0, out=None,
@@ -564,45 +586,49 @@ def rotary(x, positions, inv_freq, interleaved: bool = False, inverse: bool = Fa
     the gradient with respect to x. ``out`` may be x. Not differentiable by
     itself: ``torch.ops.fa91.rotary`` is."""
     import torch
-    if x.dtype != torch.bfloat16:
+    if x.dtype is not torch.bfloat16:
         raise TypeError("x must be bf16")
-    _check_int32(torch, positions=positions)
-    if x.dim() == 4:
-        B, H, N, d = x.shape
-        if positions.shape not in ((N,), (B, N)):
+    if positions.dtype is not torch.int32:
+        raise TypeError("positions must be int32")
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("x must be a CUDA tensor")
+    shape, pos_stride = x.shape, 0
+    if len(shape) == 4:
+        B, H, N, d = shape
+        sb, sh, sn, sd = x.stride()
+        if positions.dim() == 2 and positions.shape == (B, N):
+            pos_stride, step = positions.stride()
+        elif positions.shape == (N,):
+            step, = positions.stride()
+        else:
             raise ValueError("positions must be [N] or [B, N]")
-        xs = x.stride()[:3]
-        pos_stride = positions.stride(0) if positions.dim() == 2 else 0
-    elif x.dim() == 3:
-        N, H, d = x.shape
-        B = 1
+    elif len(shape) == 3:
+        (N, H, d), B, sb = shape, 1, 0
+        sn, sh, sd = x.stride()
         if positions.shape != (N,):
             raise ValueError("positions must be [T]")
-        xs = (0, x.stride(1), x.stride(0))
-        pos_stride = 0
+        step, = positions.stride()
     else:
         raise ValueError("x must be [B, H, N, d] or [T, H, d]")
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    if x.stride(-1) != 1 or (N > 1 and positions.stride(-1) != 1):
+    if sd != 1 or (step != 1 and N > 1):
         raise ValueError("d of x and the rows of positions must be contiguous")
-    device = x.device
-    _check_on(device, positions=positions, out=out)
-    r, freq = _rotary_dim(torch, device, inv_freq)
-    made = []
+    _elsewhere(device, (positions, out))
+    r, freq = _frequencies(torch, device, inv_freq)
+    made = ()
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
-        made.append(out)
-    elif out.dtype != torch.bfloat16 or out.shape != x.shape or out.stride(-1) != 1:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        made = (out,)
+    elif out.dtype is not torch.bfloat16 or out.shape != shape or out.stride(-1) != 1:
         raise ValueError("out must be a bf16 tensor of x's shape with d contiguous")
-    ys = out.stride()[:3] if x.dim() == 4 else (0, out.stride(1), out.stride(0))
-    lib = _lib or load_library()
-    three = ctypes.c_longlong * 3
-    _serve_launch(torch, device, stream,
-                  lambda s: lib.fa_rotary(x.data_ptr(), out.data_ptr(), positions.data_ptr(), freq, B, H, N, d,
-                                          three(*xs), three(*ys), pos_stride, r, 1 if interleaved else 0,
-                                          1 if inverse else 0, factor, s),
-                  made, "fa_rotary")
+    if len(shape) == 4:
+        tb, th, tn, _ = out.stride()
+    else:
+        (tn, th, _), tb = out.stride(), 0
+    _launch(torch, (_lib or load_library()).fa_rotary,
+            (x.data_ptr(), out.data_ptr(), positions.data_ptr(), freq, B, H, N, d, _three(sb, sh, sn),
+             _three(tb, th, tn), pos_stride, r, 1 if interleaved else 0, 1 if inverse else 0, factor), device, stream,
+            made, "fa_rotary")
     return out
 
 
@@ -619,41 +645,46 @@ def cache_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interlea
     be slices of one projection's output. float8_e4m3fn caches hold value /
     scale, with ``k_scale`` / ``v_scale`` fp32 [heads] (None: 1)."""
     import torch
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16:
-            raise TypeError("q, k, v must be bf16")
-        if t.dim() != 3 or t.shape[0] != q.shape[0] or t.shape[2] != q.shape[2]:
-            raise ValueError("q must be [T, Hq, d] and k, v [T, heads, d]")
-        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError(f"the heads of a token of {name} must be contiguous")
-    T, Hq, d = q.shape
-    if not q.is_cuda:
+    bf16 = torch.bfloat16
+    if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16:
+        raise TypeError("q, k, v must be bf16")
+    if positions.dtype is not torch.int32 or slots.dtype is not torch.int32:
+        raise TypeError("positions and slots must be int32")
+    device = q.get_device()
+    if device < 0:
         raise ValueError("all inputs must be CUDA tensors")
-    if k_cache.dim() != 4 or k.shape != v.shape or k_cache.shape[2:] != k.shape[1:]:
-        raise ValueError("k, v and the caches do not fit together")
-    _check_int32(torch, positions=positions, slots=slots)
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("q must be [T, Hq, d] and k, v [T, heads, d]")
+    T, Hq, d = q.shape
+    Tk, heads, dk = k.shape
+    if Tk != T or dk != d or k_cache.shape[2:] != (heads, d):
+        raise ValueError("q, k, v and the caches do not fit together")
     if positions.shape != (T,) or slots.shape != (T,) or not positions.is_contiguous() or not slots.is_contiguous():
         raise ValueError("positions and slots must be contiguous [T]")
-    device = q.device
-    _check_on(device, k=k, v=v, positions=positions, slots=slots, q_out=q_out, k_out=k_out)
-    cache = _paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale)
-    r, freq = _rotary_dim(torch, device, inv_freq)
-    made = []
+    _elsewhere(device, (k, v, positions, slots, q_out, k_out))
+    cache, _ = _pack_paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale)
+    r, freq = _frequencies(torch, device, inv_freq)
+    made = ()
     if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
-        made.append(q_out)
-    for t, like in ((q_out, q), (k_out, k)):
-        if t is not None and (t.dtype != torch.bfloat16 or t.shape != like.shape or t.stride(2) != 1 or
-                              (t.shape[1] > 1 and t.stride(1) != d)):
-            raise ValueError("q_out and k_out must be bf16, of q's and k's shape, a token's heads contiguous")
-    lib = _lib or load_library()
-    _serve_launch(torch, device, stream,
-                  lambda s: lib.fa_cache_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), k.stride(0),
-                                                v.stride(0), positions.data_ptr(), slots.data_ptr(), freq, cache,
-                                                q_out.data_ptr(), k_out.data_ptr() if k_out is not None else None,
-                                                q_out.stride(0), k_out.stride(0) if k_out is not None else 0, T, Hq, r,
-                                                1 if interleaved else 0, factor, s),
-                  made, "fa_cache_append")
+        q_out = torch.empty((T, Hq, d), dtype=bf16, device=q.device)
+        made = (q_out,)
+    elif q_out.dtype is not bf16 or q_out.shape != q.shape:
+        raise ValueError("q_out must be bf16 and of q's shape")
+    if k_out is not None and (k_out.dtype is not bf16 or k_out.shape != k.shape):
+        raise ValueError("k_out must be bf16 and of k's shape")
+    strides = []
+    for t, h in ((q, Hq), (k, heads), (v, heads), (q_out, Hq), (k_out, heads)):
+        if t is None:
+            strides.append(0)
+            continue
+        row, head, step = t.stride()
+        if step != 1 or (head != d and h > 1):
+            raise ValueError("the heads of a token of q, k, v, q_out and k_out must be contiguous")
+        strides.append(row)
+    _launch(torch, (_lib or load_library()).fa_cache_append,
+            (q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides[:3], positions.data_ptr(), slots.data_ptr(), freq,
+             cache, q_out.data_ptr(), k_out.data_ptr() if k_out is not None else None, *strides[3:], T, Hq, r,
+             1 if interleaved else 0, factor), device, stream, made, "fa_cache_append")
     return q_out
 
 
@@ -676,37 +707,39 @@ def page_maps(context_lens, new_lens, block_table, unused_blocks, page_size: int
     length of the token maps, which may be more than the step's tokens (the
     rest are padding: slot -1). See ``fa_page_maps`` in include/fa.h."""
     import torch
-    _check_int32(torch, context_lens=context_lens, new_lens=new_lens, block_table=block_table,
-                 unused_blocks=unused_blocks)
-    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [B, width] with contiguous rows")
-    B, width = block_table.shape
-    if not block_table.is_cuda:
+    i32 = torch.int32
+    if (context_lens.dtype is not i32 or new_lens.dtype is not i32 or block_table.dtype is not i32 or
+            unused_blocks.dtype is not i32):
+        raise TypeError("context_lens, new_lens, block_table and unused_blocks must be int32")
+    device = block_table.get_device()
+    if device < 0:
         raise ValueError("all inputs must be CUDA tensors")
-    if context_lens.shape != (B,) or new_lens.shape != (B,) or unused_blocks.dim() != 1:
-        raise ValueError("context_lens and new_lens must be [B], unused_blocks one list")
-    if not (context_lens.is_contiguous() and new_lens.is_contiguous() and unused_blocks.is_contiguous()):
-        raise ValueError("lengths and unused_blocks must be contiguous")
-    device = block_table.device
-    _check_on(device, context_lens=context_lens, new_lens=new_lens, unused_blocks=unused_blocks)
+    if block_table.dim() != 2 or unused_blocks.dim() != 1:
+        raise ValueError("block_table must be [B, width] and unused_blocks one list")
+    B, width = block_table.shape
+    row_stride, step = block_table.stride()
+    if context_lens.shape != (B,) or new_lens.shape != (B,):
+        raise ValueError("context_lens and new_lens must be [B]")
+    if ((step != 1 and width > 1) or not context_lens.is_contiguous() or not new_lens.is_contiguous() or
+            not unused_blocks.is_contiguous()):
+        raise ValueError("the rows of block_table, the lengths and unused_blocks must be contiguous")
+    _elsewhere(device, (context_lens, new_lens, unused_blocks))
     T = int(num_tokens)
     if T < 0:
         raise ValueError("num_tokens must be >= 0")
-    made = []
+    made = ()
     if out is None:
-        whole = torch.empty(2 * T + 2 * B + 5, dtype=torch.int32, device=device)
-        out = PageMaps(*whole.split((T, T, B + 1, B, 4)))
-        made.append(whole)
+        whole = torch.empty(2 * T + 2 * B + 5, dtype=i32, device=block_table.device)
+        out = PageMaps(*whole.split_with_sizes((T, T, B + 1, B, 4)))
+        made = (whole,)
     else:
         for t, n in zip(out, (T, T, B + 1, B, 4)):
-            if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.device != device:
+            if t.dtype is not i32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != device:
                 raise ValueError("out must be int32 tensors [T], [T], [B + 1], [B] and [4] on the same device")
-    lib = _lib or load_library()
-    _serve_launch(torch, device, stream,
-                  lambda s: lib.fa_page_maps(context_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-                                             unused_blocks.data_ptr() or None, out[0].data_ptr() or None,
-                                             out[1].data_ptr() or None, out[2].data_ptr(), out[3].data_ptr(),
-                                             out[4].data_ptr(), B, width, block_table.stride(0),
-                                             unused_blocks.shape[0], page_size, T, s),
-                  made, "fa_page_maps")
+    slots, positions, cu_seqlens, seq_lens, counts = out
+    _launch(torch, (_lib or load_library()).fa_page_maps,
+            (context_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), unused_blocks.data_ptr() or None,
+             slots.data_ptr() or None, positions.data_ptr() or None, cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+             counts.data_ptr(), B, width, row_stride, unused_blocks.shape[0], page_size, T), device, stream, made,
+            "fa_page_maps")
     return out

@@ -7,13 +7,17 @@
 // values from r on are copied. The map is linear, and its gradient is the
 // transposed map: the same with -sin.
 //
-// Both are bound by HBM (each value read and written once). A warp takes one
-// token and some of its heads: its lanes compute the token's cos and sin once,
-// two frequencies each, leave them in shared memory, and use them for every
-// head. Angles are exact in fixed point: f/2π as a 64-bit fraction of a turn
-// times the position, modulo 2^64, is the angle's fraction of a turn, off by
-// |position| · 2^-54 turns at most (f <= 1: the rounding of f/2π in 64 bits),
-// cut to 2^-32 turns; cos and sin follow in fp32.
+// Both are bound by HBM (each value read and written once). A lane holds 16
+// values of a head, d/16 lanes a head, and a warp the same head of 32/(d/16)
+// tokens: 1 KB contiguous in a head-major tensor, 256-byte rows in a token-major
+// one. A lane computes the cos and sin of its own eight pairs of its own token
+// once, so each is computed by one lane only and needs no exchange, and uses
+// them for every head that the warp takes, kRotHeads heads' loads in flight at
+// a time; the first loads are issued before the cos and sin.
+// Angles are exact in fixed point: f/2π as a 64-bit fraction of a turn times
+// the position, modulo 2^64, is the angle's fraction of a turn, off by
+// |position| · 2^-62 turns at most (f < 2), cut to 2^-32 turns; cos and sin
+// follow in fp32.
 #pragma once
 
 #include "fa_common.cuh"
@@ -21,6 +25,7 @@
 namespace fa {
 
 constexpr int kRotWarps = 8;
+constexpr int kRotHeads = 4;  // heads whose loads a lane has in flight
 
 // One tensor of a rotary launch: heads of token n at src + n·src_n + h·src_h.
 struct RotTensor {
@@ -51,10 +56,18 @@ struct RotParams {
     int heads_per_warp;
 };
 
-// A frequency as a fraction of a turn per position, in units of 2^-64.
+// A frequency (radians per position) as a fraction of a turn, in units of
+// 2^-64. f = m·2^(e-52) with a 53-bit m, and f/2π · 2^64 = (m·2^13/2π)·2^(e-1),
+// whose first factor is the high half of (m·2^11) · (2^66/2π). Integers all
+// through: 64-bit floats run at 1/64 of the rate here.
 __device__ __forceinline__ unsigned long long rot_turns(double inv_freq) {
-    const double turns = inv_freq * 0.15915494309189533577;
-    return __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
+    const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(inv_freq));
+    const int e = static_cast<int>(bits >> 52 & 0x7ff) - 1023;
+    const unsigned long long m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+    const unsigned long long hi = __umul64hi(m << 11, 11743562013128004906ull);  // round(2^66 / 2π)
+    const int up = e - 1;
+    const unsigned long long t = up >= 64 || up <= -64 ? 0ull : up >= 0 ? hi << up : hi >> -up;
+    return bits >> 63 ? 0ull - t : t;
 }
 
 // cos and sin of a position's angle.
@@ -116,138 +129,149 @@ __device__ __forceinline__ void rot_turn(float (&a)[8], float (&b)[8], const flo
     }
 }
 
-// The warp's cos and sin of one position in shared memory, and this lane's
-// eight of them in registers (item >= r/16: none are used).
-__device__ __forceinline__ void rot_table(float2* tab, int lane, int item, int r, int position,
-                                          const unsigned long long (&turns)[2], float factor, float sign,
-                                          float2 (&cs)[8]) {
-    __syncwarp();
+// The block's frequencies as fractions of a turn (whole block).
+__device__ __forceinline__ void rot_frequencies(unsigned long long* turns, const RotParams& p) {
+    for (int i = threadIdx.x; i < p.r / 2; i += kRotWarps * 32) turns[i] = rot_turns(p.inv_freq[i]);
+    __syncthreads();
+}
+
+// cos and sin of a lane's eight pairs.
+__device__ __forceinline__ void rot_table(const unsigned long long* turns, int item, int position, float factor,
+                                          float sign, float2 (&cs)[8]) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        if (lane + 32 * j < r / 2) tab[lane + 32 * j] = rot_cos_sin(position, turns[j], factor, sign);
-    __syncwarp();
-    if (item * 16 < r) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 v = reinterpret_cast<const float4*>(tab)[item * 4 + i];
-            cs[2 * i] = make_float2(v.x, v.y);
-            cs[2 * i + 1] = make_float2(v.z, v.w);
-        }
-    }
+    for (int i = 0; i < 8; ++i) cs[i] = rot_cos_sin(position, turns[item * 8 + i], factor, sign);
 }
 
 template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRotWarps * 32) fa_rotary_kernel(const RotParams p) {
-    constexpr int kItems = D / 16, kHeads = 32 / kItems;  // lanes per head, heads per step of a warp
-    __shared__ __align__(16) float2 tab[kRotWarps][D / 2];
+    constexpr int kItems = D / 16, kTokens = 32 / kItems;
+    __shared__ unsigned long long turns[D / 2];
+    rot_frequencies(turns, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = lane % kItems;
-    unsigned long long turns[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        if (lane + 32 * j < p.r / 2) turns[j] = rot_turns(p.inv_freq[lane + 32 * j]);
+    const unsigned row = (blockIdx.x * kRotWarps + warp) * kTokens + lane / kItems;
+    if (row >= static_cast<unsigned>(p.B) * p.N) return;  // (B·N fits an int)
+    const int h0 = blockIdx.y * p.heads_per_warp, h_end = min(p.H, h0 + p.heads_per_warp);
+    const int b = static_cast<int>(row / p.N), n = static_cast<int>(row - b * p.N);
+    const int position = p.positions[b * p.pos_b + n];
     int ca, cb;
     rot_item<INTERLEAVED>(item, p.r, ca, cb);
-    const int chunks = (p.H + p.heads_per_warp - 1) / p.heads_per_warp;
-    const long long rows = static_cast<long long>(p.B) * p.N, todo = rows * chunks;
-    for (long long w = static_cast<long long>(blockIdx.x) * kRotWarps + warp; w < todo;
-         w += static_cast<long long>(gridDim.x) * kRotWarps) {
-        const long long row = w % rows;
-        const int chunk = static_cast<int>(w / rows);
-        const int b = static_cast<int>(row / p.N), n = static_cast<int>(row % p.N);
-        float2 cs[8];
-        rot_table(tab[warp], lane, item, p.r, p.positions[b * p.pos_b + n], turns, p.factor, p.sign, cs);
-        const uint16_t* src = p.x.src + b * p.src_b + n * p.x.src_n;
-        uint16_t* dst = p.x.dst + b * p.dst_b + n * p.x.dst_n;
-        const int h_end = min(p.H, (chunk + 1) * p.heads_per_warp);
-#pragma unroll 4
-        for (int h = chunk * p.heads_per_warp + lane / kItems; h < h_end; h += kHeads) {
-            float a[8], c[8];
-            uint4 va = *reinterpret_cast<const uint4*>(src + h * p.x.src_h + ca);
-            uint4 vb = *reinterpret_cast<const uint4*>(src + h * p.x.src_h + cb);
-            if (item * 16 < p.r) {
-                rot_unpack(va, a);
-                rot_unpack(vb, c);
-                rot_turn<INTERLEAVED>(a, c, cs);
-                va = rot_pack(a);
-                vb = rot_pack(c);
+    const bool turned = item * 16 < p.r;
+    const uint16_t* src = p.x.src + b * p.src_b + n * p.x.src_n;
+    uint16_t* dst = p.x.dst + b * p.dst_b + n * p.x.dst_n;
+    float2 cs[8];
+    for (int h = h0; h < h_end; h += kRotHeads) {
+        uint4 va[kRotHeads], vb[kRotHeads];
+#pragma unroll
+        for (int i = 0; i < kRotHeads; ++i)
+            if (h + i < h_end) {
+                va[i] = *reinterpret_cast<const uint4*>(src + (h + i) * p.x.src_h + ca);
+                vb[i] = *reinterpret_cast<const uint4*>(src + (h + i) * p.x.src_h + cb);
             }
-            *reinterpret_cast<uint4*>(dst + h * p.x.dst_h + ca) = va;
-            *reinterpret_cast<uint4*>(dst + h * p.x.dst_h + cb) = vb;
+        if (turned && h == h0) rot_table(turns, item, position, p.factor, p.sign, cs);
+#pragma unroll
+        for (int i = 0; i < kRotHeads; ++i)
+            if (h + i < h_end) {
+                if (turned) {
+                    float a[8], c[8];
+                    rot_unpack(va[i], a);
+                    rot_unpack(vb[i], c);
+                    rot_turn<INTERLEAVED>(a, c, cs);
+                    va[i] = rot_pack(a);
+                    vb[i] = rot_pack(c);
+                }
+                *reinterpret_cast<uint4*>(dst + (h + i) * p.x.dst_h + ca) = va[i];
+                *reinterpret_cast<uint4*>(dst + (h + i) * p.x.dst_h + cb) = vb[i];
+            }
+    }
+}
+
+// Eight values as they go into an e4m3 cache: value times the scale's reciprocal.
+__device__ __forceinline__ void rot_store_e4m3(uint8_t* at, const float (&x)[8], float by) {
+    *reinterpret_cast<uint2*>(at) =
+        make_uint2(ptx::pack_e4m3x2(x[0] * by, x[1] * by) | ptx::pack_e4m3x2(x[2] * by, x[3] * by) << 16,
+                   ptx::pack_e4m3x2(x[4] * by, x[5] * by) | ptx::pack_e4m3x2(x[6] * by, x[7] * by) << 16);
+}
+
+// Heads [h0, h1) of one of a token's tensors (KIND 0: q, 1: k, 2: v).
+template <int D, bool INTERLEAVED, bool E4M3, int KIND>
+__device__ __forceinline__ void append_heads(const RotParams& p, const RotTensor& x, unsigned t, int h0, int h1, int ca,
+                                             int cb, bool turned, const unsigned long long* turns, int item,
+                                             int position, float2 (&cs)[8], bool& have, uint8_t* cache,
+                                             long long cache_head, const float* scale) {
+    const uint16_t* src = x.src + t * x.src_n;
+    uint16_t* dst = x.dst + t * x.dst_n;
+    for (int h = h0; h < h1; h += kRotHeads) {
+        uint4 va[kRotHeads], vb[kRotHeads];
+        float inv[kRotHeads];
+#pragma unroll
+        for (int i = 0; i < kRotHeads; ++i)
+            if (h + i < h1) {
+                va[i] = *reinterpret_cast<const uint4*>(src + (h + i) * D + ca);
+                vb[i] = *reinterpret_cast<const uint4*>(src + (h + i) * D + cb);
+                inv[i] = KIND > 0 && E4M3 && scale ? scale[h + i] : 1.f;
+            }
+        if (KIND < 2 && turned && !have) {
+            rot_table(turns, item, position, p.factor, 1.f, cs);
+            have = true;
         }
+#pragma unroll
+        for (int i = 0; i < kRotHeads; ++i)
+            if (h + i < h1) {
+                float a[8], c[8];
+                rot_unpack(va[i], a);
+                rot_unpack(vb[i], c);
+                if (KIND < 2 && turned) {
+                    rot_turn<INTERLEAVED>(a, c, cs);
+                    va[i] = rot_pack(a);
+                    vb[i] = rot_pack(c);
+                }
+                if (KIND == 0 || (KIND == 1 && x.dst != nullptr)) {
+                    *reinterpret_cast<uint4*>(dst + (h + i) * D + ca) = va[i];
+                    *reinterpret_cast<uint4*>(dst + (h + i) * D + cb) = vb[i];
+                }
+                if (KIND > 0) {
+                    uint8_t* row = cache + (h + i) * cache_head;
+                    if (E4M3) {
+                        const float by = __frcp_rn(inv[i]);
+                        rot_store_e4m3(row + ca, a, by);
+                        rot_store_e4m3(row + cb, c, by);
+                    } else {
+                        *reinterpret_cast<uint4*>(row + 2 * ca) = va[i];
+                        *reinterpret_cast<uint4*>(row + 2 * cb) = vb[i];
+                    }
+                }
+            }
     }
 }
 
-// Eight values as they go into the cache: bf16, or e4m3 of value · inv (the
-// scale's reciprocal).
-template <bool E4M3>
-__device__ __forceinline__ void rot_store_cache(uint8_t* row, int at, const float (&x)[8], float inv) {
-    if constexpr (E4M3) {
-        *reinterpret_cast<uint2*>(row + at) =
-            make_uint2(ptx::pack_e4m3x2(x[0] * inv, x[1] * inv) | ptx::pack_e4m3x2(x[2] * inv, x[3] * inv) << 16,
-                       ptx::pack_e4m3x2(x[4] * inv, x[5] * inv) | ptx::pack_e4m3x2(x[6] * inv, x[7] * inv) << 16);
-    } else {
-        *reinterpret_cast<uint4*>(row + 2 * at) = rot_pack(x);
-    }
-}
-
-// Heads of a token in the order q (Hq), k (Hkv), v (Hkv); tokens whose slot is
-// outside the cache are passed over.
+// A warp takes heads [h0, h0 + heads_per_warp) of its tokens, counted through
+// q (Hq), k (Hkv) and v (Hkv). Tokens whose slot is outside the cache are passed
+// over.
 template <int D, bool INTERLEAVED, bool E4M3>
 __global__ void __launch_bounds__(kRotWarps * 32) fa_append_kernel(const RotParams p) {
-    constexpr int kItems = D / 16, kHeads = 32 / kItems;
-    __shared__ __align__(16) float2 tab[kRotWarps][D / 2];
+    constexpr int kItems = D / 16, kTokens = 32 / kItems;
+    __shared__ unsigned long long turns[D / 2];
+    rot_frequencies(turns, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = lane % kItems;
-    unsigned long long turns[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        if (lane + 32 * j < p.r / 2) turns[j] = rot_turns(p.inv_freq[lane + 32 * j]);
+    const unsigned t = (blockIdx.x * kRotWarps + warp) * kTokens + lane / kItems;
+    if (t >= static_cast<unsigned>(p.T)) return;
+    const int h0 = blockIdx.y * p.heads_per_warp, h1 = min(p.Hq + 2 * p.Hkv, h0 + p.heads_per_warp);
+    const int slot = p.slots[t], position = p.positions[t];
+    if (slot < 0 || slot >= p.num_slots) return;
     int ca, cb;
     rot_item<INTERLEAVED>(item, p.r, ca, cb);
-    const int heads = p.Hq + 2 * p.Hkv;
-    const int chunks = (heads + p.heads_per_warp - 1) / p.heads_per_warp;
-    const long long todo = static_cast<long long>(p.T) * chunks;
-    for (long long w = static_cast<long long>(blockIdx.x) * kRotWarps + warp; w < todo;
-         w += static_cast<long long>(gridDim.x) * kRotWarps) {
-        const long long t = w / chunks;
-        const int chunk = static_cast<int>(w % chunks);
-        const int slot = p.slots[t];
-        if (slot < 0 || slot >= p.num_slots) continue;
-        float2 cs[8];
-        rot_table(tab[warp], lane, item, p.r, p.positions[t], turns, p.factor, 1.f, cs);
-        const long long block = slot >> p.page_shift, token = slot & ((1 << p.page_shift) - 1);
-        const int h_end = min(heads, (chunk + 1) * p.heads_per_warp);
-#pragma unroll 2
-        for (int h = chunk * p.heads_per_warp + lane / kItems; h < h_end; h += kHeads) {
-            const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
-            const int hh = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
-            const uint16_t* src = kind == 0   ? p.q.src + t * p.q.src_n
-                                  : kind == 1 ? p.k.src + t * p.k.src_n
-                                              : p.v.src + t * p.v.src_n;
-            uint4 va = *reinterpret_cast<const uint4*>(src + hh * D + ca);
-            uint4 vb = *reinterpret_cast<const uint4*>(src + hh * D + cb);
-            float a[8], c[8];
-            rot_unpack(va, a);
-            rot_unpack(vb, c);
-            if (kind < 2 && item * 16 < p.r) {
-                rot_turn<INTERLEAVED>(a, c, cs);
-                va = rot_pack(a);
-                vb = rot_pack(c);
-            }
-            uint16_t* dst = kind == 0 ? p.q.dst + t * p.q.dst_n : p.k.dst + t * p.k.dst_n;
-            if (kind == 0 || (kind == 1 && p.k.dst != nullptr)) {
-                *reinterpret_cast<uint4*>(dst + hh * D + ca) = va;
-                *reinterpret_cast<uint4*>(dst + hh * D + cb) = vb;
-            }
-            if (kind > 0) {
-                uint8_t* row = kind == 1 ? p.k_cache + block * p.k_block + token * p.k_token + hh * p.k_head
-                                         : p.v_cache + block * p.v_block + token * p.v_token + hh * p.v_head;
-                const float* scale = kind == 1 ? p.k_scale : p.v_scale;
-                const float inv = E4M3 && scale ? 1.f / scale[hh] : 1.f;
-                rot_store_cache<E4M3>(row, ca, a, inv);
-                rot_store_cache<E4M3>(row, cb, c, inv);
-            }
-        }
-    }
+    const bool turned = item * 16 < p.r;
+    const long long block = slot >> p.page_shift, token = slot & ((1 << p.page_shift) - 1);
+    float2 cs[8];
+    bool have = false;
+    append_heads<D, INTERLEAVED, E4M3, 0>(p, p.q, t, h0, min(h1, p.Hq), ca, cb, turned, turns, item, position, cs, have,
+                                          nullptr, 0, nullptr);
+    append_heads<D, INTERLEAVED, E4M3, 1>(p, p.k, t, max(h0 - p.Hq, 0), min(h1 - p.Hq, p.Hkv), ca, cb, turned, turns,
+                                          item, position, cs, have, p.k_cache + block * p.k_block + token * p.k_token,
+                                          p.k_head, p.k_scale);
+    append_heads<D, INTERLEAVED, E4M3, 2>(p, p.v, t, max(h0 - p.Hq - p.Hkv, 0), h1 - p.Hq - p.Hkv, ca, cb, false, turns,
+                                          item, position, cs, have, p.v_cache + block * p.v_block + token * p.v_token,
+                                          p.v_head, p.v_scale);
 }
 
 }  // namespace fa

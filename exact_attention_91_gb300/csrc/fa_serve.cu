@@ -90,10 +90,8 @@ constexpr int kMapsSmem = 2 * (fa::kMapsMaxRequests + 1) * 4;
 // The kernels' shared-memory sizes, set on the device by its first call that
 // is not being captured; a captured call needs them set already.
 int ready(int dev, cudaStream_t stream) {
-    const int cap = fa::host_capturing(stream);
-    if (cap < 0) return FA_ERR_LAUNCH;
     if (g_ready[dev].load(std::memory_order_acquire)) return FA_OK;
-    if (cap) return FA_ERR_LAUNCH;
+    if (fa::host_capturing(stream) != 0) return FA_ERR_LAUNCH;
     std::lock_guard<std::mutex> lock(g_ready_mu);
     const bool ok = set_decode<64, false, false>() && set_decode<64, false, true>() && set_decode<64, true, false>() &&
                     set_decode<64, true, true>() && set_decode<128, false, false>() &&
@@ -184,21 +182,21 @@ int check_rotary(int d, int r, const double* inv_freq, float factor) {
     return FA_OK;
 }
 
-// Heads that one warp takes of a token: all of them once the tokens alone give
-// every SM its 32 warps (the token's cos and sin are then computed once), else
-// as few as give that many, in steps of the heads that a warp holds at once.
-int heads_per_warp(long long tokens, int heads, int d, int sms) {
-    const int step = 32 / (d / 16);
-    const long long want = (32LL * sms + tokens - 1) / tokens;
-    const int steps = (heads + step - 1) / step;
-    const int chunks = static_cast<int>(std::min<long long>(steps, std::max<long long>(1, want)));
-    return (steps + chunks - 1) / chunks * step;
+// Heads that one warp takes of its tokens (the cos and sin are computed once
+// for them): kMaxHeads when the tokens alone give every SM kWant warps several
+// times over, else as few as give that many warps.
+int heads_per_warp(long long groups, int heads, int sms) {
+    constexpr int kMaxHeads = 8;
+    constexpr long long kWant = 32;
+    const long long chunks = std::max<long long>(1, (kWant * sms + groups - 1) / groups);
+    const long long per = (heads + chunks - 1) / chunks;
+    return static_cast<int>(std::min<long long>(per, kMaxHeads));
 }
 
-unsigned rotary_grid(long long tokens, int heads, int per_warp, int sms) {
-    const long long chunks = (heads + per_warp - 1) / per_warp;
-    const long long blocks = (tokens * chunks + fa::kRotWarps - 1) / fa::kRotWarps;
-    return static_cast<unsigned>(std::min<long long>(blocks, 4LL * sms));
+// Blocks of a launch: x over the warps' groups of tokens, y over the heads.
+dim3 rotary_grid(long long groups, int heads, int per_warp) {
+    return dim3(static_cast<unsigned>((groups + fa::kRotWarps - 1) / fa::kRotWarps),
+                static_cast<unsigned>((heads + per_warp - 1) / per_warp));
 }
 
 }  // namespace
@@ -288,7 +286,7 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
 int fa_rotary(const void* x, void* y, const int* positions, const double* inv_freq, int B, int H, int N, int d,
               const long long* x_strides, const long long* y_strides, long long position_stride, int rotary_dim,
               int interleaved, int inverse, float factor, void* stream) {
-    if (B < 0 || H < 0 || N < 0) return FA_ERR_BAD_SHAPE;
+    if (B < 0 || H < 0 || N < 0 || H > 0x7fff || static_cast<long long>(B) * N > 0x7fff0000LL) return FA_ERR_BAD_SHAPE;
     int rc = check_rotary(d, rotary_dim, inv_freq, factor);
     if (rc != FA_OK) return rc;
     if (B == 0 || H == 0 || N == 0) return FA_OK;
@@ -329,8 +327,9 @@ int fa_rotary(const void* x, void* y, const int* positions, const double* inv_fr
     p.x.dst_n = N > 1 ? y_strides[2] : 0;
     p.pos_b = position_stride;
     p.B = B, p.H = H, p.N = N;
-    p.heads_per_warp = heads_per_warp(tokens, H, d, sms);
-    const unsigned grid = rotary_grid(tokens, H, p.heads_per_warp, sms);
+    const long long groups = (tokens + 512 / d - 1) / (512 / d);  // of the tokens that a warp holds
+    p.heads_per_warp = heads_per_warp(groups, H, sms);
+    const dim3 grid = rotary_grid(groups, H, p.heads_per_warp);
     const int threads = fa::kRotWarps * 32;
     if (d == 64) {
         if (interleaved)
@@ -357,7 +356,7 @@ int fa_cache_append(const void* q, const void* k, const void* v, long long q_str
     const int Hkv = cache->heads, d = cache->d;
     rc = check_rotary(d, rotary_dim, inv_freq, factor);
     if (rc != FA_OK) return rc;
-    if (T < 0 || Hq < 1 || static_cast<long long>(Hq) + 2LL * Hkv > 0x7fffLL) return FA_ERR_BAD_SHAPE;
+    if (T < 0 || T > 0x7fff0000 || Hq < 1 || static_cast<long long>(Hq) + 2LL * Hkv > 0x7fffLL) return FA_ERR_BAD_SHAPE;
     if (T == 0) return FA_OK;
     if (!q || !k || !v || !q_out || !positions || !slots) return FA_ERR_NULL_PTR;
     const long long strides[5] = {q_stride, k_stride, v_stride, q_out_stride, k_out_stride};
@@ -416,8 +415,9 @@ int fa_cache_append(const void* q, const void* k, const void* v, long long q_str
     p.num_slots = static_cast<long long>(cache->num_blocks) * cache->page_size;
     p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.page_shift = c.shift;
     const int heads = Hq + 2 * Hkv;
-    p.heads_per_warp = heads_per_warp(T, heads, d, sms);
-    const unsigned grid = rotary_grid(T, heads, p.heads_per_warp, sms);
+    const long long groups = (T + 512LL / d - 1) / (512 / d);  // of the tokens that a warp holds
+    p.heads_per_warp = heads_per_warp(groups, heads, sms);
+    const dim3 grid = rotary_grid(groups, heads, p.heads_per_warp);
     const int threads = fa::kRotWarps * 32;
     const int which = (d == 128 ? 4 : 0) + (interleaved ? 2 : 0) + (c.e4m3 ? 1 : 0);
     switch (which) {

@@ -289,13 +289,14 @@ long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_typ
  *   positions   int32, device: that of (b, n) is positions[b*position_stride + n]
  *               (0: shared by the batch). Any int32 value.
  *   inv_freq    fp64 [rotary_dim/2], device, finite, in radians per position.
- *               The angle is off by |position|·2^-51 + 2^-29 radians at most
+ *               The angle is off by |position|·2^-59 + 2^-29 radians at most
  *               (frequencies up to 1).
  *   x_strides, y_strides  host arrays: elements from one b, h, n to the next
  *               (multiples of 8; x's may be 0; those of a dimension of size 1
  *               are not used); d's values are contiguous. y may be x itself
  *               with the same strides, or overlap nothing of it.
  *   rotary_dim  a multiple of 16, 0 to d.  factor finite (1: a pure rotation).
+ *   B*N at most 2^31 - 65536, H at most 32767.
  *
  * Sums and products are fp32, rounded to bf16 once.
  */
