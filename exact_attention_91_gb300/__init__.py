@@ -5,18 +5,20 @@ take raw device pointers (ints), exactly like the C ABI. ``attention_forward``
 is a convenience wrapper for torch tensors: it checks dtypes and layout,
 allocates the outputs with torch and calls ``fa_fwd`` on the current stream.
 Every step of the computation runs in the CUDA library; if the library is
-missing this module raises instead of computing anything elsewhere.
+missing this module raises instead of computing anything elsewhere. The
+serving functions (paged cache, rotary positions) do the same through the
+binding's native half, ``lib/_fa_bind.so``: their kernels are often shorter than
+what the checks and the call cost in Python.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import math
 import os
-import struct
 import typing
 
-from .build import LIB_PATH
+from .build import BIND_PATH, LIB_PATH
 
 __all__ = ["FaError", "load_library", "fa_fwd", "fa_fwd_noalloc", "fa_strerror", "fa_device_status",
            "fa_set_wait_limit_ns", "fa_abi_version", "fa_selftest_wait_timeout", "fa_fwd_varlen",
@@ -25,7 +27,7 @@ __all__ = ["FaError", "load_library", "fa_fwd", "fa_fwd_noalloc", "fa_strerror",
            "head_shards", "attention_forward_heads", "EXPORTED_SYMBOLS", "CACHE_BF16", "CACHE_E4M3",
            "FaPagedCache", "fa_decode_paged", "fa_decode_paged_workspace", "fa_rotary", "fa_cache_append",
            "fa_page_maps", "attention_decode_paged", "rotary", "rotary_inv_freq", "cache_append", "page_maps",
-           "PageMaps"]
+           "PageMaps", "load_binding"]
 
 EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_noalloc", "fa_fwd_varlen", "fa_strerror", "fa_device_status",
                     "fa_set_wait_limit_ns", "fa_abi_version", "fa_selftest_wait_timeout", "fa_varlen_num_splits",
@@ -371,79 +373,44 @@ def attention_forward_heads(q, k, v, head_start: int, head_count: int, causal: b
 # ---- serving from a paged cache, rotary positions ---------------------------
 
 
-# struct fa_paged_cache as bytes (laid out as FaPagedCache), which a call takes in
-# a tenth of the time that building the ctypes structure does
-_pack_cache = struct.Struct("PPPPqqqqqqiiiii4x").pack
+_bind = None
 
 
-def _launch(torch, fn, args, device, stream, made, what):
-    """``fn(*args, stream handle)`` with CUDA device number ``device`` current.
-    Tensors that were made for the call belong to the current stream's part of
-    the allocator; when another ``stream`` uses them it is told so, so that none
-    is handed out again while that stream's kernels may still run."""
-    if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        handle = raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
-    else:
-        handle = stream.cuda_stream
-        for t in made:
-            t.record_stream(stream)
-    if device == torch.cuda.current_device():
-        rc = fn(*args, handle or None)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, handle or None)
-    if rc != FA_OK:
-        raise FaError(rc, what)
+def load_binding():
+    """The binding's native half (``lib/_fa_bind.so``, built with libfa.so): the
+    checks, allocations and C calls of the functions below."""
+    global _bind
+    if _bind is None:
+        import torch  # noqa: F401  (its libraries, which the module is linked to)
+        if not os.path.exists(BIND_PATH):
+            raise FileNotFoundError(
+                f"{BIND_PATH} is missing: build it with `python -c \"import __graft_entry__ as g; g.build()\"`")
+        load_library()
+        spec = importlib.util.spec_from_file_location("_fa_bind", BIND_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _bind = module
+    return _bind
 
 
-def _elsewhere(device, tensors):
-    """Raises for the tensors (of those that are not None) that are not on CUDA
-    device number ``device``; -1 is the CPU."""
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError("all tensors must be on the same CUDA device")
-
-
-def _pack_paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale):
-    """(struct fa_paged_cache as bytes, its type) of caches indexed [block,
-    token, head, d]."""
-    t = k_cache.dtype
-    if t is torch.bfloat16:
-        kind = CACHE_BF16
-    elif t is torch.float8_e4m3fn:
-        kind = CACHE_E4M3
-    else:
-        raise TypeError("k_cache and v_cache must both be bf16 or both float8_e4m3fn")
-    if v_cache.dtype is not t:
-        raise TypeError("k_cache and v_cache must both be bf16 or both float8_e4m3fn")
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must both be [num_blocks, page_size, heads, d]")
-    kb, kt, kh, kd = k_cache.stride()
-    vb, vt, vh, vd = v_cache.stride()
-    if kd != 1 or vd != 1:
-        raise ValueError("the d values of a cache row must be contiguous")
-    if k_cache.get_device() != device or v_cache.get_device() != device:
-        _elsewhere(device, (k_cache, v_cache))
-    scales = [0, 0]
-    for i, x in enumerate((k_scale, v_scale)):
-        if x is not None:
-            if x.dtype is not torch.float32 or x.shape != (shape[2],) or not x.is_contiguous():
-                raise ValueError("k_scale and v_scale must be contiguous fp32 tensors of one value per key head")
-            _elsewhere(device, (x,))
-            scales[i] = x.data_ptr()
-    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), *scales, kb, kt, kh, vb, vt, vh, kind, *shape), kind
-
-
-@functools.lru_cache(maxsize=256)
-def _decode_workspace_bytes(B, Hq, Hkv, d, cache_type, page_size, table_width, device_index):
+def _made_for(stream, *shapes_and_dtypes, device):
+    """Output tensors for a call on ``stream`` that is not the current one: they
+    belong to the current stream's part of the allocator, as those of any call
+    do, and are not handed out again while ``stream`` may still write them."""
     import torch
-    sms = torch.cuda.get_device_properties(device_index).multi_processor_count
-    n = fa_decode_paged_workspace(B, Hq, Hkv, d, cache_type, page_size, table_width, sms)
-    if n < 0:
-        raise FaError(n, "fa_decode_paged_workspace")
-    return n
+    out = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in shapes_and_dtypes]
+    for t in out:
+        if t.is_cuda:
+            t.record_stream(stream)
+    return out
+
+
+def _on_stream(stream, fn, *args):
+    """fn(*args) with ``stream`` as the current one (whose part of the allocator
+    a workspace then comes from)."""
+    import torch
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
 def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None, k_scale=None,
@@ -460,53 +427,20 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: fl
     ``workspace`` (uint8, at least ``fa_decode_paged_workspace`` bytes) may be
     given to keep allocation out of the call; calls that may overlap in time
     need one each."""
-    import torch
-    if q.dtype is not torch.bfloat16:
-        raise TypeError("q must be bf16")
-    if block_table.dtype is not torch.int32 or seq_lens.dtype is not torch.int32:
-        raise TypeError("block_table and seq_lens must be int32")
-    if q.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("q must be [B, Hq, d], block_table [B, width] and seq_lens [B]")
-    device = q.get_device()
-    if device < 0:
-        raise ValueError("all inputs must be CUDA tensors")
-    B, Hq, d = q.shape
-    rows, width = block_table.shape
-    if rows != B or seq_lens.shape != (B,):
-        raise ValueError("q must be [B, Hq, d], block_table [B, width] and seq_lens [B]")
-    row_stride, step = block_table.stride()
-    if (step != 1 and width > 1) or not q.is_contiguous() or not seq_lens.is_contiguous():
-        raise ValueError("q, seq_lens and the rows of block_table must be contiguous")
-    _elsewhere(device, (block_table, seq_lens, out, lse, workspace))
-    cache, kind = _pack_paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale)
-    _, page, heads, cache_d = k_cache.shape
-    if cache_d != d:
-        raise ValueError("q and the caches must have the same d")
-    made = ()
-    if out is None:
-        out = torch.empty_like(q)
-        made = (out,)
-    elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous bf16 tensor of q's shape")
-    if lse is None:
-        if return_lse:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-            made += (lse,)
-    elif lse.dtype is not torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq]")
-    if workspace is None:
-        room = _decode_workspace_bytes(B, Hq, heads, d, kind, page, width, device)
-        workspace = torch.empty(room, dtype=torch.uint8, device=q.device)
-        made += (workspace,)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
+    decode = (_bind or load_binding()).decode
+    if stream is None:
+        r = decode(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse, return_lse, workspace)
     else:
-        room = workspace.numel()
-    _launch(torch, (_lib or load_library()).fa_decode_paged,
-            (q.data_ptr(), cache, block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-             lse.data_ptr() if lse is not None else None, B, Hq, width, row_stride, 1.0 / math.sqrt(d) if scale is None
-             else scale, workspace.data_ptr(), room), device, stream, made, "fa_decode_paged")
-    return (out, lse) if return_lse else out
+        import torch
+        if out is None:
+            out, = _made_for(stream, (q.shape, torch.bfloat16), device=q.device)
+        if lse is None and return_lse:
+            lse, = _made_for(stream, (q.shape[:2], torch.float32), device=q.device)
+        r = _on_stream(stream, decode, q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse,
+                       return_lse, workspace)
+    if type(r) is int:
+        raise FaError(r, "fa_decode_paged")
+    return r
 
 
 def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None, device=None):
@@ -562,20 +496,6 @@ def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: dict | None
     return (freq.to(device) if device is not None else freq), out_factor
 
 
-def _frequencies(torch, device, inv_freq):
-    """(rotary_dim, pointer) of the frequencies; none: (0, None)."""
-    if inv_freq is None:
-        return 0, None
-    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous fp64 tensor [rotary_dim / 2]")
-    if inv_freq.get_device() != device:
-        _elsewhere(device, (inv_freq,))
-    return 2 * inv_freq.shape[0], inv_freq.data_ptr() or None
-
-
-_three = struct.Struct("qqq").pack  # strides, as the C call reads them
-
-
 def rotary(x, positions, inv_freq, interleaved: bool = False, inverse: bool = False, factor: float = 1.0, out=None,
            stream=None):
     """Rotary positions of x (bf16, CUDA): [B, H, N, d] with int32 ``positions``
@@ -585,51 +505,16 @@ def rotary(x, positions, inv_freq, interleaved: bool = False, inverse: bool = Fa
     ``interleaved``. ``inverse`` turns back by the same angles (times factor):
     the gradient with respect to x. ``out`` may be x. Not differentiable by
     itself: ``torch.ops.fa91.rotary`` is."""
-    import torch
-    if x.dtype is not torch.bfloat16:
-        raise TypeError("x must be bf16")
-    if positions.dtype is not torch.int32:
-        raise TypeError("positions must be int32")
-    device = x.get_device()
-    if device < 0:
-        raise ValueError("x must be a CUDA tensor")
-    shape, pos_stride = x.shape, 0
-    if len(shape) == 4:
-        B, H, N, d = shape
-        sb, sh, sn, sd = x.stride()
-        if positions.dim() == 2 and positions.shape == (B, N):
-            pos_stride, step = positions.stride()
-        elif positions.shape == (N,):
-            step, = positions.stride()
-        else:
-            raise ValueError("positions must be [N] or [B, N]")
-    elif len(shape) == 3:
-        (N, H, d), B, sb = shape, 1, 0
-        sn, sh, sd = x.stride()
-        if positions.shape != (N,):
-            raise ValueError("positions must be [T]")
-        step, = positions.stride()
+    turn = (_bind or load_binding()).rotary
+    if stream is None:
+        r = turn(x, positions, inv_freq, interleaved, inverse, factor, out)
     else:
-        raise ValueError("x must be [B, H, N, d] or [T, H, d]")
-    if sd != 1 or (step != 1 and N > 1):
-        raise ValueError("d of x and the rows of positions must be contiguous")
-    _elsewhere(device, (positions, out))
-    r, freq = _frequencies(torch, device, inv_freq)
-    made = ()
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-        made = (out,)
-    elif out.dtype is not torch.bfloat16 or out.shape != shape or out.stride(-1) != 1:
-        raise ValueError("out must be a bf16 tensor of x's shape with d contiguous")
-    if len(shape) == 4:
-        tb, th, tn, _ = out.stride()
-    else:
-        (tn, th, _), tb = out.stride(), 0
-    _launch(torch, (_lib or load_library()).fa_rotary,
-            (x.data_ptr(), out.data_ptr(), positions.data_ptr(), freq, B, H, N, d, _three(sb, sh, sn),
-             _three(tb, th, tn), pos_stride, r, 1 if interleaved else 0, 1 if inverse else 0, factor), device, stream,
-            made, "fa_rotary")
-    return out
+        if out is None:
+            out, = _made_for(stream, (x.shape, x.dtype), device=x.device)
+        r = _on_stream(stream, turn, x, positions, inv_freq, interleaved, inverse, factor, out)
+    if type(r) is int:
+        raise FaError(r, "fa_rotary")
+    return r if out is None else out
 
 
 def cache_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved: bool = False,
@@ -644,48 +529,18 @@ def cache_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interlea
     negative slot is padding: nothing of it is written anywhere. q, k and v may
     be slices of one projection's output. float8_e4m3fn caches hold value /
     scale, with ``k_scale`` / ``v_scale`` fp32 [heads] (None: 1)."""
-    import torch
-    bf16 = torch.bfloat16
-    if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16:
-        raise TypeError("q, k, v must be bf16")
-    if positions.dtype is not torch.int32 or slots.dtype is not torch.int32:
-        raise TypeError("positions and slots must be int32")
-    device = q.get_device()
-    if device < 0:
-        raise ValueError("all inputs must be CUDA tensors")
-    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape:
-        raise ValueError("q must be [T, Hq, d] and k, v [T, heads, d]")
-    T, Hq, d = q.shape
-    Tk, heads, dk = k.shape
-    if Tk != T or dk != d or k_cache.shape[2:] != (heads, d):
-        raise ValueError("q, k, v and the caches do not fit together")
-    if positions.shape != (T,) or slots.shape != (T,) or not positions.is_contiguous() or not slots.is_contiguous():
-        raise ValueError("positions and slots must be contiguous [T]")
-    _elsewhere(device, (k, v, positions, slots, q_out, k_out))
-    cache, _ = _pack_paged_cache(torch, device, k_cache, v_cache, k_scale, v_scale)
-    r, freq = _frequencies(torch, device, inv_freq)
-    made = ()
-    if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=bf16, device=q.device)
-        made = (q_out,)
-    elif q_out.dtype is not bf16 or q_out.shape != q.shape:
-        raise ValueError("q_out must be bf16 and of q's shape")
-    if k_out is not None and (k_out.dtype is not bf16 or k_out.shape != k.shape):
-        raise ValueError("k_out must be bf16 and of k's shape")
-    strides = []
-    for t, h in ((q, Hq), (k, heads), (v, heads), (q_out, Hq), (k_out, heads)):
-        if t is None:
-            strides.append(0)
-            continue
-        row, head, step = t.stride()
-        if step != 1 or (head != d and h > 1):
-            raise ValueError("the heads of a token of q, k, v, q_out and k_out must be contiguous")
-        strides.append(row)
-    _launch(torch, (_lib or load_library()).fa_cache_append,
-            (q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides[:3], positions.data_ptr(), slots.data_ptr(), freq,
-             cache, q_out.data_ptr(), k_out.data_ptr() if k_out is not None else None, *strides[3:], T, Hq, r,
-             1 if interleaved else 0, factor), device, stream, made, "fa_cache_append")
-    return q_out
+    append = (_bind or load_binding()).append
+    if stream is None:
+        r = append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved, factor, k_scale, v_scale, q_out,
+                   k_out)
+    else:
+        if q_out is None:
+            q_out, = _made_for(stream, (q.shape, q.dtype), device=q.device)
+        r = _on_stream(stream, append, q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved, factor,
+                       k_scale, v_scale, q_out, k_out)
+    if type(r) is int:
+        raise FaError(r, "fa_cache_append")
+    return r if q_out is None else q_out
 
 
 class PageMaps(typing.NamedTuple):
@@ -706,40 +561,16 @@ def page_maps(context_lens, new_lens, block_table, unused_blocks, page_size: int
     order (the caller then drops the first ``counts[0]``); ``num_tokens`` is the
     length of the token maps, which may be more than the step's tokens (the
     rest are padding: slot -1). See ``fa_page_maps`` in include/fa.h."""
-    import torch
-    i32 = torch.int32
-    if (context_lens.dtype is not i32 or new_lens.dtype is not i32 or block_table.dtype is not i32 or
-            unused_blocks.dtype is not i32):
-        raise TypeError("context_lens, new_lens, block_table and unused_blocks must be int32")
-    device = block_table.get_device()
-    if device < 0:
-        raise ValueError("all inputs must be CUDA tensors")
-    if block_table.dim() != 2 or unused_blocks.dim() != 1:
-        raise ValueError("block_table must be [B, width] and unused_blocks one list")
-    B, width = block_table.shape
-    row_stride, step = block_table.stride()
-    if context_lens.shape != (B,) or new_lens.shape != (B,):
-        raise ValueError("context_lens and new_lens must be [B]")
-    if ((step != 1 and width > 1) or not context_lens.is_contiguous() or not new_lens.is_contiguous() or
-            not unused_blocks.is_contiguous()):
-        raise ValueError("the rows of block_table, the lengths and unused_blocks must be contiguous")
-    _elsewhere(device, (context_lens, new_lens, unused_blocks))
-    T = int(num_tokens)
-    if T < 0:
-        raise ValueError("num_tokens must be >= 0")
-    made = ()
-    if out is None:
-        whole = torch.empty(2 * T + 2 * B + 5, dtype=i32, device=block_table.device)
-        out = PageMaps(*whole.split_with_sizes((T, T, B + 1, B, 4)))
-        made = (whole,)
+    maps = (_bind or load_binding()).maps
+    if stream is None:
+        r = maps(context_lens, new_lens, block_table, unused_blocks, page_size, num_tokens, out)
     else:
-        for t, n in zip(out, (T, T, B + 1, B, 4)):
-            if t.dtype is not i32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != device:
-                raise ValueError("out must be int32 tensors [T], [T], [B + 1], [B] and [4] on the same device")
-    slots, positions, cu_seqlens, seq_lens, counts = out
-    _launch(torch, (_lib or load_library()).fa_page_maps,
-            (context_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), unused_blocks.data_ptr() or None,
-             slots.data_ptr() or None, positions.data_ptr() or None, cu_seqlens.data_ptr(), seq_lens.data_ptr(),
-             counts.data_ptr(), B, width, row_stride, unused_blocks.shape[0], page_size, T), device, stream, made,
-            "fa_page_maps")
-    return out
+        import torch
+        if out is None:
+            B = block_table.shape[0]
+            out = PageMaps(*_made_for(stream, *(((n,), torch.int32) for n in (num_tokens, num_tokens, B + 1, B, 4)),
+                                      device=block_table.device))
+        r = _on_stream(stream, maps, context_lens, new_lens, block_table, unused_blocks, page_size, num_tokens, out)
+    if type(r) is int:
+        raise FaError(r, "fa_page_maps")
+    return PageMaps._make(r) if out is None else out

@@ -5,14 +5,20 @@ once: ``csrc/fa_api.cu`` (attention forward) and ``csrc/fa_serve.cu`` (paged
 cache and rotary positions). It links the CUDA runtime statically and resolves
 the driver's tensor-map encoder at run time, so it needs no libcuda at link
 time.
+
+The Python binding's native half (``csrc/fa_bind.cpp``, torch's C++ API) is
+compiled beside it with the host compiler into ``lib/_fa_bind.so`` and linked to
+libfa.so.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa.so")
+BIND_PATH = os.path.join(LIB_DIR, "_fa_bind.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -32,7 +39,7 @@ def nvcc_path() -> str:
 def sources() -> list[str]:
     out = []
     for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".cu", ".cuh", ".h")):
+        if name.endswith((".cu", ".cuh", ".h", ".cpp")):
             out.append(os.path.join(CSRC, name))
     out.append(os.path.join(INCLUDE, "fa.h"))
     return out
@@ -44,10 +51,23 @@ def nvcc_cmd(out_path: str, extra: list[str] | None = None) -> list[str]:
             *(extra or []), os.path.join(CSRC, "fa_api.cu"), os.path.join(CSRC, "fa_serve.cu"), "-o", out_path]
 
 
+def bind_cmds(obj: str, out_path: str) -> tuple[list[str], list[str]]:
+    """Compile and link commands of the binding's native half."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda_home = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    cxx = os.environ.get("CXX", "g++")
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-c", "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"),
+                "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda_home, "include"),
+                os.path.join(CSRC, "fa_bind.cpp"), "-o", obj]
+    link = [cxx, "-shared", obj, "-o", out_path, "-L", LIB_DIR, "-l:libfa.so", "-L", os.path.join(torch_dir, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(BIND_PATH)):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BIND_PATH))
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
@@ -82,23 +102,33 @@ def check_ptxas_report(report: str) -> dict[str, int]:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile libfa.so if any source is newer than it. Returns its path."""
+    """Compile libfa.so and the binding if any source is newer than them.
+    Returns the path of libfa.so."""
     if not force and not extra and up_to_date():
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
+    tmp, obj, tmp_bind = (f"{path}.tmp{os.getpid()}" for path in (LIB_PATH, BIND_PATH + ".o", BIND_PATH))
     cmd = nvcc_cmd(tmp, ["-Xptxas", "-v"] + (extra or []))
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if verbose or res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-    if res.returncode != 0:
-        raise subprocess.CalledProcessError(res.returncode, cmd)
+    compile_bind, link_bind = bind_cmds(obj, tmp_bind)
     try:
+        with subprocess.Popen(compile_bind, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) as bind:
+            res = subprocess.run(cmd, capture_output=True, text=True)
+            bind_report = bind.communicate()[0]
+        if verbose or res.returncode != 0:
+            sys.stderr.write(res.stdout + res.stderr)
+        if res.returncode != 0:
+            raise subprocess.CalledProcessError(res.returncode, cmd)
         check_ptxas_report(res.stdout + res.stderr)
-    except RuntimeError:
-        os.remove(tmp)
-        raise
-    os.replace(tmp, LIB_PATH)
+        if bind.returncode != 0:
+            sys.stderr.write(bind_report)
+            raise subprocess.CalledProcessError(bind.returncode, compile_bind)
+        os.replace(tmp, LIB_PATH)
+        subprocess.run(link_bind, check=True)
+        os.replace(tmp_bind, BIND_PATH)
+    finally:
+        for path in (tmp, obj, tmp_bind):
+            if os.path.exists(path):
+                os.remove(path)
     return LIB_PATH
 
 
