@@ -77,7 +77,14 @@ struct DecodeCfg {
     static constexpr float kLazy = 8.f;
 };
 
-// Position in a worker's run: tiles [t0, t1) of unit (b, hh), then `rem` more.
+// What a segment costs besides its tiles (q, the warps' merge, the output), in
+// tiles of one worker: a run of many short requests must not count as little.
+constexpr int kSegCost = 6;
+// Least run of a worker, in tiles with the segments' costs.
+constexpr int kMinRun = 8;
+
+// Position in a worker's run: tiles [t0, t1) of unit (b, hh), then `rem` more
+// of the run. A unit counts as its tiles behind kSegCost empty ones.
 struct DecodeSeg {
     int b, hh, t0, t1, nt, len;
     long long rem;
@@ -94,24 +101,53 @@ __device__ __forceinline__ int decode_tiles(int len) {
     return len <= KEYS ? 1 : (len - 1) / KEYS + 1;  // a request without keys still has its output to write
 }
 
-template <int KEYS>
-__device__ __forceinline__ void decode_next(DecodeSeg& s, const DecodeParams& p) {
-    if (++s.hh == p.Hkv * p.row_groups) {
-        s.hh = 0;
-        ++s.b;
-        s.len = decode_len(p, s.b);
-        s.nt = decode_tiles<KEYS>(s.len);
-    }
-    s.t0 = 0;
-    s.t1 = static_cast<int>(s.rem < s.nt ? s.rem : s.nt);
-    s.rem -= s.t1;
+// The part of the current unit, from x on in its counted tiles, that the run
+// holds.
+__device__ __forceinline__ void decode_take(DecodeSeg& s, int x) {
+    const long long left = kSegCost + s.nt - x;
+    const int take = static_cast<int>(s.rem < left ? s.rem : left);
+    s.t0 = max(0, x - kSegCost);
+    s.t1 = max(0, x + take - kSegCost);
+    s.rem -= take;
 }
 
-// First tile of worker c when `total` tiles are cut for `workers`; the worker
-// of a tile.
-__device__ __forceinline__ long long decode_start(long long total, int workers, int c) { return total * c / workers; }
+// On to the next unit with a tile in the run; false at the run's end.
+template <int KEYS>
+__device__ __forceinline__ bool decode_next(DecodeSeg& s, const DecodeParams& p) {
+    do {
+        if (s.rem <= 0) return false;
+        if (++s.hh == p.Hkv * p.row_groups) {
+            s.hh = 0;
+            ++s.b;
+            s.len = decode_len(p, s.b);
+            s.nt = decode_tiles<KEYS>(s.len);
+        }
+        decode_take(s, 0);
+    } while (s.t0 >= s.t1);
+    return true;
+}
+
+// Where the run of worker c begins when `total` counted tiles are cut for
+// `workers`; the worker of a counted tile. (64-bit divisions take about 150
+// cycles each, and nothing else can start before them.)
+__device__ __forceinline__ long long decode_start(long long total, int workers, int c) {
+    if (total < (1 << 20)) return static_cast<unsigned>(total) * static_cast<unsigned>(c) / static_cast<unsigned>(workers);
+    return total * c / workers;
+}
 __device__ __forceinline__ int decode_worker_of(long long total, int workers, long long tile) {
+    if (total < (1 << 20))
+        return static_cast<int>((static_cast<unsigned>(tile + 1) * static_cast<unsigned>(workers) - 1u) /
+                                static_cast<unsigned>(total));
     return static_cast<int>(((tile + 1) * workers - 1) / total);
+}
+
+// Column (in float4) of a row of the merge buffer: swizzled so that neither the
+// fragments' writes nor the rows' reads meet in a bank.
+template <int D, bool E4M3>
+__device__ __forceinline__ int merge_col(int row, int c4) {
+    if constexpr (!E4M3) return c4 ^ ((row & 3) << 1);
+    if constexpr (D == 128) return c4 ^ (c4 >> 3 & 3) ^ ((row & 1) << 2);
+    return c4 ^ (c4 >> 3 & 1) ^ ((row & 1) << 1);
 }
 
 // Byte offset, inside a tile's K (or V), of 16-byte chunk c of row r: rows
@@ -190,8 +226,9 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     // ---- this worker's run of tiles
     const int per = (p.B + C::kThreads - 1) / C::kThreads;
     const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
-    long long mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b))) * HH;
+    long long mine = 0;  // counted tiles of requests [b_lo, b_hi)
+    for (int b = b_lo; b < b_hi; ++b)
+        mine += static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b)) + kSegCost) * HH;
     long long incl = mine;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
@@ -207,20 +244,18 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         total += sh_warp[w];
     }
     const int worker = blockIdx.x;
-    // (a worker has a tile for every warp, as long as there are that many)
-    const long long most = (total + C::kWarps - 1) / C::kWarps;
-    const int workers = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+    const int workers = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kMinRun - 1) / kMinRun));
     if (worker >= workers) {
         if (tid == 0) p.meta[worker] = make_int4(-1, 0, 0, 0);
         return;
     }
     const long long begin = decode_start(total, workers, worker), end = decode_start(total, workers, worker + 1);
     {
-        long long at = before + incl - mine;  // first tile of request b_lo
+        long long at = before + incl - mine;  // first counted tile of request b_lo
         if (begin >= at && begin < at + mine) {
             int b = b_lo;
             for (;; ++b) {
-                const long long n = static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b))) * HH;
+                const long long n = static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b)) + kSegCost) * HH;
                 if (begin < at + n) break;
                 at += n;
             }
@@ -233,26 +268,35 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     seg.b = sh_b;
     seg.len = decode_len(p, seg.b);
     seg.nt = decode_tiles<C::kKeys>(seg.len);
-    seg.hh = static_cast<int>((begin - sh_begin) / seg.nt);
-    seg.t0 = static_cast<int>((begin - sh_begin) % seg.nt);
-    seg.rem = end - begin;
-    seg.t1 = static_cast<int>(seg.rem < seg.nt - seg.t0 ? seg.t0 + seg.rem : seg.nt);
-    seg.rem -= seg.t1 - seg.t0;
-    if (tid == 0) {
-        // the join of a cut unit is done at the first cut: by the block of the worker after the unit's first
-        int4 m = make_int4(-1, 0, 0, 0);
-        if (seg.t0 > 0) {
-            const long long u0 = begin - seg.t0;
-            const int first = decode_worker_of(total, workers, u0);
-            if (first == worker - 1) {
-                m.x = seg.b;
-                m.y = seg.hh;
-                m.z = decode_start(total, workers, first) == u0 ? 2 * first : 2 * first + 1;
-                m.w = decode_worker_of(total, workers, u0 + seg.nt - 1);
+    {
+        const unsigned long long in = static_cast<unsigned long long>(begin - sh_begin);
+        const unsigned unit = static_cast<unsigned>(seg.nt + kSegCost);
+        seg.hh = static_cast<int>(in <= 0xffffffffu ? static_cast<unsigned>(in) / unit : in / unit);
+        const int x = static_cast<int>(in - static_cast<unsigned long long>(seg.hh) * unit);
+        const long long u0 = begin - x;  // first counted tile of the unit
+        seg.rem = end - begin;
+        decode_take(seg, x);
+        if (tid == 0) {
+            // The join of a cut unit is done at the first cut: by the block of the worker after the unit's first
+            // (the one that holds its tile 0).
+            int4 m = make_int4(-1, 0, 0, 0);
+            if (x > kSegCost) {
+                const int first = decode_worker_of(total, workers, u0 + kSegCost);
+                if (first == worker - 1) {
+                    m.x = seg.b;
+                    m.y = seg.hh;
+                    // (the unit's part is the first of its worker's run if the run begins in the unit)
+                    m.z = decode_start(total, workers, first) >= u0 ? 2 * first : 2 * first + 1;
+                    m.w = decode_worker_of(total, workers, u0 + kSegCost + seg.nt - 1);
+                }
             }
+            p.meta[worker] = m;
         }
-        p.meta[worker] = m;
     }
+    bool work = seg.t0 < seg.t1;
+    bool first_seg = work;  // whether the run's first unit, which may be cut at its start, has a tile here
+    if (!work) work = decode_next<C::kKeys>(seg, p);
+    if (!work) return;
 
     // ---- the ring: the next tiles to copy run ahead of the ones in use, across segments
     const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kTileBytes;
@@ -261,11 +305,10 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     bool more = true;
     auto seek = [&]() {
         while (at >= ahead.t1) {
-            if (ahead.rem == 0) {
+            if (!decode_next<C::kKeys>(ahead, p)) {
                 more = false;
                 return;
             }
-            decode_next<C::kKeys>(ahead, p);
             at = ahead.t0 + warp;
         }
     };
@@ -286,7 +329,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) load();
 
-    for (bool first_seg = true;; first_seg = false) {
+    for (;; first_seg = false) {
         const int h = seg.hh / p.row_groups, rg = seg.hh - h * p.row_groups;
         const int rows = min(p.G - rg * C::kRows, C::kRows);  // query heads of this unit
         const long long row0 = static_cast<long long>(seg.b) * p.Hkv * p.G + h * p.G + rg * C::kRows;
@@ -499,7 +542,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
 
         // ---- the warps' results of this segment, added up: 8 rows at a time
         float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat);
-        float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+        float4* merge = reinterpret_cast<float4*>(smem + C::kOffMerge);
         if constexpr (!WIDE) {
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
@@ -520,58 +563,57 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         const float vs = p.v_scale ? p.v_scale[h] : 1.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            __syncthreads();
-            float m = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < C::kWarps; ++w) m = fmaxf(m, stat[w * 16 + g + 8 * r].x);
-            const float mine_m = stat[warp * 16 + g + 8 * r].x;
-            const float f = mine_m == -INFINITY ? 0.f : ptx::ex2_approx(mine_m - m);
-            float* mrow = merge + (warp * 8 + g) * D;
+            if (r > 0) __syncthreads();
+            float4* mrow = merge + (warp * 8 + g) * (D / 4);
             if constexpr (E4M3) {
                 // value n of columns 2t4, 2t4+1 is value (column · D/8 + n)
 #pragma unroll
-                for (int n = 0; n < ND; ++n) {
-                    mrow[(2 * t4) * ND + n] = acc[n][2 * r] * f;
-                    mrow[(2 * t4 + 1) * ND + n] = acc[n][2 * r + 1] * f;
-                }
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int n = 0; n < ND; n += 4)
+                        mrow[merge_col<D, E4M3>(g, ((2 * t4 + j) * ND + n) / 4)] =
+                            make_float4(acc[n][2 * r + j], acc[n + 1][2 * r + j], acc[n + 2][2 * r + j],
+                                        acc[n + 3][2 * r + j]);
             } else {
 #pragma unroll
                 for (int n = 0; n < ND; ++n)
-                    *reinterpret_cast<float2*>(mrow + n * 8 + 2 * t4) =
-                        make_float2(acc[n][2 * r] * f, acc[n][2 * r + 1] * f);
+                    reinterpret_cast<float2*>(mrow + merge_col<D, E4M3>(g, 2 * n + t4 / 2))[t4 & 1] =
+                        make_float2(acc[n][2 * r], acc[n][2 * r + 1]);
             }
             __syncthreads();
             for (int i = tid; i < 8 * D / 4; i += C::kThreads) {
-                const int row = i / (D / 4), col = i % (D / 4) * 4;
+                const int row = i / (D / 4), c4 = i % (D / 4);
                 if (row + 8 * r >= rows) continue;
-                float ms[C::kWarps], mm = -INFINITY, l = 0.f;
+                float2 ml[C::kWarps];
+                float mm = -INFINITY, l = 0.f;
 #pragma unroll
                 for (int w = 0; w < C::kWarps; ++w) {
-                    ms[w] = stat[w * 16 + row + 8 * r].x;
-                    mm = fmaxf(mm, ms[w]);
+                    ml[w] = stat[w * 16 + row + 8 * r];
+                    mm = fmaxf(mm, ml[w].x);
                 }
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < C::kWarps; ++w) {
-                    if (ms[w] != -INFINITY) l += stat[w * 16 + row + 8 * r].y * ptx::ex2_approx(ms[w] - mm);
-                    const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * D + col);
-                    o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+                    if (ml[w].x == -INFINITY) continue;  // (its O is zero)
+                    const float f = ptx::ex2_approx(ml[w].x - mm);
+                    const float4 x = merge[(w * 8 + row) * (D / 4) + merge_col<D, E4M3>(row, c4)];
+                    l += ml[w].y * f;
+                    o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
                 }
                 if (whole) {
                     const float inv = l == 0.f ? 0.f : vs / l;
                     const long long out = row0 + row + 8 * r;
-                    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.o) + out * D + col) =
+                    reinterpret_cast<uint2*>(p.o)[out * (D / 4) + c4] =
                         make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
-                    if (col == 0 && p.lse)
+                    if (c4 == 0 && p.lse)
                         p.lse[out] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
                 } else {
-                    *reinterpret_cast<float4*>(p.part_o + ((slot * C::kRows) + row + 8 * r) * D + col) = o;
-                    if (col == 0) p.part_ml[slot * C::kRows + row + 8 * r] = make_float2(mm, l);
+                    reinterpret_cast<float4*>(p.part_o)[(slot * C::kRows + row + 8 * r) * (D / 4) + c4] = o;
+                    if (c4 == 0) p.part_ml[slot * C::kRows + row + 8 * r] = make_float2(mm, l);
                 }
             }
         }
-        if (seg.rem == 0) break;
-        decode_next<C::kKeys>(seg, p);
+        if (!decode_next<C::kKeys>(seg, p)) break;
         __syncthreads();  // stat and merge are written again
     }
 }

@@ -114,13 +114,14 @@ int launched() {
 
 // ---------------------------------------------------------------- decode
 
-// Workers (blocks) of a launch: two per SM, or one for every four tiles that
-// the batch can have at most, if those are fewer.
+// Workers (blocks) of a launch: two per SM, or as many as the longest batch of
+// these sizes has least runs, if those are fewer.
 long long decode_workers(long long B, long long Hq, long long Hkv, int d, int type, long long max_keys, int sms) {
     const int keys = 4096 / (d * (type == FA_CACHE_E4M3 ? 1 : 2));
     const long long G = Hq / Hkv, groups = (G + 15) / 16;
-    const long long tiles = B * Hkv * groups * std::max<long long>(1, (max_keys + keys - 1) / keys);
-    return std::min<long long>(static_cast<long long>(kWorkersPerSm) * sms, (tiles + 3) / 4);
+    const long long units = B * Hkv * groups, tiles = std::max<long long>(1, (max_keys + keys - 1) / keys);
+    const long long most = (units * (tiles + fa::kSegCost) + fa::kMinRun - 1) / fa::kMinRun;
+    return std::min<long long>(static_cast<long long>(kWorkersPerSm) * sms, most);
 }
 
 struct DecodeSpace {
