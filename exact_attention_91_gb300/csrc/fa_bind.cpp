@@ -178,12 +178,12 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const long long room = fa_decode_paged_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, cache.type,
                                                          cache.page_size, to_int(width), sms);
         if (room < 0) return PyLong_FromLongLong(room);
-        ws = make({room}, at::kByte, q);
+        if (room > 0) ws = make({room}, at::kByte, q);
     }
     const int rc = fa_decode_paged(q.data_ptr(), &cache, static_cast<const int*>(table.data_ptr()),
                                    static_cast<const int*>(lens.data_ptr()), out.data_ptr(),
                                    static_cast<float*>(ptr(lse)), to_int(B), to_int(Hq), to_int(width), table.stride(0),
-                                   scale, ws.data_ptr(), static_cast<size_t>(ws.numel()),
+                                   scale, ptr(ws), ws.defined() ? static_cast<size_t>(ws.numel()) : 0,
                                    c10::cuda::getCurrentCUDAStream(device.index()).stream());
     if (rc != FA_OK) return PyLong_FromLong(rc);
     return return_lse ? pair(std::move(out), std::move(lse)) : THPVariable_Wrap(std::move(out));
@@ -206,7 +206,8 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       "positions must be [N] or [B, N] (x [B, H, N, d]), or [T] (x [T, H, d])");
     TORCH_CHECK_VALUE(x.stride(-1) == 1 && dense_last(pos), "d of x and the rows of positions must be contiguous");
     TORCH_CHECK_VALUE(!out.defined() || (out.scalar_type() == at::kBFloat16 && out.sizes() == x.sizes() &&
-                                         out.stride(-1) == 1), "out must be a bf16 tensor of x's shape with d contiguous");
+                                         out.stride(-1) == 1),
+                      "out must be a bf16 tensor of x's shape with d contiguous");
     const double factor = number(a[5]);
     const c10::Device device = x.device();
     const int r = frequencies(freq, device);

@@ -20,6 +20,10 @@
 //    fp32 partial (O, reference maximum, sum) per worker in the workspace and
 //    fa_decode_join_kernel adds them up. A worker's run has at most two cut
 //    units, its first and its last: two slots each.
+//  * A batch that can be no larger than one wave of short shares (the lengths'
+//    bound is the table's width) is done by clusters instead, one per unit,
+//    whose blocks' partials meet in distributed shared memory: no scan of the
+//    lengths, no second launch.
 //  * One warp-level mma.sync m16n8k16 tile holds up to 16 query heads; tcgen05
 //    would want 128 rows (heads) or a softmax across TMEM lanes, for flops that
 //    are not the bound. With at most 8 heads the tile's rows 8-15 carry the
@@ -51,6 +55,7 @@ struct DecodeParams {
     long long table_stride;
     float scale_log2;
     int B, Hkv, G, row_groups, num_blocks, page_shift, width;
+    int cluster;            // blocks per unit of the small form
 };
 
 template <int D, bool E4M3, bool WIDE>
@@ -67,8 +72,8 @@ struct DecodeCfg {
     static constexpr int kRowsPerCopy = 32 / kRowLanes;
     static constexpr int kCopiesPerGroup = 16 / kRowsPerCopy;
     static constexpr int kOffMerge = kWarps * kStages * kTileBytes;  // fp32 [warp][8][D]
-    static constexpr int kOffStat = kOffMerge + kWarps * 8 * D * 4;  // float2 [warp][16]
-    static constexpr int kSmemBytes = kOffStat + kWarps * 16 * 8 + 64;
+    static constexpr int kOffStat = kOffMerge + kWarps * 8 * D * 4;  // float2 [warp][16], and the block's [16]
+    static constexpr int kSmemBytes = kOffStat + (kWarps + 1) * 16 * 8;
     // P is kept in 16 bits: fp16's range is used up to 2^15 (kBias + kLazy), so
     // that what falls below its smallest step, 2^-24, is below 2^-31 of the
     // largest weight.
@@ -80,6 +85,8 @@ struct DecodeCfg {
 // What a segment costs besides its tiles (q, the warps' merge, the output), in
 // tiles of one worker: a run of many short requests must not count as little.
 constexpr int kSegCost = 6;
+// Most blocks of a cluster (the portable limit).
+constexpr int kDecodeCluster = 8;
 // Least run of a worker, in tiles with the segments' costs.
 constexpr int kMinRun = 8;
 
@@ -131,7 +138,8 @@ __device__ __forceinline__ bool decode_next(DecodeSeg& s, const DecodeParams& p)
 // `workers`; the worker of a counted tile. (64-bit divisions take about 150
 // cycles each, and nothing else can start before them.)
 __device__ __forceinline__ long long decode_start(long long total, int workers, int c) {
-    if (total < (1 << 20)) return static_cast<unsigned>(total) * static_cast<unsigned>(c) / static_cast<unsigned>(workers);
+    if (total < (1 << 20))
+        return static_cast<unsigned>(total) * static_cast<unsigned>(c) / static_cast<unsigned>(workers);
     return total * c / workers;
 }
 __device__ __forceinline__ int decode_worker_of(long long total, int workers, long long tile) {
@@ -208,7 +216,10 @@ __device__ __forceinline__ int decode_page(const DecodeParams& p, const DecodeSe
     return key < s.len ? __ldg(p.table + s.b * p.table_stride + (key >> p.page_shift)) : -1;
 }
 
-template <int D, bool E4M3, bool WIDE>
+// CLUSTER: the small form. Block r of a cluster of p.cluster takes the r-th
+// share of one unit's tiles; the blocks' results are added up through
+// distributed shared memory.
+template <int D, bool E4M3, bool WIDE, bool CLUSTER>
 __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p) {
     using C = DecodeCfg<D, E4M3, WIDE>;
     constexpr int NT = C::kKeys / 8;  // score columns, 8 keys each
@@ -221,82 +232,94 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     __shared__ int sh_b;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int HH = p.Hkv * p.row_groups;
-    ptx::griddep_launch_dependents();
-
-    // ---- this worker's run of tiles
-    const int per = (p.B + C::kThreads - 1) / C::kThreads;
-    const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
-    long long mine = 0;  // counted tiles of requests [b_lo, b_hi)
-    for (int b = b_lo; b < b_hi; ++b)
-        mine += static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b)) + kSegCost) * HH;
-    long long incl = mine;
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, i);
-        if (lane >= i) incl += x;
-    }
-    if (lane == 31) sh_warp[warp] = incl;
-    __syncthreads();
-    long long total = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) {
-        if (w < warp) before += sh_warp[w];
-        total += sh_warp[w];
-    }
-    const int worker = blockIdx.x;
-    const int workers = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kMinRun - 1) / kMinRun));
-    if (worker >= workers) {
-        if (tid == 0) p.meta[worker] = make_int4(-1, 0, 0, 0);
-        return;
-    }
-    const long long begin = decode_start(total, workers, worker), end = decode_start(total, workers, worker + 1);
-    {
-        long long at = before + incl - mine;  // first counted tile of request b_lo
-        if (begin >= at && begin < at + mine) {
-            int b = b_lo;
-            for (;; ++b) {
-                const long long n = static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b)) + kSegCost) * HH;
-                if (begin < at + n) break;
-                at += n;
-            }
-            sh_b = b;
-            sh_begin = at;
-        }
-    }
-    __syncthreads();
     DecodeSeg seg;
-    seg.b = sh_b;
-    seg.len = decode_len(p, seg.b);
-    seg.nt = decode_tiles<C::kKeys>(seg.len);
-    {
-        const unsigned long long in = static_cast<unsigned long long>(begin - sh_begin);
-        const unsigned unit = static_cast<unsigned>(seg.nt + kSegCost);
-        seg.hh = static_cast<int>(in <= 0xffffffffu ? static_cast<unsigned>(in) / unit : in / unit);
-        const int x = static_cast<int>(in - static_cast<unsigned long long>(seg.hh) * unit);
-        const long long u0 = begin - x;  // first counted tile of the unit
-        seg.rem = end - begin;
-        decode_take(seg, x);
-        if (tid == 0) {
-            // The join of a cut unit is done at the first cut: by the block of the worker after the unit's first
-            // (the one that holds its tile 0).
-            int4 m = make_int4(-1, 0, 0, 0);
-            if (x > kSegCost) {
-                const int first = decode_worker_of(total, workers, u0 + kSegCost);
-                if (first == worker - 1) {
-                    m.x = seg.b;
-                    m.y = seg.hh;
-                    // (the unit's part is the first of its worker's run if the run begins in the unit)
-                    m.z = decode_start(total, workers, first) >= u0 ? 2 * first : 2 * first + 1;
-                    m.w = decode_worker_of(total, workers, u0 + kSegCost + seg.nt - 1);
-                }
-            }
-            p.meta[worker] = m;
+    bool first_seg = true;
+    const int worker = blockIdx.x;
+    if constexpr (CLUSTER) {
+        const int unit = worker / p.cluster, rank = worker - unit * p.cluster;
+        seg.b = unit / HH;
+        seg.hh = unit - seg.b * HH;
+        seg.len = decode_len(p, seg.b);
+        seg.nt = decode_tiles<C::kKeys>(seg.len);
+        seg.t0 = seg.nt * rank / p.cluster;
+        seg.t1 = seg.nt * (rank + 1) / p.cluster;
+        seg.rem = 0;
+    } else {
+        ptx::griddep_launch_dependents();
+
+        // ---- this worker's run of tiles
+        const int per = (p.B + C::kThreads - 1) / C::kThreads;
+        const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
+        auto counted = [&](int b) {
+            return static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b)) + kSegCost) * HH;
+        };
+        long long mine = 0;  // counted tiles of requests [b_lo, b_hi)
+        for (int b = b_lo; b < b_hi; ++b) mine += counted(b);
+        long long incl = mine;
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, i);
+            if (lane >= i) incl += x;
         }
+        if (lane == 31) sh_warp[warp] = incl;
+        __syncthreads();
+        long long total = 0, before = 0;
+#pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) {
+            if (w < warp) before += sh_warp[w];
+            total += sh_warp[w];
+        }
+        const int workers = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kMinRun - 1) / kMinRun));
+        if (worker >= workers) {
+            if (tid == 0) p.meta[worker] = make_int4(-1, 0, 0, 0);
+            return;
+        }
+        const long long begin = decode_start(total, workers, worker), end = decode_start(total, workers, worker + 1);
+        {
+            long long at = before + incl - mine;  // first counted tile of request b_lo
+            if (begin >= at && begin < at + mine) {
+                int b = b_lo;
+                for (;; ++b) {
+                    const long long n = counted(b);
+                    if (begin < at + n) break;
+                    at += n;
+                }
+                sh_b = b;
+                sh_begin = at;
+            }
+        }
+        __syncthreads();
+        seg.b = sh_b;
+        seg.len = decode_len(p, seg.b);
+        seg.nt = decode_tiles<C::kKeys>(seg.len);
+        {
+            const unsigned long long in = static_cast<unsigned long long>(begin - sh_begin);
+            const unsigned unit = static_cast<unsigned>(seg.nt + kSegCost);
+            seg.hh = static_cast<int>(in <= 0xffffffffu ? static_cast<unsigned>(in) / unit : in / unit);
+            const int x = static_cast<int>(in - static_cast<unsigned long long>(seg.hh) * unit);
+            const long long u0 = begin - x;  // first counted tile of the unit
+            seg.rem = end - begin;
+            decode_take(seg, x);
+            if (tid == 0) {
+                // The join of a cut unit is done at the first cut: by the block of the worker after the unit's first
+                // (the one that holds its tile 0).
+                int4 m = make_int4(-1, 0, 0, 0);
+                if (x > kSegCost) {
+                    const int first = decode_worker_of(total, workers, u0 + kSegCost);
+                    if (first == worker - 1) {
+                        m.x = seg.b;
+                        m.y = seg.hh;
+                        // (the unit's part is the first of its worker's run if the run begins in the unit)
+                        m.z = decode_start(total, workers, first) >= u0 ? 2 * first : 2 * first + 1;
+                        m.w = decode_worker_of(total, workers, u0 + kSegCost + seg.nt - 1);
+                    }
+                }
+                p.meta[worker] = m;
+            }
+        }
+        first_seg = seg.t0 < seg.t1;  // whether the run's first unit, which may be cut at its start, has a tile here
+        if (!first_seg && !decode_next<C::kKeys>(seg, p)) return;
     }
-    bool work = seg.t0 < seg.t1;
-    bool first_seg = work;  // whether the run's first unit, which may be cut at its start, has a tile here
-    if (!work) work = decode_next<C::kKeys>(seg, p);
-    if (!work) return;
 
     // ---- the ring: the next tiles to copy run ahead of the ones in use, across segments
     const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kTileBytes;
@@ -558,7 +581,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                 // (a sum of zero: no key, or scores of -inf alone; NaN is no zero and is passed on)
                 stat[warp * 16 + g + 8 * r] = make_float2(sum[r] == 0.f ? -INFINITY : m_use[r], sum[r]);
         }
-        const bool whole = seg.t0 == 0 && seg.t1 == seg.nt;
+        const bool whole = CLUSTER ? p.cluster == 1 : seg.t0 == 0 && seg.t1 == seg.nt;
         const long long slot = 2LL * worker + (first_seg ? 0 : 1);
         const float vs = p.v_scale ? p.v_scale[h] : 1.f;
 #pragma unroll
@@ -607,11 +630,54 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                         make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
                     if (c4 == 0 && p.lse)
                         p.lse[out] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+                } else if constexpr (CLUSTER) {  // (the ring is idle: every copy was waited for and read)
+                    reinterpret_cast<float4*>(smem)[(row + 8 * r) * (D / 4) + c4] = o;
+                    if (c4 == 0) stat[C::kWarps * 16 + row + 8 * r] = make_float2(mm, l);
                 } else {
                     reinterpret_cast<float4*>(p.part_o)[(slot * C::kRows + row + 8 * r) * (D / 4) + c4] = o;
                     if (c4 == 0) p.part_ml[slot * C::kRows + row + 8 * r] = make_float2(mm, l);
                 }
             }
+        }
+        if constexpr (CLUSTER) {
+            if (whole) return;
+            __syncwarp();
+            ptx::cluster_sync();
+            // element (row, c4) of the output is done by block (element % cluster)
+            const int rank = worker % p.cluster;
+            const uint32_t o_at = ptx::smem_u32(smem), ml_at = ptx::smem_u32(stat + C::kWarps * 16);
+            for (int i = tid * p.cluster + rank; i < rows * D / 4; i += C::kThreads * p.cluster) {
+                const int row = i / (D / 4), c4 = i % (D / 4);
+                float2 ml[kDecodeCluster];
+                float4 x[kDecodeCluster];
+                float mm = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kDecodeCluster; ++w) {
+                    ml[w] = make_float2(-INFINITY, 0.f);
+                    if (w < p.cluster) {
+                        ml[w] = make_float2(ptx::ld_dsmem_f32(ptx::mapa_shared(ml_at + row * 8, w)),
+                                            ptx::ld_dsmem_f32(ptx::mapa_shared(ml_at + row * 8 + 4, w)));
+                        x[w] = ptx::ld_dsmem_v4(ptx::mapa_shared(o_at + i * 16, w));
+                    }
+                    mm = fmaxf(mm, ml[w].x);
+                }
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kDecodeCluster; ++w) {
+                    if (ml[w].x == -INFINITY) continue;
+                    const float f = ptx::ex2_approx(ml[w].x - mm);
+                    l += ml[w].y * f;
+                    o.x += x[w].x * f, o.y += x[w].y * f, o.z += x[w].z * f, o.w += x[w].w * f;
+                }
+                const float inv = l == 0.f ? 0.f : vs / l;
+                const long long out = row0 + row;
+                reinterpret_cast<uint2*>(p.o)[out * (D / 4) + c4] =
+                    make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+                if (c4 == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+            }
+            __syncwarp();
+            ptx::cluster_sync();  // the other blocks' shared memory is read until here
+            return;
         }
         if (!decode_next<C::kKeys>(seg, p)) break;
         __syncthreads();  // stat and merge are written again

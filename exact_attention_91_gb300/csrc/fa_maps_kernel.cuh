@@ -38,7 +38,8 @@ struct MapsParams {
 __device__ __forceinline__ unsigned sat_add(unsigned a, unsigned b) { return min(a + b, 0x7fffffffu); }
 
 // Pages that request lengths (context, fresh) hold, and take now.
-__device__ __forceinline__ void maps_pages(unsigned c, unsigned n, int shift, int width, unsigned& held, unsigned& take) {
+__device__ __forceinline__ void maps_pages(unsigned c, unsigned n, int shift, int width, unsigned& held,
+                                           unsigned& take) {
     const unsigned round = (1u << shift) - 1;
     held = (c + round) >> shift;  // (c <= 2^31 - 1, round < 2^20: no wrap)
     const unsigned want = min((sat_add(c, n) + round) >> shift, static_cast<unsigned>(width));
@@ -137,7 +138,8 @@ __global__ void __launch_bounds__(kMapsThreads) fa_page_maps_kernel(const MapsPa
     for (unsigned i = at; i < all_page; i += stride) {
         const int b = maps_find(first, p.B + 1, i);
         const unsigned held = (max(p.context_lens[b], 0) + (1u << p.page_shift) - 1) >> p.page_shift;
-        p.table[b * p.table_stride + held + (i - first[b])] = i < static_cast<unsigned>(p.num_unused) ? p.unused[i] : -1;
+        p.table[b * p.table_stride + held + (i - first[b])] =
+            i < static_cast<unsigned>(p.num_unused) ? p.unused[i] : -1;
     }
     // ---- tokens
     for (unsigned t = at; t < static_cast<unsigned>(p.T); t += stride) {

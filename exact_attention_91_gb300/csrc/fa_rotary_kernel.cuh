@@ -72,7 +72,7 @@ __device__ __forceinline__ unsigned long long rot_turns(double inv_freq) {
 
 // cos and sin of a position's angle.
 __device__ __forceinline__ float2 rot_cos_sin(int position, unsigned long long turns, float factor, float sign) {
-    const long long phase = static_cast<long long>(static_cast<unsigned long long>(static_cast<long long>(position)) * turns);
+    const unsigned long long phase = static_cast<unsigned long long>(static_cast<long long>(position)) * turns;
     float s, c;
     sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &s, &c);
     return make_float2(c * factor, s * factor * sign);

@@ -21,6 +21,7 @@ namespace {
 constexpr int kMinPage = 16, kMaxPage = 65536;
 constexpr long long kMaxKeys = 0x7fff0000LL;  // of a request: key indexes stay in int
 constexpr int kWorkersPerSm = 2;
+constexpr int kMaxShare = 16;  // tiles (four a warp) of a block in the small form
 
 std::mutex g_ready_mu;
 std::atomic<bool> g_ready[fa::kHostMaxDevices];
@@ -82,7 +83,9 @@ bool set_smem(Kernel kernel, int bytes) {
 
 template <int D, bool E4M3, bool WIDE>
 bool set_decode() {
-    return set_smem(fa::fa_decode_kernel<D, E4M3, WIDE>, fa::DecodeCfg<D, E4M3, WIDE>::kSmemBytes);
+    constexpr int bytes = fa::DecodeCfg<D, E4M3, WIDE>::kSmemBytes;
+    return set_smem(fa::fa_decode_kernel<D, E4M3, WIDE, false>, bytes) &&
+           set_smem(fa::fa_decode_kernel<D, E4M3, WIDE, true>, bytes);
 }
 
 constexpr int kMapsSmem = 2 * (fa::kMapsMaxRequests + 1) * 4;
@@ -114,14 +117,23 @@ int launched() {
 
 // ---------------------------------------------------------------- decode
 
-// Workers (blocks) of a launch: two per SM, or as many as the longest batch of
-// these sizes has least runs, if those are fewer.
-long long decode_workers(long long B, long long Hq, long long Hkv, int d, int type, long long max_keys, int sms) {
+// How a launch is laid out, from what the host knows: the sizes and the longest
+// request that the table can hold.
+struct DecodePlan {
+    int cluster;        // blocks per unit of the small form, or 0: equal runs
+    long long workers;  // blocks of equal runs
+};
+DecodePlan decode_plan(long long B, long long Hq, long long Hkv, int d, int type, long long max_keys, int sms) {
     const int keys = 4096 / (d * (type == FA_CACHE_E4M3 ? 1 : 2));
     const long long G = Hq / Hkv, groups = (G + 15) / 16;
     const long long units = B * Hkv * groups, tiles = std::max<long long>(1, (max_keys + keys - 1) / keys);
+    const long long resident = static_cast<long long>(kWorkersPerSm) * sms;
+    // The small form, if one wave holds it and no block's share is longer than kMaxShare tiles.
+    for (int c = 1; c <= fa::kDecodeCluster && units * c <= resident; c *= 2)
+        if (tiles <= static_cast<long long>(c) * kMaxShare) return {c, 0};
+    // Equal runs: two workers per SM, or as many as the longest batch of these sizes has least runs.
     const long long most = (units * (tiles + fa::kSegCost) + fa::kMinRun - 1) / fa::kMinRun;
-    return std::min<long long>(static_cast<long long>(kWorkersPerSm) * sms, most);
+    return {0, std::min(resident, most)};
 }
 
 struct DecodeSpace {
@@ -144,25 +156,37 @@ int check_decode_sizes(long long B, long long Hq, long long Hkv, int d, int page
 }
 
 template <int D, bool E4M3, bool WIDE>
-int launch_decode(const fa::DecodeParams& p, unsigned workers, cudaStream_t s) {
+int launch_decode(const fa::DecodeParams& p, unsigned blocks, cudaStream_t s) {
     using C = fa::DecodeCfg<D, E4M3, WIDE>;
-    fa::fa_decode_kernel<D, E4M3, WIDE><<<workers, C::kThreads, C::kSmemBytes, s>>>(p);
-    if (launched() != FA_OK) return FA_ERR_LAUNCH;
-    if (workers == 1) return FA_OK;  // nothing is cut
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(workers, static_cast<unsigned>(std::min(p.G, C::kRows)), 1);
-    cfg.blockDim = dim3(128, 1, 1);
-    cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fa::fa_decode_join_kernel<D, C::kRows>, p) != cudaSuccess) {
+    if (p.cluster > 0) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, fa::fa_decode_kernel<D, E4M3, WIDE, true>, p) == cudaSuccess) return FA_OK;
         cudaGetLastError();
         return FA_ERR_LAUNCH;
     }
-    return FA_OK;
+    if (cudaLaunchKernelEx(&cfg, fa::fa_decode_kernel<D, E4M3, WIDE, false>, p) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_LAUNCH;
+    }
+    if (blocks == 1) return FA_OK;  // nothing is cut
+    cfg.gridDim = dim3(blocks, static_cast<unsigned>(std::min(p.G, C::kRows)), 1);
+    cfg.dynamicSmemBytes = 0;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fa::fa_decode_join_kernel<D, C::kRows>, p) == cudaSuccess) return FA_OK;
+    cudaGetLastError();
+    return FA_ERR_LAUNCH;
 }
 
 template <int D>
@@ -210,9 +234,9 @@ long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_typ
     if (rc != FA_OK) return rc;
     if (cache_type != FA_CACHE_BF16 && cache_type != FA_CACHE_E4M3) return FA_ERR_BAD_TYPE;
     if (sm_count < 1) return FA_ERR_BAD_SHAPE;
-    const long long w = decode_workers(B, Hq, Hkv, d, cache_type, static_cast<long long>(table_width) * page_size,
-                                       sm_count);
-    return static_cast<long long>(decode_space(w, Hq / Hkv > 8 ? 16 : 8, d).bytes);
+    const DecodePlan plan = decode_plan(B, Hq, Hkv, d, cache_type, static_cast<long long>(table_width) * page_size,
+                                        sm_count);
+    return static_cast<long long>(decode_space(plan.workers, Hq / Hkv > 8 ? 16 : 8, d).bytes);
 }
 
 int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block_table, const int* seq_lens, void* o,
@@ -248,10 +272,10 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
     rc = fa::host_probe(&dev, &sms);
     if (rc != FA_OK) return rc;
     const bool wide = Hq / Hkv > 8;
-    const long long workers = decode_workers(B, Hq, Hkv, d, cache->type,
-                                             static_cast<long long>(table_width) * cache->page_size, sms);
-    const DecodeSpace sp = decode_space(workers, wide ? 16 : 8, d);
-    if (!workspace || workspace_bytes < sp.bytes) return FA_ERR_WORKSPACE;
+    const DecodePlan plan = decode_plan(B, Hq, Hkv, d, cache->type,
+                                        static_cast<long long>(table_width) * cache->page_size, sms);
+    const DecodeSpace sp = decode_space(plan.workers, wide ? 16 : 8, d);
+    if (sp.bytes > 0 && (!workspace || workspace_bytes < sp.bytes)) return FA_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (ready(dev, s) != FA_OK) return FA_ERR_LAUNCH;
 
@@ -265,10 +289,12 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
     p.lens = seq_lens;
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.meta = reinterpret_cast<int4*>(ws + sp.meta);
-    p.part_ml = reinterpret_cast<float2*>(ws + sp.ml);
-    p.part_o = reinterpret_cast<float*>(ws + sp.o);
+    if (sp.bytes > 0) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        p.meta = reinterpret_cast<int4*>(ws + sp.meta);
+        p.part_ml = reinterpret_cast<float2*>(ws + sp.ml);
+        p.part_o = reinterpret_cast<float*>(ws + sp.o);
+    }
     p.k_block = c.k_block, p.k_token = c.k_token, p.k_head = c.k_head;
     p.v_block = c.v_block, p.v_token = c.v_token, p.v_head = c.v_head;
     p.table_stride = B > 1 ? table_stride : 0;
@@ -280,7 +306,9 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
     p.num_blocks = cache->num_blocks;
     p.page_shift = c.shift;
     p.width = table_width;
-    const unsigned w = static_cast<unsigned>(workers);
+    p.cluster = plan.cluster;
+    const long long units = static_cast<long long>(B) * Hkv * p.row_groups;
+    const unsigned w = static_cast<unsigned>(plan.cluster > 0 ? units * plan.cluster : plan.workers);
     return d == 64 ? launch_decode_any<64>(c.e4m3, wide, p, w, s) : launch_decode_any<128>(c.e4m3, wide, p, w, s);
 }
 
@@ -481,7 +509,7 @@ int fa_page_maps(const int* context_lens, const int* new_lens, int* block_table,
     p.num_unused = num_unused;
     p.T = T;
     // one token per thread up to one block per SM
-    const long long blocks = std::max<long long>(1, (static_cast<long long>(T) + fa::kMapsThreads - 1) / fa::kMapsThreads);
+    const long long blocks = std::max<long long>(1, (T + fa::kMapsThreads - 1LL) / fa::kMapsThreads);
     const unsigned grid = static_cast<unsigned>(std::min<long long>(blocks, sms));
     fa::fa_page_maps_kernel<<<grid, fa::kMapsThreads, 2 * (B + 1) * 4, s>>>(p);
     return launched();

@@ -255,7 +255,7 @@ typedef struct fa_paged_cache {
  *                More than table_width*page_size counts as that many
  *                (at most 2^31 - 65536).
  *   workspace    device, 16-byte aligned, at least fa_decode_paged_workspace()
- *                bytes; needs no initial value, holds nothing after the call's
+ *                bytes (NULL if that is 0: a small batch needs none); needs no initial value, holds nothing after the call's
  *                kernels. Calls (or graph replays) that may overlap in time
  *                need workspaces of their own.
  *

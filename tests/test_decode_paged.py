@@ -54,6 +54,16 @@ def make(lens, hq, hkv, d, page, e4m3=False, order="token", seed=0, extra=2, wid
     return dict(q=q, k=k, v=v, table=table.cuda(), lens=torch.tensor(lens, dtype=torch.int32).cuda(), ks=ks, vs=vs)
 
 
+def small_form(fa, x):
+    """Whether the call is done by clusters, one per request and key head (it
+    then needs no workspace), and not cut into equal runs."""
+    B, hq, d = x["q"].shape
+    _, page, hkv, _ = x["k"].shape
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    kind = fa.CACHE_E4M3 if x["k"].dtype == torch.float8_e4m3fn else fa.CACHE_BF16
+    return fa.fa_decode_paged_workspace(B, hq, hkv, d, kind, page, x["table"].shape[1], sms) == 0
+
+
 def call(fa, x, **kw):
     return fa.attention_decode_paged(x["q"], x["k"], x["v"], x["table"], x["lens"], k_scale=x["ks"], v_scale=x["vs"],
                                      **kw)
@@ -80,8 +90,27 @@ EDGES = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200]
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (8, 1), (6, 2), (16, 2), (18, 2), (16, 1), (40, 1)])
 def test_lengths_around_tiles_and_pages(d, e4m3, hq, hkv):
+    """Both forms: the table's width alone decides which."""
     fa = _fa()
-    check(fa, make(EDGES, hq, hkv, d, 16, e4m3, seed=hq * 100 + hkv))
+    x = make(EDGES, hq, hkv, d, 16, e4m3, seed=hq * 100 + hkv)
+    assert small_form(fa, x)
+    check(fa, x)
+    x = make(EDGES, hq, hkv, d, 16, e4m3, seed=hq * 100 + hkv, width=5000)
+    assert not small_form(fa, x)
+    check(fa, x)
+
+
+@pytest.mark.parametrize("d,e4m3,hq,hkv", [(128, False, 4, 1), (64, True, 24, 2), (128, True, 3, 3), (64, False, 20, 1)])
+@pytest.mark.parametrize("tiles", [3, 16, 17, 32, 33, 64, 100, 128, 129])
+def test_cluster_sizes(d, e4m3, hq, hkv, tiles):
+    """Tables of 1 to 128 tiles (clusters of 1 to 8 blocks, shares with and
+    without tiles) and the first past them."""
+    fa = _fa()
+    keys = 4096 // (d if e4m3 else 2 * d)
+    n = tiles * keys
+    x = make([n, n - 1, 1, 0, keys + 1, n // 2], hq, hkv, d, 16, e4m3, seed=tiles)
+    assert small_form(fa, x) == (tiles <= 128)
+    check(fa, x)
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 256])
