@@ -573,4 +573,4 @@ def page_maps(context_lens, new_lens, block_table, unused_blocks, page_size: int
         r = _on_stream(stream, maps, context_lens, new_lens, block_table, unused_blocks, page_size, num_tokens, out)
     if type(r) is int:
         raise FaError(r, "fa_page_maps")
-    return PageMaps._make(r) if out is None else out
+    return tuple.__new__(PageMaps, r) if out is None else out

@@ -309,8 +309,20 @@ PyObject* maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (const Tensor* t : {&ctx, &fresh, &unused}) on(*t, device);
     for (const Tensor& t : out) on(t, device);
     const c10::cuda::CUDAGuard guard(device);
-    if (a[6] == Py_None)
-        for (int i = 0; i < 5; ++i) out[i] = make({sizes[i]}, at::kInt, table);
+    if (a[6] == Py_None) {
+        // five parts of one allocation (each at a 16-byte boundary): allocations take most of a short call
+        int64_t at = 0;
+        for (int64_t n : sizes) at += (n + 3) / 4 * 4;
+        const Tensor whole = make({at}, at::kInt, table);
+        at = 0;
+        for (int i = 0; i < 5; ++i) {
+            out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()),
+                                                              whole.key_set(), whole.dtype());
+            out[i].unsafeGetTensorImpl()->set_storage_offset(at);
+            out[i].unsafeGetTensorImpl()->set_sizes_contiguous({sizes[i]});
+            at += (sizes[i] + 3) / 4 * 4;
+        }
+    }
     int* p[5];
     for (int i = 0; i < 5; ++i) p[i] = static_cast<int*>(out[i].data_ptr());
     const int rc = fa_page_maps(static_cast<const int*>(ctx.data_ptr()), static_cast<const int*>(fresh.data_ptr()),

@@ -21,7 +21,7 @@ namespace {
 constexpr int kMinPage = 16, kMaxPage = 65536;
 constexpr long long kMaxKeys = 0x7fff0000LL;  // of a request: key indexes stay in int
 constexpr int kWorkersPerSm = 2;
-constexpr int kMaxShare = 16;  // tiles (four a warp) of a block in the small form
+constexpr int kShare = 8, kMaxShare = 32;  // tiles (two and eight a warp) of a block in the small form
 
 std::mutex g_ready_mu;
 std::atomic<bool> g_ready[fa::kHostMaxDevices];
@@ -128,9 +128,11 @@ DecodePlan decode_plan(long long B, long long Hq, long long Hkv, int d, int type
     const long long G = Hq / Hkv, groups = (G + 15) / 16;
     const long long units = B * Hkv * groups, tiles = std::max<long long>(1, (max_keys + keys - 1) / keys);
     const long long resident = static_cast<long long>(kWorkersPerSm) * sms;
-    // The small form, if one wave holds it and no block's share is longer than kMaxShare tiles.
-    for (int c = 1; c <= fa::kDecodeCluster && units * c <= resident; c *= 2)
-        if (tiles <= static_cast<long long>(c) * kMaxShare) return {c, 0};
+    // The small form, if one wave holds it and no block's share is longer than kMaxShare tiles: clusters as
+    // large as bring the shares down to kShare, or as one wave holds.
+    int c = 1;
+    while (c < fa::kDecodeCluster && 2 * c * units <= resident && tiles > static_cast<long long>(c) * kShare) c *= 2;
+    if (c * units <= resident && tiles <= static_cast<long long>(c) * kMaxShare) return {c, 0};
     // Equal runs: two workers per SM, or as many as the longest batch of these sizes has least runs.
     const long long most = (units * (tiles + fa::kSegCost) + fa::kMinRun - 1) / fa::kMinRun;
     return {0, std::min(resident, most)};

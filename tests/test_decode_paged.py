@@ -101,15 +101,15 @@ def test_lengths_around_tiles_and_pages(d, e4m3, hq, hkv):
 
 
 @pytest.mark.parametrize("d,e4m3,hq,hkv", [(128, False, 4, 1), (64, True, 24, 2), (128, True, 3, 3), (64, False, 20, 1)])
-@pytest.mark.parametrize("tiles", [3, 16, 17, 32, 33, 64, 100, 128, 129])
+@pytest.mark.parametrize("tiles", [3, 8, 9, 16, 17, 32, 33, 100, 256, 257])
 def test_cluster_sizes(d, e4m3, hq, hkv, tiles):
-    """Tables of 1 to 128 tiles (clusters of 1 to 8 blocks, shares with and
+    """Tables of 1 to 256 tiles (clusters of 1 to 8 blocks, shares with and
     without tiles) and the first past them."""
     fa = _fa()
     keys = 4096 // (d if e4m3 else 2 * d)
     n = tiles * keys
     x = make([n, n - 1, 1, 0, keys + 1, n // 2], hq, hkv, d, 16, e4m3, seed=tiles)
-    assert small_form(fa, x) == (tiles <= 128)
+    assert small_form(fa, x) == (tiles <= 256)
     check(fa, x)
 
 
