@@ -235,6 +235,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     DecodeSeg seg;
     bool first_seg = true;
     const int worker = blockIdx.x;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     if constexpr (CLUSTER) {
         const int unit = worker / p.cluster, rank = worker - unit * p.cluster;
         seg.b = unit / HH;
@@ -245,8 +247,6 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         seg.t1 = seg.nt * (rank + 1) / p.cluster;
         seg.rem = 0;
     } else {
-        ptx::griddep_launch_dependents();
-
         // ---- this worker's run of tiles
         const int per = (p.B + C::kThreads - 1) / C::kThreads;
         const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
@@ -693,6 +693,7 @@ __global__ void __launch_bounds__(128) fa_decode_join_kernel(const DecodeParams 
     constexpr int kCols = D / 4, kParts = 128 / kCols;
     __shared__ float4 sh_o[128];
     __shared__ float2 sh_ml[kParts];
+    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int4 meta = p.meta[blockIdx.x];
     const int row = blockIdx.y;

@@ -68,6 +68,8 @@ __global__ void __launch_bounds__(kMapsThreads) fa_page_maps_kernel(const MapsPa
     const int per = (p.B + kMapsThreads - 1) / kMapsThreads;
     const int lo = min(tid * per, p.B), hi = min(lo + per, p.B);
     if (tid == 0) sh_beyond = 0;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     unsigned tok = 0, page = 0;
     for (int b = lo; b < hi; ++b) {
         const unsigned c = max(p.context_lens[b], 0), n = max(p.new_lens[b], 0);

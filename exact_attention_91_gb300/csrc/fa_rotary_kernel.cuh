@@ -146,6 +146,8 @@ template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRotWarps * 32) fa_rotary_kernel(const RotParams p) {
     constexpr int kItems = D / 16, kTokens = 32 / kItems;
     __shared__ unsigned long long turns[D / 2];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     rot_frequencies(turns, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = lane % kItems;
     const unsigned row = (blockIdx.x * kRotWarps + warp) * kTokens + lane / kItems;
@@ -251,6 +253,8 @@ template <int D, bool INTERLEAVED, bool E4M3>
 __global__ void __launch_bounds__(kRotWarps * 32) fa_append_kernel(const RotParams p) {
     constexpr int kItems = D / 16, kTokens = 32 / kItems;
     __shared__ unsigned long long turns[D / 2];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     rot_frequencies(turns, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = lane % kItems;
     const unsigned t = (blockIdx.x * kRotWarps + warp) * kTokens + lane / kItems;

@@ -110,8 +110,32 @@ int ready(int dev, cudaStream_t stream) {
     return FA_OK;
 }
 
-int launched() {
-    if (cudaGetLastError() == cudaSuccess) return FA_OK;
+// Every kernel here is launched with programmatic stream serialization, lets its
+// own successor start early, and waits for its predecessors (griddepcontrol.wait)
+// before it touches memory: of a step's chain of short kernels each one's launch
+// overlaps the one before. Every block waits, so a kernel's end means that all
+// before it have ended.
+template <typename Params>
+int launch(void (*kernel)(Params), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Params& p,
+           int cluster = 1) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return FA_OK;
+    cudaGetLastError();
     return FA_ERR_LAUNCH;
 }
 
@@ -160,35 +184,14 @@ int check_decode_sizes(long long B, long long Hq, long long Hkv, int d, int page
 template <int D, bool E4M3, bool WIDE>
 int launch_decode(const fa::DecodeParams& p, unsigned blocks, cudaStream_t s) {
     using C = fa::DecodeCfg<D, E4M3, WIDE>;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(blocks, 1, 1);
-    cfg.blockDim = dim3(C::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = C::kSmemBytes;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    if (p.cluster > 0) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, fa::fa_decode_kernel<D, E4M3, WIDE, true>, p) == cudaSuccess) return FA_OK;
-        cudaGetLastError();
+    if (p.cluster > 0)
+        return launch(fa::fa_decode_kernel<D, E4M3, WIDE, true>, dim3(blocks), C::kThreads, C::kSmemBytes, s, p,
+                      p.cluster);
+    if (launch(fa::fa_decode_kernel<D, E4M3, WIDE, false>, dim3(blocks), C::kThreads, C::kSmemBytes, s, p) != FA_OK)
         return FA_ERR_LAUNCH;
-    }
-    if (cudaLaunchKernelEx(&cfg, fa::fa_decode_kernel<D, E4M3, WIDE, false>, p) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_LAUNCH;
-    }
     if (blocks == 1) return FA_OK;  // nothing is cut
-    cfg.gridDim = dim3(blocks, static_cast<unsigned>(std::min(p.G, C::kRows)), 1);
-    cfg.dynamicSmemBytes = 0;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fa::fa_decode_join_kernel<D, C::kRows>, p) == cudaSuccess) return FA_OK;
-    cudaGetLastError();
-    return FA_ERR_LAUNCH;
+    const unsigned rows = static_cast<unsigned>(std::min(p.G, C::kRows));
+    return launch(fa::fa_decode_join_kernel<D, C::kRows>, dim3(blocks, rows), 128, 0, s, p);
 }
 
 template <int D>
@@ -361,19 +364,9 @@ int fa_rotary(const void* x, void* y, const int* positions, const double* inv_fr
     const long long groups = (tokens + 512 / d - 1) / (512 / d);  // of the tokens that a warp holds
     p.heads_per_warp = heads_per_warp(groups, H, sms);
     const dim3 grid = rotary_grid(groups, H, p.heads_per_warp);
-    const int threads = fa::kRotWarps * 32;
-    if (d == 64) {
-        if (interleaved)
-            fa::fa_rotary_kernel<64, true><<<grid, threads, 0, s>>>(p);
-        else
-            fa::fa_rotary_kernel<64, false><<<grid, threads, 0, s>>>(p);
-    } else {
-        if (interleaved)
-            fa::fa_rotary_kernel<128, true><<<grid, threads, 0, s>>>(p);
-        else
-            fa::fa_rotary_kernel<128, false><<<grid, threads, 0, s>>>(p);
-    }
-    return launched();
+    auto kernel = d == 64 ? (interleaved ? fa::fa_rotary_kernel<64, true> : fa::fa_rotary_kernel<64, false>)
+                          : (interleaved ? fa::fa_rotary_kernel<128, true> : fa::fa_rotary_kernel<128, false>);
+    return launch(kernel, grid, fa::kRotWarps * 32, 0, s, p);
 }
 
 int fa_cache_append(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
@@ -449,19 +442,13 @@ int fa_cache_append(const void* q, const void* k, const void* v, long long q_str
     const long long groups = (T + 512LL / d - 1) / (512 / d);  // of the tokens that a warp holds
     p.heads_per_warp = heads_per_warp(groups, heads, sms);
     const dim3 grid = rotary_grid(groups, heads, p.heads_per_warp);
-    const int threads = fa::kRotWarps * 32;
-    const int which = (d == 128 ? 4 : 0) + (interleaved ? 2 : 0) + (c.e4m3 ? 1 : 0);
-    switch (which) {
-        case 0: fa::fa_append_kernel<64, false, false><<<grid, threads, 0, s>>>(p); break;
-        case 1: fa::fa_append_kernel<64, false, true><<<grid, threads, 0, s>>>(p); break;
-        case 2: fa::fa_append_kernel<64, true, false><<<grid, threads, 0, s>>>(p); break;
-        case 3: fa::fa_append_kernel<64, true, true><<<grid, threads, 0, s>>>(p); break;
-        case 4: fa::fa_append_kernel<128, false, false><<<grid, threads, 0, s>>>(p); break;
-        case 5: fa::fa_append_kernel<128, false, true><<<grid, threads, 0, s>>>(p); break;
-        case 6: fa::fa_append_kernel<128, true, false><<<grid, threads, 0, s>>>(p); break;
-        default: fa::fa_append_kernel<128, true, true><<<grid, threads, 0, s>>>(p); break;
-    }
-    return launched();
+    constexpr void (*kernels[8])(fa::RotParams) = {
+        fa::fa_append_kernel<64, false, false>,  fa::fa_append_kernel<64, false, true>,
+        fa::fa_append_kernel<64, true, false>,   fa::fa_append_kernel<64, true, true>,
+        fa::fa_append_kernel<128, false, false>, fa::fa_append_kernel<128, false, true>,
+        fa::fa_append_kernel<128, true, false>,  fa::fa_append_kernel<128, true, true>};
+    return launch(kernels[(d == 128 ? 4 : 0) + (interleaved ? 2 : 0) + (c.e4m3 ? 1 : 0)], grid, fa::kRotWarps * 32, 0, s,
+                  p);
 }
 
 int fa_page_maps(const int* context_lens, const int* new_lens, int* block_table, const int* unused_blocks, int* slots,
@@ -513,8 +500,7 @@ int fa_page_maps(const int* context_lens, const int* new_lens, int* block_table,
     // one token per thread up to one block per SM
     const long long blocks = std::max<long long>(1, (T + fa::kMapsThreads - 1LL) / fa::kMapsThreads);
     const unsigned grid = static_cast<unsigned>(std::min<long long>(blocks, sms));
-    fa::fa_page_maps_kernel<<<grid, fa::kMapsThreads, 2 * (B + 1) * 4, s>>>(p);
-    return launched();
+    return launch(fa::fa_page_maps_kernel, dim3(grid), fa::kMapsThreads, 2 * (B + 1) * 4, s, p);
 }
 
 }  // extern "C"
