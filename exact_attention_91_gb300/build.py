@@ -60,7 +60,7 @@ def bind_cmds(obj: str, out_path: str) -> tuple[list[str], list[str]]:
                 "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda_home, "include"),
                 os.path.join(CSRC, "fa_bind.cpp"), "-o", obj]
     link = [cxx, "-shared", obj, "-o", out_path, "-L", LIB_DIR, "-l:libfa.so", "-L", os.path.join(torch_dir, "lib"),
-            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     return compile_, link
 
 

@@ -15,7 +15,7 @@
 #include <cstdint>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -83,7 +83,7 @@ int to_int(int64_t x) {  // (a size past int is refused by the C call's own limi
 }
 
 Tensor make(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
-    return at::empty(shape, like.options().dtype(type).memory_format(c10::nullopt).requires_grad(false));
+    return at::detail::empty_cuda(shape, type, like.device(), c10::nullopt);  // (no dispatcher on the way)
 }
 
 void arguments(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "wrong number of arguments"); }

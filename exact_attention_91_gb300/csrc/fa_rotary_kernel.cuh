@@ -78,17 +78,21 @@ __device__ __forceinline__ float2 rot_cos_sin(int position, unsigned long long t
     return make_float2(c * factor, s * factor * sign);
 }
 
-// The 16 values that one lane handles of a head: two 16-byte chunks. Item i <
-// r/16 holds the pairs 8i .. 8i + 7; later items hold 16 values to copy.
-template <bool INTERLEAVED>
+// The 16 values that one lane handles of a head: two chunks of 8, at a and b.
+// Item i < r/16 holds eight pairs (see rot_pair), a later one values to copy.
+// In either layout the chunks of neighbouring lanes are neighbours.
+template <int D>
 __device__ __forceinline__ void rot_item(int i, int r, int& a, int& b) {
-    if (!INTERLEAVED && i * 16 < r) {
-        a = i * 8;
-        b = a + r / 2;
-    } else {
-        a = i * 16;
-        b = a + 8;
-    }
+    const bool turned = i * 16 < r;
+    a = turned ? i * 8 : r + (i - r / 16) * 8;
+    b = a + (turned ? r : D - r) / 2;
+}
+
+// Pair number j (0 to 7) of item i: half layout, pairs (a[j], b[j]); interleaved,
+// pairs (a[2j], a[2j + 1]) for j < 4, then those of b.
+template <bool INTERLEAVED>
+__device__ __forceinline__ int rot_pair(int i, int j, int r) {
+    return INTERLEAVED ? i * 4 + (j & 3) + (j < 4 ? 0 : r / 4) : i * 8 + j;
 }
 
 __device__ __forceinline__ void rot_unpack(const uint4& v, float (&x)[8]) {
@@ -136,10 +140,12 @@ __device__ __forceinline__ void rot_frequencies(unsigned long long* turns, const
 }
 
 // cos and sin of a lane's eight pairs.
-__device__ __forceinline__ void rot_table(const unsigned long long* turns, int item, int position, float factor,
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rot_table(const unsigned long long* turns, int item, int r, int position, float factor,
                                           float sign, float2 (&cs)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = rot_cos_sin(position, turns[item * 8 + i], factor, sign);
+    for (int j = 0; j < 8; ++j)
+        cs[j] = rot_cos_sin(position, turns[rot_pair<INTERLEAVED>(item, j, r)], factor, sign);
 }
 
 template <int D, bool INTERLEAVED>
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kRotWarps * 32) fa_rotary_kernel(const RotPara
     const int b = static_cast<int>(row / p.N), n = static_cast<int>(row - b * p.N);
     const int position = p.positions[b * p.pos_b + n];
     int ca, cb;
-    rot_item<INTERLEAVED>(item, p.r, ca, cb);
+    rot_item<D>(item, p.r, ca, cb);
     const bool turned = item * 16 < p.r;
     const uint16_t* src = p.x.src + b * p.src_b + n * p.x.src_n;
     uint16_t* dst = p.x.dst + b * p.dst_b + n * p.x.dst_n;
@@ -169,7 +175,7 @@ __global__ void __launch_bounds__(kRotWarps * 32) fa_rotary_kernel(const RotPara
                 va[i] = *reinterpret_cast<const uint4*>(src + (h + i) * p.x.src_h + ca);
                 vb[i] = *reinterpret_cast<const uint4*>(src + (h + i) * p.x.src_h + cb);
             }
-        if (turned && h == h0) rot_table(turns, item, position, p.factor, p.sign, cs);
+        if (turned && h == h0) rot_table<INTERLEAVED>(turns, item, p.r, position, p.factor, p.sign, cs);
 #pragma unroll
         for (int i = 0; i < kRotHeads; ++i)
             if (h + i < h_end) {
@@ -213,7 +219,7 @@ __device__ __forceinline__ void append_heads(const RotParams& p, const RotTensor
                 inv[i] = KIND > 0 && E4M3 && scale ? scale[h + i] : 1.f;
             }
         if (KIND < 2 && turned && !have) {
-            rot_table(turns, item, position, p.factor, 1.f, cs);
+            rot_table<INTERLEAVED>(turns, item, p.r, position, p.factor, 1.f, cs);
             have = true;
         }
 #pragma unroll
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kRotWarps * 32) fa_append_kernel(const RotPara
     const int slot = p.slots[t], position = p.positions[t];
     if (slot < 0 || slot >= p.num_slots) return;
     int ca, cb;
-    rot_item<INTERLEAVED>(item, p.r, ca, cb);
+    rot_item<D>(item, p.r, ca, cb);
     const bool turned = item * 16 < p.r;
     const long long block = slot >> p.page_shift, token = slot & ((1 << p.page_shift) - 1);
     float2 cs[8];
