@@ -24,7 +24,7 @@
 
 namespace fa {
 
-constexpr int kRotWarps = 8;
+constexpr int kRotWarps = 4;
 constexpr int kRotHeads = 4;  // heads whose loads a lane has in flight
 
 // One tensor of a rotary launch: heads of token n at src + n·src_n + h·src_h.
@@ -256,7 +256,7 @@ __device__ __forceinline__ void append_heads(const RotParams& p, const RotTensor
 // q (Hq), k (Hkv) and v (Hkv). Tokens whose slot is outside the cache are passed
 // over.
 template <int D, bool INTERLEAVED, bool E4M3>
-__global__ void __launch_bounds__(kRotWarps * 32) fa_append_kernel(const RotParams p) {
+__global__ void __launch_bounds__(kRotWarps * 32, 6) fa_append_kernel(const RotParams p) {
     constexpr int kItems = D / 16, kTokens = 32 / kItems;
     __shared__ unsigned long long turns[D / 2];
     ptx::griddep_launch_dependents();
