@@ -213,7 +213,7 @@ template <int D, bool E4M3, bool WIDE>
 __device__ __forceinline__ int decode_page(const DecodeParams& p, const DecodeSeg& s, int t, int lane) {
     using C = DecodeCfg<D, E4M3, WIDE>;
     const int key = t * C::kKeys + (lane % C::kGroups) * 16;
-    return key < s.len ? __ldg(p.table + s.b * p.table_stride + (key >> p.page_shift)) : -1;
+    return key < s.len ? p.table[s.b * p.table_stride + (key >> p.page_shift)] : -1;
 }
 
 // CLUSTER: the small form. Block r of a cluster of p.cluster takes the r-th
@@ -336,43 +336,62 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         }
     };
     seek();
+    // (the first two tiles' pages are looked up together, later ones a tile ahead)
     int entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
+    const bool two = more && at + C::kWarps < ahead.t1;
+    const int second = two ? decode_page<D, E4M3, WIDE>(p, ahead, at + C::kWarps, lane) : -1;
     uint32_t slot_in = 0, slot_out = 0, ok_bits = 0;
-    auto load = [&]() {
+    auto load = [&](bool first) {
         if (more) {
             const uint32_t ok = decode_load<D, E4M3, WIDE>(p, ahead, at, entry, ring + slot_in * C::kTileBytes, lane);
             ok_bits = (ok_bits & ~(((1u << C::kGroups) - 1) << (slot_in * C::kGroups))) | ok << (slot_in * C::kGroups);
             at += C::kWarps;
-            seek();
-            entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
+            if (first && two) {
+                entry = second;
+            } else {
+                seek();
+                entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
+            }
         }
         slot_in = slot_in + 1 == C::kStages ? 0 : slot_in + 1;
         ptx::cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) load();
 
-    for (;; first_seg = false) {
+    // ---- q of a segment as bf16 pairs, in the order of the tensor core's fragments
+    uint32_t qa[KS][2 * R];
+    auto load_q = [&]() {
         const int h = seg.hh / p.row_groups, rg = seg.hh - h * p.row_groups;
-        const int rows = min(p.G - rg * C::kRows, C::kRows);  // query heads of this unit
+        const int rows = min(p.G - rg * C::kRows, C::kRows);
         const long long row0 = static_cast<long long>(seg.b) * p.Hkv * p.G + h * p.G + rg * C::kRows;
-
-        // ---- q fragments, and each row's factor from q·k to base-2 scores
-        uint32_t qa[KS][2 * R];
-        float cs[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const bool have = g + 8 * r < rows;
-            const uint32_t* qrow = reinterpret_cast<const uint32_t*>(p.q) + (row0 + (have ? g + 8 * r : 0)) * (D / 2);
-            cs[r] = p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.f);
+            const uint32_t* qrow = static_cast<const uint32_t*>(p.q) + (row0 + (have ? g + 8 * r : 0)) * (D / 2);
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     // which pair of values meets the j-th register of the cache's fragment of step s
                     const int pair = E4M3 ? ((t4 + 4 * (s / 4)) * 16 + 4 * (s % 4) + 2 * j) / 2 : s * 8 + t4 + 4 * j;
-                    qa[s][R * j + r] = have ? __ldg(qrow + pair) : 0u;
+                    qa[s][R * j + r] = have ? qrow[pair] : 0u;
                 }
+        }
+    };
+    load_q();
+    load(true);
+#pragma unroll
+    for (int i = 1; i < C::kStages - 1; ++i) load(false);
+
+    for (;; first_seg = false) {
+        const int h = seg.hh / p.row_groups, rg = seg.hh - h * p.row_groups;
+        const int rows = min(p.G - rg * C::kRows, C::kRows);  // query heads of this unit
+        const long long row0 = static_cast<long long>(seg.b) * p.Hkv * p.G + h * p.G + rg * C::kRows;
+
+        // ---- each row's factor from q·k to base-2 scores; e4m3: q as fp16, scaled by a power of two
+        float cs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            cs[r] = p.scale_log2 * (p.k_scale ? p.k_scale[h] : 1.f);
             if constexpr (E4M3) {
                 float top = 0.f;
 #pragma unroll
@@ -412,7 +431,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         for (int t = seg.t0 + warp; t < seg.t1; t += C::kWarps) {
             ptx::cp_async_wait<C::kStages - 2>();
             __syncwarp();
-            load();  // into the slot read in the previous step
+            load(false);  // into the slot read in the previous step
             const uint32_t kt = ring + slot_out * C::kTileBytes, vt = kt + C::kHalfBytes;
             const uint32_t ok = ok_bits >> (slot_out * C::kGroups) & ((1u << C::kGroups) - 1);
             slot_out = slot_out + 1 == C::kStages ? 0 : slot_out + 1;
@@ -648,17 +667,19 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             const uint32_t o_at = ptx::smem_u32(smem), ml_at = ptx::smem_u32(stat + C::kWarps * 16);
             for (int i = tid * p.cluster + rank; i < rows * D / 4; i += C::kThreads * p.cluster) {
                 const int row = i / (D / 4), c4 = i % (D / 4);
+                // (all loads first: one takes some 250 cycles; past the cluster's size, one of it again)
                 float2 ml[kDecodeCluster];
                 float4 x[kDecodeCluster];
+#pragma unroll
+                for (int w = 0; w < kDecodeCluster; ++w) {
+                    const uint32_t from = static_cast<uint32_t>(w & (p.cluster - 1));
+                    ml[w] = ptx::ld_dsmem_v2(ptx::mapa_shared(ml_at + row * 8, from));
+                    x[w] = ptx::ld_dsmem_v4(ptx::mapa_shared(o_at + i * 16, from));
+                }
                 float mm = -INFINITY, l = 0.f;
 #pragma unroll
                 for (int w = 0; w < kDecodeCluster; ++w) {
-                    ml[w] = make_float2(-INFINITY, 0.f);
-                    if (w < p.cluster) {
-                        ml[w] = make_float2(ptx::ld_dsmem_f32(ptx::mapa_shared(ml_at + row * 8, w)),
-                                            ptx::ld_dsmem_f32(ptx::mapa_shared(ml_at + row * 8 + 4, w)));
-                        x[w] = ptx::ld_dsmem_v4(ptx::mapa_shared(o_at + i * 16, w));
-                    }
+                    if (w >= p.cluster) ml[w].x = -INFINITY;
                     mm = fmaxf(mm, ml[w].x);
                 }
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -676,10 +697,11 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                 if (c4 == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
             }
             __syncwarp();
-            ptx::cluster_sync();  // the other blocks' shared memory is read until here
+            ptx::cluster_leave();  // the other blocks' shared memory is read until here
             return;
         }
         if (!decode_next<C::kKeys>(seg, p)) break;
+        load_q();
         __syncthreads();  // stat and merge are written again
     }
 }
