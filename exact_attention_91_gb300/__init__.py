@@ -405,10 +405,12 @@ def _made_for(stream, *shapes_and_dtypes, device):
     return out
 
 
-def _on_stream(stream, fn, *args):
+def _on_stream(stream, device, fn, *args):
     """fn(*args) with ``stream`` as the current one (whose part of the allocator
     a workspace then comes from)."""
     import torch
+    if stream.device != device:
+        raise ValueError("stream must be one of the tensors' device")
     with torch.cuda.stream(stream):
         return fn(*args)
 
@@ -436,8 +438,8 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: fl
             out, = _made_for(stream, (q.shape, torch.bfloat16), device=q.device)
         if lse is None and return_lse:
             lse, = _made_for(stream, (q.shape[:2], torch.float32), device=q.device)
-        r = _on_stream(stream, decode, q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse,
-                       return_lse, workspace)
+        r = _on_stream(stream, q.device, decode, q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale,
+                       out, lse, return_lse, workspace)
     if type(r) is int:
         raise FaError(r, "fa_decode_paged")
     return r
@@ -511,7 +513,7 @@ def rotary(x, positions, inv_freq, interleaved: bool = False, inverse: bool = Fa
     else:
         if out is None:
             out, = _made_for(stream, (x.shape, x.dtype), device=x.device)
-        r = _on_stream(stream, turn, x, positions, inv_freq, interleaved, inverse, factor, out)
+        r = _on_stream(stream, x.device, turn, x, positions, inv_freq, interleaved, inverse, factor, out)
     if type(r) is int:
         raise FaError(r, "fa_rotary")
     return r if out is None else out
@@ -536,8 +538,8 @@ def cache_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interlea
     else:
         if q_out is None:
             q_out, = _made_for(stream, (q.shape, q.dtype), device=q.device)
-        r = _on_stream(stream, append, q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved, factor,
-                       k_scale, v_scale, q_out, k_out)
+        r = _on_stream(stream, q.device, append, q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved,
+                       factor, k_scale, v_scale, q_out, k_out)
     if type(r) is int:
         raise FaError(r, "fa_cache_append")
     return r if q_out is None else q_out
@@ -570,7 +572,8 @@ def page_maps(context_lens, new_lens, block_table, unused_blocks, page_size: int
             B = block_table.shape[0]
             out = PageMaps(*_made_for(stream, *(((n,), torch.int32) for n in (num_tokens, num_tokens, B + 1, B, 4)),
                                       device=block_table.device))
-        r = _on_stream(stream, maps, context_lens, new_lens, block_table, unused_blocks, page_size, num_tokens, out)
+        r = _on_stream(stream, block_table.device, maps, context_lens, new_lens, block_table, unused_blocks, page_size,
+                       num_tokens, out)
     if type(r) is int:
         raise FaError(r, "fa_page_maps")
     return tuple.__new__(PageMaps, r) if out is None else out

@@ -154,6 +154,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(q.is_contiguous() && lens.is_contiguous() && dense_last(table),
                       "q, seq_lens and the rows of block_table must be contiguous");
     const int64_t B = q.size(0), Hq = q.size(1), d = q.size(2), width = table.size(1);
+    const float scale = static_cast<float>(a[5] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[5]));
     TORCH_CHECK_VALUE(k.dim() == 4 && k.size(3) == d, "q and the caches must have the same d");
     TORCH_CHECK_VALUE(!out.defined() || (out.scalar_type() == at::kBFloat16 && out.sizes() == q.sizes() &&
                                          out.is_contiguous()), "out must be a contiguous bf16 tensor of q's shape");
@@ -168,7 +169,6 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             static_cast<const Tensor*>(&ws)})
         on(*t, device);
     const c10::cuda::CUDAGuard guard(device);
-    const float scale = static_cast<float>(a[5] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[5]));
     if (!out.defined()) out = make(q.sizes(), at::kBFloat16, q);
     if (!lse.defined() && return_lse) lse = make({B, Hq}, at::kFloat, q);
     if (!ws.defined()) {
@@ -209,6 +209,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                          out.stride(-1) == 1),
                       "out must be a bf16 tensor of x's shape with d contiguous");
     const double factor = number(a[5]);
+    const bool interleaved = truth(a[3]), inverse = truth(a[4]);
     const c10::Device device = x.device();
     const int r = frequencies(freq, device);
     cuda(x);
@@ -220,7 +221,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long ys[3] = {four ? out.stride(0) : 0, out.stride(1), four ? out.stride(2) : out.stride(0)};
     const int rc = fa_rotary(x.data_ptr(), out.data_ptr(), static_cast<const int*>(pos.data_ptr()),
                              static_cast<const double*>(ptr(freq)), to_int(B), to_int(H), to_int(N), to_int(d), xs, ys,
-                             each ? pos.stride(0) : 0, r, truth(a[3]), truth(a[4]), static_cast<float>(factor),
+                             each ? pos.stride(0) : 0, r, interleaved, inverse, static_cast<float>(factor),
                              c10::cuda::getCurrentCUDAStream(device.index()).stream());
     if (rc != FA_OK) return PyLong_FromLong(rc);
     return THPVariable_Wrap(std::move(out));
@@ -257,6 +258,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(!t->defined() || (t->stride(2) == 1 && (t->size(1) <= 1 || t->stride(1) == d)),
                           "the heads of a token of q, k, v, q_out and k_out must be contiguous");
     const double factor = number(a[9]);
+    const bool interleaved = truth(a[8]);
     const c10::Device device = q.device();
     const fa_paged_cache cache = paged_cache(kc, vc, ks, vs, device);
     const int r = frequencies(freq, device);
@@ -268,7 +270,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    static_cast<const int*>(pos.data_ptr()), static_cast<const int*>(slots.data_ptr()),
                                    static_cast<const double*>(ptr(freq)), &cache, q_out.data_ptr(), ptr(k_out),
                                    q_out.stride(0), k_out.defined() ? k_out.stride(0) : 0, to_int(T), to_int(Hq), r,
-                                   truth(a[8]), static_cast<float>(factor),
+                                   interleaved, static_cast<float>(factor),
                                    c10::cuda::getCurrentCUDAStream(device.index()).stream());
     if (rc != FA_OK) return PyLong_FromLong(rc);
     return THPVariable_Wrap(std::move(q_out));

@@ -40,6 +40,21 @@ int log2_page(int page) {
     return s;
 }
 
+// Whether rows of `row` elements, size[i] of them at stride[i] in three
+// dimensions, are known not to overlap: each stride clears all that the smaller
+// ones span.
+bool rows_apart(const long long (&size)[3], const long long (&stride)[3], long long row) {
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int a, int b) { return stride[a] < stride[b]; });
+    long long span = row;
+    for (int i : order) {
+        if (size[i] <= 1) continue;
+        if (stride[i] < span) return false;
+        span += (size[i] - 1) * stride[i];
+    }
+    return true;
+}
+
 // A cache as the kernels take it: strides in bytes.
 struct Cache {
     long long k_block, k_token, k_head, v_block, v_token, v_head;
@@ -338,6 +353,8 @@ int fa_rotary(const void* x, void* y, const int* positions, const double* inv_fr
         bytes[0] += static_cast<size_t>((dims[i] - 1) * x_strides[i]) * 2;
         bytes[1] += static_cast<size_t>((dims[i] - 1) * y_strides[i]) * 2;
     }
+    const long long ys[3] = {y_strides[0], y_strides[1], y_strides[2]};
+    if (!rows_apart(dims, ys, d)) return FA_ERR_ALIAS;
     bool same = x == y;  // in place: every value is read and written by the same thread
     for (int i = 0; i < 3; ++i) same = same && (dims[i] == 1 || x_strides[i] == y_strides[i]);
     if (!same && overlap(x, bytes[0], y, bytes[1])) return FA_ERR_ALIAS;
@@ -400,6 +417,11 @@ int fa_cache_append(const void* q, const void* k, const void* v, long long q_str
         bytes[i] += static_cast<size_t>((T - 1) * strides[i]) * 2;
     }
     if (misaligned(positions, 4) || misaligned(slots, 4)) return FA_ERR_MISALIGNED;
+    // what is written must not overlap itself
+    const long long dims[3] = {cache->num_blocks, cache->page_size, cache->heads};
+    const long long ks[3] = {cache->k_block, cache->k_token, cache->k_head};
+    const long long vs[3] = {cache->v_block, cache->v_token, cache->v_head};
+    if (!rows_apart(dims, ks, d) || !rows_apart(dims, vs, d) || cache->k == cache->v) return FA_ERR_ALIAS;
     // q and k may be rotated in place; apart from that the outputs and the caches overlap nothing
     const bool q_same = q_out == q && (T == 1 || q_out_stride == q_stride);
     const bool k_same = k_out == k && (T == 1 || k_out_stride == k_stride);
@@ -449,8 +471,8 @@ int fa_cache_append(const void* q, const void* k, const void* v, long long q_str
         fa::fa_append_kernel<64, true, false>,   fa::fa_append_kernel<64, true, true>,
         fa::fa_append_kernel<128, false, false>, fa::fa_append_kernel<128, false, true>,
         fa::fa_append_kernel<128, true, false>,  fa::fa_append_kernel<128, true, true>};
-    return launch(kernels[(d == 128 ? 4 : 0) + (interleaved ? 2 : 0) + (c.e4m3 ? 1 : 0)], grid, fa::kRotWarps * 32, 0, s,
-                  p);
+    const int which = (d == 128 ? 4 : 0) + (interleaved ? 2 : 0) + (c.e4m3 ? 1 : 0);
+    return launch(kernels[which], grid, fa::kRotWarps * 32, 0, s, p);
 }
 
 int fa_page_maps(const int* context_lens, const int* new_lens, int* block_table, const int* unused_blocks, int* slots,

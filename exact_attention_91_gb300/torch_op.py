@@ -92,8 +92,8 @@ def _rotary_setup(ctx, inputs, output):
 def _rotary_backward(ctx, grad):
     # the map is linear: its gradient is the transposed map, the turn back by the same angles
     positions, inv_freq = ctx.saved_tensors
-    if grad.stride(-1) != 1 or any(s % 8 for s in grad.stride()[:-1]):  # (a reduction's broadcast gradient)
-        grad = grad.contiguous()
+    if grad.stride(-1) != 1 or grad.storage_offset() % 8 or any(s % 8 for s in grad.stride()[:-1]):
+        grad = grad.clone(memory_format=torch.contiguous_format)  # (a reduction's broadcast gradient, a slice)
     dx = torch.ops.fa91.rotary(grad, positions, inv_freq, ctx.interleaved, not ctx.inverse, ctx.factor)
     return dx, None, None, None, None, None
 

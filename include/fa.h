@@ -293,8 +293,9 @@ long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_typ
  *               (frequencies up to 1).
  *   x_strides, y_strides  host arrays: elements from one b, h, n to the next
  *               (multiples of 8; x's may be 0; those of a dimension of size 1
- *               are not used); d's values are contiguous. y may be x itself
- *               with the same strides, or overlap nothing of it.
+ *               are not used); d's values are contiguous. y's rows do not
+ *               overlap (each stride is past all that the smaller ones span); y
+ *               may be x itself with the same strides, or overlap nothing of it.
  *   rotary_dim  a multiple of 16, 0 to d.  factor finite (1: a pure rotation).
  *   B*N at most 2^31 - 65536, H at most 32767.
  *
@@ -316,6 +317,7 @@ int fa_rotary(const void* x, void* y, const int* positions, const double* inv_fr
  *   positions, slots  int32 [T], device. Slot s is token s % page_size of block
  *               s / page_size. A token whose slot is negative or past the cache
  *               is padding: nothing of it is written, in no output.
+ *               The cache's rows do not overlap, as y's above, nor k's with v's.
  *               Slots of one call are distinct (of two tokens with the same
  *               slot, either's values are kept, in pieces of 8 or 16 values).
  *
