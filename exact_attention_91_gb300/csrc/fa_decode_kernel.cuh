@@ -20,6 +20,11 @@
 //    fp32 partial (O, reference maximum, sum) per worker in the workspace and
 //    fa_decode_join_kernel adds them up. A worker's run has at most two cut
 //    units, its first and its last: two slots each.
+//  * Within a worker, the four warps either share a unit's tiles (and add up
+//    their results in shared memory at its end), or, where the runs are long
+//    enough and the key heads come in fours, take one key head each: the unit
+//    is then four heads wide, four heads' rows of the same keys are read at the
+//    same time, and a warp writes its own output without meeting the others.
 //  * A batch that can be no larger than one wave of short shares (the lengths'
 //    bound is the table's width) is done by clusters instead, one per unit,
 //    whose blocks' partials meet in distributed shared memory: no scan of the
@@ -48,14 +53,15 @@ struct DecodeParams {
     const int* lens;        // [B]
     const float* k_scale;   // [Hkv] or null
     const float* v_scale;
-    float* part_o;          // workspace: [2 * workers][rows][D]
-    float2* part_ml;        // [2 * workers][rows]: (reference maximum, sum)
+    float* part_o;          // workspace: [2 * workers][1 or 4 heads][rows][D]
+    float2* part_ml;        // [2 * workers][1 or 4][rows]: (reference maximum, sum)
     int4* meta;             // [workers]: the cut unit that continues into this worker
     long long k_block, k_token, k_head, v_block, v_token, v_head;
     long long table_stride;
     float scale_log2;
     int B, Hkv, G, row_groups, num_blocks, page_shift, width;
     int cluster;            // blocks per unit of the small form
+    int fours;              // key heads (times row groups) are a multiple of four: a warp may take one each
 };
 
 template <int D, bool E4M3, bool WIDE>
@@ -82,18 +88,36 @@ struct DecodeCfg {
     static constexpr float kLazy = 8.f;
 };
 
-// What a segment costs besides its tiles (q, the warps' merge, the output), in
-// tiles of one worker: a run of many short requests must not count as little.
-constexpr int kSegCost = 6;
-// Most blocks of a cluster (the portable limit).
-constexpr int kDecodeCluster = 8;
+// How a launch's warps share out its units. A unit counts as its tiles behind
+// `cost` empty ones: what a segment takes besides its tiles (q, the warps' merge,
+// the output), so that a run of many short requests does not count as little.
+struct DecodeWay {
+    int units;     // per request
+    int cost;
+    int heads;     // key heads (times row groups) of a unit: 1, or 4 with one per warp
+    int step, off; // this warp's tiles of a segment: t0 + off, every step-th
+    int add;       // its head: unit * heads + add
+};
+constexpr int kSegCost = 6, kSegCostFours = 2;
+// The four-heads way is taken when there is a unit of four for every worker (few
+// are cut then) and the cache is token-major, so that the four heads' rows are
+// neighbours, or the requests are short (at most kFoursShort tiles in the mean:
+// the warps' merge is what it saves); and, token-major, when a worker's run is
+// kFoursRun tiles or more. Measured (us, four heads / one): 2 x 65536 keys of 32
+// heads, d 128, 303 / 315; 15 x 40000 keys of 8 heads, d 64, 189 / 214; 109 x
+// 120 keys of 32 heads, d 64, e4m3, 23 / 40; against it 1 x 61000 keys of 4
+// heads, 35 / 28 (every worker cuts); head-major 128 x 4480 keys of 8 heads,
+// e4m3, 197 / 190.
+constexpr int kFoursRun = 20, kFoursShort = 32;
 // Least run of a worker, in tiles with the segments' costs.
 constexpr int kMinRun = 8;
+// Most blocks of a cluster (the portable limit).
+constexpr int kDecodeCluster = 8;
 
-// Position in a worker's run: tiles [t0, t1) of unit (b, hh), then `rem` more
-// of the run. A unit counts as its tiles behind kSegCost empty ones.
+// Position in a worker's run: tiles [t0, t1) of unit u of request b, then `rem`
+// more counted tiles of the run.
 struct DecodeSeg {
-    int b, hh, t0, t1, nt, len;
+    int b, u, t0, t1, nt, len;
     long long rem;
 };
 
@@ -110,26 +134,26 @@ __device__ __forceinline__ int decode_tiles(int len) {
 
 // The part of the current unit, from x on in its counted tiles, that the run
 // holds.
-__device__ __forceinline__ void decode_take(DecodeSeg& s, int x) {
-    const long long left = kSegCost + s.nt - x;
+__device__ __forceinline__ void decode_take(DecodeSeg& s, int x, int cost) {
+    const long long left = cost + s.nt - x;
     const int take = static_cast<int>(s.rem < left ? s.rem : left);
-    s.t0 = max(0, x - kSegCost);
-    s.t1 = max(0, x + take - kSegCost);
+    s.t0 = max(0, x - cost);
+    s.t1 = max(0, x + take - cost);
     s.rem -= take;
 }
 
 // On to the next unit with a tile in the run; false at the run's end.
 template <int KEYS>
-__device__ __forceinline__ bool decode_next(DecodeSeg& s, const DecodeParams& p) {
+__device__ __forceinline__ bool decode_next(DecodeSeg& s, const DecodeParams& p, const DecodeWay& way) {
     do {
         if (s.rem <= 0) return false;
-        if (++s.hh == p.Hkv * p.row_groups) {
-            s.hh = 0;
+        if (++s.u == way.units) {
+            s.u = 0;
             ++s.b;
             s.len = decode_len(p, s.b);
             s.nt = decode_tiles<KEYS>(s.len);
         }
-        decode_take(s, 0);
+        decode_take(s, 0, way.cost);
     } while (s.t0 >= s.t1);
     return true;
 }
@@ -177,11 +201,11 @@ __device__ __forceinline__ uint32_t decode_chunk(int r, int c) {
 // Starts the copies of tile t of the segment's unit into ring slot `dst` and
 // returns which of its 16-key groups lie in a page of the cache (bit g).
 template <int D, bool E4M3, bool WIDE>
-__device__ __forceinline__ uint32_t decode_load(const DecodeParams& p, const DecodeSeg& s, int t, int page_entry,
-                                                uint32_t dst, int lane) {
+__device__ __forceinline__ uint32_t decode_load(const DecodeParams& p, const DecodeSeg& s, int hh, int t,
+                                                int page_entry, uint32_t dst, int lane) {
     using C = DecodeCfg<D, E4M3, WIDE>;
     const int lr = lane / C::kRowLanes, lc = lane % C::kRowLanes;
-    const int h = s.hh / p.row_groups;
+    const int h = hh / p.row_groups;
     uint32_t ok_mask = 0;
 #pragma unroll
     for (int g = 0; g < C::kGroups; ++g) {
@@ -233,6 +257,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int HH = p.Hkv * p.row_groups;
     DecodeSeg seg;
+    DecodeWay way{HH, kSegCost, 1, C::kWarps, warp, 0};
     bool first_seg = true;
     const int worker = blockIdx.x;
     ptx::griddep_launch_dependents();
@@ -240,7 +265,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     if constexpr (CLUSTER) {
         const int unit = worker / p.cluster, rank = worker - unit * p.cluster;
         seg.b = unit / HH;
-        seg.hh = unit - seg.b * HH;
+        seg.u = unit - seg.b * HH;
         seg.len = decode_len(p, seg.b);
         seg.nt = decode_tiles<C::kKeys>(seg.len);
         seg.t0 = seg.nt * rank / p.cluster;
@@ -250,11 +275,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         // ---- this worker's run of tiles
         const int per = (p.B + C::kThreads - 1) / C::kThreads;
         const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
-        auto counted = [&](int b) {
-            return static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b)) + kSegCost) * HH;
-        };
-        long long mine = 0;  // counted tiles of requests [b_lo, b_hi)
-        for (int b = b_lo; b < b_hi; ++b) mine += counted(b);
+        long long mine = 0;  // tiles of one key head of requests [b_lo, b_hi)
+        for (int b = b_lo; b < b_hi; ++b) mine += decode_tiles<C::kKeys>(decode_len(p, b));
         long long incl = mine;
 #pragma unroll
         for (int i = 1; i < 32; i <<= 1) {
@@ -263,12 +285,19 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         }
         if (lane == 31) sh_warp[warp] = incl;
         __syncthreads();
-        long long total = 0, before = 0;
+        long long tiles = 0, before = 0;
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
             if (w < warp) before += sh_warp[w];
-            total += sh_warp[w];
+            tiles += sh_warp[w];
         }
+        const long long grid = gridDim.x, fours = HH / 4;
+        const bool token_major = p.k_head < p.k_token;
+        if (p.fours && (p.B * fours >= grid ? token_major || tiles <= static_cast<long long>(p.B) * kFoursShort
+                                            : token_major && tiles * fours >= grid * kFoursRun))
+            way = DecodeWay{HH / 4, kSegCostFours, 4, 1, 0, warp};
+        // counted tiles of all requests, and of those before b_lo
+        const long long total = (tiles + static_cast<long long>(p.B) * way.cost) * way.units;
         const int workers = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kMinRun - 1) / kMinRun));
         if (worker >= workers) {
             if (tid == 0) p.meta[worker] = make_int4(-1, 0, 0, 0);
@@ -276,11 +305,12 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         }
         const long long begin = decode_start(total, workers, worker), end = decode_start(total, workers, worker + 1);
         {
-            long long at = before + incl - mine;  // first counted tile of request b_lo
-            if (begin >= at && begin < at + mine) {
+            long long at = (before + incl - mine + static_cast<long long>(b_lo) * way.cost) * way.units;
+            if (begin >= at && begin < at + (mine + static_cast<long long>(b_hi - b_lo) * way.cost) * way.units) {
                 int b = b_lo;
                 for (;; ++b) {
-                    const long long n = counted(b);
+                    const long long n =
+                        static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b)) + way.cost) * way.units;
                     if (begin < at + n) break;
                     at += n;
                 }
@@ -294,58 +324,56 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         seg.nt = decode_tiles<C::kKeys>(seg.len);
         {
             const unsigned long long in = static_cast<unsigned long long>(begin - sh_begin);
-            const unsigned unit = static_cast<unsigned>(seg.nt + kSegCost);
-            seg.hh = static_cast<int>(in <= 0xffffffffu ? static_cast<unsigned>(in) / unit : in / unit);
-            const int x = static_cast<int>(in - static_cast<unsigned long long>(seg.hh) * unit);
+            const unsigned unit = static_cast<unsigned>(seg.nt + way.cost);
+            seg.u = static_cast<int>(in <= 0xffffffffu ? static_cast<unsigned>(in) / unit : in / unit);
+            const int x = static_cast<int>(in - static_cast<unsigned long long>(seg.u) * unit);
             const long long u0 = begin - x;  // first counted tile of the unit
             seg.rem = end - begin;
-            decode_take(seg, x);
+            decode_take(seg, x, way.cost);
             if (tid == 0) {
-                // The join of a cut unit is done at the first cut: by the block of the worker after the unit's first
-                // (the one that holds its tile 0).
+                // For the join of a cut unit: request, unit, the slot of its first part, its last worker. (Its tile 0
+                // is in the first worker's run, and is the first part of that run if the run begins in the unit.)
                 int4 m = make_int4(-1, 0, 0, 0);
-                if (x > kSegCost) {
-                    const int first = decode_worker_of(total, workers, u0 + kSegCost);
-                    if (first == worker - 1) {
-                        m.x = seg.b;
-                        m.y = seg.hh;
-                        // (the unit's part is the first of its worker's run if the run begins in the unit)
-                        m.z = decode_start(total, workers, first) >= u0 ? 2 * first : 2 * first + 1;
-                        m.w = decode_worker_of(total, workers, u0 + kSegCost + seg.nt - 1);
-                    }
+                if (x > way.cost) {
+                    const int first = decode_worker_of(total, workers, u0 + way.cost);
+                    m.x = seg.b;
+                    m.y = seg.u;
+                    m.z = decode_start(total, workers, first) >= u0 ? 2 * first : 2 * first + 1;
+                    m.w = decode_worker_of(total, workers, u0 + way.cost + seg.nt - 1) * 8 + way.heads;
                 }
                 p.meta[worker] = m;
             }
         }
         first_seg = seg.t0 < seg.t1;  // whether the run's first unit, which may be cut at its start, has a tile here
-        if (!first_seg && !decode_next<C::kKeys>(seg, p)) return;
+        if (!first_seg && !decode_next<C::kKeys>(seg, p, way)) return;
     }
 
     // ---- the ring: the next tiles to copy run ahead of the ones in use, across segments
     const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kTileBytes;
     DecodeSeg ahead = seg;
-    int at = ahead.t0 + warp;  // next tile of this warp to copy
+    int at = ahead.t0 + way.off;  // next tile of this warp to copy
     bool more = true;
     auto seek = [&]() {
         while (at >= ahead.t1) {
-            if (!decode_next<C::kKeys>(ahead, p)) {
+            if (!decode_next<C::kKeys>(ahead, p, way)) {
                 more = false;
                 return;
             }
-            at = ahead.t0 + warp;
+            at = ahead.t0 + way.off;
         }
     };
     seek();
     // (the first two tiles' pages are looked up together, later ones a tile ahead)
     int entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
-    const bool two = more && at + C::kWarps < ahead.t1;
-    const int second = two ? decode_page<D, E4M3, WIDE>(p, ahead, at + C::kWarps, lane) : -1;
+    const bool two = more && at + way.step < ahead.t1;
+    const int second = two ? decode_page<D, E4M3, WIDE>(p, ahead, at + way.step, lane) : -1;
     uint32_t slot_in = 0, slot_out = 0, ok_bits = 0;
     auto load = [&](bool first) {
         if (more) {
-            const uint32_t ok = decode_load<D, E4M3, WIDE>(p, ahead, at, entry, ring + slot_in * C::kTileBytes, lane);
+            const uint32_t ok = decode_load<D, E4M3, WIDE>(p, ahead, ahead.u * way.heads + way.add, at, entry,
+                                                           ring + slot_in * C::kTileBytes, lane);
             ok_bits = (ok_bits & ~(((1u << C::kGroups) - 1) << (slot_in * C::kGroups))) | ok << (slot_in * C::kGroups);
-            at += C::kWarps;
+            at += way.step;
             if (first && two) {
                 entry = second;
             } else {
@@ -360,7 +388,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     // ---- q of a segment as bf16 pairs, in the order of the tensor core's fragments
     uint32_t qa[KS][2 * R];
     auto load_q = [&]() {
-        const int h = seg.hh / p.row_groups, rg = seg.hh - h * p.row_groups;
+        const int hh = seg.u * way.heads + way.add, h = hh / p.row_groups, rg = hh - h * p.row_groups;
         const int rows = min(p.G - rg * C::kRows, C::kRows);
         const long long row0 = static_cast<long long>(seg.b) * p.Hkv * p.G + h * p.G + rg * C::kRows;
 #pragma unroll
@@ -383,7 +411,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     for (int i = 1; i < C::kStages - 1; ++i) load(false);
 
     for (;; first_seg = false) {
-        const int h = seg.hh / p.row_groups, rg = seg.hh - h * p.row_groups;
+        const int hh = seg.u * way.heads + way.add, h = hh / p.row_groups, rg = hh - h * p.row_groups;
         const int rows = min(p.G - rg * C::kRows, C::kRows);  // query heads of this unit
         const long long row0 = static_cast<long long>(seg.b) * p.Hkv * p.G + h * p.G + rg * C::kRows;
 
@@ -428,7 +456,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             sum[r] = 0.f;
         }
 
-        for (int t = seg.t0 + warp; t < seg.t1; t += C::kWarps) {
+        for (int t = seg.t0 + way.off; t < seg.t1; t += way.step) {
             ptx::cp_async_wait<C::kStages - 2>();
             __syncwarp();
             load(false);  // into the slot read in the previous step
@@ -582,9 +610,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             }
         }
 
-        // ---- the warps' results of this segment, added up: 8 rows at a time
-        float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat);
-        float4* merge = reinterpret_cast<float4*>(smem + C::kOffMerge);
+        // ---- the result of the warp, in rows g (and g + 8): O relative to 2^m, the reference m, the sum
+        float2 ml[R];
         if constexpr (!WIDE) {
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
@@ -596,13 +623,67 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         for (int r = 0; r < R; ++r) {
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-            if (t4 == 0)
-                // (a sum of zero: no key, or scores of -inf alone; NaN is no zero and is passed on)
-                stat[warp * 16 + g + 8 * r] = make_float2(sum[r] == 0.f ? -INFINITY : m_use[r], sum[r]);
+            // (a sum of zero: no key, or scores of -inf alone; NaN is no zero and is passed on)
+            ml[r] = make_float2(sum[r] == 0.f ? -INFINITY : m_use[r], sum[r]);
         }
         const bool whole = CLUSTER ? p.cluster == 1 : seg.t0 == 0 && seg.t1 == seg.nt;
         const long long slot = 2LL * worker + (first_seg ? 0 : 1);
         const float vs = p.v_scale ? p.v_scale[h] : 1.f;
+
+        if (!CLUSTER && way.heads > 1) {
+            // ---- one head per warp: the output, or the partial result, straight from the fragments
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int row = g + 8 * r;
+                if (row >= rows) continue;
+                const float f = whole ? (ml[r].y == 0.f ? 0.f : vs / ml[r].y) : 1.f;
+                const long long out = row0 + row, part = (slot * 4 + warp) * C::kRows + row;
+                if (t4 == 0) {
+                    if (!whole)
+                        p.part_ml[part] = ml[r];
+                    else if (p.lse)
+                        p.lse[out] = ml[r].y == 0.f ? -INFINITY : (ml[r].x + log2f(ml[r].y)) * 0.69314718055994531f;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int n = 0; n < ND; n += 4) {
+                        // e4m3: four values of one column block; bf16: two values each of columns n.., n + 2..
+                        if constexpr (E4M3) {
+                            const int c4 = ((2 * t4 + j) * ND + n) / 4;
+                            const float x[4] = {acc[n][2 * r + j] * f, acc[n + 1][2 * r + j] * f,
+                                                acc[n + 2][2 * r + j] * f, acc[n + 3][2 * r + j] * f};
+                            if (whole)
+                                reinterpret_cast<uint2*>(p.o)[out * (D / 4) + c4] =
+                                    make_uint2(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]));
+                            else
+                                reinterpret_cast<float4*>(p.part_o)[part * (D / 4) + c4] =
+                                    make_float4(x[0], x[1], x[2], x[3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int nn = n + 2 * j + i, c2 = nn * 4 + t4;
+                                const float x0 = acc[nn][2 * r] * f, x1 = acc[nn][2 * r + 1] * f;
+                                if (whole)
+                                    reinterpret_cast<uint32_t*>(p.o)[out * (D / 2) + c2] = ptx::pack_bf16x2(x0, x1);
+                                else
+                                    reinterpret_cast<float2*>(p.part_o)[part * (D / 2) + c2] = make_float2(x0, x1);
+                            }
+                        }
+                    }
+            }
+            if (!decode_next<C::kKeys>(seg, p, way)) break;
+            load_q();
+            continue;
+        }
+
+        // ---- the warps' results of one unit, added up: 8 rows at a time
+        float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat);
+        float4* merge = reinterpret_cast<float4*>(smem + C::kOffMerge);
+        if (t4 == 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) stat[warp * 16 + g + 8 * r] = ml[r];
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (r > 0) __syncthreads();
@@ -626,20 +707,20 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             for (int i = tid; i < 8 * D / 4; i += C::kThreads) {
                 const int row = i / (D / 4), c4 = i % (D / 4);
                 if (row + 8 * r >= rows) continue;
-                float2 ml[C::kWarps];
+                float2 each[C::kWarps];
                 float mm = -INFINITY, l = 0.f;
 #pragma unroll
                 for (int w = 0; w < C::kWarps; ++w) {
-                    ml[w] = stat[w * 16 + row + 8 * r];
-                    mm = fmaxf(mm, ml[w].x);
+                    each[w] = stat[w * 16 + row + 8 * r];
+                    mm = fmaxf(mm, each[w].x);
                 }
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < C::kWarps; ++w) {
-                    if (ml[w].x == -INFINITY) continue;  // (its O is zero)
-                    const float f = ptx::ex2_approx(ml[w].x - mm);
+                    if (each[w].x == -INFINITY) continue;  // (its O is zero)
+                    const float f = ptx::ex2_approx(each[w].x - mm);
                     const float4 x = merge[(w * 8 + row) * (D / 4) + merge_col<D, E4M3>(row, c4)];
-                    l += ml[w].y * f;
+                    l += each[w].y * f;
                     o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
                 }
                 if (whole) {
@@ -668,26 +749,26 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             for (int i = tid * p.cluster + rank; i < rows * D / 4; i += C::kThreads * p.cluster) {
                 const int row = i / (D / 4), c4 = i % (D / 4);
                 // (all loads first: one takes some 250 cycles; past the cluster's size, one of it again)
-                float2 ml[kDecodeCluster];
+                float2 each[kDecodeCluster];
                 float4 x[kDecodeCluster];
 #pragma unroll
                 for (int w = 0; w < kDecodeCluster; ++w) {
                     const uint32_t from = static_cast<uint32_t>(w & (p.cluster - 1));
-                    ml[w] = ptx::ld_dsmem_v2(ptx::mapa_shared(ml_at + row * 8, from));
+                    each[w] = ptx::ld_dsmem_v2(ptx::mapa_shared(ml_at + row * 8, from));
                     x[w] = ptx::ld_dsmem_v4(ptx::mapa_shared(o_at + i * 16, from));
                 }
                 float mm = -INFINITY, l = 0.f;
 #pragma unroll
                 for (int w = 0; w < kDecodeCluster; ++w) {
-                    if (w >= p.cluster) ml[w].x = -INFINITY;
-                    mm = fmaxf(mm, ml[w].x);
+                    if (w >= p.cluster) each[w].x = -INFINITY;
+                    mm = fmaxf(mm, each[w].x);
                 }
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < kDecodeCluster; ++w) {
-                    if (ml[w].x == -INFINITY) continue;
-                    const float f = ptx::ex2_approx(ml[w].x - mm);
-                    l += ml[w].y * f;
+                    if (each[w].x == -INFINITY) continue;
+                    const float f = ptx::ex2_approx(each[w].x - mm);
+                    l += each[w].y * f;
                     o.x += x[w].x * f, o.y += x[w].y * f, o.z += x[w].z * f, o.w += x[w].w * f;
                 }
                 const float inv = l == 0.f ? 0.f : vs / l;
@@ -700,72 +781,82 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             ptx::cluster_leave();  // the other blocks' shared memory is read until here
             return;
         }
-        if (!decode_next<C::kKeys>(seg, p)) break;
+        if (!decode_next<C::kKeys>(seg, p, way)) break;
         load_q();
         __syncthreads();  // stat and merge are written again
     }
 }
 
-// Adds up the partial results of the cut units. Block (c, row) does row `row`
-// of the unit whose first cut lies between workers c - 1 and c, if there is
-// one: the threads share out the workers, then add across in shared memory.
-// Bound by latency: a few KB per block.
+// Adds up the partial results of the cut units. Every cut has a block: those of
+// one unit share out its output (4 values of a row each, an element here), and a
+// block's threads the partials of its elements where those are few. Bound by
+// latency: the run's description, then the partials, a few KB per block.
+constexpr int kJoinThreads = 256;
 template <int D, int ROWS>
-__global__ void __launch_bounds__(128) fa_decode_join_kernel(const DecodeParams p) {
-    constexpr int kCols = D / 4, kParts = 128 / kCols;
-    __shared__ float4 sh_o[128];
-    __shared__ float2 sh_ml[kParts];
+__global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const DecodeParams p) {
+    constexpr int kCols = D / 4, kBatch = 4;
+    __shared__ float4 sh_o[kJoinThreads];
+    __shared__ float2 sh_ml[kJoinThreads];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int4 meta = p.meta[blockIdx.x];
-    const int row = blockIdx.y;
+    const int c = blockIdx.x, tid = threadIdx.x;
+    const int4 meta = p.meta[c];
     if (meta.x < 0) return;
-    const int h = meta.y / p.row_groups, rg = meta.y - h * p.row_groups;
-    if (row >= p.G - rg * ROWS) return;
-    const int tid = threadIdx.x, part = tid / kCols, col = tid % kCols;
-    const int n = meta.w - static_cast<int>(blockIdx.x) + 2;  // partials: the first worker's, then one per worker
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = part; i < n; i += kParts) {
-        const long long slot = i == 0 ? meta.z : 2LL * (blockIdx.x + i - 1);
-        const float2 ml = p.part_ml[slot * ROWS + row];
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + (slot * ROWS + row) * D + col * 4);
-        const float mm = fmaxf(m, ml.x);
-        const float fa_ = m == -INFINITY ? 0.f : ptx::ex2_approx(m - mm);
-        const float fb = ml.x == -INFINITY ? 0.f : ptx::ex2_approx(ml.x - mm);
-        l = l * fa_ + ml.y * fb;
-        o.x = o.x * fa_ + x.x * fb;
-        o.y = o.y * fa_ + x.y * fb;
-        o.z = o.z * fa_ + x.z * fb;
-        o.w = o.w * fa_ + x.w * fb;
-        m = mm;
-    }
-    sh_o[tid] = o;
-    if (col == 0) sh_ml[part] = make_float2(m, l);
-    __syncthreads();
-    if (part != 0) return;
-    float mm = -INFINITY;
+    const int heads = meta.w & 7, last = meta.w >> 3, first = meta.z >> 1;
+    const int n = last - first + 1, cuts = last - first;  // partials: the first worker's, then one per cut
+    const int rows = min(p.G, ROWS), all = heads * rows * kCols;
+    const int e0 = all * (c - first - 1) / cuts, e1 = all * (c - first) / cuts;
+    int wide = 1, parts = 1;  // threads across elements, and across partials
+    while (wide < e1 - e0 && wide < kJoinThreads) wide *= 2;
+    while (wide * parts < kJoinThreads && parts < n) parts *= 2;
+    const int part = tid / wide;
+    for (int e = e0 + tid % wide; e - tid % wide < e1; e += wide) {
+        const int item = e / kCols, col = e % kCols, head = item / rows, row = item % rows;
+        const int hh = meta.y * heads + head, h = hh / p.row_groups, rg = hh - h * p.row_groups;
+        const bool mine = e < e1 && part < parts && row < p.G - rg * ROWS;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float2 ml, float4 x) {
+            const float mm = fmaxf(m, ml.x);
+            const float fa_ = m == -INFINITY ? 0.f : ptx::ex2_approx(m - mm);
+            const float fb = ml.x == -INFINITY ? 0.f : ptx::ex2_approx(ml.x - mm);
+            l = l * fa_ + ml.y * fb;
+            o.x = o.x * fa_ + x.x * fb, o.y = o.y * fa_ + x.y * fb;
+            o.z = o.z * fa_ + x.z * fb, o.w = o.w * fa_ + x.w * fb;
+            m = mm;
+        };
+        if (mine) {
+            for (int i0 = part; i0 < n; i0 += kBatch * parts) {
+                float2 ml[kBatch];
+                float4 x[kBatch];
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) mm = fmaxf(mm, sh_ml[i].x);
-    l = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < kBatch; ++k) {
+                    const int i = min(i0 + k * parts, n - 1);
+                    const long long at = ((i == 0 ? meta.z : 2LL * (first + i)) * heads + head) * ROWS + row;
+                    ml[k] = p.part_ml[at];
+                    x[k] = reinterpret_cast<const float4*>(p.part_o)[at * kCols + col];
+                }
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) {
-        if (sh_ml[i].x == -INFINITY) continue;
-        const float f = ptx::ex2_approx(sh_ml[i].x - mm);
-        const float4 x = sh_o[i * kCols + col];
-        l += sh_ml[i].y * f;
-        o.x += x.x * f;
-        o.y += x.y * f;
-        o.z += x.z * f;
-        o.w += x.w * f;
+                for (int k = 0; k < kBatch; ++k)
+                    if (i0 + k * parts < n) add(ml[k], x[k]);
+            }
+        }
+        for (int half = parts / 2; half > 0; half /= 2) {  // (parts > 1: one pass, the block's own)
+            if (part >= half && part < 2 * half) {
+                sh_o[tid] = o;
+                sh_ml[tid] = make_float2(m, l);
+            }
+            __syncthreads();
+            if (part < half) add(sh_ml[tid + half * wide], sh_o[tid + half * wide]);
+            __syncthreads();
+        }
+        if (!mine || part != 0) continue;
+        const float inv = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[h] : 1.f) / l;
+        const long long out = static_cast<long long>(meta.x) * p.Hkv * p.G + h * p.G + rg * ROWS + row;
+        reinterpret_cast<uint2*>(p.o)[out * kCols + col] =
+            make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+        if (col == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
-    const float inv = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[h] : 1.f) / l;
-    const long long out = static_cast<long long>(meta.x) * p.Hkv * p.G + h * p.G + rg * ROWS + row;
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.o) + out * D + col * 4) =
-        make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
-    if (col == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace fa

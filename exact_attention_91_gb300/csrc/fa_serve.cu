@@ -177,10 +177,14 @@ DecodePlan decode_plan(long long B, long long Hq, long long Hkv, int d, int type
     return {0, std::min(resident, most)};
 }
 
+// Whether a warp may take one key head (or row group of one) of four.
+bool decode_fours(long long Hq, long long Hkv) { return Hkv * ((Hq / Hkv + 15) / 16) % 4 == 0; }
+
 struct DecodeSpace {
     size_t meta, ml, o, bytes;
 };
-DecodeSpace decode_space(long long workers, int rows, int d) {
+DecodeSpace decode_space(long long workers, long long Hq, long long Hkv, int d) {
+    const size_t rows = (Hq / Hkv > 8 ? 16 : 8) * (decode_fours(Hq, Hkv) ? 4 : 1);
     DecodeSpace s;
     s.meta = 0;
     s.ml = static_cast<size_t>(workers) * 16;
@@ -205,8 +209,7 @@ int launch_decode(const fa::DecodeParams& p, unsigned blocks, cudaStream_t s) {
     if (launch(fa::fa_decode_kernel<D, E4M3, WIDE, false>, dim3(blocks), C::kThreads, C::kSmemBytes, s, p) != FA_OK)
         return FA_ERR_LAUNCH;
     if (blocks == 1) return FA_OK;  // nothing is cut
-    const unsigned rows = static_cast<unsigned>(std::min(p.G, C::kRows));
-    return launch(fa::fa_decode_join_kernel<D, C::kRows>, dim3(blocks, rows), 128, 0, s, p);
+    return launch(fa::fa_decode_join_kernel<D, C::kRows>, dim3(blocks), fa::kJoinThreads, 0, s, p);
 }
 
 template <int D>
@@ -258,7 +261,7 @@ long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_typ
     if (sm_count < 1) return FA_ERR_BAD_SHAPE;
     const DecodePlan plan = decode_plan(B, Hq, Hkv, d, cache_type, static_cast<long long>(table_width) * page_size,
                                         sm_count);
-    return static_cast<long long>(decode_space(plan.workers, Hq / Hkv > 8 ? 16 : 8, d).bytes);
+    return static_cast<long long>(decode_space(plan.workers, Hq, Hkv, d).bytes);
 }
 
 int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block_table, const int* seq_lens, void* o,
@@ -296,7 +299,7 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
     const bool wide = Hq / Hkv > 8;
     const DecodePlan plan = decode_plan(B, Hq, Hkv, d, cache->type,
                                         static_cast<long long>(table_width) * cache->page_size, sms);
-    const DecodeSpace sp = decode_space(plan.workers, wide ? 16 : 8, d);
+    const DecodeSpace sp = decode_space(plan.workers, Hq, Hkv, d);
     if (sp.bytes > 0 && (!workspace || workspace_bytes < sp.bytes)) return FA_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (ready(dev, s) != FA_OK) return FA_ERR_LAUNCH;
@@ -329,6 +332,7 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
     p.page_shift = c.shift;
     p.width = table_width;
     p.cluster = plan.cluster;
+    p.fours = decode_fours(Hq, Hkv) ? 1 : 0;
     const long long units = static_cast<long long>(B) * Hkv * p.row_groups;
     const unsigned w = static_cast<unsigned>(plan.cluster > 0 ? units * plan.cluster : plan.workers);
     return d == 64 ? launch_decode_any<64>(c.e4m3, wide, p, w, s) : launch_decode_any<128>(c.e4m3, wide, p, w, s);

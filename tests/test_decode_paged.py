@@ -128,6 +128,35 @@ def test_requests_cut_across_blocks(d, e4m3, hq, hkv, lens):
     check(fa, make(lens, hq, hkv, d, 32, e4m3, seed=len(lens)))
 
 
+@pytest.mark.parametrize("d,e4m3,hq,hkv", [(64, False, 4, 4), (128, True, 32, 8), (128, False, 64, 4), (64, True, 48, 4),
+                                           (128, False, 80, 4), (64, True, 12, 12)])
+def test_one_head_per_warp(d, e4m3, hq, hkv):
+    """Enough work that each warp takes a key head (or a row group of one) of
+    its own: cut and whole units, no keys, hidden pages, NaN in unfilled places."""
+    fa = _fa()
+    keys = 4096 // (d if e4m3 else 2 * d)
+    heads = hkv * -(-(hq // hkv) // 16)
+    lens = [0, 1, keys, keys + 1, 9000, 3 * keys - 1] + [(i * 61) % 700 for i in range(90)] + [5003]
+    workers = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    while sum(max(1, -(-n // keys)) for n in lens) * (heads // 4) < 20 * workers:
+        lens += [4001, 0, 777, 2500]
+    x = make(lens, hq, hkv, d, 16, e4m3, seed=hq)
+    x["table"][4, 7] = -1
+    x["table"][4, 100:140] = x["k"].shape[0]
+    table = x["table"].cpu()
+    for b in (1, 3, 5, 9):                                 # behind the last key of these requests
+        n = lens[b]
+        if n % 16:
+            for name in ("k", "v"):
+                t = x[name][table[b, n // 16].item()].float()
+                t[n % 16:] = float("nan")
+                x[name][table[b, n // 16].item()] = t.to(x[name].dtype)
+    check(fa, x)
+    o1, l1 = call(fa, x)
+    o2, l2 = call(fa, x)
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
 def test_many_requests():
     """More requests than a block has threads, and more units than blocks."""
     fa = _fa()
