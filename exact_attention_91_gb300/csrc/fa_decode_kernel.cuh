@@ -98,7 +98,7 @@ struct DecodeWay {
     int step, off; // this warp's tiles of a segment: t0 + off, every step-th
     int add;       // its head: unit * heads + add
 };
-constexpr int kSegCost = 6, kSegCostFours = 2;
+constexpr int kSegCost = 8, kSegCostFours = 2;
 // The four-heads way is taken when there is a unit of four for every worker (few
 // are cut then) and the cache is token-major, so that the four heads' rows are
 // neighbours, or the requests are short (at most kFoursShort tiles in the mean:
