@@ -5,13 +5,15 @@
 //   LSE_i = ln Σ_j exp s_ij;  no key: O = 0, LSE = -inf
 // in one pass with the online softmax, in base 2 (log2 e folded into the scale).
 //
-// The keys and values are read once, 2·D·len bytes per key head, and meet
-// 4·G flops per value: the kernel is bound by HBM, so everything serves a
-// steady stream of loads.
+// The keys and values are read once, 2·D·len elements per key head, and meet
+// 4·G flops each: the kernel is bound by HBM, so everything serves a steady
+// stream of loads.
 //  * A tile is one warp's step: 8 KB of cache (kKeys keys, K and V). Each warp
 //    owns a ring of kStages tiles in shared memory, filled with 16-byte
 //    cp.async and read back by itself alone, so the loop has no block barrier
-//    and about 130 KB per SM stay in flight.
+//    and about 130 KB per SM are in flight. (Two stages: decode_batch below 167
+//    us; three with the copy issued before the wait, so that 192 KB are in
+//    flight: 169.)
 //  * The tiles of the whole batch, in the order (request, key head, tile), are
 //    cut into equal runs, one per worker (block), whatever the lengths are:
 //    the lengths are read on the GPU. A worker's loads run on across the
@@ -31,15 +33,28 @@
 //    lengths, no second launch.
 //  * One warp-level mma.sync m16n8k16 tile holds up to 16 query heads; tcgen05
 //    would want 128 rows (heads) or a softmax across TMEM lanes, for flops that
-//    are not the bound. With at most 8 heads the tile's rows 8-15 carry the
-//    rounding remainder of P: p = hi + lo, both 16 bits, so P·V keeps about
-//    16 (bf16) or 22 (fp16) bits of p at no extra instruction.
+//    are not the bound (the tensor pipe is busy 19% of the time with 4 query
+//    heads per key head, 37% with 8 on an e4m3 cache). With at most 8 heads the
+//    tile's rows 8-15 carry the rounding remainder of P: p = hi + lo, both 16
+//    bits, so P·V keeps about 16 (bf16) or 22 (fp16) bits of p at no extra
+//    instruction.
 //  * e4m3 caches are widened to fp16 (exact) in registers; q is scaled by a
 //    power of two per head into fp16's range (exact but for values 2^-14
 //    below the head's largest, whose low bits are below 2^-24 of it).
+//
+// Measured on GB300 (a call, of calls back to back on three sets of inputs;
+// bytes of the keys and values over time):
+//   64 requests of 300 to 8192 keys, 32/8 heads, d 128        160.5 us  6.62 TB/s
+//   2 requests of 65536 keys, 32/32 heads, d 128               301.5 us  7.12 TB/s
+//   128 requests of 777 to 8190 keys, 64/8 heads, e4m3         180.7 us  6.53 TB/s
+//   1 request of 1000 keys, 32/8 heads (5.1 us replayed)        5.5 us
+// The main kernel alone reads at 6.5 to 7.1 TB/s (dram__bytes_read within 0.1%
+// of the keys' and values' bytes); what is left is the start of a launch (the
+// chain lengths, pages, first tiles: about 4 us) and the join (about 4 us).
 #pragma once
 
 #include "fa_common.cuh"
+#include "serve_ptx.cuh"
 
 namespace fa {
 

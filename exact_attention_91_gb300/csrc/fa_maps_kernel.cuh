@@ -11,9 +11,14 @@
 // L2) rather than wait for another block, then does its share of the pages and
 // tokens by binary search. No value that a block reads is written by another:
 // the pages taken are read from the list of unused ones, not from the table.
+//
+// Measured on GB300, replayed: 256 requests of one new token 3.5 us; 60 requests
+// with 123000 new tokens (1 MB of maps written) 3.9 us. A call from Python takes
+// 5.0 and 5.5 us of host time, half of it the launch.
 #pragma once
 
 #include "fa_common.cuh"
+#include "serve_ptx.cuh"
 
 namespace fa {
 
