@@ -7,8 +7,8 @@ allocates the outputs with torch and calls ``fa_fwd`` on the current stream.
 Every step of the computation runs in the CUDA library; if the library is
 missing this module raises instead of computing anything elsewhere. The
 serving functions (paged cache, rotary positions) do the same through the
-binding's native half, ``lib/_fa_bind.so``: their kernels are often shorter than
-what the checks and the call cost in Python.
+binding's native half, ``lib/_fa_bind-torch<version>.so``: their kernels are
+often shorter than what the checks and the call cost in Python.
 """
 from __future__ import annotations
 
@@ -377,8 +377,8 @@ _bind = None
 
 
 def load_binding():
-    """The binding's native half (``lib/_fa_bind.so``, built with libfa.so): the
-    checks, allocations and C calls of the functions below."""
+    """The binding's native half (``lib/_fa_bind-torch<version>.so``, built with
+    libfa.so): the checks, allocations and C calls of the functions below."""
     global _bind
     if _bind is None:
         import torch  # noqa: F401  (its libraries, which the module is linked to)
@@ -528,9 +528,10 @@ def cache_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interlea
     ``v_cache`` [num_blocks, page_size, heads, d], q returned turned (in
     ``q_out`` where given; it may be q). ``k_out`` [T, heads, d] also receives
     the turned k (for a prompt's own attention; it may be k). A token with a
-    negative slot is padding: nothing of it is written anywhere. q, k and v may
-    be slices of one projection's output. float8_e4m3fn caches hold value /
-    scale, with ``k_scale`` / ``v_scale`` fp32 [heads] (None: 1)."""
+    negative slot is padding: nothing of it is written anywhere (its row of a
+    q_out that the call makes is not initialised). q, k and v may be slices of
+    one projection's output. float8_e4m3fn caches hold value / scale, with
+    ``k_scale`` / ``v_scale`` fp32 [heads] (None: 1)."""
     append = (_bind or load_binding()).append
     if stream is None:
         r = append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved, factor, k_scale, v_scale, q_out,

@@ -7,11 +7,12 @@ the driver's tensor-map encoder at run time, so it needs no libcuda at link
 time.
 
 The Python binding's native half (``csrc/fa_bind.cpp``, torch's C++ API) is
-compiled beside it with the host compiler into ``lib/_fa_bind.so`` and linked to
-libfa.so.
+compiled beside it with the host compiler into ``lib/_fa_bind-torch<version>.so``
+and linked to libfa.so.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import importlib.util
 import os
 import re
@@ -26,7 +27,19 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa.so")
-BIND_PATH = os.path.join(LIB_DIR, "_fa_bind.so")
+
+
+def bind_path() -> str:
+    """The binding's native half, named after the torch that it is built for
+    (another torch's C++ API may differ)."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "none"
+    return os.path.join(LIB_DIR, f"_fa_bind-torch{version}.so")
+
+
+BIND_PATH = bind_path()
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

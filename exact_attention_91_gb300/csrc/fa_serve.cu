@@ -55,6 +55,17 @@ bool rows_apart(const long long (&size)[3], const long long (&stride)[3], long l
     return true;
 }
 
+// Whether the rows of two bf16 tensors whose extents overlap may meet: unless
+// they run side by side, with one stride, as slices of a wider tensor do.
+bool rows_meet(const void* a, long long a_row, long long a_stride, const void* b, long long b_row, long long b_stride,
+               int rows) {
+    if (rows == 1 || a_stride != b_stride) return true;
+    const long long stride = a_stride * 2;
+    const long long apart = (reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) % stride;
+    const long long off = apart < 0 ? apart + stride : apart;
+    return off < a_row * 2 || stride - off < b_row * 2;
+}
+
 // A cache as the kernels take it: strides in bytes.
 struct Cache {
     long long k_block, k_token, k_head, v_block, v_token, v_head;
@@ -409,8 +420,9 @@ int fa_cache_append(const void* q, const void* k, const void* v, long long q_str
     const long long strides[5] = {q_stride, k_stride, v_stride, q_out_stride, k_out_stride};
     const void* ptrs[5] = {q, k, v, q_out, k_out};
     size_t bytes[5];
+    long long rows[5];
     for (int i = 0; i < 5; ++i) {
-        const long long row = static_cast<long long>(i == 0 || i == 3 ? Hq : Hkv) * d;
+        const long long row = rows[i] = static_cast<long long>(i == 0 || i == 3 ? Hq : Hkv) * d;
         bytes[i] = 0;
         if (!ptrs[i]) continue;
         if (misaligned(ptrs[i], 16)) return FA_ERR_MISALIGNED;
@@ -426,16 +438,16 @@ int fa_cache_append(const void* q, const void* k, const void* v, long long q_str
     const long long ks[3] = {cache->k_block, cache->k_token, cache->k_head};
     const long long vs[3] = {cache->v_block, cache->v_token, cache->v_head};
     if (!rows_apart(dims, ks, d) || !rows_apart(dims, vs, d) || cache->k == cache->v) return FA_ERR_ALIAS;
-    // q and k may be rotated in place; apart from that the outputs and the caches overlap nothing
+    // q and k may be rotated in place; apart from that the outputs overlap nothing
     const bool q_same = q_out == q && (T == 1 || q_out_stride == q_stride);
     const bool k_same = k_out == k && (T == 1 || k_out_stride == k_stride);
-    const bool one_buffer = q_stride == k_stride && k_stride == v_stride;  // slices of one projection's rows
-    for (int i = 0; i < 3; ++i) {
-        const bool interleaves = one_buffer && T > 1;
-        if (!(q_same && (i == 0 || interleaves)) && overlap(q_out, bytes[3], ptrs[i], bytes[i])) return FA_ERR_ALIAS;
-        if (!(k_same && (i == 1 || interleaves)) && overlap(k_out, bytes[4], ptrs[i], bytes[i])) return FA_ERR_ALIAS;
-    }
-    if (!(q_same && k_same && one_buffer) && overlap(q_out, bytes[3], k_out, bytes[4])) return FA_ERR_ALIAS;
+    for (int i = 3; i < 5; ++i)
+        for (int j = 0; j < i; ++j) {
+            if ((i == 3 && j == 0 && q_same) || (i == 4 && j == 1 && k_same)) continue;
+            if (overlap(ptrs[i], bytes[i], ptrs[j], bytes[j]) &&
+                rows_meet(ptrs[i], rows[i], strides[i], ptrs[j], rows[j], strides[j], T))
+                return FA_ERR_ALIAS;
+        }
     for (int i = 0; i < 5; ++i)
         if (overlap(cache->k, c.k_bytes, ptrs[i], bytes[i]) || overlap(cache->v, c.v_bytes, ptrs[i], bytes[i]))
             return FA_ERR_ALIAS;

@@ -208,6 +208,9 @@ int fa_varlen_num_splits(int B, int H, int total_k, int max_seqlen_q, int sm_cou
  * call of any of them (a captured call before then returns FA_ERR_LAUNCH).
  * They keep no state on the device either: calls on different streams and
  * replays of different graphs share nothing but the buffers given to them.
+ * Their kernels allow programmatic dependent launch as fa_fwd's do, and are
+ * themselves launched that way: they wait for what precedes them on the stream
+ * before they read or write.
  * ---------------------------------------------------------------------------
  */
 

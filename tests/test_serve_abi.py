@@ -158,8 +158,17 @@ def test_append_calls_that_pass_the_checks():
         for kw in (dict(), dict(k_out=0), dict(q_out=3 * P), dict(k_out=4 * P), dict(r=0, freq=0), dict(T=1, qs=0, qos=0),
                    # slices of one projection, turned in place
                    dict(q=3 * P, k=3 * P + 512, v=3 * P + 768, qs=row, ks=row, vs=row, q_out=3 * P, qos=row,
-                        k_out=3 * P + 512, kos=row)):
+                        k_out=3 * P + 512, kos=row),
+                   # outputs side by side in one buffer
+                   dict(q_out=9 * P, qos=row, k_out=9 * P + 512, kos=row)):
             assert append(**kw) == -5, kw
+        for kw in (dict(q=3 * P, k=3 * P, v=3 * P + 768, qs=row, ks=row, vs=row, q_out=3 * P, qos=row),     # k is q's first heads
+                   dict(q=3 * P, k=3 * P + 512, v=3 * P + 512, qs=row, ks=row, vs=row, q_out=3 * P, qos=row,
+                        k_out=3 * P + 512, kos=row),                                                        # v is k
+                   dict(q=3 * P, k=3 * P + 384, v=3 * P + 768, qs=row, ks=row, vs=row, q_out=3 * P, qos=row),
+                   dict(q=3 * P, k=3 * P + row * 2 * 3 + 768, v=5 * P, qs=row, ks=row, q_out=3 * P, qos=row, k_out=3 * P + 768,
+                        kos=row)):                                                                          # k_out is k, three tokens on
+            assert append(**kw) == -10, kw
 
 
 def maps(ctx=P, fresh=2 * P, table=3 * P, unused=4 * P, slots=5 * P, pos=6 * P, cu=7 * P, lens=8 * P, counts=9 * P, B=4,
