@@ -37,7 +37,8 @@
 //    heads per key head, 37% with 8 on an e4m3 cache). With at most 8 heads the
 //    tile's rows 8-15 carry the rounding remainder of P: p = hi + lo, both 16
 //    bits, so P·V keeps about 16 (bf16) or 22 (fp16) bits of p at no extra
-//    instruction.
+//    instruction. (9 to 16 heads: a second instruction in bf16; none in fp16,
+//    where p keeps 11 bits.)
 //  * e4m3 caches are widened to fp16 (exact) in registers; q is scaled by a
 //    power of two per head into fp16's range (exact but for values 2^-14
 //    below the head's largest, whose low bits are below 2^-24 of it).
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     constexpr int ND = D / 8;         // output columns, 8 values each
     constexpr int KS = D / 16;        // steps of 16 of q·k
     constexpr int R = WIDE ? 2 : 1;   // query rows of a lane: g (and g + 8)
+    constexpr bool kOneP = WIDE && E4M3;  // P without its remainder
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long sh_warp[C::kWarps];
     __shared__ long long sh_begin;
@@ -430,7 +432,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         const int rows = min(p.G - rg * C::kRows, C::kRows);  // query heads of this unit
         const long long row0 = static_cast<long long>(seg.b) * p.Hkv * p.G + h * p.G + rg * C::kRows;
 
-        // ---- each row's factor from q·k to base-2 scores; e4m3: q as fp16, scaled by a power of two
+        // ---- each row's factor from q·k to base-2 scores, made positive (a mask's -inf is multiplied by it): a
+        // negative one's sign goes to q. e4m3: q as fp16, scaled by a power of two
         float cs[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -458,17 +461,26 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                         qa[s][R * j + r] = ptx::pack_f16x2(x.x * down, x.y * down);
                     }
             }
+            if (cs[r] < 0.f) {
+                cs[r] = -cs[r];
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) qa[s][R * j + r] ^= 0x80008000u;
+            }
+            if (cs[r] == 0.f) cs[r] = 1.17549435e-38f;  // (a scale of 0: every score is 0, or next to it)
         }
 
         float acc[ND][4];
 #pragma unroll
         for (int n = 0; n < ND; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-        float m_ref[R], m_use[R], sum[R];  // reference maximum (-inf: no key yet), the one subtracted, row sum
+        float m_ref[R], m_use[R];  // reference maximum (-inf: no key yet), the one subtracted
+        float2 sum[R];             // row sum, even and odd keys
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             m_ref[r] = -INFINITY;
             m_use[r] = 0.f;
-            sum[r] = 0.f;
+            sum[r] = make_float2(0.f, 0.f);
         }
 
         for (int t = seg.t0 + way.off; t < seg.t1; t += way.step) {
@@ -516,22 +528,24 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             // ---- mask, maximum, exponentials
             const int key0 = t * C::kKeys;
             const bool ragged = key0 + C::kKeys > seg.len || ok != (1u << C::kGroups) - 1;
-            float top[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
+            if (ragged) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float x = s[n][2 * r + j] * cs[r];
-                        if (ragged && (key0 + n * 8 + 2 * t4 + j >= seg.len || !(ok >> (n / 2) & 1))) x = -INFINITY;
-                        s[n][2 * r + j] = x;
-                    }
+                    for (int j = 0; j < 2; ++j)
+                        if (key0 + n * 8 + 2 * t4 + j >= seg.len || !(ok >> (n / 2) & 1)) {
+#pragma unroll
+                            for (int r = 0; r < R; ++r) s[n][2 * r + j] = -INFINITY;
+                        }
+            }
+            float top[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
                 top[r] = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
 #pragma unroll
                 for (int n = 1; n < NT; ++n) top[r] = ptx::fmax3(top[r], s[n][2 * r], s[n][2 * r + 1]);
                 top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)) * cs[r];
             }
             bool rise = false;
 #pragma unroll
@@ -545,7 +559,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                         m_ref[r] = top[r];
                         m_use[r] = top[r] - C::kBias;
                     }
-                    sum[r] *= alpha;
+                    sum[r].x *= alpha;
+                    sum[r].y *= alpha;
 #pragma unroll
                     for (int n = 0; n < ND; ++n) {
                         acc[n][2 * r] *= alpha;
@@ -558,7 +573,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                 }
             }
 
-            // ---- P = hi + lo in 16 bits, O += P V, 16 keys at a time
+            // ---- P in 16 bits, O += P V, 16 keys at a time. P = hi + lo, except for 16 rows of fp16: its 11 bits
+            // (2^-11 of each weight, against O's own 2^-8) cost nothing there, and the second half a fifth of the time
 #pragma unroll
             for (int kg = 0; kg < C::kGroups; ++kg) {
                 uint32_t hi[2 * R], lo[2 * R];  // [16-bit pairs of keys 2t4.. | 2t4+8..][row]
@@ -566,23 +582,23 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                 for (int r = 0; r < R; ++r)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float p0 = ptx::ex2_approx(s[2 * kg + j][2 * r] - m_use[r]);
-                        const float p1 = ptx::ex2_approx(s[2 * kg + j][2 * r + 1] - m_use[r]);
-                        sum[r] += p0 + p1;
-                        if constexpr (E4M3) {
-                            hi[R * j + r] = ptx::pack_f16x2(p0, p1);
-                            const float2 w = ptx::unpack_f16x2(hi[R * j + r]);
-                            lo[R * j + r] = ptx::pack_f16x2(p0 - w.x, p1 - w.y);
-                        } else {
-                            hi[R * j + r] = ptx::pack_bf16x2(p0, p1);
-                            const float2 w = ptx::unpack_bf16x2(hi[R * j + r]);
-                            lo[R * j + r] = ptx::pack_bf16x2(p0 - w.x, p1 - w.y);
+                        const float(&x)[4] = s[2 * kg + j];
+                        const float2 e = ptx::ffma2(make_float2(x[2 * r], x[2 * r + 1]), make_float2(cs[r], cs[r]),
+                                                    make_float2(-m_use[r], -m_use[r]));
+                        const float2 w = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
+                        sum[r] = ptx::fadd2(sum[r], w);
+                        uint32_t& h16 = hi[R * j + r];
+                        h16 = E4M3 ? ptx::pack_f16x2(w.x, w.y) : ptx::pack_bf16x2(w.x, w.y);
+                        if constexpr (!kOneP) {
+                            const float2 back = E4M3 ? ptx::unpack_f16x2(h16) : ptx::unpack_bf16x2(h16);
+                            const float2 rest = ptx::fadd2(w, make_float2(-back.x, -back.y));
+                            lo[R * j + r] = E4M3 ? ptx::pack_f16x2(rest.x, rest.y) : ptx::pack_bf16x2(rest.x, rest.y);
                         }
                     }
                 auto pv = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
                     if constexpr (WIDE) {
                         ptx::mma_16816<E4M3>(c, hi[0], hi[1], hi[2], hi[3], b0, b1);
-                        ptx::mma_16816<E4M3>(c, lo[0], lo[1], lo[2], lo[3], b0, b1);
+                        if constexpr (!kOneP) ptx::mma_16816<E4M3>(c, lo[0], lo[1], lo[2], lo[3], b0, b1);
                     } else {
                         ptx::mma_16816<E4M3>(c, hi[0], lo[0], hi[1], lo[1], b0, b1);
                     }
@@ -636,10 +652,11 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+            float l = sum[r].x + sum[r].y;
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
             // (a sum of zero: no key, or scores of -inf alone; NaN is no zero and is passed on)
-            ml[r] = make_float2(sum[r] == 0.f ? -INFINITY : m_use[r], sum[r]);
+            ml[r] = make_float2(l == 0.f ? -INFINITY : m_use[r], l);
         }
         const bool whole = CLUSTER ? p.cluster == 1 : seg.t0 == 0 && seg.t1 == seg.nt;
         const long long slot = 2LL * worker + (first_seg ? 0 : 1);

@@ -79,7 +79,8 @@ def want(x, scale=None):
 def check(fa, x, **kw):
     o, lse = call(fa, x, **kw)
     torch.cuda.synchronize()
-    so.assert_decode(so.f64(o), so.f64(lse), want(x, kw.get("scale")))
+    one_p = x["ks"] is not None and x["q"].shape[1] > 8 * x["k"].shape[2]
+    so.assert_decode(so.f64(o), so.f64(lse), want(x, kw.get("scale")), one_p)
     return o, lse
 
 
@@ -172,6 +173,20 @@ def test_scale_and_large_scores():
         x["q"] = (x["q"].float() * 6).bfloat16()
         check(fa, x, scale=0.5)
         check(fa, x, scale=0.01)
+
+
+@pytest.mark.parametrize("e4m3,hq", [(False, 4), (False, 16), (True, 4), (True, 16)])
+@pytest.mark.parametrize("width", [None, 3001])
+def test_negative_and_zero_scales_of_the_cache(e4m3, hq, width):
+    """A key scale below zero turns the order of the scores round, one of zero
+    makes them equal; hidden keys stay hidden."""
+    fa = _fa()
+    x = make([700, 33, 0, 129], hq, 1, 64, 16, e4m3, seed=15, width=width)
+    x["table"][0, 5] = -1
+    for value in (-0.7, 0.0):
+        x["ks"] = torch.full((1,), value, device="cuda")
+        x["vs"] = torch.full((1,), -1.5, device="cuda")
+        check(fa, x)
 
 
 def test_rising_scores_rescale_every_tile():
