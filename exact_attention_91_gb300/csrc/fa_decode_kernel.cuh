@@ -218,7 +218,7 @@ __device__ __forceinline__ uint32_t decode_chunk(int r, int c) {
 // returns which of its 16-key groups lie in a page of the cache (bit g).
 template <int D, bool E4M3, bool WIDE>
 __device__ __forceinline__ uint32_t decode_load(const DecodeParams& p, const DecodeSeg& s, int hh, int t,
-                                                int page_entry, uint32_t dst, int lane) {
+                                                int page_entry, uint32_t dst, int lane, uint64_t policy) {
     using C = DecodeCfg<D, E4M3, WIDE>;
     const int lr = lane / C::kRowLanes, lc = lane % C::kRowLanes;
     const int h = hh / p.row_groups;
@@ -238,8 +238,8 @@ __device__ __forceinline__ uint32_t decode_load(const DecodeParams& p, const Dec
         for (int i = 0; i < C::kCopiesPerGroup; ++i) {
             const uint32_t bytes = i * C::kRowsPerCopy < left ? 16u : 0u;
             const uint32_t off = decode_chunk<D, E4M3>(g * 16 + i * C::kRowsPerCopy + lr, lc);
-            ptx::cp_async16(dst + off, ks, bytes);
-            ptx::cp_async16(dst + C::kHalfBytes + off, vs, bytes);
+            ptx::cp_async16(dst + off, ks, bytes, policy);
+            ptx::cp_async16(dst + C::kHalfBytes + off, vs, bytes, policy);
             ks += C::kRowsPerCopy * p.k_token;
             vs += C::kRowsPerCopy * p.v_token;
         }
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long sh_warp[C::kWarps];
     __shared__ long long sh_begin;
-    __shared__ int sh_b;
+    __shared__ int sh_b, sh_len;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int HH = p.Hkv * p.row_groups;
     DecodeSeg seg;
@@ -324,48 +324,49 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         {
             long long at = (before + incl - mine + static_cast<long long>(b_lo) * way.cost) * way.units;
             if (begin >= at && begin < at + (mine + static_cast<long long>(b_hi - b_lo) * way.cost) * way.units) {
-                int b = b_lo;
+                int b = b_lo, len = 0;
                 for (;; ++b) {
-                    const long long n =
-                        static_cast<long long>(decode_tiles<C::kKeys>(decode_len(p, b)) + way.cost) * way.units;
+                    len = decode_len(p, b);
+                    const long long n = static_cast<long long>(decode_tiles<C::kKeys>(len) + way.cost) * way.units;
                     if (begin < at + n) break;
                     at += n;
                 }
                 sh_b = b;
+                sh_len = len;
                 sh_begin = at;
             }
         }
         __syncthreads();
         seg.b = sh_b;
-        seg.len = decode_len(p, seg.b);
+        seg.len = sh_len;
         seg.nt = decode_tiles<C::kKeys>(seg.len);
-        {
-            const unsigned long long in = static_cast<unsigned long long>(begin - sh_begin);
-            const unsigned unit = static_cast<unsigned>(seg.nt + way.cost);
-            seg.u = static_cast<int>(in <= 0xffffffffu ? static_cast<unsigned>(in) / unit : in / unit);
-            const int x = static_cast<int>(in - static_cast<unsigned long long>(seg.u) * unit);
-            const long long u0 = begin - x;  // first counted tile of the unit
-            seg.rem = end - begin;
-            decode_take(seg, x, way.cost);
-            if (tid == 0) {
-                // For the join of a cut unit: request, unit, the slot of its first part, its last worker. (Its tile 0
-                // is in the first worker's run, and is the first part of that run if the run begins in the unit.)
-                int4 m = make_int4(-1, 0, 0, 0);
-                if (x > way.cost) {
-                    const int first = decode_worker_of(total, workers, u0 + way.cost);
-                    m.x = seg.b;
-                    m.y = seg.u;
-                    m.z = decode_start(total, workers, first) >= u0 ? 2 * first : 2 * first + 1;
-                    m.w = decode_worker_of(total, workers, u0 + way.cost + seg.nt - 1) * 8 + way.heads;
-                }
-                p.meta[worker] = m;
+        const unsigned long long in = static_cast<unsigned long long>(begin - sh_begin);
+        const unsigned unit = static_cast<unsigned>(seg.nt + way.cost);
+        seg.u = static_cast<int>(in <= 0xffffffffu ? static_cast<unsigned>(in) / unit : in / unit);
+        const int x = static_cast<int>(in - static_cast<unsigned long long>(seg.u) * unit);
+        seg.rem = end - begin;
+        decode_take(seg, x, way.cost);
+        if (tid == C::kThreads - 1) {
+            // For the join of a cut unit: request, unit, the slot of its first part, its last worker. (Its tile 0
+            // is in the first worker's run, and is the first part of that run if the run begins in the unit.)
+            int4 m = make_int4(-1, 0, 0, 0);
+            if (x > way.cost) {
+                const long long u0 = begin - x;  // first counted tile of the unit
+                const int first = decode_worker_of(total, workers, u0 + way.cost);
+                m.x = seg.b;
+                m.y = seg.u;
+                m.z = decode_start(total, workers, first) >= u0 ? 2 * first : 2 * first + 1;
+                m.w = decode_worker_of(total, workers, u0 + way.cost + seg.nt - 1) * 8 + way.heads;
             }
+            p.meta[worker] = m;
         }
         first_seg = seg.t0 < seg.t1;  // whether the run's first unit, which may be cut at its start, has a tile here
         if (!first_seg && !decode_next<C::kKeys>(seg, p, way)) return;
     }
 
     // ---- the ring: the next tiles to copy run ahead of the ones in use, across segments
+    // (keys and values are read once: they leave L2 first, so that lengths, tables, q and partials stay)
+    const uint64_t once = ptx::policy_evict_first();
     const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kTileBytes;
     DecodeSeg ahead = seg;
     int at = ahead.t0 + way.off;  // next tile of this warp to copy
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     auto load = [&](bool first) {
         if (more) {
             const uint32_t ok = decode_load<D, E4M3, WIDE>(p, ahead, ahead.u * way.heads + way.add, at, entry,
-                                                           ring + slot_in * C::kTileBytes, lane);
+                                                           ring + slot_in * C::kTileBytes, lane, once);
             ok_bits = (ok_bits & ~(((1u << C::kGroups) - 1) << (slot_in * C::kGroups))) | ok << (slot_in * C::kGroups);
             at += way.step;
             if (first && two) {

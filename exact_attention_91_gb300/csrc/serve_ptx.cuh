@@ -24,10 +24,13 @@ __device__ __forceinline__ float2 ld_dsmem_v2(uint32_t addr) {
 
 // ---- warp-level copies and matrix instructions -----------------------------
 
-// 16 bytes from global to shared memory, past L1; `bytes` (16 or 0) are read
-// and the rest of the 16 is filled with zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16 bytes from global to shared memory, past L1, with an L2 eviction policy
+// (from createpolicy); `bytes` (16 or 0) are read and the rest of the 16 is
+// filled with zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes),
+                 "l"(policy)
+                 : "memory");
 }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
