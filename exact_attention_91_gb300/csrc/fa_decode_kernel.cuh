@@ -77,6 +77,7 @@ struct DecodeParams {
     float scale_log2;
     int B, Hkv, G, row_groups, num_blocks, page_shift, width;
     int cluster;            // blocks per unit of the small form
+    int once;               // small form: keys and values leave L2 first
     int fours;              // key heads (times row groups) are a multiple of four: a warp may take one each
 };
 
@@ -125,6 +126,11 @@ constexpr int kSegCost = 8, kSegCostFours = 2;
 // heads, 35 / 28 (every worker cuts); head-major 128 x 4480 keys of 8 heads,
 // e4m3, 197 / 190.
 constexpr int kFoursRun = 20, kFoursShort = 32;
+// Tiles (32 MB of keys and values) from which on they are to leave L2 first, so
+// that lengths, tables, q and partials stay there: 166 MB, 33.3 us against 36.2;
+// 66 MB, 13.7 against 14.6. Less is kept as it comes: 28 MB, 9.7 us against 10.4,
+// when the next call finds some of it.
+constexpr int kOnceTiles = (32 << 20) / 8192;
 // Least run of a worker, in tiles with the segments' costs.
 constexpr int kMinRun = 8;
 // Most blocks of a cluster (the portable limit).
@@ -276,11 +282,13 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     DecodeSeg seg;
     DecodeWay way{HH, kSegCost, 1, C::kWarps, warp, 0};
     bool first_seg = true;
+    uint64_t policy = ptx::policy_evict_normal();
     const int worker = blockIdx.x;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     if constexpr (CLUSTER) {
         const int unit = worker / p.cluster, rank = worker - unit * p.cluster;
+        if (p.once) policy = ptx::policy_evict_first();
         seg.b = unit / HH;
         seg.u = unit - seg.b * HH;
         seg.len = decode_len(p, seg.b);
@@ -313,6 +321,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         if (p.fours && (p.B * fours >= grid ? token_major || tiles <= static_cast<long long>(p.B) * kFoursShort
                                             : token_major && tiles * fours >= grid * kFoursRun))
             way = DecodeWay{HH / 4, kSegCostFours, 4, 1, 0, warp};
+        if (tiles * HH >= kOnceTiles) policy = ptx::policy_evict_first();
         // counted tiles of all requests, and of those before b_lo
         const long long total = (tiles + static_cast<long long>(p.B) * way.cost) * way.units;
         const int workers = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kMinRun - 1) / kMinRun));
@@ -365,8 +374,6 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     }
 
     // ---- the ring: the next tiles to copy run ahead of the ones in use, across segments
-    // (keys and values are read once: they leave L2 first, so that lengths, tables, q and partials stay)
-    const uint64_t once = ptx::policy_evict_first();
     const uint32_t ring = ptx::smem_u32(smem) + warp * C::kStages * C::kTileBytes;
     DecodeSeg ahead = seg;
     int at = ahead.t0 + way.off;  // next tile of this warp to copy
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     auto load = [&](bool first) {
         if (more) {
             const uint32_t ok = decode_load<D, E4M3, WIDE>(p, ahead, ahead.u * way.heads + way.add, at, entry,
-                                                           ring + slot_in * C::kTileBytes, lane, once);
+                                                           ring + slot_in * C::kTileBytes, lane, policy);
             ok_bits = (ok_bits & ~(((1u << C::kGroups) - 1) << (slot_in * C::kGroups))) | ok << (slot_in * C::kGroups);
             at += way.step;
             if (first && two) {

@@ -172,6 +172,7 @@ int launch(void (*kernel)(Params), dim3 grid, int threads, size_t smem, cudaStre
 struct DecodePlan {
     int cluster;        // blocks per unit of the small form, or 0: equal runs
     long long workers;  // blocks of equal runs
+    long long tiles;    // of the largest batch of these sizes
 };
 DecodePlan decode_plan(long long B, long long Hq, long long Hkv, int d, int type, long long max_keys, int sms) {
     const int keys = 4096 / (d * (type == FA_CACHE_E4M3 ? 1 : 2));
@@ -182,10 +183,10 @@ DecodePlan decode_plan(long long B, long long Hq, long long Hkv, int d, int type
     // large as bring the shares down to kShare, or as one wave holds.
     int c = 1;
     while (c < fa::kDecodeCluster && 2 * c * units <= resident && tiles > static_cast<long long>(c) * kShare) c *= 2;
-    if (c * units <= resident && tiles <= static_cast<long long>(c) * kMaxShare) return {c, 0};
+    if (c * units <= resident && tiles <= static_cast<long long>(c) * kMaxShare) return {c, 0, units * tiles};
     // Equal runs: two workers per SM, or as many as the longest batch of these sizes has least runs.
     const long long most = (units * (tiles + fa::kSegCost) + fa::kMinRun - 1) / fa::kMinRun;
-    return {0, std::min(resident, most)};
+    return {0, std::min(resident, most), units * tiles};
 }
 
 // Whether a warp may take one key head (or row group of one) of four.
@@ -343,6 +344,7 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
     p.page_shift = c.shift;
     p.width = table_width;
     p.cluster = plan.cluster;
+    p.once = plan.tiles >= 2 * fa::kOnceTiles;  // (ragged lengths fill about half of the bound)
     p.fours = decode_fours(Hq, Hkv) ? 1 : 0;
     const long long units = static_cast<long long>(B) * Hkv * p.row_groups;
     const unsigned w = static_cast<unsigned>(plan.cluster > 0 ? units * plan.cluster : plan.workers);
