@@ -45,13 +45,15 @@
 //
 // Measured on GB300 (a call, of calls back to back on three sets of inputs;
 // bytes of the keys and values over time):
-//   64 requests of 300 to 8192 keys, 32/8 heads, d 128        160.5 us  6.62 TB/s
-//   2 requests of 65536 keys, 32/32 heads, d 128               301.5 us  7.12 TB/s
-//   128 requests of 777 to 8190 keys, 64/8 heads, e4m3         180.7 us  6.53 TB/s
-//   1 request of 1000 keys, 32/8 heads (5.1 us replayed)        5.5 us
-// The main kernel alone reads at 6.5 to 7.1 TB/s (dram__bytes_read within 0.1%
+//   64 requests of 300 to 8192 keys, 32/8 heads, d 128        158.5 us  6.70 TB/s
+//   2 requests of 65536 keys, 32/32 heads, d 128               300.0 us  7.16 TB/s
+//   128 requests of 777 to 8190 keys, 64/8 heads, e4m3         175.4 us  6.72 TB/s
+//   256 requests of 10 to 300 keys, 32/8 heads, d 128           33.4 us  4.98 TB/s
+//   1 request of 1000 keys, 32/8 heads (4.5 us replayed)         5.4 us
+// The main kernel alone reads at 6.6 to 7.1 TB/s (dram__bytes_read within 0.1%
 // of the keys' and values' bytes); what is left is the start of a launch (the
-// chain lengths, pages, first tiles: about 4 us) and the join (about 4 us).
+// chain lengths, pages, first tiles: 4 to 5 us until the first tile is there),
+// workers that end up to 4% apart, and the join (about 3 us).
 #pragma once
 
 #include "fa_common.cuh"
