@@ -300,7 +300,9 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
         if (overlap(outs[i], out_bytes[i], q, q_bytes) || overlap(outs[i], out_bytes[i], cache->k, c.k_bytes) ||
             overlap(outs[i], out_bytes[i], cache->v, c.v_bytes) ||
             overlap(outs[i], out_bytes[i], block_table, table_bytes) ||
-            overlap(outs[i], out_bytes[i], seq_lens, static_cast<size_t>(B) * 4))
+            overlap(outs[i], out_bytes[i], seq_lens, static_cast<size_t>(B) * 4) ||
+            overlap(outs[i], out_bytes[i], cache->k_scale, cache->k_scale ? static_cast<size_t>(Hkv) * 4 : 0) ||
+            overlap(outs[i], out_bytes[i], cache->v_scale, cache->v_scale ? static_cast<size_t>(Hkv) * 4 : 0))
             return FA_ERR_ALIAS;
         for (int j = 0; j < i; ++j)
             if (overlap(outs[i], out_bytes[i], outs[j], out_bytes[j])) return FA_ERR_ALIAS;
@@ -375,6 +377,10 @@ int fa_rotary(const void* x, void* y, const int* positions, const double* inv_fr
     bool same = x == y;  // in place: every value is read and written by the same thread
     for (int i = 0; i < 3; ++i) same = same && (dims[i] == 1 || x_strides[i] == y_strides[i]);
     if (!same && overlap(x, bytes[0], y, bytes[1])) return FA_ERR_ALIAS;
+    if (B > 1 && position_stride < 0) return FA_ERR_BAD_SHAPE;
+    if (overlap(y, bytes[1], positions, (static_cast<size_t>(B - 1) * (B > 1 ? position_stride : 0) + N) * 4) ||
+        overlap(y, bytes[1], inv_freq, static_cast<size_t>(rotary_dim) * 4))
+        return FA_ERR_ALIAS;
     const long long tokens = static_cast<long long>(B) * N;
     int dev = 0, sms = 0;
     rc = fa::host_probe(&dev, &sms);
@@ -395,7 +401,7 @@ int fa_rotary(const void* x, void* y, const int* positions, const double* inv_fr
     p.dst_b = B > 1 ? y_strides[0] : 0;
     p.x.dst_h = H > 1 ? y_strides[1] : 0;
     p.x.dst_n = N > 1 ? y_strides[2] : 0;
-    p.pos_b = position_stride;
+    p.pos_b = B > 1 ? position_stride : 0;
     p.B = B, p.H = H, p.N = N;
     const long long groups = (tokens + 512 / d - 1) / (512 / d);  // of the tokens that a warp holds
     p.heads_per_warp = heads_per_warp(groups, H, 4, sms);
@@ -452,6 +458,16 @@ int fa_cache_append(const void* q, const void* k, const void* v, long long q_str
         }
     for (int i = 0; i < 5; ++i)
         if (overlap(cache->k, c.k_bytes, ptrs[i], bytes[i]) || overlap(cache->v, c.v_bytes, ptrs[i], bytes[i]))
+            return FA_ERR_ALIAS;
+    const size_t scale_bytes = static_cast<size_t>(Hkv) * 4;
+    const void* small[5] = {positions, slots, inv_freq, cache->k_scale, cache->v_scale};
+    const size_t small_bytes[5] = {static_cast<size_t>(T) * 4, static_cast<size_t>(T) * 4,
+                                   static_cast<size_t>(rotary_dim) * 4, cache->k_scale ? scale_bytes : 0,
+                                   cache->v_scale ? scale_bytes : 0};
+    for (int i = 0; i < 5; ++i)
+        if (overlap(q_out, bytes[3], small[i], small_bytes[i]) || overlap(k_out, bytes[4], small[i], small_bytes[i]) ||
+            overlap(cache->k, c.k_bytes, small[i], small_bytes[i]) ||
+            overlap(cache->v, c.v_bytes, small[i], small_bytes[i]))
             return FA_ERR_ALIAS;
     int dev = 0, sms = 0;
     rc = fa::host_probe(&dev, &sms);

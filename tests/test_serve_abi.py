@@ -107,6 +107,7 @@ def rotary(x=P, y=2 * P, pos=3 * P, freq=4 * P, B=2, H=3, N=4, d=64, xs=(768, 25
     (dict(x=P + 8), -4), (dict(y=2 * P + 4), -4), (dict(pos=3 * P + 2), -4), (dict(freq=4 * P + 4), -4),
     (dict(factor=float("nan")), -9), (dict(factor=float("inf")), -9),
     (dict(y=P + 64), -10), (dict(y=P, ys=(768, 64, 192)), -10),
+    (dict(pos=2 * P + 64), -10), (dict(freq=2 * P + 128), -10), (dict(ps=-4), -2),
     (dict(ys=(768, 64, 64)), -10), (dict(ys=(512, 256, 64)), -10),   # rows of y on one another
 ])
 def test_bad_rotary_calls_are_rejected(kw, code):
@@ -137,6 +138,7 @@ def append(c=None, q=3 * P, k=4 * P, v=5 * P, qs=256, ks=128, vs=128, pos=6 * P,
     (dict(qs=257), -4), (dict(vs=129), -4), (dict(q=3 * P + 8), -4), (dict(k_out=10 * P + 2), -4), (dict(pos=6 * P + 1), -4),
     (dict(slots=7 * P + 2), -4), (dict(freq=8 * P + 4), -4), (dict(factor=float("inf")), -9),
     (dict(q_out=4 * P), -10), (dict(q_out=3 * P + 64), -10), (dict(q_out=3 * P, qos=512), -10), (dict(k_out=3 * P), -10),
+    (dict(pos=9 * P), -10), (dict(slots=10 * P), -10), (dict(freq=P), -10), (dict(slots=2 * P), -10),
     (dict(k_out=9 * P), -10), (dict(q_out=P), -10), (dict(v=2 * P), -10), (dict(k_out=5 * P), -10),
 ])
 def test_bad_append_calls_are_rejected(kw, code):
@@ -149,6 +151,11 @@ def test_bad_append_calls_are_rejected(kw, code):
 ])
 def test_append_to_rows_on_one_another_is_rejected(kw):
     assert append(cache(**kw)) == -10
+
+
+def test_scales_inside_what_is_written_are_rejected():
+    assert append(cache(ks=9 * P)) == -10 and append(cache(vs=P)) == -10
+    assert decode(cache(ks=6 * P)) == -10 and decode(cache(vs=7 * P)) == -10
 
 
 def test_append_calls_that_pass_the_checks():

@@ -305,6 +305,66 @@ def test_a_chain_of_dependent_calls():
     assert all(torch.equal(a, b) for a, b in zip(chain(True), chain(False)))
 
 
+def test_other_streams_are_waited_for():
+    """An early launch overlaps its predecessor on the stream only: work that the
+    stream was told to wait for (an event of another stream, a copy) is done
+    before the kernel reads."""
+    fa = _fa()
+    freq = fa.rotary_inv_freq(128, device="cuda")[0]
+    pos = torch.arange(64, dtype=torch.int32, device="cuda")
+    a, b = (torch.zeros(64, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    src = torch.randn(64, 8, 128, device="cuda").bfloat16()
+    want = fa.rotary(src, pos, freq)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(40):
+        with torch.cuda.stream(main):
+            b.zero_()
+            fa.rotary(a, pos, freq, out=a)                 # the predecessor on the stream
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200000)
+            if i % 2:
+                b.copy_(src)
+            else:
+                fa.rotary(src, torch.zeros_like(pos), freq, out=b)   # position 0: a copy
+        main.wait_stream(side)
+        with torch.cuda.stream(main):
+            y = fa.rotary(b, pos, freq)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+
+
+def test_a_graph_with_branches_between_the_calls():
+    """Captured: a call, a branch on another stream that makes the input of the
+    next call, and that call after the join."""
+    fa = _fa()
+    freq = fa.rotary_inv_freq(128, device="cuda")[0]
+    pos = torch.arange(64, dtype=torch.int32, device="cuda")
+    src, a, b = (torch.randn(64, 8, 128, device="cuda").bfloat16() for _ in range(3))
+    zero = torch.zeros_like(pos)
+    fa.rotary(src, pos, freq)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.zero_()
+        fa.rotary(a, zero, freq, out=a)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100000)
+            fa.rotary(src, zero, freq, out=b)
+        fa.rotary(a, zero, freq, out=a)
+        torch.cuda.current_stream().wait_stream(side)
+        y = fa.rotary(b, pos, freq)
+        z = fa.rotary(y, pos, freq, inverse=True)
+    for _ in range(10):
+        src.copy_(torch.randn_like(src))
+        graph.replay()
+        want = fa.rotary(src, pos, freq)
+        assert torch.equal(y, want) and torch.equal(z, fa.rotary(want, pos, freq, inverse=True))
+
+
 def test_rotary_gradient_in_a_graph():
     fa = _fa()
     from exact_attention_91_gb300 import torch_op  # noqa: F401
