@@ -389,6 +389,7 @@ def load_binding():
         spec = importlib.util.spec_from_file_location("_fa_bind", BIND_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
+        module.setup(FaError, PageMaps)
         _bind = module
     return _bind
 
@@ -431,18 +432,15 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: fl
     need one each."""
     decode = (_bind or load_binding()).decode
     if stream is None:
-        r = decode(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse, return_lse, workspace)
-    else:
-        import torch
-        if out is None:
-            out, = _made_for(stream, (q.shape, torch.bfloat16), device=q.device)
-        if lse is None and return_lse:
-            lse, = _made_for(stream, (q.shape[:2], torch.float32), device=q.device)
-        r = _on_stream(stream, q.device, decode, q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale,
-                       out, lse, return_lse, workspace)
-    if type(r) is int:
-        raise FaError(r, "fa_decode_paged")
-    return r
+        return decode(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse, return_lse,
+                      workspace)
+    import torch
+    if out is None:
+        out, = _made_for(stream, (q.shape, torch.bfloat16), device=q.device)
+    if lse is None and return_lse:
+        lse, = _made_for(stream, (q.shape[:2], torch.float32), device=q.device)
+    return _on_stream(stream, q.device, decode, q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale,
+                      out, lse, return_lse, workspace)
 
 
 def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None, device=None):
@@ -509,14 +507,10 @@ def rotary(x, positions, inv_freq, interleaved: bool = False, inverse: bool = Fa
     itself: ``torch.ops.fa91.rotary`` is."""
     turn = (_bind or load_binding()).rotary
     if stream is None:
-        r = turn(x, positions, inv_freq, interleaved, inverse, factor, out)
-    else:
-        if out is None:
-            out, = _made_for(stream, (x.shape, x.dtype), device=x.device)
-        r = _on_stream(stream, x.device, turn, x, positions, inv_freq, interleaved, inverse, factor, out)
-    if type(r) is int:
-        raise FaError(r, "fa_rotary")
-    return r if out is None else out
+        return turn(x, positions, inv_freq, interleaved, inverse, factor, out)
+    if out is None:
+        out, = _made_for(stream, (x.shape, x.dtype), device=x.device)
+    return _on_stream(stream, x.device, turn, x, positions, inv_freq, interleaved, inverse, factor, out)
 
 
 def cache_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved: bool = False,
@@ -534,16 +528,12 @@ def cache_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interlea
     ``k_scale`` / ``v_scale`` fp32 [heads] (None: 1)."""
     append = (_bind or load_binding()).append
     if stream is None:
-        r = append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved, factor, k_scale, v_scale, q_out,
-                   k_out)
-    else:
-        if q_out is None:
-            q_out, = _made_for(stream, (q.shape, q.dtype), device=q.device)
-        r = _on_stream(stream, q.device, append, q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved,
-                       factor, k_scale, v_scale, q_out, k_out)
-    if type(r) is int:
-        raise FaError(r, "fa_cache_append")
-    return r if q_out is None else q_out
+        return append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved, factor, k_scale, v_scale,
+                      q_out, k_out)
+    if q_out is None:
+        q_out, = _made_for(stream, (q.shape, q.dtype), device=q.device)
+    return _on_stream(stream, q.device, append, q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved,
+                      factor, k_scale, v_scale, q_out, k_out)
 
 
 class PageMaps(typing.NamedTuple):
@@ -566,15 +556,10 @@ def page_maps(context_lens, new_lens, block_table, unused_blocks, page_size: int
     rest are padding: slot -1). See ``fa_page_maps`` in include/fa.h."""
     maps = (_bind or load_binding()).maps
     if stream is None:
-        r = maps(context_lens, new_lens, block_table, unused_blocks, page_size, num_tokens, out)
-    else:
-        import torch
-        if out is None:
-            B = block_table.shape[0]
-            out = PageMaps(*_made_for(stream, *(((n,), torch.int32) for n in (num_tokens, num_tokens, B + 1, B, 4)),
-                                      device=block_table.device))
-        r = _on_stream(stream, block_table.device, maps, context_lens, new_lens, block_table, unused_blocks, page_size,
-                       num_tokens, out)
-    if type(r) is int:
-        raise FaError(r, "fa_page_maps")
-    return tuple.__new__(PageMaps, r) if out is None else out
+        return maps(context_lens, new_lens, block_table, unused_blocks, page_size, num_tokens, out)
+    import torch
+    if out is None:
+        sizes = (num_tokens, num_tokens, block_table.shape[0] + 1, block_table.shape[0], 4)
+        out = PageMaps(*_made_for(stream, *(((n,), torch.int32) for n in sizes), device=block_table.device))
+    return _on_stream(stream, block_table.device, maps, context_lens, new_lens, block_table, unused_blocks, page_size,
+                      num_tokens, out)

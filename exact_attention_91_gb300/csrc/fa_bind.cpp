@@ -7,8 +7,8 @@
 // here 2-4 us. libfa.so itself stays free of torch types.
 //
 // Every function takes its arguments by position (the Python wrappers name and
-// document them) and returns tensors, or an int: the negative status of the C
-// call, for the wrapper to raise.
+// document them). A C call's negative status is raised as FaError; setup() hands
+// in that class, and PageMaps, the class of maps()'s result.
 #include <Python.h>
 
 #include <cmath>
@@ -30,6 +30,28 @@ int host_probe(int* device, int* sm_count);  // fa_host.h, without its CUDA head
 namespace {
 
 using at::Tensor;
+
+PyObject* g_error = nullptr;
+PyTypeObject* g_page_maps = nullptr;
+
+PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 2 || !PyType_Check(a[1]) || !PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(a[1]), &PyTuple_Type)) {
+        PyErr_SetString(PyExc_TypeError, "setup(FaError, PageMaps)");
+        return nullptr;
+    }
+    g_error = Py_NewRef(a[0]);
+    g_page_maps = reinterpret_cast<PyTypeObject*>(Py_NewRef(a[1]));
+    Py_RETURN_NONE;
+}
+
+PyObject* failed(long long status, const char* what) {
+    PyObject* e = PyObject_CallFunction(g_error, "Ls", status, what);
+    if (e) {
+        PyErr_SetObject(g_error, e);
+        Py_DECREF(e);
+    }
+    return nullptr;
+}
 
 // A tensor argument, or the type error.
 const Tensor& tensor(PyObject* o, const char* name) {
@@ -174,10 +196,10 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!ws.defined()) {
         int dev = 0, sms = 0;
         int rc = fa::host_probe(&dev, &sms);
-        if (rc != FA_OK) return PyLong_FromLong(rc);
+        if (rc != FA_OK) return failed(rc, "fa_decode_paged");
         const long long room = fa_decode_paged_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, cache.type,
                                                          cache.page_size, to_int(width), sms);
-        if (room < 0) return PyLong_FromLongLong(room);
+        if (room < 0) return failed(room, "fa_decode_paged");
         if (room > 0) ws = make({room}, at::kByte, q);
     }
     const int rc = fa_decode_paged(q.data_ptr(), &cache, static_cast<const int*>(table.data_ptr()),
@@ -185,7 +207,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    static_cast<float*>(ptr(lse)), to_int(B), to_int(Hq), to_int(width), table.stride(0),
                                    scale, ptr(ws), ws.defined() ? static_cast<size_t>(ws.numel()) : 0,
                                    c10::cuda::getCurrentCUDAStream(device.index()).stream());
-    if (rc != FA_OK) return PyLong_FromLong(rc);
+    if (rc != FA_OK) return failed(rc, "fa_decode_paged");
     return return_lse ? pair(std::move(out), std::move(lse)) : THPVariable_Wrap(std::move(out));
     END_HANDLE_TH_ERRORS
 }
@@ -223,7 +245,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              static_cast<const double*>(ptr(freq)), to_int(B), to_int(H), to_int(N), to_int(d), xs, ys,
                              each ? pos.stride(0) : 0, r, interleaved, inverse, static_cast<float>(factor),
                              c10::cuda::getCurrentCUDAStream(device.index()).stream());
-    if (rc != FA_OK) return PyLong_FromLong(rc);
+    if (rc != FA_OK) return failed(rc, "fa_rotary");
     return THPVariable_Wrap(std::move(out));
     END_HANDLE_TH_ERRORS
 }
@@ -272,13 +294,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    q_out.stride(0), k_out.defined() ? k_out.stride(0) : 0, to_int(T), to_int(Hq), r,
                                    interleaved, static_cast<float>(factor),
                                    c10::cuda::getCurrentCUDAStream(device.index()).stream());
-    if (rc != FA_OK) return PyLong_FromLong(rc);
+    if (rc != FA_OK) return failed(rc, "fa_cache_append");
     return THPVariable_Wrap(std::move(q_out));
     END_HANDLE_TH_ERRORS
 }
 
 // context_lens, new_lens, block_table, unused_blocks, page_size, num_tokens, out
-// (None or a sequence of five tensors). Returns a tuple of five.
+// (None or a PageMaps). Returns a PageMaps.
 PyObject* maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     arguments(n, 7);
@@ -332,9 +354,9 @@ PyObject* maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 p[1], p[2], p[3], p[4], to_int(B), to_int(width), table.stride(0),
                                 to_int(unused.numel()), to_int(page), to_int(T),
                                 c10::cuda::getCurrentCUDAStream(device.index()).stream());
-    if (rc != FA_OK) return PyLong_FromLong(rc);
+    if (rc != FA_OK) return failed(rc, "fa_page_maps");
     if (a[6] != Py_None) return Py_NewRef(a[6]);
-    PyObject* t = PyTuple_New(5);
+    PyObject* t = g_page_maps->tp_alloc(g_page_maps, 5);  // a named tuple: filled as one
     if (!t) throw python_error();
     for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(t, i, THPVariable_Wrap(std::move(out[i])));
     return t;
@@ -342,7 +364,8 @@ PyObject* maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define FA_FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
-PyMethodDef kMethods[] = {{"decode", FA_FAST(decode), METH_FASTCALL, nullptr},
+PyMethodDef kMethods[] = {{"setup", FA_FAST(setup), METH_FASTCALL, nullptr},
+                          {"decode", FA_FAST(decode), METH_FASTCALL, nullptr},
                           {"rotary", FA_FAST(rotary), METH_FASTCALL, nullptr},
                           {"append", FA_FAST(append), METH_FASTCALL, nullptr},
                           {"maps", FA_FAST(maps), METH_FASTCALL, nullptr},

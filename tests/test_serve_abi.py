@@ -271,6 +271,18 @@ def test_bad_python_page_map_calls(kw, error):
         fa.page_maps(**a)
 
 
+def test_statuses_are_raised_as_errors():
+    """A status of the C call becomes FaError with its code and text."""
+    bind = fa.load_binding()
+    assert fa.load_binding() is bind
+    with pytest.raises(TypeError):
+        bind.setup(1, 2)
+    if torch.cuda.is_available():
+        return
+    e = fa.FaError(-2, "fa_rotary")
+    assert e.status == -2 and "fa_rotary" in str(e) and fa.fa_strerror(-2) in str(e)
+
+
 def test_fake_implementations_give_shapes():
     from torch._subclasses.fake_tensor import FakeTensorMode
 

@@ -479,3 +479,31 @@ def test_a_capture_before_the_first_call_is_refused():
     env = dict(os.environ, PYTHONPATH=root + os.pathsep + os.environ.get("PYTHONPATH", ""))
     r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, env=env, timeout=300, cwd=root)
     assert r.returncode == 0 and "first-call-in-capture OK" in r.stdout, (r.stdout[-2000:], r.stderr[-3000:])
+
+
+def test_refusals_reach_python_as_errors():
+    """What only the C call refuses is raised with its status."""
+    fa = _fa()
+    from .test_decode_paged import make
+    x = make([5], 2, 1, 64, 16, seed=1)
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    freq = fa.rotary_inv_freq(24, device="cuda")[0]
+    cases = [
+        (-2, lambda: fa.rotary(x["q"], pos, freq)),                                     # 24 is no multiple of 16
+        (-9, lambda: fa.rotary(x["q"], pos, None, factor=float("nan"))),
+        (-9, lambda: fa.attention_decode_paged(x["q"], x["k"], x["v"], x["table"], x["lens"], scale=-1.0)),
+        (-10, lambda: fa.attention_decode_paged(x["q"], x["k"], x["v"], x["table"], x["lens"], out=x["q"])),
+        (-11, lambda: fa.attention_decode_paged(x["q"], x["k"], x["v"], x["table"].repeat(1, 9000), x["lens"],
+                                                workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))),
+        (-2, lambda: fa.cache_append(x["q"], x["q"][:, :1], x["q"][:, :1], pos, pos, None, x["k"][:, :9], x["v"][:, :9])),
+        (-2, lambda: fa.page_maps(pos, pos, x["table"], pos, 48, 0)),
+        (-10, lambda: fa.page_maps(pos, pos, x["table"], x["table"][0], 16, 0)),
+    ]
+    for status, f in cases:
+        with pytest.raises(fa.FaError) as e:
+            f()
+        assert e.value.status == status, (status, str(e.value))
+    with pytest.raises(ValueError):
+        fa.rotary(x["q"], pos.cpu(), None)                                              # another device
+    o, lse = fa.attention_decode_paged(x["q"], x["k"], x["v"], x["table"], x["lens"])   # and nothing is left behind
+    assert torch.isfinite(lse).all()
