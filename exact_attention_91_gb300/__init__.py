@@ -394,26 +394,20 @@ def load_binding():
     return _bind
 
 
-def _made_for(stream, *shapes_and_dtypes, device):
-    """Output tensors for a call on ``stream`` that is not the current one: they
-    belong to the current stream's part of the allocator, as those of any call
-    do, and are not handed out again while ``stream`` may still write them."""
-    import torch
-    out = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in shapes_and_dtypes]
-    for t in out:
-        if t.is_cuda:
-            t.record_stream(stream)
-    return out
-
-
 def _on_stream(stream, device, fn, *args):
-    """fn(*args) with ``stream`` as the current one (whose part of the allocator
-    a workspace then comes from)."""
+    """fn(*args) with ``stream`` as the current one. What the call allocates then
+    belongs to that stream's part of the allocator (memory that the current
+    stream's earlier work may still use is not written), and results are not
+    handed out again there while the current stream may still read them."""
     import torch
     if stream.device != device:
         raise ValueError("stream must be one of the tensors' device")
+    current = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
-        return fn(*args)
+        r = fn(*args)
+    for t in r if isinstance(r, tuple) else (r,):
+        t.record_stream(current)
+    return r
 
 
 def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None, k_scale=None,
@@ -434,11 +428,6 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: fl
     if stream is None:
         return decode(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse, return_lse,
                       workspace)
-    import torch
-    if out is None:
-        out, = _made_for(stream, (q.shape, torch.bfloat16), device=q.device)
-    if lse is None and return_lse:
-        lse, = _made_for(stream, (q.shape[:2], torch.float32), device=q.device)
     return _on_stream(stream, q.device, decode, q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale,
                       out, lse, return_lse, workspace)
 
@@ -508,8 +497,6 @@ def rotary(x, positions, inv_freq, interleaved: bool = False, inverse: bool = Fa
     turn = (_bind or load_binding()).rotary
     if stream is None:
         return turn(x, positions, inv_freq, interleaved, inverse, factor, out)
-    if out is None:
-        out, = _made_for(stream, (x.shape, x.dtype), device=x.device)
     return _on_stream(stream, x.device, turn, x, positions, inv_freq, interleaved, inverse, factor, out)
 
 
@@ -530,8 +517,6 @@ def cache_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interlea
     if stream is None:
         return append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved, factor, k_scale, v_scale,
                       q_out, k_out)
-    if q_out is None:
-        q_out, = _made_for(stream, (q.shape, q.dtype), device=q.device)
     return _on_stream(stream, q.device, append, q, k, v, positions, slots, inv_freq, k_cache, v_cache, interleaved,
                       factor, k_scale, v_scale, q_out, k_out)
 
@@ -557,9 +542,5 @@ def page_maps(context_lens, new_lens, block_table, unused_blocks, page_size: int
     maps = (_bind or load_binding()).maps
     if stream is None:
         return maps(context_lens, new_lens, block_table, unused_blocks, page_size, num_tokens, out)
-    import torch
-    if out is None:
-        sizes = (num_tokens, num_tokens, block_table.shape[0] + 1, block_table.shape[0], 4)
-        out = PageMaps(*_made_for(stream, *(((n,), torch.int32) for n in sizes), device=block_table.device))
     return _on_stream(stream, block_table.device, maps, context_lens, new_lens, block_table, unused_blocks, page_size,
                       num_tokens, out)

@@ -221,8 +221,9 @@ def test_graphs_replayed_on_two_streams_at_once():
 
 
 def test_calls_on_another_stream():
-    """stream=: work is ordered there, and what the call allocated is not handed
-    out again while that stream may still use it."""
+    """stream=: work is ordered there, what the call allocates is not memory that
+    the current stream's work still uses, and is not handed out again while
+    either stream may still use it."""
     fa = _fa()
     from .test_decode_paged import make
     x = make([4000, 900, 3333], 8, 2, 128, 16, seed=61)
@@ -246,6 +247,23 @@ def test_calls_on_another_stream():
     side.synchronize()
     for o, lse in kept:
         assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    del kept
+    for _ in range(10):
+        # memory freed on the current stream while its work is still to read it
+        held = torch.full_like(ref[0], 3.0)
+        torch.cuda._sleep(2000000)
+        seen = held.clone()
+        del held
+        o, lse = fa.attention_decode_paged(x["q"], x["k"], x["v"], x["table"], x["lens"], stream=side)
+        # a result that the current stream still reads when it is dropped
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(2000000)
+        o_seen = o.clone()
+        del o, lse
+        for _ in range(3):
+            p, _ = fa.attention_decode_paged(x["q"] * 2, x["k"], x["v"], x["table"], x["lens"], stream=side)
+        torch.cuda.synchronize()
+        assert (seen == 3).all() and torch.equal(o_seen, ref[0])
     pos = torch.arange(3, dtype=torch.int32, device="cuda")
     want = fa.rotary(x["q"], pos, freq)
     torch.cuda.synchronize()
