@@ -171,9 +171,9 @@ template <int KEYS>
 __device__ __forceinline__ bool decode_next(DecodeSeg& s, const DecodeParams& p, const DecodeWay& way) {
     do {
         if (s.rem <= 0) return false;
-        if (++s.u == way.units) {
+        if (++s.u >= way.units) {
             s.u = 0;
-            ++s.b;
+            if (++s.b >= p.B) return false;  // (only if the lengths changed under the launch)
             s.len = decode_len(p, s.b);
             s.nt = decode_tiles<KEYS>(s.len);
         }
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                 for (;; ++b) {
                     len = decode_len(p, b);
                     const long long n = static_cast<long long>(decode_tiles<C::kKeys>(len) + way.cost) * way.units;
-                    if (begin < at + n) break;
+                    if (begin < at + n || b + 1 >= b_hi) break;
                     at += n;
                 }
                 sh_b = b;
@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         const unsigned long long in = static_cast<unsigned long long>(begin - sh_begin);
         const unsigned unit = static_cast<unsigned>(seg.nt + way.cost);
         seg.u = static_cast<int>(in <= 0xffffffffu ? static_cast<unsigned>(in) / unit : in / unit);
+        seg.u = min(seg.u, way.units - 1);  // (no effect, here and in the join's description, unless lengths change)
         const int x = static_cast<int>(in - static_cast<unsigned long long>(seg.u) * unit);
         seg.rem = end - begin;
         decode_take(seg, x, way.cost);
@@ -363,11 +364,12 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             int4 m = make_int4(-1, 0, 0, 0);
             if (x > way.cost) {
                 const long long u0 = begin - x;  // first counted tile of the unit
-                const int first = decode_worker_of(total, workers, u0 + way.cost);
+                const int first = max(0, min(decode_worker_of(total, workers, u0 + way.cost), worker - 1));
+                const int last = decode_worker_of(total, workers, u0 + way.cost + seg.nt - 1);
                 m.x = seg.b;
                 m.y = seg.u;
                 m.z = decode_start(total, workers, first) >= u0 ? 2 * first : 2 * first + 1;
-                m.w = decode_worker_of(total, workers, u0 + way.cost + seg.nt - 1) * 8 + way.heads;
+                m.w = max(worker, min(last, workers - 1)) * 8 + way.heads;
             }
             p.meta[worker] = m;
         }

@@ -145,8 +145,9 @@ __global__ void __launch_bounds__(kMapsThreads) fa_page_maps_kernel(const MapsPa
     for (unsigned i = at; i < all_page; i += stride) {
         const int b = maps_find(first, p.B + 1, i);
         const unsigned held = (max(p.context_lens[b], 0) + (1u << p.page_shift) - 1) >> p.page_shift;
-        p.table[b * p.table_stride + held + (i - first[b])] =
-            i < static_cast<unsigned>(p.num_unused) ? p.unused[i] : -1;
+        const unsigned col = held + (i - first[b]);
+        if (col < static_cast<unsigned>(p.width))  // (always, unless the lengths change under the launch)
+            p.table[b * p.table_stride + col] = i < static_cast<unsigned>(p.num_unused) ? p.unused[i] : -1;
     }
     // ---- tokens
     for (unsigned t = at; t < static_cast<unsigned>(p.T); t += stride) {
