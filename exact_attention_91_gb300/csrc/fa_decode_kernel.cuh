@@ -498,7 +498,10 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
         for (int t = seg.t0 + way.off; t < seg.t1; t += way.step) {
             ptx::cp_async_wait<C::kStages - 2>();
             __syncwarp();
-            load(false);  // into the slot read in the previous step
+            // The next copies go into the slot read in the previous step: at once where a warp has few tiles and their
+            // latency counts (decode_short_d64 9.9 us; after the scores 10.3), behind the scores where HBM is the bound
+            // (decode_batch 155.2 us; at once 156.4).
+            if (CLUSTER) load(false);
             const uint32_t kt = ring + slot_out * C::kTileBytes, vt = kt + C::kHalfBytes;
             const uint32_t ok = ok_bits >> (slot_out * C::kGroups) & ((1u << C::kGroups) - 1);
             slot_out = slot_out + 1 == C::kStages ? 0 : slot_out + 1;
@@ -536,6 +539,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                         }
                     }
             }
+
+            if (!CLUSTER) load(false);
 
             // ---- mask, maximum, exponentials
             const int key0 = t * C::kKeys;
