@@ -792,11 +792,17 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             if (whole) return;
             __syncwarp();
             ptx::cluster_sync();
-            // element (row, c4) of the output is done by block (element % cluster)
-            const int rank = worker % p.cluster;
+            // element (row, c4) of the output is done by block (element % cluster); of a thread's, at most kMost
+            constexpr int kMost = (C::kRows * D / 4 + 2 * C::kThreads - 1) / (2 * C::kThreads);
+            const int rank = worker % p.cluster, all = rows * D / 4;
             const uint32_t o_at = ptx::smem_u32(smem), ml_at = ptx::smem_u32(stat + C::kWarps * 16);
-            for (int i = tid * p.cluster + rank; i < rows * D / 4; i += C::kThreads * p.cluster) {
-                const int row = i / (D / 4), c4 = i % (D / 4);
+            uint2 done[kMost];
+            float done_lse[kMost];
+#pragma unroll
+            for (int k = 0; k < kMost; ++k) {
+                const int i = (k * C::kThreads + tid) * p.cluster + rank;
+                if (i >= all) continue;
+                const int row = i / (D / 4);
                 // (all loads first: one takes some 250 cycles; past the cluster's size, one of it again)
                 float2 each[kDecodeCluster];
                 float4 x[kDecodeCluster];
@@ -821,13 +827,24 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                     o.x += x[w].x * f, o.y += x[w].y * f, o.z += x[w].z * f, o.w += x[w].w * f;
                 }
                 const float inv = l == 0.f ? 0.f : vs / l;
-                const long long out = row0 + row;
-                reinterpret_cast<uint2*>(p.o)[out * (D / 4) + c4] =
-                    make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
-                if (c4 == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+                done[k] = make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+                done_lse[k] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+            }
+            // No block exits before all have read its shared memory. The arrival releases: some of the loads above
+            // are of no one's use, so nothing else would wait for them. It comes before the stores, which it would
+            // wait for too.
+            __syncwarp();
+            ptx::cluster_arrive();
+#pragma unroll
+            for (int k = 0; k < kMost; ++k) {
+                const int i = (k * C::kThreads + tid) * p.cluster + rank;
+                if (i >= all) continue;
+                const int row = i / (D / 4), c4 = i % (D / 4);
+                reinterpret_cast<uint2*>(p.o)[(row0 + row) * (D / 4) + c4] = done[k];
+                if (c4 == 0 && p.lse) p.lse[row0 + row] = done_lse[k];
             }
             __syncwarp();
-            ptx::cluster_leave();  // the other blocks' shared memory is read until here
+            ptx::cluster_wait();
             return;
         }
         if (!decode_next<C::kKeys>(seg, p, way)) break;

@@ -8,13 +8,11 @@
 namespace fa {
 namespace ptx {
 
-// Cluster-wide barrier without memory ordering (the release of cluster_sync
-// waits for this thread's global stores): no CTA of the cluster exits before
-// all have come here.
-__device__ __forceinline__ void cluster_leave() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\t"
-                 "barrier.cluster.wait.aligned;" ::: "memory");
-}
+// The halves of cluster_sync: arrive releases this thread's earlier memory
+// operations (reads of other CTAs' shared memory among them), wait acquires the
+// others'.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float2 ld_dsmem_v2(uint32_t addr) {
     float2 v;
