@@ -264,6 +264,13 @@ __device__ __forceinline__ int decode_page(const DecodeParams& p, const DecodeSe
     return key < s.len ? p.table[s.b * p.table_stride + (key >> p.page_shift)] : -1;
 }
 
+// The upper bf16 halves of w (cut, not rounded); returns what is left, exactly.
+__device__ __forceinline__ float2 cut_bf16x2(float2 w, uint32_t& half) {
+    const uint32_t x = __float_as_uint(w.x), y = __float_as_uint(w.y);
+    half = __byte_perm(x, y, 0x7632);
+    return ptx::fadd2(w, make_float2(-__uint_as_float(x & 0xffff0000u), -__uint_as_float(y & 0xffff0000u)));
+}
+
 // CLUSTER: the small form. Block r of a cluster of p.cluster takes the r-th
 // share of one unit's tiles; the blocks' results are added up through
 // distributed shared memory.
@@ -590,11 +597,12 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                 }
             }
 
-            // ---- P in 16 bits, O += P V, 16 keys at a time. P = hi + lo, except for 16 rows of fp16: its 11 bits
-            // (2^-11 of each weight, against O's own 2^-8) cost nothing there, and the second half a fifth of the time
+            // ---- P in 16-bit parts, O += P V, 16 keys at a time. bf16: P = hi + mid + lo, the three bytes of its
+            // significand cut apart: exact. fp16: P = hi + lo, except for 16 rows: its 11 bits (2^-11 of each weight,
+            // against O's own 2^-8) cost nothing there, and the second half a fifth of the time
 #pragma unroll
             for (int kg = 0; kg < C::kGroups; ++kg) {
-                uint32_t hi[2 * R], lo[2 * R];  // [16-bit pairs of keys 2t4.. | 2t4+8..][row]
+                uint32_t hi[2 * R], mid[2 * R], lo[2 * R];  // [16-bit pairs of keys 2t4.. | 2t4+8..][row]
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -604,20 +612,29 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                                                     make_float2(-m_use[r], -m_use[r]));
                         const float2 w = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
                         sum[r] = ptx::fadd2(sum[r], w);
-                        uint32_t& h16 = hi[R * j + r];
-                        h16 = E4M3 ? ptx::pack_f16x2(w.x, w.y) : ptx::pack_bf16x2(w.x, w.y);
-                        if constexpr (!kOneP) {
-                            const float2 back = E4M3 ? ptx::unpack_f16x2(h16) : ptx::unpack_bf16x2(h16);
-                            const float2 rest = ptx::fadd2(w, make_float2(-back.x, -back.y));
-                            lo[R * j + r] = E4M3 ? ptx::pack_f16x2(rest.x, rest.y) : ptx::pack_bf16x2(rest.x, rest.y);
+                        const int i = R * j + r;
+                        if constexpr (!E4M3) {
+                            const float2 x2 = cut_bf16x2(w, hi[i]), x3 = cut_bf16x2(x2, mid[i]);
+                            cut_bf16x2(x3, lo[i]);
+                        } else {
+                            hi[i] = ptx::pack_f16x2(w.x, w.y);
+                            if constexpr (!kOneP) {
+                                const float2 back = ptx::unpack_f16x2(hi[i]);
+                                const float2 rest = ptx::fadd2(w, make_float2(-back.x, -back.y));
+                                lo[i] = ptx::pack_f16x2(rest.x, rest.y);
+                            }
                         }
                     }
                 auto pv = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
                     if constexpr (WIDE) {
                         ptx::mma_16816<E4M3>(c, hi[0], hi[1], hi[2], hi[3], b0, b1);
+                        if constexpr (!E4M3) ptx::mma_16816<E4M3>(c, mid[0], mid[1], mid[2], mid[3], b0, b1);
                         if constexpr (!kOneP) ptx::mma_16816<E4M3>(c, lo[0], lo[1], lo[2], lo[3], b0, b1);
-                    } else {
+                    } else if constexpr (E4M3) {
                         ptx::mma_16816<E4M3>(c, hi[0], lo[0], hi[1], lo[1], b0, b1);
+                    } else {
+                        ptx::mma_16816<E4M3>(c, hi[0], mid[0], hi[1], mid[1], b0, b1);
+                        ptx::mma_16816<E4M3>(c, lo[0], 0u, lo[1], 0u, b0, b1);
                     }
                 };
                 if constexpr (!E4M3) {

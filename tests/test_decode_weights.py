@@ -1,0 +1,102 @@
+"""How many bits a weight keeps on its way into P V of the paged decode. The
+values are made to cancel, so that O is next to nothing and what is left of it
+is the error of the weights, not bf16's rounding."""
+import math
+
+import numpy as np
+import pytest
+
+from . import serve_oracle as so
+from .test_decode_paged import _fa, call
+
+torch = pytest.importorskip("torch")
+
+LOG2E = np.float32(1.4426950408889634)
+
+
+def to_bf16(x):
+    return torch.as_tensor(np.asarray(x, np.float64)).bfloat16().double().numpy()
+
+
+def to_e4m3(x):
+    return torch.as_tensor(np.asarray(x, np.float64)).float().to(torch.float8_e4m3fn).float().double().numpy()
+
+
+def two_part_error(p, cut):
+    """Relative error of p (fp32) as the sum of two 16-bit values."""
+    hi = cut(p)
+    return (hi + cut(p - hi) - p) / p
+
+
+def pick(e4m3):
+    """Scores of a tile's keys: one above the others (weight 1), then keys whose
+    weights two bf16 parts (one fp16 part) give too large and too small by the
+    most, in turn, then keys to cancel with."""
+    grid = np.unique((to_e4m3 if e4m3 else to_bf16)(np.linspace(-0.7, -0.02, 4001)))
+    p = np.exp2(grid * float(LOG2E)).astype(np.float32).astype(np.float64)
+    if e4m3:
+        err = (p.astype(np.float16).astype(np.float64) - p) / p
+    else:
+        err = two_part_error(p, to_bf16)
+    order = np.argsort(err)
+    high, low = grid[order[::-1][:3]], grid[order[:3]]
+    return [0.0, *high, *low, -0.5, -0.25, -0.125, -0.375, -0.4375], err[order[-3]], err[order[2]]
+
+
+def cancelling_values(scores, d, cut):
+    """v [keys, d]: column by column one key of either kind, and four that take up
+    what their rounded values leave; 64-bit weights."""
+    p = np.exp(np.asarray(scores))
+    v = np.zeros((len(scores), d))
+    for c in range(d):
+        a, b = 1 + c % 3, 4 + c // 3 % 3
+        v[a, c] = cut(128.0 * (1 + (c % 8) / 8) * (-1) ** c)
+        left = p[a] * v[a, c]
+        for key in (b, 7, 8, 9, 10):
+            v[key, c] = cut(-left / p[key])
+            left += p[key] * v[key, c]
+    return v
+
+
+def test_the_chosen_keys_err():
+    """What the cases rest on: two bf16 parts lose 2^-18 of such a weight, one
+    fp16 part 2^-12; O cancels."""
+    for e4m3, size in ((False, 0.7 * 2.0 ** -18), (True, 0.7 * 2.0 ** -12)):
+        scores, high, low = pick(e4m3)
+        assert high > size and low < -size
+        v = cancelling_values(scores, 128, to_e4m3 if e4m3 else to_bf16)
+        p = np.exp(np.asarray(scores))
+        assert np.all(np.abs(p @ v) <= 2.0 ** -15 * (p @ np.abs(v)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e4m3", [False])
+@pytest.mark.parametrize("hq,width", [(1, None), (8, None), (9, None), (16, None), (20, None), (3, 5000), (16, 5000)])
+def test_weights_keep_the_bits_of_fp32(d, e4m3, hq, width):
+    """All keys are of one warp's tile. A weight is off by ex2's 2^-22, the
+    exponent's rounding (below 1 in size: 2^-25) and that of scale and log2 e
+    (2^-24); a tensor-core step's sum of 16 products by less than 2^-21 of the sum
+    of their magnitudes; so O by 2^-20 of A = softmax |v| in all, and by its own
+    rounding. (Two bf16 parts: 2^-18.4 of A; one fp16 part: 2^-12.4.)"""
+    fa = _fa()
+    cut = to_e4m3 if e4m3 else to_bf16
+    scores, _, _ = pick(e4m3)
+    n, t = len(scores), torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    k, v = torch.zeros(2, 16, 1, d), torch.zeros(2, 16, 1, d)
+    k[1, :n, 0, 0] = torch.tensor(scores)
+    v[1, :n, 0] = torch.from_numpy(cancelling_values(scores, d, cut)).float()
+    q = torch.zeros(1, hq, d)
+    q[:, :, 0] = 1.0
+    table = torch.full((1, width or 1), -1, dtype=torch.int32)
+    table[0, 0] = 1
+    x = dict(q=q.bfloat16().cuda(), k=k.to(t).cuda(), v=v.to(t).cuda(), table=table.cuda(),
+             lens=torch.tensor([n], dtype=torch.int32).cuda(), ks=None, vs=None)
+    o, lse = call(fa, x, scale=1.0)
+    o_ref, lse_ref, a, _ = so.decode(so.f64(x["q"]), so.f64(x["k"]), so.f64(x["v"]), table.numpy(), [n], 1.0)
+    assert np.all(so.BF16_HALF * np.abs(o_ref) <= 2.0 ** -22 * a)        # next to nothing
+    bound = 2.0 ** -20 * a + so.BF16_HALF * np.abs(o_ref)
+    off = np.abs(so.f64(o) - o_ref)
+    assert np.all(off <= bound), float((off / bound).max())
+    assert np.all(np.abs(so.f64(lse) - lse_ref) <= 2.0 ** -20)
+    assert math.isfinite(off.sum())
