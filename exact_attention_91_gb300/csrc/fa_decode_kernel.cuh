@@ -490,9 +490,11 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             if (cs[r] == 0.f) cs[r] = 1.17549435e-38f;  // (a scale of 0: every score is 0, or next to it)
         }
 
-        float acc[ND][4];
+        float2 acc[ND][R];  // columns 2·t4, 2·t4+1 of each 8-value column block
 #pragma unroll
-        for (int n = 0; n < ND; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+        for (int n = 0; n < ND; ++n)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[n][r] = make_float2(0.f, 0.f);
         float m_ref[R], m_use[R];  // reference maximum (-inf: no key yet), the one subtracted
         float2 sum[R];             // row sum, even and odd keys
 #pragma unroll
@@ -587,22 +589,20 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                     sum[r].y *= alpha;
 #pragma unroll
                     for (int n = 0; n < ND; ++n) {
-                        acc[n][2 * r] *= alpha;
-                        acc[n][2 * r + 1] *= alpha;
-                        if constexpr (!WIDE) {
-                            acc[n][2] *= alpha;
-                            acc[n][3] *= alpha;
-                        }
+                        acc[n][r].x *= alpha;
+                        acc[n][r].y *= alpha;
                     }
                 }
             }
 
-            // ---- P in 16-bit parts, O += P V, 16 keys at a time. bf16: P = hi + mid + lo, the three bytes of its
-            // significand cut apart: exact. fp16: P = hi + lo, except for 16 rows: its 11 bits (2^-11 of each weight,
-            // against O's own 2^-8) cost nothing there, and the second half a fifth of the time
+            // ---- P in 16-bit parts. bf16: P = hi + mid + lo, the three bytes of its significand cut apart: exact.
+            // fp16: P = hi + lo, except for 16 rows: its 11 bits (2^-11 of each weight, against O's own 2^-8) cost
+            // nothing there, and the second half a fifth of the time
+            uint32_t hi[C::kGroups][2 * R], mid[C::kGroups][2 * R], lo[C::kGroups][2 * R];  // [pairs of keys 2t4.. |
+                                                                                           // 2t4+8..][row]
+            float2 part[R];  // the tile's sum: added to the row's at once
 #pragma unroll
-            for (int kg = 0; kg < C::kGroups; ++kg) {
-                uint32_t hi[2 * R], mid[2 * R], lo[2 * R];  // [16-bit pairs of keys 2t4.. | 2t4+8..][row]
+            for (int kg = 0; kg < C::kGroups; ++kg)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -611,79 +611,107 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                         const float2 e = ptx::ffma2(make_float2(x[2 * r], x[2 * r + 1]), make_float2(cs[r], cs[r]),
                                                     make_float2(-m_use[r], -m_use[r]));
                         const float2 w = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
-                        sum[r] = ptx::fadd2(sum[r], w);
+                        part[r] = kg + j == 0 ? w : ptx::fadd2(part[r], w);
                         const int i = R * j + r;
                         if constexpr (!E4M3) {
-                            const float2 x2 = cut_bf16x2(w, hi[i]), x3 = cut_bf16x2(x2, mid[i]);
-                            cut_bf16x2(x3, lo[i]);
+                            const float2 x2 = cut_bf16x2(w, hi[kg][i]), x3 = cut_bf16x2(x2, mid[kg][i]);
+                            cut_bf16x2(x3, lo[kg][i]);
                         } else {
-                            hi[i] = ptx::pack_f16x2(w.x, w.y);
+                            hi[kg][i] = ptx::pack_f16x2(w.x, w.y);
                             if constexpr (!kOneP) {
-                                const float2 back = ptx::unpack_f16x2(hi[i]);
+                                const float2 back = ptx::unpack_f16x2(hi[kg][i]);
                                 const float2 rest = ptx::fadd2(w, make_float2(-back.x, -back.y));
-                                lo[i] = ptx::pack_f16x2(rest.x, rest.y);
+                                lo[kg][i] = ptx::pack_f16x2(rest.x, rest.y);
                             }
                         }
                     }
-                auto pv = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
-                    if constexpr (WIDE) {
-                        ptx::mma_16816<E4M3>(c, hi[0], hi[1], hi[2], hi[3], b0, b1);
-                        if constexpr (!E4M3) ptx::mma_16816<E4M3>(c, mid[0], mid[1], mid[2], mid[3], b0, b1);
-                        if constexpr (!kOneP) ptx::mma_16816<E4M3>(c, lo[0], lo[1], lo[2], lo[3], b0, b1);
-                    } else if constexpr (E4M3) {
-                        ptx::mma_16816<E4M3>(c, hi[0], lo[0], hi[1], lo[1], b0, b1);
-                    } else {
-                        ptx::mma_16816<E4M3>(c, hi[0], mid[0], hi[1], mid[1], b0, b1);
-                        ptx::mma_16816<E4M3>(c, lo[0], 0u, lo[1], 0u, b0, b1);
-                    }
-                };
-                if constexpr (!E4M3) {
+
 #pragma unroll
-                    for (int n = 0; n < ND; n += 2) {
+            for (int r = 0; r < R; ++r) sum[r] = ptx::fadd2(sum[r], part[r]);
+
+            // ---- O += P V. The tensor core adds up a tile's keys, starting from zero, and the tiles are added here: its
+            // sums are cut towards zero, not rounded (over 800 tiles O lost 2^-14 of itself)
+            auto pv = [&](float(&c)[4], int kg, uint32_t b0, uint32_t b1) {
+                auto mma = [&](bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                    if (first)
+                        ptx::mma_16816_from_zero<E4M3>(c, a0, a1, a2, a3, b0, b1);
+                    else
+                        ptx::mma_16816<E4M3>(c, a0, a1, a2, a3, b0, b1);
+                };
+                const uint32_t(&p0)[2 * R] = hi[kg], (&p1)[2 * R] = mid[kg], (&p2)[2 * R] = lo[kg];
+                if constexpr (WIDE) {
+                    mma(kg == 0, p0[0], p0[1], p0[2], p0[3]);
+                    if constexpr (!E4M3) mma(false, p1[0], p1[1], p1[2], p1[3]);
+                    if constexpr (!kOneP) mma(false, p2[0], p2[1], p2[2], p2[3]);
+                } else if constexpr (E4M3) {
+                    mma(kg == 0, p0[0], p2[0], p0[1], p2[1]);
+                } else {
+                    mma(kg == 0, p0[0], p1[0], p0[1], p1[1]);
+                    mma(false, p2[0], 0u, p2[1], 0u);
+                }
+            };
+            auto add = [&](int n, const float(&c)[4]) {
+                const float2 c0 = make_float2(c[0], c[1]), c1 = make_float2(c[2], c[3]);
+                if constexpr (WIDE) {
+                    acc[n][0] = ptx::fadd2(acc[n][0], c0);
+                    acc[n][R - 1] = ptx::fadd2(acc[n][R - 1], c1);
+                } else {
+                    acc[n][0] = ptx::fadd2(acc[n][0], ptx::fadd2(c0, c1));
+                }
+            };
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int n = 0; n < ND; n += 2) {
+                    float c0[4], c1[4];
+#pragma unroll
+                    for (int kg = 0; kg < C::kGroups; ++kg) {
                         uint32_t b[4];
                         ptx::ldmatrix_x4_trans(
                             b, vt + decode_chunk<D, E4M3>(kg * 16 + (lane & 7) + (lane >> 3 & 1) * 8, n + (lane >> 4)));
-                        pv(acc[n], b[0], b[1]);
-                        pv(acc[n + 1], b[2], b[3]);
+                        pv(c0, kg, b[0], b[1]);
+                        pv(c1, kg, b[2], b[3]);
                     }
-                } else {
-                    // lane (g, t4) reads D/8 values, from column g·D/8 on, of keys 2t4, 2t4+1, 2t4+8, 2t4+9
-                    uint32_t w[4][D / 32];
+                    add(n, c0);
+                    add(n + 1, c1);
+                }
+            } else {
+                // lane (g, t4) reads D/8 values, from column g·D/8 on, of keys 2t4, 2t4+1, 2t4+8, 2t4+9
+                uint32_t w[C::kGroups][4][D / 32];
+#pragma unroll
+                for (int kg = 0; kg < C::kGroups; ++kg)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = kg * 16 + 2 * t4 + (i & 1) + (i >> 1) * 8;
                         if constexpr (D == 128) {
                             const uint4 x = ptx::lds128(vt + decode_chunk<D, E4M3>(r, g));
-                            w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                            w[kg][i][0] = x.x, w[kg][i][1] = x.y, w[kg][i][2] = x.z, w[kg][i][3] = x.w;
                         } else {
                             const uint2 x = ptx::lds64(vt + decode_chunk<D, E4M3>(r, g >> 1) + (g & 1) * 8);
-                            w[i][0] = x.x, w[i][1] = x.y;
+                            w[kg][i][0] = x.x, w[kg][i][1] = x.y;
                         }
                     }
 #pragma unroll
-                    for (int n = 0; n < ND; n += 2) {
+                for (int n = 0; n < ND; n += 2) {
+                    float c0[4], c1[4];
+#pragma unroll
+                    for (int kg = 0; kg < C::kGroups; ++kg) {
                         // bytes (key a, key b) of values n, n + 1
                         const uint32_t sel = n % 4 == 0 ? 0x5140u : 0x7362u;
-                        const uint32_t x = __byte_perm(w[0][n / 4], w[1][n / 4], sel);
-                        const uint32_t y = __byte_perm(w[2][n / 4], w[3][n / 4], sel);
-                        pv(acc[n], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x)),
+                        const uint32_t x = __byte_perm(w[kg][0][n / 4], w[kg][1][n / 4], sel);
+                        const uint32_t y = __byte_perm(w[kg][2][n / 4], w[kg][3][n / 4], sel);
+                        pv(c0, kg, ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x)),
                            ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(y)));
-                        pv(acc[n + 1], ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16)),
+                        pv(c1, kg, ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16)),
                            ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(y >> 16)));
                     }
+                    add(n, c0);
+                    add(n + 1, c1);
                 }
             }
         }
 
         // ---- the result of the warp, in rows g (and g + 8): O relative to 2^m, the reference m, the sum
         float2 ml[R];
-        if constexpr (!WIDE) {
-#pragma unroll
-            for (int n = 0; n < ND; ++n) {
-                acc[n][0] += acc[n][2];
-                acc[n][1] += acc[n][3];
-            }
-        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float l = sum[r].x + sum[r].y;
@@ -692,6 +720,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             // (a sum of zero: no key, or scores of -inf alone; NaN is no zero and is passed on)
             ml[r] = make_float2(l == 0.f ? -INFINITY : m_use[r], l);
         }
+        auto of = [](const float2& x, int j) { return j ? x.y : x.x; };
         const bool whole = CLUSTER ? p.cluster == 1 : seg.t0 == 0 && seg.t1 == seg.nt;
         const long long slot = 2LL * worker + (first_seg ? 0 : 1);
         const float vs = p.v_scale ? p.v_scale[h] : 1.f;
@@ -717,8 +746,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                         // e4m3: four values of one column block; bf16: two values each of columns n.., n + 2..
                         if constexpr (E4M3) {
                             const int c4 = ((2 * t4 + j) * ND + n) / 4;
-                            const float x[4] = {acc[n][2 * r + j] * f, acc[n + 1][2 * r + j] * f,
-                                                acc[n + 2][2 * r + j] * f, acc[n + 3][2 * r + j] * f};
+                            const float x[4] = {of(acc[n][r], j) * f, of(acc[n + 1][r], j) * f,
+                                                of(acc[n + 2][r], j) * f, of(acc[n + 3][r], j) * f};
                             if (whole)
                                 reinterpret_cast<uint2*>(p.o)[out * (D / 4) + c4] =
                                     make_uint2(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]));
@@ -729,7 +758,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const int nn = n + 2 * j + i, c2 = nn * 4 + t4;
-                                const float x0 = acc[nn][2 * r] * f, x1 = acc[nn][2 * r + 1] * f;
+                                const float x0 = acc[nn][r].x * f, x1 = acc[nn][r].y * f;
                                 if (whole)
                                     reinterpret_cast<uint32_t*>(p.o)[out * (D / 2) + c2] = ptx::pack_bf16x2(x0, x1);
                                 else
@@ -761,13 +790,12 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
 #pragma unroll
                     for (int n = 0; n < ND; n += 4)
                         mrow[merge_col<D, E4M3>(g, ((2 * t4 + j) * ND + n) / 4)] =
-                            make_float4(acc[n][2 * r + j], acc[n + 1][2 * r + j], acc[n + 2][2 * r + j],
-                                        acc[n + 3][2 * r + j]);
+                            make_float4(of(acc[n][r], j), of(acc[n + 1][r], j), of(acc[n + 2][r], j),
+                                        of(acc[n + 3][r], j));
             } else {
 #pragma unroll
                 for (int n = 0; n < ND; ++n)
-                    reinterpret_cast<float2*>(mrow + merge_col<D, E4M3>(g, 2 * n + t4 / 2))[t4 & 1] =
-                        make_float2(acc[n][2 * r], acc[n][2 * r + 1]);
+                    reinterpret_cast<float2*>(mrow + merge_col<D, E4M3>(g, 2 * n + t4 / 2))[t4 & 1] = acc[n][r];
             }
             __syncthreads();
             for (int i = tid; i < 8 * D / 4; i += C::kThreads) {

@@ -100,3 +100,44 @@ def test_weights_keep_the_bits_of_fp32(d, e4m3, hq, width):
     assert np.all(off <= bound), float((off / bound).max())
     assert np.all(np.abs(so.f64(lse) - lse_ref) <= 2.0 ** -20)
     assert math.isfinite(off.sum())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 1), (16, 1), (64, 4)])
+def test_long_sums_are_rounded_not_cut(d, e4m3, hq, hkv):
+    """v is 1 for the first half of 16384 keys and -1 for the second, which has the
+    same scores in another order: O is 0, and the sum on its way there climbs to
+    half of A = 1 (times the keys' weight) and comes back. As many requests as blocks,
+    so that each takes a whole one. Rounded to nearest, at most 1024 additions
+    are off by 2^-25 of A each (half a step of a sum below A/2) in either direction:
+    2^-21.8 at one sigma of their uniform errors, here 2^-19 (seven). Cut towards
+    zero, one step of a matrix instruction loses 2^-25 in the mean, always of the
+    same sign: 2^-15 of A and more.
+
+    LSE: a lane adds up its tiles' sums one after the other, each addition off by at
+    most 2^-24 of a sum that is half of the last one in the mean, so by tiles·2^-25
+    in all; the tile's own sum, the exponential, the logarithm and the rounding of an
+    LSE below 16 make up less than 2^-20."""
+    fa = _fa()
+    n, page = 16384, 64
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator().manual_seed(d + hq)
+    half = torch.rand(n // 2, generator=g) * -0.7
+    scores = torch.cat((half, half[torch.randperm(n // 2, generator=g)]))
+    t = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    k, v = torch.zeros(n, hkv, d), torch.ones(n, hkv, d)
+    k[:, :, 0] = scores[:, None].bfloat16().float()
+    v[n // 2:] = -1.0
+    k, v = (x.view(n // page, page, hkv, d).to(t).cuda() for x in (k, v))
+    q = torch.zeros(B, hq, d)
+    q[:, :, 0] = 1.0
+    table = torch.arange(n // page, dtype=torch.int32).expand(B, -1).contiguous()       # all over the same pages
+    x = dict(q=q.bfloat16().cuda(), k=k, v=v, table=table.cuda(), lens=torch.full((B,), n, dtype=torch.int32).cuda(),
+             ks=None, vs=None)
+    o, lse = call(fa, x, scale=1.0)
+    assert o.float().abs().max().item() <= 2.0 ** -19
+    s = so.f64(k).reshape(n, hkv, d)[:, 0, 0]
+    tiles = n * d * k.element_size() // 4096
+    assert np.abs(so.f64(lse) - math.log(np.exp(s).sum())).max() <= tiles * 2.0 ** -25 + 2.0 ** -20
