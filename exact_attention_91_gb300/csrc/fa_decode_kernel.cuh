@@ -35,10 +35,10 @@
 //    would want 128 rows (heads) or a softmax across TMEM lanes, for flops that
 //    are not the bound (the tensor pipe is busy 19% of the time with 4 query
 //    heads per key head, 37% with 8 on an e4m3 cache). With at most 8 heads the
-//    tile's rows 8-15 carry the rounding remainder of P: p = hi + lo, both 16
-//    bits, so P·V keeps about 16 (bf16) or 22 (fp16) bits of p at no extra
-//    instruction. (9 to 16 heads: a second instruction in bf16; none in fp16,
-//    where p keeps 11 bits.)
+//    tile's rows 8-15 carry a second part of P. A weight has as many bits as in
+//    fp32: bf16 in three parts (exact, at a second instruction for the third),
+//    fp16 in two (22 bits and rounding). With 9 to 16 heads every part is an
+//    instruction (64 requests, 64/4 heads, e4m3: 66.3 us; one part: 60.7).
 //  * e4m3 caches are widened to fp16 (exact) in registers; q is scaled by a
 //    power of two per head into fp16's range (exact but for values 2^-14
 //    below the head's largest, whose low bits are below 2^-24 of it).
@@ -281,7 +281,6 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     constexpr int ND = D / 8;         // output columns, 8 values each
     constexpr int KS = D / 16;        // steps of 16 of q·k
     constexpr int R = WIDE ? 2 : 1;   // query rows of a lane: g (and g + 8)
-    constexpr bool kOneP = WIDE && E4M3;  // P without its remainder
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long sh_warp[C::kWarps];
     __shared__ long long sh_begin;
@@ -595,119 +594,119 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                 }
             }
 
-            // ---- P in 16-bit parts. bf16: P = hi + mid + lo, the three bytes of its significand cut apart: exact.
-            // fp16: P = hi + lo, except for 16 rows: its 11 bits (2^-11 of each weight, against O's own 2^-8) cost
-            // nothing there, and the second half a fifth of the time
-            uint32_t hi[C::kGroups][2 * R], mid[C::kGroups][2 * R], lo[C::kGroups][2 * R];  // [pairs of keys 2t4.. |
-                                                                                           // 2t4+8..][row]
-            float2 part[R];  // the tile's sum: added to the row's at once
+            // ---- P in 16-bit parts, O += P V. bf16: P = hi + mid + lo, the three bytes of its significand cut apart: exact.
+            // fp16: P = hi + lo, 22 bits.
+            // The tensor core adds up a tile's keys (or 16 of them, where registers are short), starting from zero,
+            // and these sums are added here: its own are cut towards zero, not rounded (over 800 tiles O lost 2^-14
+            // of itself)
+            // (one request of 1000 keys, 64/4 heads, e4m3, d 128: 7.8 us; a tile's two groups at once spill: 8.4)
+            constexpr int kSum = WIDE && E4M3 && D == 128 ? 1 : C::kGroups;
+            float2 part[R];  // the tile's row sum
 #pragma unroll
-            for (int kg = 0; kg < C::kGroups; ++kg)
+            for (int k0 = 0; k0 < C::kGroups; k0 += kSum) {
+                uint32_t hi[kSum][2 * R], mid[kSum][2 * R], lo[kSum][2 * R];  // [pairs of keys 2t4.. | 2t4+8..][row]
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int kg = 0; kg < kSum; ++kg)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float(&x)[4] = s[2 * kg + j];
-                        const float2 e = ptx::ffma2(make_float2(x[2 * r], x[2 * r + 1]), make_float2(cs[r], cs[r]),
-                                                    make_float2(-m_use[r], -m_use[r]));
-                        const float2 w = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
-                        part[r] = kg + j == 0 ? w : ptx::fadd2(part[r], w);
-                        const int i = R * j + r;
-                        if constexpr (!E4M3) {
-                            const float2 x2 = cut_bf16x2(w, hi[kg][i]), x3 = cut_bf16x2(x2, mid[kg][i]);
-                            cut_bf16x2(x3, lo[kg][i]);
-                        } else {
-                            hi[kg][i] = ptx::pack_f16x2(w.x, w.y);
-                            if constexpr (!kOneP) {
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float(&x)[4] = s[2 * (k0 + kg) + j];
+                            const float2 e = ptx::ffma2(make_float2(x[2 * r], x[2 * r + 1]), make_float2(cs[r], cs[r]),
+                                                        make_float2(-m_use[r], -m_use[r]));
+                            const float2 w = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
+                            part[r] = k0 + kg + j == 0 ? w : ptx::fadd2(part[r], w);
+                            const int i = R * j + r;
+                            if constexpr (!E4M3) {
+                                const float2 x2 = cut_bf16x2(w, hi[kg][i]), x3 = cut_bf16x2(x2, mid[kg][i]);
+                                cut_bf16x2(x3, lo[kg][i]);
+                            } else {
+                                hi[kg][i] = ptx::pack_f16x2(w.x, w.y);
                                 const float2 back = ptx::unpack_f16x2(hi[kg][i]);
                                 const float2 rest = ptx::fadd2(w, make_float2(-back.x, -back.y));
                                 lo[kg][i] = ptx::pack_f16x2(rest.x, rest.y);
                             }
                         }
+                auto pv = [&](float(&c)[4], int kg, uint32_t b0, uint32_t b1) {
+                    auto mma = [&](bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                        if (first)
+                            ptx::mma_16816_from_zero<E4M3>(c, a0, a1, a2, a3, b0, b1);
+                        else
+                            ptx::mma_16816<E4M3>(c, a0, a1, a2, a3, b0, b1);
+                    };
+                    const uint32_t(&p0)[2 * R] = hi[kg], (&p1)[2 * R] = mid[kg], (&p2)[2 * R] = lo[kg];
+                    if constexpr (WIDE) {
+                        mma(kg == 0, p0[0], p0[1], p0[2], p0[3]);
+                        if constexpr (!E4M3) mma(false, p1[0], p1[1], p1[2], p1[3]);
+                        mma(false, p2[0], p2[1], p2[2], p2[3]);
+                    } else if constexpr (E4M3) {
+                        mma(kg == 0, p0[0], p2[0], p0[1], p2[1]);
+                    } else {
+                        mma(kg == 0, p0[0], p1[0], p0[1], p1[1]);
+                        mma(false, p2[0], 0u, p2[1], 0u);
                     }
-
-#pragma unroll
-            for (int r = 0; r < R; ++r) sum[r] = ptx::fadd2(sum[r], part[r]);
-
-            // ---- O += P V. The tensor core adds up a tile's keys, starting from zero, and the tiles are added here: its
-            // sums are cut towards zero, not rounded (over 800 tiles O lost 2^-14 of itself)
-            auto pv = [&](float(&c)[4], int kg, uint32_t b0, uint32_t b1) {
-                auto mma = [&](bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-                    if (first)
-                        ptx::mma_16816_from_zero<E4M3>(c, a0, a1, a2, a3, b0, b1);
-                    else
-                        ptx::mma_16816<E4M3>(c, a0, a1, a2, a3, b0, b1);
                 };
-                const uint32_t(&p0)[2 * R] = hi[kg], (&p1)[2 * R] = mid[kg], (&p2)[2 * R] = lo[kg];
-                if constexpr (WIDE) {
-                    mma(kg == 0, p0[0], p0[1], p0[2], p0[3]);
-                    if constexpr (!E4M3) mma(false, p1[0], p1[1], p1[2], p1[3]);
-                    if constexpr (!kOneP) mma(false, p2[0], p2[1], p2[2], p2[3]);
-                } else if constexpr (E4M3) {
-                    mma(kg == 0, p0[0], p2[0], p0[1], p2[1]);
-                } else {
-                    mma(kg == 0, p0[0], p1[0], p0[1], p1[1]);
-                    mma(false, p2[0], 0u, p2[1], 0u);
-                }
-            };
-            auto add = [&](int n, const float(&c)[4]) {
-                const float2 c0 = make_float2(c[0], c[1]), c1 = make_float2(c[2], c[3]);
-                if constexpr (WIDE) {
-                    acc[n][0] = ptx::fadd2(acc[n][0], c0);
-                    acc[n][R - 1] = ptx::fadd2(acc[n][R - 1], c1);
-                } else {
-                    acc[n][0] = ptx::fadd2(acc[n][0], ptx::fadd2(c0, c1));
-                }
-            };
-            if constexpr (!E4M3) {
-#pragma unroll
-                for (int n = 0; n < ND; n += 2) {
-                    float c0[4], c1[4];
-#pragma unroll
-                    for (int kg = 0; kg < C::kGroups; ++kg) {
-                        uint32_t b[4];
-                        ptx::ldmatrix_x4_trans(
-                            b, vt + decode_chunk<D, E4M3>(kg * 16 + (lane & 7) + (lane >> 3 & 1) * 8, n + (lane >> 4)));
-                        pv(c0, kg, b[0], b[1]);
-                        pv(c1, kg, b[2], b[3]);
+                auto add = [&](int n, const float(&c)[4]) {
+                    const float2 c0 = make_float2(c[0], c[1]), c1 = make_float2(c[2], c[3]);
+                    if constexpr (WIDE) {
+                        acc[n][0] = ptx::fadd2(acc[n][0], c0);
+                        acc[n][R - 1] = ptx::fadd2(acc[n][R - 1], c1);
+                    } else {
+                        acc[n][0] = ptx::fadd2(acc[n][0], ptx::fadd2(c0, c1));
                     }
-                    add(n, c0);
-                    add(n + 1, c1);
-                }
-            } else {
-                // lane (g, t4) reads D/8 values, from column g·D/8 on, of keys 2t4, 2t4+1, 2t4+8, 2t4+9
-                uint32_t w[C::kGroups][4][D / 32];
+                };
+                if constexpr (!E4M3) {
 #pragma unroll
-                for (int kg = 0; kg < C::kGroups; ++kg)
+                    for (int n = 0; n < ND; n += 2) {
+                        float c0[4], c1[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = kg * 16 + 2 * t4 + (i & 1) + (i >> 1) * 8;
-                        if constexpr (D == 128) {
-                            const uint4 x = ptx::lds128(vt + decode_chunk<D, E4M3>(r, g));
-                            w[kg][i][0] = x.x, w[kg][i][1] = x.y, w[kg][i][2] = x.z, w[kg][i][3] = x.w;
-                        } else {
-                            const uint2 x = ptx::lds64(vt + decode_chunk<D, E4M3>(r, g >> 1) + (g & 1) * 8);
-                            w[kg][i][0] = x.x, w[kg][i][1] = x.y;
+                        for (int kg = 0; kg < kSum; ++kg) {
+                            const int row = (k0 + kg) * 16 + (lane & 7) + (lane >> 3 & 1) * 8;
+                            uint32_t b[4];
+                            ptx::ldmatrix_x4_trans(b, vt + decode_chunk<D, E4M3>(row, n + (lane >> 4)));
+                            pv(c0, kg, b[0], b[1]);
+                            pv(c1, kg, b[2], b[3]);
                         }
+                        add(n, c0);
+                        add(n + 1, c1);
                     }
+                } else {
+                    // lane (g, t4) reads D/8 values, from column g·D/8 on, of keys 2t4, 2t4+1, 2t4+8, 2t4+9
+                    uint32_t w[kSum][4][D / 32];
 #pragma unroll
-                for (int n = 0; n < ND; n += 2) {
-                    float c0[4], c1[4];
+                    for (int kg = 0; kg < kSum; ++kg)
 #pragma unroll
-                    for (int kg = 0; kg < C::kGroups; ++kg) {
-                        // bytes (key a, key b) of values n, n + 1
-                        const uint32_t sel = n % 4 == 0 ? 0x5140u : 0x7362u;
-                        const uint32_t x = __byte_perm(w[kg][0][n / 4], w[kg][1][n / 4], sel);
-                        const uint32_t y = __byte_perm(w[kg][2][n / 4], w[kg][3][n / 4], sel);
-                        pv(c0, kg, ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x)),
-                           ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(y)));
-                        pv(c1, kg, ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16)),
-                           ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(y >> 16)));
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = (k0 + kg) * 16 + 2 * t4 + (i & 1) + (i >> 1) * 8;
+                            if constexpr (D == 128) {
+                                const uint4 x = ptx::lds128(vt + decode_chunk<D, E4M3>(row, g));
+                                w[kg][i][0] = x.x, w[kg][i][1] = x.y, w[kg][i][2] = x.z, w[kg][i][3] = x.w;
+                            } else {
+                                const uint2 x = ptx::lds64(vt + decode_chunk<D, E4M3>(row, g >> 1) + (g & 1) * 8);
+                                w[kg][i][0] = x.x, w[kg][i][1] = x.y;
+                            }
+                        }
+#pragma unroll
+                    for (int n = 0; n < ND; n += 2) {
+                        float c0[4], c1[4];
+#pragma unroll
+                        for (int kg = 0; kg < kSum; ++kg) {
+                            // bytes (key a, key b) of values n, n + 1
+                            const uint32_t sel = n % 4 == 0 ? 0x5140u : 0x7362u;
+                            const uint32_t x = __byte_perm(w[kg][0][n / 4], w[kg][1][n / 4], sel);
+                            const uint32_t y = __byte_perm(w[kg][2][n / 4], w[kg][3][n / 4], sel);
+                            pv(c0, kg, ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x)),
+                               ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(y)));
+                            pv(c1, kg, ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16)),
+                               ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(y >> 16)));
+                        }
+                        add(n, c0);
+                        add(n + 1, c1);
                     }
-                    add(n, c0);
-                    add(n + 1, c1);
                 }
             }
+#pragma unroll
+            for (int r = 0; r < R; ++r) sum[r] = ptx::fadd2(sum[r], part[r]);
         }
 
         // ---- the result of the warp, in rows g (and g + 8): O relative to 2^m, the reference m, the sum

@@ -71,7 +71,7 @@ def test_the_chosen_keys_err():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("e4m3", [False])
+@pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("hq,width", [(1, None), (8, None), (9, None), (16, None), (20, None), (3, 5000), (16, 5000)])
 def test_weights_keep_the_bits_of_fp32(d, e4m3, hq, width):
     """All keys are of one warp's tile. A weight is off by ex2's 2^-22, the
