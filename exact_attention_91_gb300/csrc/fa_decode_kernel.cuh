@@ -38,7 +38,7 @@
 //    tile's rows 8-15 carry a second part of P. A weight has as many bits as in
 //    fp32: bf16 in three parts (exact, at a second instruction for the third),
 //    fp16 in two (22 bits and rounding). With 9 to 16 heads every part is an
-//    instruction (64 requests, 64/4 heads, e4m3: 66.3 us; one part: 60.7).
+//    instruction (64 requests, 64/4 heads, e4m3: 69.4 us; one part: 60.7).
 //  * e4m3 caches are widened to fp16 (exact) in registers; q is scaled by a
 //    power of two per head into fp16's range (exact but for values 2^-14
 //    below the head's largest, whose low bits are below 2^-24 of it).
@@ -99,10 +99,11 @@ struct DecodeCfg {
     static constexpr int kOffMerge = kWarps * kStages * kTileBytes;  // fp32 [warp][8][D]
     static constexpr int kOffStat = kOffMerge + kWarps * 8 * D * 4;  // float2 [warp][16], and the block's [16]
     static constexpr int kSmemBytes = kOffStat + (kWarps + 1) * 16 * 8;
-    // P is kept in 16 bits: fp16's range is used up to 2^15 (kBias + kLazy), so
-    // that what falls below its smallest step, 2^-24, is below 2^-31 of the
-    // largest weight.
+    // P's fp16 parts: the first's range is used up to 2^15 (kBias + kLazy); the
+    // second, its remainder, is at most 2^3 and is scaled up. What falls below its
+    // smallest step, 2^-24, is then below 2^-43 of the largest weight.
     static constexpr float kBias = E4M3 ? 7.f : 0.f;
+    static constexpr float kLoScale = 4096.f;
     // O and the sum are rescaled only when the row maximum rises by more.
     static constexpr float kLazy = 8.f;
 };
@@ -595,12 +596,13 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             }
 
             // ---- P in 16-bit parts, O += P V. bf16: P = hi + mid + lo, the three bytes of its significand cut apart: exact.
-            // fp16: P = hi + lo, 22 bits.
+            // fp16: P = hi + lo / 2^12, so that small weights' remainders stay above fp16's smallest step.
             // The tensor core adds up a tile's keys (or 16 of them, where registers are short), starting from zero,
             // and these sums are added here: its own are cut towards zero, not rounded (over 800 tiles O lost 2^-14
             // of itself)
             // (one request of 1000 keys, 64/4 heads, e4m3, d 128: 7.8 us; a tile's two groups at once spill: 8.4)
             constexpr int kSum = WIDE && E4M3 && D == 128 ? 1 : C::kGroups;
+            constexpr uint32_t kSmallV = 0x0c000c00u;                        // 1 / kLoScale, twice
             float2 part[R];  // the tile's row sum
 #pragma unroll
             for (int k0 = 0; k0 < C::kGroups; k0 += kSum) {
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                                 hi[kg][i] = ptx::pack_f16x2(w.x, w.y);
                                 const float2 back = ptx::unpack_f16x2(hi[kg][i]);
                                 const float2 rest = ptx::fadd2(w, make_float2(-back.x, -back.y));
-                                lo[kg][i] = ptx::pack_f16x2(rest.x, rest.y);
+                                lo[kg][i] = ptx::pack_f16x2(rest.x * C::kLoScale, rest.y * C::kLoScale);
                             }
                         }
                 auto pv = [&](float(&c)[4], int kg, uint32_t b0, uint32_t b1) {
@@ -638,6 +640,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                     if constexpr (WIDE) {
                         mma(kg == 0, p0[0], p0[1], p0[2], p0[3]);
                         if constexpr (!E4M3) mma(false, p1[0], p1[1], p1[2], p1[3]);
+                        // (lo meets v / 2^12, exact in fp16: v is a multiple of 2^-9)
+                        if constexpr (E4M3) b0 = ptx::mul_f16x2(b0, kSmallV), b1 = ptx::mul_f16x2(b1, kSmallV);
                         mma(false, p2[0], p2[1], p2[2], p2[3]);
                     } else if constexpr (E4M3) {
                         mma(kg == 0, p0[0], p2[0], p0[1], p2[1]);
@@ -652,7 +656,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                         acc[n][0] = ptx::fadd2(acc[n][0], c0);
                         acc[n][R - 1] = ptx::fadd2(acc[n][R - 1], c1);
                     } else {
-                        acc[n][0] = ptx::fadd2(acc[n][0], ptx::fadd2(c0, c1));
+                        constexpr float kLo = E4M3 ? 1.f / C::kLoScale : 1.f;
+                        acc[n][0] = ptx::fadd2(acc[n][0], ptx::ffma2(c1, make_float2(kLo, kLo), c0));
                     }
                 };
                 if constexpr (!E4M3) {

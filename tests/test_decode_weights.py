@@ -141,3 +141,42 @@ def test_long_sums_are_rounded_not_cut(d, e4m3, hq, hkv):
     s = so.f64(k).reshape(n, hkv, d)[:, 0, 0]
     tiles = n * d * k.element_size() // 4096
     assert np.abs(so.f64(lse) - math.log(np.exp(s).sum())).max() <= tiles * 2.0 ** -25 + 2.0 ** -20
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (16, 1), (64, 4)])
+@pytest.mark.parametrize("above", [14, 18, 20, 22, 24])
+def test_small_weights_beside_a_dominant_one(d, hq, hkv, above):
+    """The first key of each warp's run is `above` (natural) higher than the other
+    16000, which share one score, and has no value: O is the others' sum alone. A
+    weight's parts are fp16, biased by 2^7, the second one scaled by 2^12: its
+    rounding is off by at most half of fp16's smallest step, 2^-25-12-7 = 2^-44 of
+    the largest weight, and all are equal, so they are off alike. (Not scaled:
+    2^-32, a tenth of such a weight at 20 and all of it at 24.)"""
+    fa = _fa()
+    keys, page = 4096 // d, 64
+    n = 4 * keys * (16000 // (4 * keys))
+    B = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    k, v = torch.zeros(n, hkv, d), torch.full((n, hkv, d), 2.0)
+    first = slice(0, 1) if hkv == 4 else slice(0, 4 * keys, keys)       # four warps share one head's tiles
+    k[first, :, 0] = float(above)
+    v[first] = 0.0
+    k, v = (x.view(n // page, page, hkv, d).to(torch.float8_e4m3fn).cuda() for x in (k, v))
+    q = torch.zeros(B, hq, d)
+    q[:, :, 0] = 1.0
+    table = torch.arange(n // page, dtype=torch.int32).expand(B, -1).contiguous()
+    x = dict(q=q.bfloat16().cuda(), k=k, v=v, table=table.cuda(), lens=torch.full((B,), n, dtype=torch.int32).cuda(),
+             ks=None, vs=None)
+    o, lse = call(fa, x, scale=1.0)
+    many = 1 if hkv == 4 else 4
+    total = many + (n - many) * math.exp(-above)
+    want = 2 * (n - many) * math.exp(-above) / total
+    # The exponent is below 2^6 in size: its rounding is 2^-19 of a weight. The row's sum has its full size from the
+    # first tile on: each of the others, added to it, is rounded by 2^-24 of it at most, all alike. The LSE: that, and
+    # m (below 2^6: 2^-19 with its factor's rounding), its sum with the logarithm (2^-19) and the product with ln 2
+    # (2^-19 in all), times ln 2: below 2^-18.
+    tiles = n / keys
+    bound = so.BF16_HALF * want + 2 * n * 2.0 ** -44 / total + want * (2.0 ** -18 + tiles * 2.0 ** -24)
+    off = np.abs(so.f64(o) - want).max()
+    assert off <= bound * (1 + so.BF16_HALF), off / bound
+    assert np.abs(so.f64(lse) - (above + math.log(total))).max() <= 2.0 ** -18 + tiles * 2.0 ** -24
