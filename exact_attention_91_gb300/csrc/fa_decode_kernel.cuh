@@ -265,11 +265,12 @@ __device__ __forceinline__ int decode_page(const DecodeParams& p, const DecodeSe
     return key < s.len ? p.table[s.b * p.table_stride + (key >> p.page_shift)] : -1;
 }
 
-// The upper bf16 halves of w (cut, not rounded); returns what is left, exactly.
+// The largest bf16 below each of w (zero for zero); returns what is left: exact,
+// and above zero.
 __device__ __forceinline__ float2 cut_bf16x2(float2 w, uint32_t& half) {
-    const uint32_t x = __float_as_uint(w.x), y = __float_as_uint(w.y);
+    const int x = __viaddmax_s32(__float_as_int(w.x), -1, 0), y = __viaddmax_s32(__float_as_int(w.y), -1, 0);
     half = __byte_perm(x, y, 0x7632);
-    return ptx::fadd2(w, make_float2(-__uint_as_float(x & 0xffff0000u), -__uint_as_float(y & 0xffff0000u)));
+    return ptx::fadd2(w, make_float2(-__int_as_float(x & 0xffff0000), -__int_as_float(y & 0xffff0000)));
 }
 
 // CLUSTER: the small form. Block r of a cluster of p.cluster takes the r-th
@@ -595,7 +596,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                 }
             }
 
-            // ---- P in 16-bit parts, O += P V. bf16: P = hi + mid + lo, the three bytes of its significand cut apart: exact.
+            // ---- P in 16-bit parts, O += P V. bf16: P = hi + mid + lo, eight bits of its significand each: exact.
+            // None is zero, nor is a row of theirs, so that an infinite v gives an infinity.
             // fp16: P = hi + lo / 2^12, so that small weights' remainders stay above fp16's smallest step.
             // The tensor core adds up a tile's keys (or 16 of them, where registers are short), starting from zero,
             // and these sums are added here: its own are cut towards zero, not rounded (over 800 tiles O lost 2^-14
@@ -621,7 +623,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                             const int i = R * j + r;
                             if constexpr (!E4M3) {
                                 const float2 x2 = cut_bf16x2(w, hi[kg][i]), x3 = cut_bf16x2(x2, mid[kg][i]);
-                                cut_bf16x2(x3, lo[kg][i]);
+                                lo[kg][i] = WIDE ? ptx::pack_bf16x2(x3.x, x3.y) : ptx::pack_bf16x2(x3.x * .5f, x3.y * .5f);
                             } else {
                                 hi[kg][i] = ptx::pack_f16x2(w.x, w.y);
                                 const float2 back = ptx::unpack_f16x2(hi[kg][i]);
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                         mma(kg == 0, p0[0], p2[0], p0[1], p2[1]);
                     } else {
                         mma(kg == 0, p0[0], p1[0], p0[1], p1[1]);
-                        mma(false, p2[0], 0u, p2[1], 0u);
+                        mma(false, p2[0], p2[0], p2[1], p2[1]);  // (halves)
                     }
                 };
                 auto add = [&](int n, const float(&c)[4]) {
