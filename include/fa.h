@@ -294,8 +294,8 @@ long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_typ
  *   positions   int32, device: that of (b, n) is positions[b*position_stride + n]
  *               (0: shared by the batch). Any int32 value.
  *   inv_freq    fp64 [rotary_dim/2], device, finite, in radians per position.
- *               The angle is off by |position|·2^-59 + 2^-29 radians at most
- *               (frequencies up to 1).
+ *               The angle is off by |position|·2^-59 + 2^-30 radians at most
+ *               (frequencies up to 1), its cos and sin by 2^-24 beside that.
  *   x_strides, y_strides  host arrays: elements from one b, h, n to the next
  *               (multiples of 8; x's may be 0; those of a dimension of size 1
  *               are not used); d's values are contiguous. y's rows do not
