@@ -326,8 +326,8 @@ int fa_rotary(const void* x, void* y, const int* positions, const double* inv_fr
  *               Slots of one call are distinct (of two tokens with the same
  *               slot, either's values are kept, in pieces of 8 or 16 values).
  *
- * FA_CACHE_E4M3: code = e4m3(x / scale[head]) from the fp32 value, by the
- * scale's fp32 reciprocal, round to nearest even, past ±448 to ±448, NaN kept.
+ * FA_CACHE_E4M3: code = e4m3(x / scale[head]), the quotient of fp32 values
+ * rounded to fp32 and that to nearest even, past ±448 to ±448, NaN kept.
  */
 int fa_cache_append(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
                     long long v_stride, const int* positions, const int* slots, const double* inv_freq,
