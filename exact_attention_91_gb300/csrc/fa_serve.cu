@@ -101,6 +101,45 @@ int check_cache(const fa_paged_cache* c, Cache* out) {
     return FA_OK;
 }
 
+// One dimension of the caches: how many, and the byte strides of keys and values.
+struct CacheDim {
+    long long size, k, v;
+};
+
+// Whether rows of the keys and of the values, these `off` bytes on, may meet. Over
+// the dimensions from the largest stride down (a stride is past all that the smaller
+// ones span, in either): with equal strides it is enough to look at the few
+// differences of index that bring what lies within together; with other ones, what
+// meets there is taken to meet.
+bool rows_of_caches_meet(const CacheDim* dim, int dims, long long row, long long off) {
+    long long k_span = row, v_span = row;
+    for (int i = 0; i < dims; ++i) {
+        k_span += (dim[i].size - 1) * dim[i].k;
+        v_span += (dim[i].size - 1) * dim[i].v;
+    }
+    if (off >= k_span || off <= -v_span) return false;
+    if (dims == 0) return true;
+    if (dim[0].k != dim[0].v) return true;
+    const long long near = off / dim[0].k;
+    for (long long by = near - 1; by <= near + 1; ++by)
+        if (by > -dim[0].size && by < dim[0].size &&
+            rows_of_caches_meet(dim + 1, dims - 1, row, off - by * dim[0].k))
+            return true;
+    return false;
+}
+
+bool caches_meet(const fa_paged_cache* cache, const Cache& c) {
+    CacheDim dim[3] = {{cache->num_blocks, c.k_block, c.v_block},
+                       {cache->page_size, c.k_token, c.v_token},
+                       {cache->heads, c.k_head, c.v_head}};
+    int dims = 0;
+    for (const CacheDim& x : dim)
+        if (x.size > 1) dim[dims++] = x;
+    std::sort(dim, dim + dims, [](const CacheDim& a, const CacheDim& b) { return a.k > b.k; });
+    return rows_of_caches_meet(dim, dims, cache->d * (c.e4m3 ? 1 : 2),
+                               static_cast<const char*>(cache->v) - static_cast<const char*>(cache->k));
+}
+
 template <typename Kernel>
 bool set_smem(Kernel kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
@@ -445,7 +484,7 @@ int fa_cache_append(const void* q, const void* k, const void* v, long long q_str
     const long long dims[3] = {cache->num_blocks, cache->page_size, cache->heads};
     const long long ks[3] = {cache->k_block, cache->k_token, cache->k_head};
     const long long vs[3] = {cache->v_block, cache->v_token, cache->v_head};
-    if (!rows_apart(dims, ks, d) || !rows_apart(dims, vs, d) || cache->k == cache->v) return FA_ERR_ALIAS;
+    if (!rows_apart(dims, ks, d) || !rows_apart(dims, vs, d) || caches_meet(cache, c)) return FA_ERR_ALIAS;
     // q and k may be rotated in place; apart from that the outputs overlap nothing
     const bool q_same = q_out == q && (T == 1 || q_out_stride == q_stride);
     const bool k_same = k_out == k && (T == 1 || k_out_stride == k_stride);
