@@ -247,7 +247,9 @@ def attention_forward(q, k, v, causal: bool = False, scale: float | None = None,
     """O (bf16) and LSE (fp32) for bf16 CUDA tensors q, k, v of shape [B, H, N, d].
 
     ``out`` / ``lse`` may be given to reuse buffers. Runs on ``stream`` (a
-    torch.cuda.Stream) or the current stream.
+    torch.cuda.Stream) or the current stream. On another stream than the current
+    one the caller keeps the tensors, results included, until the work is done
+    (``Tensor.record_stream``): their memory belongs to the current stream.
     """
     import torch
     if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
@@ -281,7 +283,7 @@ def attention_forward_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: 
     sequences of different lengths: q [total_q, H, d], k and v [total_k, H, d]
     (bf16, CUDA, contiguous), int32 CUDA offsets ``cu_seqlens_q`` /
     ``cu_seqlens_k`` of B + 1 entries. Under ``causal`` each sequence's last
-    query is aligned with its last key."""
+    query is aligned with its last key. ``stream`` as in ``attention_forward``."""
     import torch
     if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise TypeError("q, k, v must be bf16")
@@ -339,7 +341,8 @@ def attention_forward_heads(q, k, v, head_start: int, head_count: int, causal: b
     not given), nothing is copied, and the other heads of ``out`` and ``lse``
     are left as they were. Returns (out, lse) for the whole [B, H, N, d] /
     [B, H, N] shape. Each rank of a head-sharded job calls this on the range
-    ``head_shards(B*H, world)[rank]`` of tensors in its own device memory."""
+    ``head_shards(B*H, world)[rank]`` of tensors in its own device memory.
+    ``stream`` as in ``attention_forward``."""
     import torch
     if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise TypeError("q, k, v must be bf16")
@@ -398,13 +401,18 @@ def _on_stream(stream, device, fn, *args):
     """fn(*args) with ``stream`` as the current one. What the call allocates then
     belongs to that stream's part of the allocator (memory that the current
     stream's earlier work may still use is not written), and results are not
-    handed out again there while the current stream may still read them."""
+    handed out again there while the current stream may still read them, nor the
+    memory of tensors given (temporaries) while ``stream`` may still use it."""
     import torch
     if stream.device != device:
         raise ValueError("stream must be one of the tensors' device")
     current = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
         r = fn(*args)
+    for a in args:
+        for t in a if isinstance(a, tuple) else (a,):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
     for t in r if isinstance(r, tuple) else (r,):
         t.record_stream(current)
     return r
@@ -423,7 +431,11 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: fl
 
     ``workspace`` (uint8, at least ``fa_decode_paged_workspace`` bytes) may be
     given to keep allocation out of the call; calls that may overlap in time
-    need one each."""
+    need one each.
+
+    Runs on ``stream`` (a torch.cuda.Stream) or the current stream, as the
+    functions below do. The work is ordered on that stream alone; the memory of
+    tensors that are dropped meanwhile is not handed out again before it is done."""
     decode = (_bind or load_binding()).decode
     if stream is None:
         return decode(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse, return_lse,
