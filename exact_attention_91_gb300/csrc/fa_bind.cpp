@@ -108,6 +108,12 @@ Tensor make(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
     return at::detail::empty_cuda(shape, type, like.device(), c10::nullopt);  // (no dispatcher on the way)
 }
 
+// A tensor that the call was given and wrote to: what autograd saved of it before is
+// no longer that (a backward pass that needs it raises instead of using it).
+void wrote(const Tensor& t) {
+    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void arguments(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "wrong number of arguments"); }
 
 // The C description of caches indexed [block, token, head, d].
@@ -208,6 +214,9 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    scale, ptr(ws), ws.defined() ? static_cast<size_t>(ws.numel()) : 0,
                                    c10::cuda::getCurrentCUDAStream(device.index()).stream());
     if (rc != FA_OK) return failed(rc, "fa_decode_paged");
+    wrote(out);
+    wrote(lse);
+    wrote(ws);
     return return_lse ? pair(std::move(out), std::move(lse)) : THPVariable_Wrap(std::move(out));
     END_HANDLE_TH_ERRORS
 }
@@ -246,6 +255,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              each ? pos.stride(0) : 0, r, interleaved, inverse, static_cast<float>(factor),
                              c10::cuda::getCurrentCUDAStream(device.index()).stream());
     if (rc != FA_OK) return failed(rc, "fa_rotary");
+    wrote(out);
     return THPVariable_Wrap(std::move(out));
     END_HANDLE_TH_ERRORS
 }
@@ -295,6 +305,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    interleaved, static_cast<float>(factor),
                                    c10::cuda::getCurrentCUDAStream(device.index()).stream());
     if (rc != FA_OK) return failed(rc, "fa_cache_append");
+    wrote(q_out);
+    wrote(k_out);
+    wrote(kc);
+    wrote(vc);
     return THPVariable_Wrap(std::move(q_out));
     END_HANDLE_TH_ERRORS
 }
@@ -355,7 +369,11 @@ PyObject* maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 to_int(unused.numel()), to_int(page), to_int(T),
                                 c10::cuda::getCurrentCUDAStream(device.index()).stream());
     if (rc != FA_OK) return failed(rc, "fa_page_maps");
-    if (a[6] != Py_None) return Py_NewRef(a[6]);
+    wrote(table);
+    if (a[6] != Py_None) {
+        for (const Tensor& t : out) wrote(t);
+        return Py_NewRef(a[6]);
+    }
     PyObject* t = g_page_maps->tp_alloc(g_page_maps, 5);  // a named tuple: filled as one
     if (!t) throw python_error();
     for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(t, i, THPVariable_Wrap(std::move(out[i])));
