@@ -6,6 +6,9 @@
 // 10.8 us, page maps 13.8 us), more than the kernels of a small step take, and
 // here 2-4 us. libfa.so itself stays free of torch types.
 //
+// Allocations and launches may wait for the GPU, and the GPU for a Python function of
+// its stream: they run without the interpreter's lock.
+//
 // Every function takes its arguments by position (the Python wrappers name and
 // document them). A C call's negative status is raised as FaError; setup() hands
 // in that class, and PageMaps, the class of maps()'s result.
@@ -104,6 +107,12 @@ int to_int(int64_t x) {  // (a size past int is refused by the C call's own limi
     return x > 0x7fffffffLL ? -1 : static_cast<int>(x);
 }
 
+// The interpreter's lock, let go.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 Tensor make(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
     return at::detail::empty_cuda(shape, type, like.device(), c10::nullopt);  // (no dispatcher on the way)
 }
@@ -196,23 +205,26 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (const Tensor* t : {&table, &lens, static_cast<const Tensor*>(&out), static_cast<const Tensor*>(&lse),
                             static_cast<const Tensor*>(&ws)})
         on(*t, device);
-    const c10::cuda::CUDAGuard guard(device);
-    if (!out.defined()) out = make(q.sizes(), at::kBFloat16, q);
-    if (!lse.defined() && return_lse) lse = make({B, Hq}, at::kFloat, q);
-    if (!ws.defined()) {
-        int dev = 0, sms = 0;
-        int rc = fa::host_probe(&dev, &sms);
-        if (rc != FA_OK) return failed(rc, "fa_decode_paged");
-        const long long room = fa_decode_paged_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, cache.type,
-                                                         cache.page_size, to_int(width), sms);
-        if (room < 0) return failed(room, "fa_decode_paged");
-        if (room > 0) ws = make({room}, at::kByte, q);
-    }
-    const int rc = fa_decode_paged(q.data_ptr(), &cache, static_cast<const int*>(table.data_ptr()),
-                                   static_cast<const int*>(lens.data_ptr()), out.data_ptr(),
-                                   static_cast<float*>(ptr(lse)), to_int(B), to_int(Hq), to_int(width), table.stride(0),
-                                   scale, ptr(ws), ws.defined() ? static_cast<size_t>(ws.numel()) : 0,
-                                   c10::cuda::getCurrentCUDAStream(device.index()).stream());
+    const long long rc = [&]() -> long long {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard(device);
+        if (!out.defined()) out = make(q.sizes(), at::kBFloat16, q);
+        if (!lse.defined() && return_lse) lse = make({B, Hq}, at::kFloat, q);
+        if (!ws.defined()) {
+            int dev = 0, sms = 0;
+            const int probed = fa::host_probe(&dev, &sms);
+            if (probed != FA_OK) return probed;
+            const long long room = fa_decode_paged_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, cache.type,
+                                                             cache.page_size, to_int(width), sms);
+            if (room < 0) return room;
+            if (room > 0) ws = make({room}, at::kByte, q);
+        }
+        return fa_decode_paged(q.data_ptr(), &cache, static_cast<const int*>(table.data_ptr()),
+                               static_cast<const int*>(lens.data_ptr()), out.data_ptr(), static_cast<float*>(ptr(lse)),
+                               to_int(B), to_int(Hq), to_int(width), table.stride(0), scale, ptr(ws),
+                               ws.defined() ? static_cast<size_t>(ws.numel()) : 0,
+                               c10::cuda::getCurrentCUDAStream(device.index()).stream());
+    }();
     if (rc != FA_OK) return failed(rc, "fa_decode_paged");
     wrote(out);
     wrote(lse);
@@ -246,14 +258,17 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     cuda(x);
     on(pos, device);
     on(out, device);
-    const c10::cuda::CUDAGuard guard(device);
-    if (!out.defined()) out = make(x.sizes(), at::kBFloat16, x);
-    const long long xs[3] = {four ? x.stride(0) : 0, x.stride(1), four ? x.stride(2) : x.stride(0)};
-    const long long ys[3] = {four ? out.stride(0) : 0, out.stride(1), four ? out.stride(2) : out.stride(0)};
-    const int rc = fa_rotary(x.data_ptr(), out.data_ptr(), static_cast<const int*>(pos.data_ptr()),
-                             static_cast<const double*>(ptr(freq)), to_int(B), to_int(H), to_int(N), to_int(d), xs, ys,
-                             each ? pos.stride(0) : 0, r, interleaved, inverse, static_cast<float>(factor),
-                             c10::cuda::getCurrentCUDAStream(device.index()).stream());
+    const int rc = [&] {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard(device);
+        if (!out.defined()) out = make(x.sizes(), at::kBFloat16, x);
+        const long long xs[3] = {four ? x.stride(0) : 0, x.stride(1), four ? x.stride(2) : x.stride(0)};
+        const long long ys[3] = {four ? out.stride(0) : 0, out.stride(1), four ? out.stride(2) : out.stride(0)};
+        return fa_rotary(x.data_ptr(), out.data_ptr(), static_cast<const int*>(pos.data_ptr()),
+                         static_cast<const double*>(ptr(freq)), to_int(B), to_int(H), to_int(N), to_int(d), xs, ys,
+                         each ? pos.stride(0) : 0, r, interleaved, inverse, static_cast<float>(factor),
+                         c10::cuda::getCurrentCUDAStream(device.index()).stream());
+    }();
     if (rc != FA_OK) return failed(rc, "fa_rotary");
     wrote(out);
     return THPVariable_Wrap(std::move(out));
@@ -296,14 +311,17 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int r = frequencies(freq, device);
     cuda(q);
     for (const Tensor* t : {&k, &v, &pos, &slots, static_cast<const Tensor*>(&q_out), &k_out}) on(*t, device);
-    const c10::cuda::CUDAGuard guard(device);
-    if (!q_out.defined()) q_out = make(q.sizes(), at::kBFloat16, q);
-    const int rc = fa_cache_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), k.stride(0), v.stride(0),
-                                   static_cast<const int*>(pos.data_ptr()), static_cast<const int*>(slots.data_ptr()),
-                                   static_cast<const double*>(ptr(freq)), &cache, q_out.data_ptr(), ptr(k_out),
-                                   q_out.stride(0), k_out.defined() ? k_out.stride(0) : 0, to_int(T), to_int(Hq), r,
-                                   interleaved, static_cast<float>(factor),
-                                   c10::cuda::getCurrentCUDAStream(device.index()).stream());
+    const int rc = [&] {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard(device);
+        if (!q_out.defined()) q_out = make(q.sizes(), at::kBFloat16, q);
+        return fa_cache_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), k.stride(0), v.stride(0),
+                               static_cast<const int*>(pos.data_ptr()), static_cast<const int*>(slots.data_ptr()),
+                               static_cast<const double*>(ptr(freq)), &cache, q_out.data_ptr(), ptr(k_out),
+                               q_out.stride(0), k_out.defined() ? k_out.stride(0) : 0, to_int(T), to_int(Hq), r,
+                               interleaved, static_cast<float>(factor),
+                               c10::cuda::getCurrentCUDAStream(device.index()).stream());
+    }();
     if (rc != FA_OK) return failed(rc, "fa_cache_append");
     wrote(q_out);
     wrote(k_out);
@@ -346,31 +364,34 @@ PyObject* maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
     cuda(table);
     for (const Tensor* t : {&ctx, &fresh, &unused}) on(*t, device);
     for (const Tensor& t : out) on(t, device);
-    const c10::cuda::CUDAGuard guard(device);
-    if (a[6] == Py_None) {
-        // five parts of one allocation (each at a 16-byte boundary): allocations take most of a short call
-        int64_t at = 0;
-        for (int64_t n : sizes) at += (n + 3) / 4 * 4;
-        const Tensor whole = make({at}, at::kInt, table);
-        at = 0;
-        for (int i = 0; i < 5; ++i) {
-            out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()),
-                                                              whole.key_set(), whole.dtype());
-            out[i].unsafeGetTensorImpl()->set_storage_offset(at);
-            out[i].unsafeGetTensorImpl()->set_sizes_contiguous({sizes[i]});
-            at += (sizes[i] + 3) / 4 * 4;
+    const bool given = a[6] != Py_None;
+    const int rc = [&] {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard(device);
+        if (!given) {
+            // five parts of one allocation (each at a 16-byte boundary): allocations take most of a short call
+            int64_t at = 0;
+            for (int64_t n : sizes) at += (n + 3) / 4 * 4;
+            const Tensor whole = make({at}, at::kInt, table);
+            at = 0;
+            for (int i = 0; i < 5; ++i) {
+                out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()),
+                                                                  whole.key_set(), whole.dtype());
+                out[i].unsafeGetTensorImpl()->set_storage_offset(at);
+                out[i].unsafeGetTensorImpl()->set_sizes_contiguous({sizes[i]});
+                at += (sizes[i] + 3) / 4 * 4;
+            }
         }
-    }
-    int* p[5];
-    for (int i = 0; i < 5; ++i) p[i] = static_cast<int*>(out[i].data_ptr());
-    const int rc = fa_page_maps(static_cast<const int*>(ctx.data_ptr()), static_cast<const int*>(fresh.data_ptr()),
-                                static_cast<int*>(table.data_ptr()), static_cast<const int*>(unused.data_ptr()), p[0],
-                                p[1], p[2], p[3], p[4], to_int(B), to_int(width), table.stride(0),
-                                to_int(unused.numel()), to_int(page), to_int(T),
-                                c10::cuda::getCurrentCUDAStream(device.index()).stream());
+        int* p[5];
+        for (int i = 0; i < 5; ++i) p[i] = static_cast<int*>(out[i].data_ptr());
+        return fa_page_maps(static_cast<const int*>(ctx.data_ptr()), static_cast<const int*>(fresh.data_ptr()),
+                            static_cast<int*>(table.data_ptr()), static_cast<const int*>(unused.data_ptr()), p[0], p[1],
+                            p[2], p[3], p[4], to_int(B), to_int(width), table.stride(0), to_int(unused.numel()),
+                            to_int(page), to_int(T), c10::cuda::getCurrentCUDAStream(device.index()).stream());
+    }();
     if (rc != FA_OK) return failed(rc, "fa_page_maps");
     wrote(table);
-    if (a[6] != Py_None) {
+    if (given) {
         for (const Tensor& t : out) wrote(t);
         return Py_NewRef(a[6]);
     }
