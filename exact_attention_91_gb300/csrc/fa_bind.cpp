@@ -104,7 +104,7 @@ bool truth(PyObject* o) {
 }
 
 int to_int(int64_t x) {  // (a size past int is refused by the C call's own limits)
-    return x > 0x7fffffffLL ? -1 : static_cast<int>(x);
+    return x > 0x7fffffffLL || x < 0 ? -1 : static_cast<int>(x);
 }
 
 // The interpreter's lock, let go.
