@@ -180,3 +180,37 @@ def test_small_weights_beside_a_dominant_one(d, hq, hkv, above):
     off = np.abs(so.f64(o) - want).max()
     assert off <= bound * (1 + so.BF16_HALF), off / bound
     assert np.abs(so.f64(lse) - (above + math.log(total))).max() <= 2.0 ** -18 + tiles * 2.0 ** -24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,width", [(1, None), (8, 3000), (16, None), (20, 3000)])
+@pytest.mark.parametrize("size", [2.0 ** -100, 1.0, 2.0 ** 100, 2.0 ** 127])
+@pytest.mark.parametrize("below", [1, 13, 16, 20])
+def test_small_values_of_q_over_an_e4m3_cache(d, hq, width, size, below):
+    """q's largest value meets keys that are zero there; the one that counts is about
+    2^below smaller and has all of bf16's bits. Its products are exact; the factor of
+    scale and log2 e and the exponent round by 2^-24 of the score each, m and the LSE
+    by 2^-23 of it in all; the rest of either as in the tests above."""
+    fa = _fa()
+    k, v = torch.zeros(2, 16, 1, d), torch.zeros(2, 16, 1, d)
+    k[1, 0, 0, 1], k[1, 1, 0, 1] = 448.0, 416.0
+    v[1, 0, 0], v[1, 1, 0] = 1.0, 2.0
+    q = torch.zeros(1, hq, d, dtype=torch.float64)
+    q[:, :, 0] = size
+    q[:, :, 1] = size * 2.0 ** -below * (1 + 127 / 128)
+    q = q.bfloat16()
+    little = q[0, 0, 1].double().item()
+    scale = float(np.float32(max(12.0 / (448.0 * little), 2.0 ** -125)))
+    table = torch.full((1, width or 1), -1, dtype=torch.int32)
+    table[0, 0] = 1
+    t = torch.float8_e4m3fn
+    x = dict(q=q.cuda(), k=k.to(t).cuda(), v=v.to(t).cuda(), table=table.cuda(),
+             lens=torch.tensor([2], dtype=torch.int32).cuda(), ks=None, vs=None)
+    o, lse = call(fa, x, scale=scale)
+    s = np.array([448.0, 416.0]) * little * scale
+    w = np.exp(s - s.max())
+    want, size = (w[0] + 2 * w[1]) / w.sum(), s.max() + math.log(w.sum())
+    off = s.max() * 2.0 ** -22 + 2.0 ** -20
+    assert np.abs(so.f64(o) - want).max() <= want * (so.BF16_HALF + 2 * off)
+    assert np.abs(so.f64(lse) - size).max() <= off, np.abs(so.f64(lse) - size).max() / off
