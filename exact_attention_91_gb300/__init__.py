@@ -500,8 +500,8 @@ def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: dict | None
 def rotary(x, positions, inv_freq, interleaved: bool = False, inverse: bool = False, factor: float = 1.0, out=None,
            stream=None):
     """Rotary positions of x (bf16, CUDA): [B, H, N, d] with int32 ``positions``
-    [N] or [B, N], or token-major [T, H, d] with positions [T]. Any strides with
-    d contiguous. ``inv_freq`` (fp64 [rotary_dim / 2]) and ``factor`` are those of
+    [N] or [B, N], or token-major [T, H, d] with positions [T]. Any strides that
+    are multiples of 8, d contiguous, at a 16-byte boundary. ``inv_freq`` (fp64 [rotary_dim / 2]) and ``factor`` are those of
     ``rotary_inv_freq``; pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1) when
     ``interleaved``. ``inverse`` turns back by the same angles (times factor):
     the gradient with respect to x. ``out`` may be x. Not differentiable by

@@ -11,9 +11,7 @@
 //  * A tile is one warp's step: 8 KB of cache (kKeys keys, K and V). Each warp
 //    owns a ring of kStages tiles in shared memory, filled with 16-byte
 //    cp.async and read back by itself alone, so the loop has no block barrier
-//    and about 130 KB per SM are in flight. (Two stages: decode_batch below 167
-//    us; three with the copy issued before the wait, so that 192 KB are in
-//    flight: 169.)
+//    and 64 to 128 KB per SM are in flight.
 //  * The tiles of the whole batch, in the order (request, key head, tile), are
 //    cut into equal runs, one per worker (block), whatever the lengths are:
 //    the lengths are read on the GPU. A worker's loads run on across the
@@ -33,8 +31,10 @@
 //    lengths, no second launch.
 //  * One warp-level mma.sync m16n8k16 tile holds up to 16 query heads; tcgen05
 //    would want 128 rows (heads) or a softmax across TMEM lanes, for flops that
-//    are not the bound (the tensor pipe is busy 19% of the time with 4 query
-//    heads per key head, 37% with 8 on an e4m3 cache). With at most 8 heads the
+//    are not the bound (the tensor pipe is busy 28% of the time with 4 query
+//    heads per key head, 37% with 8 on an e4m3 cache, 39% with 16, whose 45% of
+//    the issue slots are no limit either: there the few warps wait on one
+//    another's latencies). With at most 8 heads the
 //    tile's rows 8-15 carry a second part of P. A weight has as many bits as in
 //    fp32: bf16 in three parts (exact, at a second instruction for the third),
 //    fp16 in two (22 bits and rounding). With 9 to 16 heads every part is an
@@ -45,15 +45,17 @@
 //
 // Measured on GB300 (a call, of calls back to back on three sets of inputs;
 // bytes of the keys and values over time):
-//   64 requests of 300 to 8192 keys, 32/8 heads, d 128        158.5 us  6.70 TB/s
-//   2 requests of 65536 keys, 32/32 heads, d 128               300.0 us  7.16 TB/s
-//   128 requests of 777 to 8190 keys, 64/8 heads, e4m3         175.4 us  6.72 TB/s
-//   256 requests of 10 to 300 keys, 32/8 heads, d 128           33.4 us  4.98 TB/s
-//   1 request of 1000 keys, 32/8 heads (4.5 us replayed)         5.4 us
+//   64 requests of 300 to 8192 keys, 32/8 heads, d 128        157.9 us  6.72 TB/s
+//   2 requests of 65536 keys, 32/32 heads, d 128               299.3 us  7.17 TB/s
+//   128 requests of 777 to 8190 keys, 64/8 heads, e4m3         175.7 us  6.71 TB/s
+//   256 requests of 10 to 300 keys, 32/8 heads, replayed        33.9 us  4.91 TB/s
+//   9 requests of 1 to 2001 keys, 12/12 heads, d 64             10.8 us
+//   1 request of 1000 keys, 32/8 heads (4.8 us replayed)         5.9 us
 // The main kernel alone reads at 6.6 to 7.1 TB/s (dram__bytes_read within 0.1%
 // of the keys' and values' bytes); what is left is the start of a launch (the
 // chain lengths, pages, first tiles: 4 to 5 us until the first tile is there),
-// workers that end up to 4% apart, and the join (about 3 us).
+// workers that end up to 4% apart, and the join (about 3 us). Of the small form's
+// 10.8 us, 0.9 are the third part of P (9.8 with two, which lose 2^-18 of it).
 #pragma once
 
 #include "fa_common.cuh"
@@ -118,23 +120,30 @@ struct DecodeWay {
     int step, off; // this warp's tiles of a segment: t0 + off, every step-th
     int add;       // its head: unit * heads + add
 };
+// (kSegCostFours: 256 x 10-300 keys 33.6 us with 1 or 2, 34.3 with 4. kSegCost: 700 x
+// 1-90 keys, d 64, 14.8 us with 8, 15.5 with 4, 14.2 with 16; against it 25 x 557-1410
+// keys of 5 heads, 17.3, 17.4 and 17.6.)
 constexpr int kSegCost = 8, kSegCostFours = 2;
 // The four-heads way is taken when there is a unit of four for every worker (few
 // are cut then) and the cache is token-major, so that the four heads' rows are
 // neighbours, or the requests are short (at most kFoursShort tiles in the mean:
 // the warps' merge is what it saves); and, token-major, when a worker's run is
 // kFoursRun tiles or more. Measured (us, four heads / one): 2 x 65536 keys of 32
-// heads, d 128, 303 / 315; 15 x 40000 keys of 8 heads, d 64, 189 / 214; 109 x
-// 120 keys of 32 heads, d 64, e4m3, 23 / 40; against it 1 x 61000 keys of 4
-// heads, 35 / 28 (every worker cuts); head-major 128 x 4480 keys of 8 heads,
-// e4m3, 197 / 190.
+// heads, d 128, 302 / 315; 15 x 40000 keys of 8 heads, d 64, 187 / 212; 109 x
+// 120 keys of 32 heads, d 64, e4m3, 20 / 34; against it 1 x 61000 keys of 4
+// heads, 27.2 / 25.3 (every worker cuts); head-major 128 x 4480 keys of 8 heads,
+// e4m3, 175 either way.
 constexpr int kFoursRun = 20, kFoursShort = 32;
 // Tiles (32 MB of keys and values) from which on they are to leave L2 first, so
-// that lengths, tables, q and partials stay there: 166 MB, 33.3 us against 36.2;
-// 66 MB, 13.7 against 14.6. Less is kept as it comes: 28 MB, 9.7 us against 10.4,
-// when the next call finds some of it.
+// that lengths, tables, q and partials stay there: 12 caches of 166 MB in turn, as of
+// a model's layers, 32.7 us a call against 34.1; of 66 MB, 18.5 against 19.1;
+// decode_e4m3 175.1 against 179.6 (decode_long 301.8 against 299.3). Less is kept as
+// it comes, which pays when a call finds its cache again: decode_short_d64 on three
+// caches of 28 MB 10.6 us against 11.3; 12 caches of 28 MB in turn lose by it, 11.1
+// against 10.7.
 constexpr int kOnceTiles = (32 << 20) / 8192;
-// Least run of a worker, in tiles with the segments' costs.
+// Least run of a worker, in tiles with the segments' costs. (4 and 16: 1 x 8000 keys
+// 13.4 and 13.0 us for 13.4, others the same.)
 constexpr int kMinRun = 8;
 // Most blocks of a cluster (the portable limit).
 constexpr int kDecodeCluster = 8;
@@ -509,8 +518,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             ptx::cp_async_wait<C::kStages - 2>();
             __syncwarp();
             // The next copies go into the slot read in the previous step: at once where a warp has few tiles and their
-            // latency counts (decode_short_d64 9.9 us; after the scores 10.3), behind the scores where HBM is the bound
-            // (decode_batch 155.2 us; at once 156.4).
+            // latency counts (decode_short_d64 10.6 us; after the scores 10.7), behind the scores where HBM is the
+            // bound (decode_batch 158.5 us, decode_long 301.8; at once 159.7 and 305.5).
             if (CLUSTER) load(false);
             const uint32_t kt = ring + slot_out * C::kTileBytes, vt = kt + C::kHalfBytes;
             const uint32_t ok = ok_bits >> (slot_out * C::kGroups) & ((1u << C::kGroups) - 1);
@@ -623,7 +632,8 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                             const int i = R * j + r;
                             if constexpr (!E4M3) {
                                 const float2 x2 = cut_bf16x2(w, hi[kg][i]), x3 = cut_bf16x2(x2, mid[kg][i]);
-                                lo[kg][i] = WIDE ? ptx::pack_bf16x2(x3.x, x3.y) : ptx::pack_bf16x2(x3.x * .5f, x3.y * .5f);
+                                constexpr float kPart = WIDE ? 1.f : .5f;  // (rows 8-15 take the other half)
+                                lo[kg][i] = ptx::pack_bf16x2(x3.x * kPart, x3.y * kPart);
                             } else {
                                 hi[kg][i] = ptx::pack_f16x2(w.x, w.y);
                                 const float2 back = ptx::unpack_f16x2(hi[kg][i]);
@@ -649,7 +659,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                         mma(kg == 0, p0[0], p2[0], p0[1], p2[1]);
                     } else {
                         mma(kg == 0, p0[0], p1[0], p0[1], p1[1]);
-                        mma(false, p2[0], p2[0], p2[1], p2[1]);  // (halves)
+                        mma(false, p2[0], p2[0], p2[1], p2[1]);
                     }
                 };
                 auto add = [&](int n, const float(&c)[4]) {

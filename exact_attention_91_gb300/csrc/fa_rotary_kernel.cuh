@@ -18,7 +18,7 @@
 // position, modulo 2^64, is the angle's fraction of a turn, off by |position| ·
 // 2^-62 turns at most (f < 2), rounded to 2^-32 turns; cos and sin follow in fp32.
 //
-// Measured on GB300: 4 x 32 x 4096 x 128 forward and gradient 81.3 us, 6.60 TB/s
+// Measured on GB300: 4 x 32 x 4096 x 128 forward and gradient 80.8 us, 6.65 TB/s
 // read and written (a warp per token that exchanged its cos and sin through
 // shared memory: 102.5); append of 16411 tokens of 32 + 2 x 8 heads, d 128, with
 // the rotated keys as well, 66.3 us, 6.59 TB/s; of 20000 tokens of 64 + 2 x 8
@@ -89,7 +89,7 @@ __device__ __forceinline__ float2 rot_cos_sin(int position, unsigned long long t
     const unsigned angle = static_cast<unsigned>(phase >> 32) + (static_cast<unsigned>(phase) >> 31);  // 2^-32 turns
     const unsigned quarter = (angle + 0x20000000u) >> 30;
     const int rest = static_cast<int>(angle - (quarter << 30));
-    const float hi = __int_as_float(0x4b400000 + (rest >> 8)) - 12582912.f;  // (an int below 2^22: in a float's last bits)
+    const float hi = __int_as_float(0x4b400000 + (rest >> 8)) - 12582912.f;  // (ints in the last bits of a float)
     const float lo = __int_as_float(0x4b000000 | (rest & 255)) - 8388608.f;
     constexpr double kTurn = 6.283185307179586477;
     constexpr float kHi = static_cast<float>(kTurn * 0x1p-24), kLo = static_cast<float>(kTurn * 0x1p-32);

@@ -21,7 +21,12 @@ namespace {
 constexpr int kMinPage = 16, kMaxPage = 65536;
 constexpr long long kMaxKeys = 0x7fff0000LL;  // of a request: key indexes stay in int
 constexpr int kWorkersPerSm = 2;
-constexpr int kShare = 8, kMaxShare = 32;  // tiles (two and eight a warp) of a block in the small form
+// Tiles (two and eight a warp) of a block in the small form: as many blocks to a unit as
+// bring its share down to kShare (4 x 1000 keys of 8 heads 6.0 us, with 16 7.4, with 4 6.0;
+// 4 x 500 keys 5.7, 6.2 and 5.2), and the other form from kMaxShare on (1 x 2500 keys of 8
+// heads 6.8 us, with 16 9.4; 1 x 8000 keys 13.4, with 64 15.8; against it 25 x 557-1410
+// keys of 5 heads 17.3, with 64 15.3).
+constexpr int kShare = 8, kMaxShare = 32;
 
 std::mutex g_ready_mu;
 std::atomic<bool> g_ready[fa::kHostMaxDevices];
@@ -283,10 +288,11 @@ int check_rotary(int d, int r, const double* inv_freq, float factor) {
 
 // Heads that one warp takes of its tokens (their cos and sin are computed once
 // for them): `most` when the tokens alone give every SM kWant warps several
-// times over, else as few as give that many warps. `most` is 4 for fa_rotary
-// (measured at 4x32x4096x128, forward and gradient: 81.5 us; 8: 83.1, 16: 85.1)
-// and 8 for fa_cache_append, whose heads are side by side (20000 tokens of 80
-// heads into e4m3: 116.2 us; 4: 118.9).
+// times over, else as few as give that many warps. `most` is 4 for fa_rotary and 8
+// for fa_cache_append, whose heads are side by side. (Measured with sincospif and
+// products in place of the quotients: 4x32x4096x128, forward and gradient, 81.5 us
+// with 4, 83.1 with 8, 85.1 with 16; 20000 tokens of 80 heads into e4m3, 116.2 us
+// with 8, 118.9 with 4.)
 int heads_per_warp(long long groups, int heads, int most, int sms) {
     constexpr long long kWant = 32;
     const long long chunks = std::max<long long>(1, (kWant * sms + groups - 1) / groups);

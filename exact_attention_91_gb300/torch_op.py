@@ -10,7 +10,9 @@ attention operators are forward-only: the attention backward pass is not part
 of this library. ``torch.ops.fa91.rotary`` (rotary positions) is
 differentiable. ``attention_decode_paged``, ``cache_append`` and ``page_maps``
 serve from a paged cache, as the functions of the same names do; the last two
-change their caches or block table in place. The fake (meta) implementations
+change their caches or block table in place. (``cache_append`` here has no
+``k_out``: a prompt's own attention takes its keys from ``torch.ops.fa91.rotary``.)
+The fake (meta) implementations
 give output shapes and dtypes without a GPU, so the operators can be traced.
 """
 from __future__ import annotations

@@ -258,13 +258,19 @@ typedef struct fa_paged_cache {
  *                More than table_width*page_size counts as that many
  *                (at most 2^31 - 65536).
  *   workspace    device, 16-byte aligned, at least fa_decode_paged_workspace()
- *                bytes (NULL if that is 0: a small batch needs none); needs no initial value, holds nothing after the call's
- *                kernels. Calls (or graph replays) that may overlap in time
- *                need workspaces of their own.
+ *                bytes (NULL if that is 0: a small batch needs none); needs no
+ *                initial value, holds nothing after the call's kernels. Calls
+ *                (or graph replays) that may overlap in time need workspaces
+ *                of their own.
  *
  * Keys whose block is outside [0, num_blocks) are hidden, as if they were not
  * there; table entries past a request's last key are not read. Values in
- * hidden and unfilled places of a page (NaN included) have no effect.
+ * hidden and unfilled places of a page (NaN included) have no effect. In visible
+ * ones NaN is passed on, and an infinity of v gives an infinity (NaN where two of
+ * opposite sign meet, or a weight is below fp32's range).
+ * Weights and sums are fp32; over FA_CACHE_E4M3 a weight is off by 2^-44 of the row's
+ * largest at most beside its own rounding, and values of q 2^-28 below their head's
+ * largest lose bits (fp16's smallest step).
  * seq_lens, block_table and the cache must not change while the call runs (lengths
  * that do give wrong values, but no access outside the buffers given).
  * The result does not depend on what else runs; which partial sums are joined
@@ -322,7 +328,9 @@ int fa_rotary(const void* x, void* y, const int* positions, const double* inv_fr
  *   positions, slots  int32 [T], device. Slot s is token s % page_size of block
  *               s / page_size. A token whose slot is negative or past the cache
  *               is padding: nothing of it is written, in no output.
- *               The cache's rows do not overlap, as y's above, nor k's with v's.
+ *               The cache's rows do not overlap, as y's above, nor k's with v's
+ *               (caches of one buffer with other strides each are taken if what
+ *               their differing dimensions span lies apart).
  *               Slots of one call are distinct (of two tokens with the same
  *               slot, either's values are kept, in pieces of 8 or 16 values).
  *
