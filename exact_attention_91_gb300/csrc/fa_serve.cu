@@ -112,10 +112,9 @@ struct CacheDim {
 };
 
 // Whether rows of the keys and of the values, these `off` bytes on, may meet. Over
-// the dimensions from the largest stride down (a stride is past all that the smaller
-// ones span, in either): with equal strides it is enough to look at the few
-// differences of index that bring what lies within together; with other ones, what
-// meets there is taken to meet.
+// the dimensions from the keys' largest stride down: where the values' is the same and
+// past all that the smaller ones span, it is enough to look at the few differences of
+// index that bring what lies within together; otherwise spans that meet are taken for rows that do.
 bool rows_of_caches_meet(const CacheDim* dim, int dims, long long row, long long off) {
     long long k_span = row, v_span = row;
     for (int i = 0; i < dims; ++i) {
@@ -124,7 +123,8 @@ bool rows_of_caches_meet(const CacheDim* dim, int dims, long long row, long long
     }
     if (off >= k_span || off <= -v_span) return false;
     if (dims == 0) return true;
-    if (dim[0].k != dim[0].v) return true;
+    const long long within = v_span - (dim[0].size - 1) * dim[0].v;  // (the keys' fits its strides: rows_apart)
+    if (dim[0].k != dim[0].v || within > dim[0].k) return true;
     const long long near = off / dim[0].k;
     for (long long by = near - 1; by <= near + 1; ++by)
         if (by > -dim[0].size && by < dim[0].size &&

@@ -116,3 +116,32 @@ def test_answers_are_those_of_the_bytes():
         seen[m] += 1
         assert (call(c) == -10) == m, (order, sizes, st, off)
     assert min(seen.values()) > 300
+
+
+def test_nothing_that_meets_is_taken_whatever_the_orders():
+    """Keys and values with strides of their own, also one stride in common and the
+    rest in another order: a meeting is never missed."""
+    rng = random.Random(8)
+    seen = 0
+    for _ in range(6000):
+        d, page, heads, blocks = 64, 16, rng.choice([1, 2, 3, 5]), rng.choice([1, 2, 3, 7])
+        sizes = dict(block=blocks, token=page, head=heads)
+
+        def lay(order, keep=None):
+            st, span = {}, d
+            for x in reversed(order):
+                st[x] = keep[1] if keep and x == keep[0] and keep[1] >= span else span + rng.choice([0, 0, 64, 512])
+                span = st[x] * (sizes[x] - 1) + span
+            return st, span
+
+        orders = list(itertools.permutations(("block", "token", "head")))
+        ks, span = lay(rng.choice(orders))
+        same = rng.choice(["block", "token", "head"])
+        vs, vspan = lay(rng.choice(orders), (same, ks[same]))
+        off = rng.randrange(-vspan, span, 8)
+        c = cache(KV, KV + 2 * off, page=page, heads=heads, d=d, blocks=blocks, **{f"k_{x}": ks[x] for x in ks},
+                  **{f"v_{x}": vs[x] for x in vs})
+        if meet(c):
+            seen += 1
+            assert call(c) == -10, (sizes, ks, vs, off)
+    assert seen > 1000
