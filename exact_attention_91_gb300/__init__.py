@@ -27,12 +27,14 @@ __all__ = ["FaError", "load_library", "fa_fwd", "fa_fwd_noalloc", "fa_strerror",
            "head_shards", "attention_forward_heads", "EXPORTED_SYMBOLS", "CACHE_BF16", "CACHE_E4M3",
            "FaPagedCache", "fa_decode_paged", "fa_decode_paged_workspace", "fa_rotary", "fa_cache_append",
            "fa_page_maps", "attention_decode_paged", "rotary", "rotary_inv_freq", "cache_append", "page_maps",
-           "PageMaps", "load_binding"]
+           "PageMaps", "load_binding", "fa_bwd", "fa_bwd_varlen", "fa_bwd_workspace", "attention_backward",
+           "attention_backward_varlen"]
 
 EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_noalloc", "fa_fwd_varlen", "fa_strerror", "fa_device_status",
                     "fa_set_wait_limit_ns", "fa_abi_version", "fa_selftest_wait_timeout", "fa_varlen_num_splits",
                     "fa_selftest_exp2", "fa_selftest_ex2_rate", "fa_decode_paged", "fa_decode_paged_workspace",
-                    "fa_rotary", "fa_cache_append", "fa_page_maps")
+                    "fa_rotary", "fa_cache_append", "fa_page_maps", "fa_bwd",
+                    "fa_bwd_varlen", "fa_bwd_workspace")
 
 FA_OK = 0
 FA_ERR_DEVICE_TIMEOUT = -8
@@ -104,6 +106,12 @@ def load_library(path: str | None = None):
     lib.fa_cache_append.restype = i
     lib.fa_page_maps.argtypes = [vp] * 9 + [i, i, ll, i, i, i, vp]
     lib.fa_page_maps.restype = i
+    lib.fa_bwd.argtypes = [vp] * 10 + [i, i, i, i, f, i, vp, ctypes.c_size_t, vp]
+    lib.fa_bwd.restype = i
+    lib.fa_bwd_varlen.argtypes = [vp] * 12 + [i] * 7 + [f, i, vp, ctypes.c_size_t, vp]
+    lib.fa_bwd_varlen.restype = i
+    lib.fa_bwd_workspace.argtypes = [ll, i]
+    lib.fa_bwd_workspace.restype = ll
     if path is None:
         _lib = lib
     return lib
@@ -201,6 +209,30 @@ def fa_decode_paged_workspace(B: int, Hq: int, Hkv: int, d: int, cache_type: int
     """The C ``fa_decode_paged_workspace`` (host only): workspace bytes of
     ``fa_decode_paged`` for these sizes, or a negative status."""
     return load_library().fa_decode_paged_workspace(B, Hq, Hkv, d, cache_type, page_size, table_width, sm_count)
+
+
+def fa_bwd(dout: int, q: int, k: int, v: int, o: int, lse: int, dlse: int | None, dq: int, dk: int, dv: int, B: int,
+           H: int, N: int, d: int, scale: float, causal: bool, workspace: int, workspace_bytes: int,
+           stream: int | None) -> int:
+    """The C ``fa_bwd``: device pointers as ints, returns the status code."""
+    return load_library().fa_bwd(dout, q, k, v, o, lse, dlse or None, dq, dk, dv, B, H, N, d, scale, int(bool(causal)),
+                                 workspace or None, workspace_bytes, stream or None)
+
+
+def fa_bwd_varlen(dout: int, q: int, k: int, v: int, o: int, lse: int, dlse: int | None, dq: int, dk: int, dv: int,
+                  cu_q: int, cu_k: int, B: int, H: int, total_q: int, total_k: int, max_seqlen_q: int,
+                  max_seqlen_k: int, d: int, scale: float, causal: bool, workspace: int, workspace_bytes: int,
+                  stream: int | None) -> int:
+    """The C ``fa_bwd_varlen``: device pointers as ints, returns the status code."""
+    return load_library().fa_bwd_varlen(dout, q, k, v, o, lse, dlse or None, dq, dk, dv, cu_q, cu_k, B, H, total_q,
+                                        total_k, max_seqlen_q, max_seqlen_k, d, scale, int(bool(causal)),
+                                        workspace or None, workspace_bytes, stream or None)
+
+
+def fa_bwd_workspace(queries: int, H: int) -> int:
+    """The C ``fa_bwd_workspace`` (host only): workspace bytes of a backward
+    pass over this many queries of H heads, or a negative status."""
+    return load_library().fa_bwd_workspace(queries, H)
 
 
 def fa_rotary(x: int, y: int, positions: int, inv_freq: int | None, B: int, H: int, N: int, d: int, x_strides,
@@ -442,6 +474,40 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: fl
                       workspace)
     return _on_stream(stream, q.device, decode, q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale,
                       out, lse, return_lse, workspace)
+
+
+def attention_backward(dout, q, k, v, out, lse, causal: bool = False, scale: float | None = None, dlse=None, dq=None,
+                       dk=None, dv=None, workspace=None, stream=None):
+    """(dq, dk, dv) of ``attention_forward``: the gradients of a loss with
+    respect to q, k and v (bf16 [B, H, N, d]), from its gradient ``dout`` with
+    respect to O and, where the loss uses LSE too, ``dlse`` (fp32 [B, H, N]).
+    ``out`` and ``lse`` are what the forward pass gave for the same q, k, v,
+    ``causal`` and ``scale``. All contiguous CUDA tensors. ``dq``, ``dk``, ``dv``
+    and ``workspace`` (uint8, at least ``fa_bwd_workspace(B * N, H)`` bytes) may
+    be given to keep allocation out of the call; calls that may overlap in time
+    need a workspace each. The same call gives the same bits. Runs on ``stream``
+    as ``attention_decode_paged`` does. ``torch.ops.fa91.attention_forward`` is
+    differentiable through it."""
+    backward = (_bind or load_binding()).backward
+    if stream is None:
+        return backward(dout, q, k, v, out, lse, dlse, causal, scale, dq, dk, dv, workspace)
+    return _on_stream(stream, q.device, backward, dout, q, k, v, out, lse, dlse, causal, scale, dq, dk, dv, workspace)
+
+
+def attention_backward_varlen(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                              max_seqlen_k: int, causal: bool = False, scale: float | None = None, dlse=None, dq=None,
+                              dk=None, dv=None, workspace=None, stream=None):
+    """(dq, dk, dv) of ``attention_forward_varlen``: dout, q, out, dq [total_q, H,
+    d], k, v, dk, dv [total_k, H, d], lse and dlse [H, total_q], int32 offsets
+    as there. ``max_seqlen_q`` and ``max_seqlen_k`` bound the sequences' query and
+    key counts. Rows behind the last sequence are padding: not read, and their
+    gradients are not written (in results that the call makes, not initialised).
+    The rest as in ``attention_backward``; the workspace is
+    ``fa_bwd_workspace(total_q, H)`` bytes."""
+    backward = (_bind or load_binding()).backward_varlen
+    args = (dout, q, k, v, out, lse, dlse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, scale, dq,
+            dk, dv, workspace)
+    return backward(*args) if stream is None else _on_stream(stream, q.device, backward, *args)
 
 
 def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None, device=None):

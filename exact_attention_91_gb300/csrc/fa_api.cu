@@ -434,6 +434,17 @@ int host_probe(int* device, int* sm_count) {
 
 int host_capturing(cudaStream_t stream) { return capturing(stream); }
 
+int host_map_rows(CUtensorMap* map, const void* ptr, int BH, int N, int d) { return encode_map(map, ptr, BH, N, d); }
+
+int host_map_tokens(CUtensorMap* map, const void* ptr, int total, int H, int d) {
+    return encode_map_tokens(map, ptr, total, H, d);
+}
+
+unsigned long long host_wait_limit_ns() {
+    std::lock_guard<std::mutex> lock(g_mu);
+    return g_wait_limit_ns;
+}
+
 }  // namespace fa
 
 extern "C" {
@@ -514,13 +525,15 @@ int fa_device_status(void* stream, unsigned* bits) {
         cudaGetLastError();
         return FA_ERR_NO_DEVICE;
     }
-    unsigned word = 0;
+    unsigned word = 0, grad = 0;
     const unsigned zero = 0;
     if (cudaMemcpyFromSymbol(&word, fa::g_status, sizeof(word)) != cudaSuccess ||
         cudaMemcpyToSymbol(fa::g_status, &zero, sizeof(zero)) != cudaSuccess) {
         cudaGetLastError();
         return FA_ERR_LAUNCH;
     }
+    if (fa::grad_status(&grad) != FA_OK) return FA_ERR_LAUNCH;
+    word |= grad;
     if (bits) *bits = word;
     return word ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
 }

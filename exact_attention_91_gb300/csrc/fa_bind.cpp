@@ -1,4 +1,5 @@
-// Native half of the Python binding of the serving operators: the checks on
+// Native half of the Python binding of the serving operators and the backward
+// passes: the checks on
 // torch tensors, the allocation of outputs and workspace, and the call of the
 // C ABI, in one step per operator. A serving step makes four short calls per
 // layer or step; from Python objects through ctypes each costs 10-14 us of host
@@ -233,6 +234,116 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+PyObject* three(Tensor a, Tensor b, Tensor c) {
+    PyObject* t = PyTuple_New(3);
+    if (!t) throw python_error();
+    PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(std::move(a)));
+    PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(std::move(b)));
+    PyTuple_SET_ITEM(t, 2, THPVariable_Wrap(std::move(c)));
+    return t;
+}
+
+// A contiguous bf16 tensor of this shape, or none.
+void bf16_of(const Tensor& t, at::IntArrayRef shape, const char* name) {
+    TORCH_CHECK_TYPE(!t.defined() || t.scalar_type() == at::kBFloat16, name, " must be bf16");
+    TORCH_CHECK_VALUE(!t.defined() || (t.sizes() == shape && t.is_contiguous()), name,
+                      " must be contiguous and of the shape ", shape);
+}
+
+void fp32_of(const Tensor& t, at::IntArrayRef shape, const char* name) {
+    TORCH_CHECK_TYPE(!t.defined() || t.scalar_type() == at::kFloat, name, " must be fp32");
+    TORCH_CHECK_VALUE(!t.defined() || (t.sizes() == shape && t.is_contiguous()), name,
+                      " must be contiguous and of the shape ", shape);
+}
+
+// Both backward passes: dout, q, k, v, out, lse, dlse, then (packed) the offsets and the longest counts, then causal,
+// scale, dq, dk, dv, workspace
+PyObject* backward_any(PyObject* const* a, bool packed) {
+    const Tensor &dout = tensor(a[0], "dout"), &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+    const Tensor &o = tensor(a[4], "out"), &lse = tensor(a[5], "lse"), &dlse = tensor_or_none(a[6], "dlse");
+    static const Tensor none;
+    const Tensor& cu_q = packed ? tensor(a[7], "cu_seqlens_q") : none;
+    const Tensor& cu_k = packed ? tensor(a[8], "cu_seqlens_k") : none;
+    const int64_t max_q = packed ? integer(a[9]) : 0, max_k = packed ? integer(a[10]) : 0;
+    PyObject* const* b = a + (packed ? 11 : 7);
+    const bool causal = truth(b[0]);
+    Tensor dq = tensor_or_none(b[2], "dq"), dk = tensor_or_none(b[3], "dk"), dv = tensor_or_none(b[4], "dv");
+    Tensor ws = tensor_or_none(b[5], "workspace");
+    TORCH_CHECK_VALUE(packed ? q.dim() == 3 && k.dim() == 3 && q.size(1) == k.size(1) && q.size(2) == k.size(2)
+                             : q.dim() == 4 && k.sizes() == q.sizes(),
+                      packed ? "q must be [total_q, H, d] and k, v [total_k, H, d]" : "q, k, v must all be [B, H, N, d]");
+    const at::DimVector qs(q.sizes()), ks(k.sizes());
+    bf16_of(q, qs, "q");
+    bf16_of(k, ks, "k");
+    bf16_of(v, ks, "v");
+    bf16_of(o, qs, "out");
+    bf16_of(dout, qs, "dout");
+    bf16_of(dq, qs, "dq");
+    bf16_of(dk, ks, "dk");
+    bf16_of(dv, ks, "dv");
+    const int64_t d = q.size(-1), H = q.size(1);
+    const at::DimVector stats = packed ? at::DimVector{H, q.size(0)} : at::DimVector{q.size(0), H, q.size(2)};
+    fp32_of(lse, stats, "lse");
+    fp32_of(dlse, stats, "dlse");
+    if (packed) {
+        int32(cu_q, "cu_seqlens_q");
+        int32(cu_k, "cu_seqlens_k");
+        TORCH_CHECK_VALUE(cu_q.dim() == 1 && cu_k.sizes() == cu_q.sizes() && cu_q.numel() >= 2 &&
+                              cu_q.is_contiguous() && cu_k.is_contiguous(),
+                          "cu_seqlens_q and cu_seqlens_k must both hold B + 1 offsets");
+    }
+    TORCH_CHECK_VALUE(!ws.defined() || (ws.scalar_type() == at::kByte && ws.is_contiguous()),
+                      "workspace must be a contiguous uint8 tensor");
+    const float scale = static_cast<float>(b[1] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(b[1]));
+    const c10::Device device = q.device();
+    cuda(q);
+    for (const Tensor* t : {&dout, &k, &v, &o, &lse, &dlse, &cu_q, &cu_k, static_cast<const Tensor*>(&dq),
+                            static_cast<const Tensor*>(&dk), static_cast<const Tensor*>(&dv),
+                            static_cast<const Tensor*>(&ws)})
+        on(*t, device);
+    const int64_t rows = packed ? q.size(0) : q.size(0) * q.size(2);
+    const long long rc = [&]() -> long long {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard(device);
+        if (!dq.defined()) dq = make(qs, at::kBFloat16, q);
+        if (!dk.defined()) dk = make(ks, at::kBFloat16, q);
+        if (!dv.defined()) dv = make(ks, at::kBFloat16, q);
+        if (!ws.defined()) {
+            const long long room = fa_bwd_workspace(rows, to_int(H));
+            if (room < 0) return room;
+            if (room > 0) ws = make({room}, at::kByte, q);
+        }
+        const size_t room = ws.defined() ? static_cast<size_t>(ws.numel()) : 0;
+        void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+        const auto stat = [](const Tensor& t) { return static_cast<const float*>(ptr(t)); };
+        if (!packed)
+            return fa_bwd(ptr(dout), ptr(q), ptr(k), ptr(v), ptr(o), stat(lse), stat(dlse), ptr(dq), ptr(dk), ptr(dv),
+                          to_int(q.size(0)), to_int(H), to_int(q.size(2)), to_int(d), scale, causal, ptr(ws), room,
+                          stream);
+        return fa_bwd_varlen(ptr(dout), ptr(q), ptr(k), ptr(v), ptr(o), stat(lse), stat(dlse), ptr(dq), ptr(dk),
+                             ptr(dv), static_cast<const int*>(cu_q.data_ptr()), static_cast<const int*>(cu_k.data_ptr()),
+                             to_int(cu_q.numel() - 1), to_int(H), to_int(q.size(0)), to_int(k.size(0)), to_int(max_q),
+                             to_int(max_k), to_int(d), scale, causal, ptr(ws), room, stream);
+    }();
+    if (rc != FA_OK) return failed(rc, packed ? "fa_bwd_varlen" : "fa_bwd");
+    for (const Tensor* t : {&dq, &dk, &dv, &ws}) wrote(*t);
+    return three(std::move(dq), std::move(dk), std::move(dv));
+}
+
+PyObject* backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments(n, 13);
+    return backward_any(a, false);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject* backward_varlen(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments(n, 17);
+    return backward_any(a, true);
+    END_HANDLE_TH_ERRORS
+}
+
 // x, positions, inv_freq, interleaved, inverse, factor, out
 PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -405,6 +516,8 @@ PyObject* maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define FA_FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
 PyMethodDef kMethods[] = {{"setup", FA_FAST(setup), METH_FASTCALL, nullptr},
                           {"decode", FA_FAST(decode), METH_FASTCALL, nullptr},
+                          {"backward", FA_FAST(backward), METH_FASTCALL, nullptr},
+                          {"backward_varlen", FA_FAST(backward_varlen), METH_FASTCALL, nullptr},
                           {"rotary", FA_FAST(rotary), METH_FASTCALL, nullptr},
                           {"append", FA_FAST(append), METH_FASTCALL, nullptr},
                           {"maps", FA_FAST(maps), METH_FASTCALL, nullptr},

@@ -1,6 +1,6 @@
 /*
- * fa.h — C ABI of the GB300 (sm_103a) exact-attention forward library
- * (libfa.so).
+ * fa.h — C ABI of the GB300 (sm_103a) exact-attention library (libfa.so):
+ * forward and backward pass, and serving from a paged cache.
  *
  * The operation is exact softmax attention computed tile by tile with the
  * online softmax, never writing the N×N score matrix to memory:
@@ -190,6 +190,57 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
  * sm_count < 1.
  */
 int fa_varlen_num_splits(int B, int H, int total_k, int max_seqlen_q, int sm_count);
+
+/*
+ * fa_bwd — attention's backward pass: the gradients of a loss with respect to q, k and v from its
+ * gradient with respect to O (and LSE), with the probabilities recomputed tile by tile:
+ *
+ *   P_ij = exp(scale · q_i·k_j - LSE_i)   (0 where the mask hides key j from query i)
+ *   δ_i  = dO_i·O_i - dLSE_i,   dS_ij = P_ij (dO_i·v_j - δ_i)
+ *   dV_j = Σ_i P_ij dO_i,  dK_j = scale Σ_i dS_ij q_i,  dQ_i = scale Σ_j dS_ij k_j
+ *
+ * (The source pages treat the forward pass alone.)
+ *
+ * dout, q, k, v, o  device, bf16, contiguous [B, H, N, d], 16-byte aligned; o and lse are what
+ *          fa_fwd gave for q, k, v with the same scale and causal. Read only.
+ * lse      device, fp32, contiguous [B, H, N]. A query with LSE = -inf saw no key: it adds nothing, and
+ *          its dQ is 0.
+ * dlse     device, fp32, contiguous [B, H, N]: the loss's gradient with respect to LSE, or NULL for 0.
+ * dq, dk, dv  device, bf16, contiguous [B, H, N, d], 16-byte aligned. Written, and overlap nothing else.
+ * workspace  device, 16-byte aligned, at least fa_bwd_workspace() bytes: needs no initial value, holds
+ *          nothing after the call's kernels. Calls (or graph replays) that may overlap in time need
+ *          workspaces of their own.
+ *
+ * Every sum is fp32; P and dS are rounded to bf16 for the tensor cores, as fa_fwd rounds P. No atomics:
+ * the same call gives the same bits. Sizes, scale, errors, ownership and streams are as for fa_fwd, except
+ * that B*H*ceil(N/128) <= 2^31 - 65537. Two kernels, launched with programmatic stream serialization
+ * (they wait for what precedes them on the stream before they read or write, and let their own successor
+ * start early). May be captured into CUDA graphs once the device has had one ordinary call of fa_bwd or
+ * fa_bwd_varlen (a captured call before then returns FA_ERR_LAUNCH).
+ */
+int fa_bwd(const void* dout, const void* q, const void* k, const void* v, const void* o, const float* lse,
+           const float* dlse, void* dq, void* dk, void* dv, int B, int H, int N, int d, float scale, int causal,
+           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_bwd_varlen — the same over packed sequences with their own query and key counts (fa_fwd_varlen's
+ * layouts, offsets and mask): dout, q, o, dq bf16 [total_q, H, d]; k, v, dk, dv bf16 [total_k, H, d]; lse,
+ * dlse fp32 [H, total_q]. Every query count is at most max_seqlen_q and every key count at most
+ * max_seqlen_k (bounds that cost little where they are loose; total_q and total_k will do). Offsets are read
+ * only on the GPU and taken into [0, total]. Rows behind the last sequence (cu_seqlens[B] < total) are
+ * padding: nothing in them is read, and their gradients are left as they were. A key that no query sees gets
+ * dK = dV = 0, a query that sees no key dQ = 0. A tensor without rows may be NULL.
+ */
+int fa_bwd_varlen(const void* dout, const void* q, const void* k, const void* v, const void* o, const float* lse,
+                  const float* dlse, void* dq, void* dk, void* dv, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                  int B, int H, int total_q, int total_k, int max_seqlen_q, int max_seqlen_k, int d, float scale,
+                  int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_bwd_workspace — host-only: workspace bytes of a backward pass over this many queries (fa_bwd: B*N,
+ * fa_bwd_varlen: total_q) of H heads: 4 for each, or FA_ERR_BAD_SHAPE.
+ */
+long long fa_bwd_workspace(long long queries, int H);
 
 /*
  * ---------------------------------------------------------------------------
