@@ -11,9 +11,9 @@
 // Two kernels, so that every sum has one owner: no atomics, the same bits from the same
 // call, no fp32 copy of dQ in memory. The price is that S and dP are computed twice, seven
 // products of a pair of tiles in place of five.
-//  * fa_bwd_dq_kernel: a CTA owns 128 queries of a head and walks the key tiles. It also
-//    computes δ and leaves it in the workspace for
-//  * fa_bwd_dkv_kernel: a CTA owns 128 keys and walks the query tiles that see them. Its
+//  * fa_bwd_dq_kernel: a unit is 128 queries of a head, and walks the key tiles. Its blocks
+//    also compute δ and leave it in the workspace for
+//  * fa_bwd_dkv_kernel: a unit is 128 keys, and walks the query tiles that see them. Its
 //    scores are transposed (keys are TMEM lanes), so that P and dS are the A operands of
 //    dV += P·dO and dK += dS·Q where the elementwise warps wrote them, in TMEM.
 // Both products' operands are bf16 tiles that TMA put into shared memory once and that serve
@@ -21,9 +21,17 @@
 // P and dS are rounded to bf16 for the tensor core (relative 2^-9 each, averaged over the
 // keys or queries of a sum), as the forward pass rounds P; everything else is fp32.
 //
-// Roles (12 warps): 0-7 elementwise (a thread holds one TMEM lane and 64 of a tile's 128
-// columns, warps 0-3 the first ones and 4-7 the others), 8 issues every MMA and owns TMEM,
-// 9 loads by TMA, 10 (dkv) brings each query tile's LSE and δ.
+// One block per SM takes units from a counter as it frees up, longest walks first. The loads
+// of the next unit run on behind those of the last, so a unit's end costs its last products
+// and its output, not a block's start.
+//
+// Roles (19 and 20 warps): 0-15 elementwise (four warps for each 32 of a tile's 128 columns, each of
+// them 32 TMEM lanes), 16 issues the MMAs of S and dP and owns TMEM, 17 claims units and loads
+// by TMA, 18 issues the MMAs of the gradients, 19 (dkv) brings LSE and δ of each query tile.
+// (One warp for all MMAs held up a gradient's, and with it the slot that its operand frees,
+// where the next tile was late.)
+// Where two products or warps may be a whole tile apart, each buffer has a barrier of its own:
+// a wait by parity tells a phase from the next, not from the one after it.
 #pragma once
 
 #include "fa_fwd_kernel.cuh"
@@ -32,6 +40,7 @@
 namespace fa {
 
 struct BwdParams {
+    const void* q;      // bf16
     const void* o;      // bf16, as q
     const void* dout;   // bf16, as q
     const float* lse;   // equal length: [B*H, N]; variable length: [H, total_q]
@@ -49,6 +58,8 @@ struct BwdParams {
     int heads;
     int B, total_q, total_k;
     int q_tiles, k_tiles;  // 128-row blocks of a launch per head: of each sequence, or (packed) of all of them
+    int q_units, k_units;  // blocks of all heads
+    unsigned* next;        // counters of the units taken (dq, dkv), zero at the start; null: one unit per block
     int packed;            // variable length: blocks are numbered through all sequences (bit 0: dq, bit 1: dkv)
 };
 
@@ -139,34 +150,42 @@ __device__ __forceinline__ long long bwd_stat(const BwdParams& p, const BwdUnit&
     return static_cast<long long>(w.bh) * p.N + row;
 }
 
-template <int D>
+constexpr int kBwdWarps = 16;  // elementwise
+constexpr int kBwdScore = 16, kBwdLoad = 17, kBwdGrad = 18, kBwdStat = 19;
+constexpr int kBwdDqThreads = 19 * 32, kBwdDkvThreads = 20 * 32;
+
+// Shared memory: the unit's two held tiles (dq: Q, dO; dkv: K, V), then two rings: the operand that both a score
+// product and a gradient product read (dq: K; dkv: Q), and the other (dq: V; dkv: dO), whose slots are free sooner.
+// (Q and dO as operands in TMEM, where d = 64 leaves room, halve what their products read of shared memory, but
+// measured 750 us for 673 of the dq kernel on 16384 x 16384 x 8 heads.)
+template <int D, bool DQ>
 struct BwdCfg {
-    static constexpr int kThreads = 384;
+    static constexpr int kD = D;
     static constexpr int kTileBytes = D * kBlockM * 2;
-    // The two held tiles (dq: Q, dO; dkv: K, V), then two rings: the operand that both a score product and a
-    // gradient product read (dq: K; dkv: Q), and the other (dq: V; dkv: dO), whose slots are free sooner.
-    static constexpr int kStagesA = D == 128 ? 3 : 4;
-    static constexpr int kStagesB = D == 128 ? 2 : 4;
-    static constexpr int kStatSlots = 2;
-    static constexpr int kOffHeld = 0;
+    static constexpr int kStagesA = D == 128 ? 3 : 5;
+    static constexpr int kStagesB = D == 128 ? 2 : 5;
+    static constexpr int kRoles = DQ ? 2 : 3;  // warps that take units beside the elementwise ones and the loader
+    static constexpr uint32_t kReadersB = DQ ? 1 : 2;  // (dO serves dPᵀ and dV, in either order)
+    static constexpr uint32_t kArrivalsS = DQ ? 1 : 2;  // (dkv: a score tile is there when LSE and δ are too)
+    static constexpr uint32_t kReadersHeld = DQ ? 1 + kBwdWarps : 1;  // (dq: δ is made of the held dO)
     static constexpr int kOffA = 2 * kTileBytes;
     static constexpr int kOffB = kOffA + kStagesA * kTileBytes;
-    static constexpr int kOffStat = kOffB + kStagesB * kTileBytes;  // fp32 [slot][2][128]
-    static constexpr int kOffBar = kOffStat + kStatSlots * 2 * kBlockM * 4;
-    static constexpr int kNumBars = 17 + 2 * kStagesA + 2 * kStagesB;
-    static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM slot, abort flag
+    static constexpr int kOffStat = kOffB + kStagesB * kTileBytes;  // fp32 [slot][2][128]: -LSE·log2 e and -δ
+    static constexpr int kOffBar = kOffStat + 2 * 2 * kBlockM * 4;
+    static constexpr int kFixedBars = 29;
+    static constexpr int kNumBars = kFixedBars + 2 * kStagesA + 2 * kStagesB;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM slot, abort flag, unit queue
     // A block's shared memory starts on a 1024-byte boundary in practice; kSlack would move it there from any
-    // 256-byte one (the kernels look, and report instead of running past the end).
-    static constexpr int kSlack = 768;
-    static constexpr int kSmemBytes = kOffMisc + 8 + kSlack;
+    // 512-byte one (the kernels look, and report instead of running past the end).
+    static constexpr int kSlack = 512;
+    static constexpr int kSmemBytes = kOffMisc + 16 + kSlack;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static_assert(kOffBar % 8 == 0);
-    static constexpr uint32_t kTmemS = 0, kTmemDp = 128;
 };
 
-template <int D>
+template <int D, bool DQ>
 struct BwdSmem {
-    using Cfg = BwdCfg<D>;
+    using Cfg = BwdCfg<D, DQ>;
     static constexpr int A = Cfg::kStagesA, B = Cfg::kStagesB;
     uint8_t* base;
     uint32_t sbase;
@@ -179,24 +198,29 @@ struct BwdSmem {
     }
     __device__ __forceinline__ uint32_t bar(int i) const { return sbase + Cfg::kOffBar + 8u * i; }
     __device__ __forceinline__ uint32_t held_full() const { return bar(0); }
-    __device__ __forceinline__ uint32_t fix() const { return bar(1); }  // a load whose tail is zeroed before use
-    __device__ __forceinline__ uint32_t s_full() const { return bar(2); }
-    __device__ __forceinline__ uint32_t s_free() const { return bar(3); }
-    __device__ __forceinline__ uint32_t dp_full() const { return bar(4); }
-    __device__ __forceinline__ uint32_t dp_free() const { return bar(5); }
-    __device__ __forceinline__ uint32_t p_full() const { return bar(6); }
-    __device__ __forceinline__ uint32_t ds_full() const { return bar(7); }
-    __device__ __forceinline__ uint32_t p_free() const { return bar(8); }
-    __device__ __forceinline__ uint32_t ds_free(int b) const { return bar(9 + b); }
-    __device__ __forceinline__ uint32_t acc_full() const { return bar(11); }
-    __device__ __forceinline__ uint32_t fin() const { return bar(12); }
-    __device__ __forceinline__ uint32_t stat_full(int i) const { return bar(13 + i); }
-    __device__ __forceinline__ uint32_t stat_free(int i) const { return bar(15 + i); }
-    __device__ __forceinline__ uint32_t a_full(int i) const { return bar(17 + i); }
-    __device__ __forceinline__ uint32_t a_free(int i) const { return bar(17 + A + i); }
-    __device__ __forceinline__ uint32_t b_full(int i) const { return bar(17 + 2 * A + i); }
-    __device__ __forceinline__ uint32_t b_free(int i) const { return bar(17 + 2 * A + B + i); }
-    __device__ __forceinline__ uint32_t held(int i) const { return sbase + Cfg::kOffHeld + i * Cfg::kTileBytes; }
+    __device__ __forceinline__ uint32_t held_free() const { return bar(1); }
+    __device__ __forceinline__ uint32_t fix() const { return bar(2); }  // a load whose tail is zeroed before use
+    __device__ __forceinline__ uint32_t s_full(int b) const { return bar(3 + b); }
+    __device__ __forceinline__ uint32_t s_free() const { return bar(5); }
+    __device__ __forceinline__ uint32_t dp_full() const { return bar(6); }
+    __device__ __forceinline__ uint32_t dp_free() const { return bar(7); }
+    __device__ __forceinline__ uint32_t p_full(int b) const { return bar(8 + b); }
+    __device__ __forceinline__ uint32_t p_free(int b) const { return bar(10 + b); }
+    __device__ __forceinline__ uint32_t ds_full(int b) const { return bar(12 + b); }
+    __device__ __forceinline__ uint32_t ds_free(int b) const { return bar(14 + b); }
+    __device__ __forceinline__ uint32_t s_issued() const { return bar(16); }
+    __device__ __forceinline__ uint32_t acc_full() const { return bar(17); }
+    __device__ __forceinline__ uint32_t acc_free() const { return bar(18); }
+    __device__ __forceinline__ uint32_t fin(int m) const { return bar(19 + m); }
+    __device__ __forceinline__ uint32_t stat_full(int i) const { return bar(21 + i); }
+    __device__ __forceinline__ uint32_t stat_free(int i) const { return bar(23 + i); }
+    __device__ __forceinline__ uint32_t u_full(int i) const { return bar(25 + i); }
+    __device__ __forceinline__ uint32_t u_free(int i) const { return bar(27 + i); }
+    __device__ __forceinline__ uint32_t a_full(int i) const { return bar(Cfg::kFixedBars + i); }
+    __device__ __forceinline__ uint32_t a_free(int i) const { return bar(Cfg::kFixedBars + A + i); }
+    __device__ __forceinline__ uint32_t b_full(int i) const { return bar(Cfg::kFixedBars + 2 * A + i); }
+    __device__ __forceinline__ uint32_t b_free(int i) const { return bar(Cfg::kFixedBars + 2 * A + B + i); }
+    __device__ __forceinline__ uint32_t held(int i) const { return sbase + i * Cfg::kTileBytes; }
     __device__ __forceinline__ int a_off(int i) const { return Cfg::kOffA + i * Cfg::kTileBytes; }
     __device__ __forceinline__ int b_off(int i) const { return Cfg::kOffB + i * Cfg::kTileBytes; }
     __device__ __forceinline__ float* stat(int slot, int which) const {
@@ -206,16 +230,60 @@ struct BwdSmem {
     __device__ __forceinline__ volatile int* abort_flag() const {
         return reinterpret_cast<volatile int*>(base + Cfg::kOffMisc + 4);
     }
+    __device__ __forceinline__ volatile int* unit_slot(int i) const {
+        return reinterpret_cast<volatile int*>(base + Cfg::kOffMisc + 8) + i;
+    }
 };
+
+// What a role waits with.
+struct BwdWait {
+    volatile int* abort_flag;
+    unsigned long long lim;
+    // A whole warp waits for the n-th phase (0, 1, ..) of a barrier; false if the wait gave up.
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t n, unsigned site) const {
+        return __all_sync(0xffffffffu, wait_phase(bar, n & 1, abort_flag, site, lim));
+    }
+};
+
+template <class Smem>
+__device__ __forceinline__ void bwd_init_barriers(const Smem& sm, int lane) {
+    using Cfg = typename Smem::Cfg;
+    for (int i = lane; i < Cfg::kNumBars; i += 32) {
+        const uint32_t b = sm.bar(i);
+        uint32_t count = 1;
+        if (b == sm.s_free() || b == sm.dp_free() || b == sm.acc_free()) count = kBwdWarps;
+        for (int k = 0; k < 2; ++k) {
+            if (b == sm.p_full(k) || b == sm.ds_full(k) || b == sm.stat_free(k)) count = kBwdWarps;
+            if (b == sm.s_full(k)) count = Cfg::kArrivalsS;
+            if (b == sm.u_free(k)) count = kBwdWarps + Cfg::kRoles;
+        }
+        if (b == sm.held_full()) count = 2;
+        if (b == sm.held_free()) count = Cfg::kReadersHeld;
+        if (b >= sm.b_free(0)) count = Cfg::kReadersB;  // (the last barriers)
+        ptx::mbar_init(b, count);
+    }
+    if (lane == 0) *sm.abort_flag() = 0;
+    ptx::fence_mbar_init();
+}
+
+// The block's it-th unit; -1: no more, -2: the wait gave up.
+template <class Smem>
+__device__ __forceinline__ int bwd_next(const Smem& sm, const BwdWait& wait, uint32_t it, int lane) {
+    if (!wait(sm.u_full(it & 1), it >> 1, kStatusTimeoutOther)) return -2;
+    const int u = *sm.unit_slot(it & 1);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(sm.u_free(it & 1));
+    return u;
+}
 
 // Loads a tile of 128 rows, from row `row` of the sequence at token t0 with n rows, into `off`, completing `full`.
 // VARLEN: rows past the sequence's end are another's, or no one's (padding): they are zeroed before `full`
 // completes, so that a weight of zero never meets a NaN there.
-template <int D, bool VARLEN>
+template <class Smem, bool VARLEN>
 struct BwdLoader {
-    const BwdSmem<D>& sm;
-    volatile int* abort_flag;
-    unsigned long long lim;
+    static constexpr int D = Smem::Cfg::kD;
+    const Smem& sm;
+    const BwdWait& wait;
     int lane;
     uint32_t fixes = 0;
 
@@ -224,12 +292,12 @@ struct BwdLoader {
         const int y = VARLEN ? w.head : row, z = VARLEN ? t0 + row : w.bh;
         const bool ragged = VARLEN && row + kBlockM > n;
         const uint32_t bar = ragged ? sm.fix() : full;
-        ptx::mbar_arrive_expect_tx_elect(bar, BwdCfg<D>::kTileBytes);
+        ptx::mbar_arrive_expect_tx_elect(bar, Smem::Cfg::kTileBytes);
 #pragma unroll
         for (int c = 0; c < D / kBoxCols; ++c)
             ptx::tma_load_3d_hint_elect(sm.sbase + off + c * kBoxBytes, &map, bar, c * kBoxCols, y, z, policy);
         if (ragged) {
-            const bool ok = wait_phase_warp(sm.fix(), fixes & 1, abort_flag, kStatusTimeoutLoad, lim);
+            const bool ok = wait(sm.fix(), fixes, kStatusTimeoutLoad);
             ++fixes;
             if (!ok) return false;
             // a box's rows are 128 bytes each, in order: the swizzle moves chunks within a row
@@ -245,6 +313,81 @@ struct BwdLoader {
     }
 };
 
+// The loading role: claims units, hands them to the other roles one ahead, and loads their tiles. `range(w)` sets a
+// unit's walk; held(loader, w) loads its two held tiles, pair(loader, w, i, sa, sb, which) a tile of its walk.
+template <bool VARLEN, bool QUERIES, class Smem, class Range, class Held, class Pair>
+__device__ __forceinline__ void bwd_load_role(const Smem& sm, const BwdWait& wait, const BwdParams& p, int lane,
+                                              Range&& range, Held&& held, Pair&& pair) {
+    using Cfg = typename Smem::Cfg;
+    constexpr unsigned long long kDrainNs = 100000000ull;
+    const int units = QUERIES ? p.q_units : p.k_units;
+    BwdLoader<Smem, VARLEN> load{sm, wait, lane};
+    uint32_t cnt = 0, a_cnt = 0, b_cnt = 0, helds = 0;
+    bool ok = true;
+    // the next unit with rows, from u on
+    auto settle = [&](int u, BwdUnit& w) {
+        while (u < units && !bwd_unit<VARLEN, QUERIES>(p, u, w)) {
+            if (p.next == nullptr) return units;
+            u = 0;
+            if (lane == 0) u = static_cast<int>(atomicAdd(p.next + (QUERIES ? 0 : 1), 1u) + gridDim.x);
+            u = __shfl_sync(0xffffffffu, u, 0);
+        }
+        return min(u, units);
+    };
+    auto publish = [&](uint32_t it, int u) {
+        if (it >= 2 && !wait(sm.u_free(it & 1), (it >> 1) - 1, kStatusTimeoutOther)) return false;
+        if (lane == 0) {
+            *sm.unit_slot(it & 1) = u < units ? u : -1;
+            ptx::mbar_arrive(sm.u_full(it & 1));
+        }
+        __syncwarp();
+        return true;
+    };
+    BwdUnit w, ahead;
+    int u = settle(static_cast<int>(blockIdx.x), w);
+    ok = publish(0, u);
+    for (uint32_t it = 0; ok && u < units; ++it) {
+        range(w);
+        int next = units;
+        bool handed = false;
+        auto hand_on = [&]() {
+            if (p.next != nullptr) {
+                if (lane == 0) next = static_cast<int>(atomicAdd(p.next + (QUERIES ? 0 : 1), 1u) + gridDim.x);
+                next = settle(__shfl_sync(0xffffffffu, next, 0), ahead);
+            }
+            handed = true;
+            return publish(it + 1, next);
+        };
+        if (w.n > 0) {
+            ok = helds == 0 || wait(sm.held_free(), helds - 1, kStatusTimeoutFree);
+            if (ok) ok = held(load, w);
+            ++helds;
+        }
+        for (int i = 0; i < w.n && ok; ++i, ++cnt) {
+            const uint32_t sa = cnt % Cfg::kStagesA, sb = cnt % Cfg::kStagesB;
+            ok = cnt < Cfg::kStagesA || wait(sm.a_free(sa), cnt / Cfg::kStagesA - 1, kStatusTimeoutFree);
+            if (ok) ok = pair(load, w, i, sa, sb, 0);
+            if (!ok) break;
+            ++a_cnt;
+            ok = cnt < Cfg::kStagesB || wait(sm.b_free(sb), cnt / Cfg::kStagesB - 1, kStatusTimeoutFree);
+            if (ok) ok = pair(load, w, i, sa, sb, 1);
+            if (!ok) break;
+            ++b_cnt;
+            if (i == 1) ok = hand_on();  // (the claim's latency behind the first loads)
+        }
+        if (ok && !handed) ok = hand_on();
+        u = next;
+        w = ahead;
+    }
+    if (ok) return;
+    // a block that gave up on something exits only when its copies in flight have landed
+    if (helds > 0) wait_drain(sm.held_full(), (helds - 1) & 1, kDrainNs);
+    for (uint32_t i = a_cnt > Cfg::kStagesA ? a_cnt - Cfg::kStagesA : 0; i < a_cnt; ++i)
+        wait_drain(sm.a_full(i % Cfg::kStagesA), (i / Cfg::kStagesA) & 1, kDrainNs);
+    for (uint32_t i = b_cnt > Cfg::kStagesB ? b_cnt - Cfg::kStagesB : 0; i < b_cnt; ++i)
+        wait_drain(sm.b_full(i % Cfg::kStagesB), (i / Cfg::kStagesB) & 1, kDrainNs);
+}
+
 // D[128 x 128] = A·Bᵀ over D: both K-major tiles.
 template <int D>
 __device__ __forceinline__ void bwd_score_mma(uint32_t d_tmem, uint32_t a, uint32_t b) {
@@ -257,55 +400,35 @@ __device__ __forceinline__ void bwd_score_mma(uint32_t d_tmem, uint32_t a, uint3
     }
 }
 
-// D[128 x D] (+)= A·B over 128: A in TMEM, its first 64 values of a row at a_tmem and the others at a_tmem + second;
-// B an MN-major tile.
+// D[128 x D] (+)= A·B over 128: A in TMEM, 16 packed columns for each 32 values of a row, `pitch` columns apart; B an
+// MN-major tile.
 template <int D>
-__device__ __forceinline__ void bwd_grad_mma(uint32_t d_tmem, uint32_t a_tmem, uint32_t second, uint32_t b,
+__device__ __forceinline__ void bwd_grad_mma(uint32_t d_tmem, uint32_t a_tmem, uint32_t pitch, uint32_t b,
                                              bool accumulate) {
     constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(128, D, false, true);
     const uint64_t b0 = ptx::sdesc_sw128(b, kBoxBytes, 1024);
 #pragma unroll
     for (int kk = 0; kk < kBlockN / 16; ++kk)
-        ptx::mma_ts_elect(d_tmem, a_tmem + (kk < 4 ? kk * 8 : second + (kk - 4) * 8),
+        ptx::mma_ts_elect(d_tmem, a_tmem + (kk >> 1) * pitch + (kk & 1) * 8,
                           b0 + static_cast<uint32_t>(kk * (2048 >> 4)), kIdesc, accumulate || kk > 0 ? 1u : 0u);
 }
 
-// ds = p (dp - δ) over 64 columns of dP, packed to bf16 pairs; delta(c) gives the pair of δ of columns c, c + 1.
-template <class Delta>
-__device__ __forceinline__ void bwd_ds(const float (&p)[64], uint32_t dp_addr, uint32_t (&r)[32], Delta&& delta) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t x[32];
-        ptx::tmem_ld_32x32b_x32(dp_addr + h * 32, x);
-        ptx::tmem_wait_ld(x);
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            const float2 nd = delta(h * 32 + c);
-            const float2 t = ptx::fadd2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), nd);
-            const float2 ds = ptx::fmul2(make_float2(p[h * 32 + c], p[h * 32 + c + 1]), t);
-            r[(h * 32 + c) / 2] = ptx::pack_bf16x2(ds.x, ds.y);
-        }
-    }
-}
-
-// n columns (a multiple of 32) of an accumulator, times f, to bf16 at `to`.
+// COLS columns of an accumulator, times f, to bf16 at `to`.
 template <int COLS>
 __device__ __forceinline__ void bwd_store(uint32_t taddr, float f, void* to, bool have) {
 #pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
-        uint32_t x[32];
-        ptx::tmem_ld_32x32b_x32(taddr + c, x);
+    for (int c = 0; c < COLS; c += 16) {
+        uint32_t x[8], y[8];
+        ptx::tmem_ld_32x32b_x8(taddr + c, x);
+        ptx::tmem_ld_32x32b_x8(taddr + c + 8, y);
         ptx::tmem_wait_ld(x);
+        ptx::tmem_wait_ld(y);
         if (!have) continue;
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-            uint4 v;
-            auto two = [&](int k) {
-                return ptx::pack_bf16x2(__uint_as_float(x[i + k]) * f, __uint_as_float(x[i + k + 1]) * f);
-            };
-            v.x = two(0), v.y = two(2), v.z = two(4), v.w = two(6);
-            reinterpret_cast<uint4*>(to)[(c + i) / 8] = v;
-        }
+        auto two = [&](const uint32_t(&v)[8], int k) {
+            return ptx::pack_bf16x2(__uint_as_float(v[k]) * f, __uint_as_float(v[k + 1]) * f);
+        };
+        reinterpret_cast<uint4*>(to)[c / 8] = make_uint4(two(x, 0), two(x, 2), two(x, 4), two(x, 6));
+        reinterpret_cast<uint4*>(to)[c / 8 + 1] = make_uint4(two(y, 0), two(y, 2), two(y, 4), two(y, 6));
     }
 }
 
@@ -315,453 +438,564 @@ __device__ __forceinline__ void bwd_store_zero(void* to) {
     for (int c = 0; c < COLS; c += 8) reinterpret_cast<uint4*>(to)[c / 8] = make_uint4(0, 0, 0, 0);
 }
 
-// Barrier counts: 8 where every elementwise warp arrives, else 1.
-template <int D>
-__device__ __forceinline__ void bwd_init_barriers(const BwdSmem<D>& sm, int lane) {
-    for (int i = lane; i < BwdCfg<D>::kNumBars; i += 32) {
-        const uint32_t b = sm.bar(i);
-        const bool eight = b == sm.s_free() || b == sm.dp_free() || b == sm.p_full() || b == sm.ds_full() ||
-                           b == sm.stat_free(0) || b == sm.stat_free(1);
-        // (the held tiles are two loads)
-        ptx::mbar_init(b, eight ? 8 : b == sm.held_full() ? 2 : 1);
+constexpr uint32_t kBwdBarPair = 1;
+
+// Ends an MMA-issuing warp: every MMA that it issued is done before TMEM is freed.
+template <class Smem>
+__device__ __forceinline__ void bwd_drain_mmas(const Smem& sm, int m, int lane) {
+    __syncwarp();
+    if (lane == 0) {
+        ptx::mma_commit(sm.fin(m));
+        wait_drain(sm.fin(m), 0, 100000000ull);
     }
-    if (lane == 0) *sm.abort_flag() = 0;
-    ptx::fence_mbar_init();
+    __syncwarp();
 }
 
-// Waits until copies in flight have landed before a block that gave up on something else exits.
-template <int D>
-__device__ __forceinline__ void bwd_drain_loads(const BwdSmem<D>& sm, uint32_t a_cnt, uint32_t b_cnt) {
-    constexpr unsigned long long kDrainNs = 100000000ull;
-    for (uint32_t i = a_cnt > BwdCfg<D>::kStagesA ? a_cnt - BwdCfg<D>::kStagesA : 0; i < a_cnt; ++i)
-        wait_drain(sm.a_full(i % BwdCfg<D>::kStagesA), (i / BwdCfg<D>::kStagesA) & 1, kDrainNs);
-    for (uint32_t i = b_cnt > BwdCfg<D>::kStagesB ? b_cnt - BwdCfg<D>::kStagesB : 0; i < b_cnt; ++i)
-        wait_drain(sm.b_full(i % BwdCfg<D>::kStagesB), (i / BwdCfg<D>::kStagesB) & 1, kDrainNs);
+// Start of a block: whether it may go on, the barriers and TMEM.
+template <class Smem>
+__device__ __forceinline__ bool bwd_begin(const Smem& sm, int warp, int lane) {
+    ptx::griddep_launch_dependents();
+    if (!sm.fits) {
+        if (threadIdx.x == 0) atomicOr(&g_status, static_cast<unsigned>(kStatusTimeoutOther));
+        return false;
+    }
+    if (warp == kBwdScore) {
+        ptx::tmem_alloc(ptx::smem_u32(sm.tmem_slot()), 512);
+        ptx::tmem_relinquish();
+    }
+    if (warp == kBwdLoad) bwd_init_barriers(sm, lane);
+    ptx::griddep_wait();
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    return true;
 }
 
-constexpr uint32_t kBwdBarPair = 1, kBwdBarAll = 15;
+__device__ __forceinline__ void bwd_end(uint32_t tmem, int warp) {
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kBwdScore) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// What a thread brings of a query unit before its walk: a quarter of its query's row of O, LSE and dLSE. Loaded a unit
+// ahead, behind the last products of the one before.
+template <int D, bool VARLEN>
+struct BwdRow {
+    uint4 o[D / 32];
+    float lse, dlse;
+    long long stat;
+    bool have;
+
+    __device__ __forceinline__ void load(const BwdParams& p, const BwdUnit& w, int part, int row) {
+        have = w.r0 + row < w.nq;
+        const int at_row = have ? w.r0 + row : w.r0;
+        const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.o) +
+                                                           bwd_row<D, VARLEN>(p, w, w.tq0, at_row) + part * (D / 4));
+        stat = bwd_stat<VARLEN>(p, w, at_row);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] = from[i];
+        lse = p.lse[stat];
+        dlse = p.dlse ? p.dlse[stat] : 0.f;
+    }
+    // O·dO of the quarter; `tile`: dO in shared memory (boxes of 64 columns, 128-byte swizzle)
+    __device__ __forceinline__ float dot(const uint8_t* tile, int part, int row) const {
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const int chunk = part * (D / 32) + i;
+            const uint4 y = *reinterpret_cast<const uint4*>(tile + (chunk >> 3) * kBoxBytes + sw128_offset(row, chunk & 7));
+            const uint32_t xs[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum = ptx::ffma2(ptx::unpack_bf16x2(xs[k]), ptx::unpack_bf16x2(ys[k]), sum);
+        }
+        return sum.x + sum.y;
+    }
+};
 
 // ---------------------------------------------------------------- dQ (and δ)
 // TMEM: S [0, 128), dP [128, 256), dQ [256, 256 + D), dS in two buffers [384, 448), [448, 512).
 template <int D, bool CAUSAL, bool VARLEN>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(kBwdDqThreads, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                      const BwdParams p) {
-    using Cfg = BwdCfg<D>;
-    constexpr uint32_t kTmemDq = 256, kTmemDs = 384;
-    const BwdSmem<D> sm;
+    using Smem = BwdSmem<D, true>;
+    using Cfg = typename Smem::Cfg;
+    constexpr uint32_t kTmemS = 0, kTmemDp = 128, kTmemDq = 256, kTmemDs = 384;
+    const Smem sm;
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-    const unsigned long long lim = p.wait_limit_ns;
-    volatile int* abort_flag = sm.abort_flag();
-    ptx::griddep_launch_dependents();
-    if (!sm.fits) {
-        if (threadIdx.x == 0) atomicOr(&g_status, static_cast<unsigned>(kStatusTimeoutOther));
-        return;
-    }
-    ptx::griddep_wait();
-    BwdUnit w;
-    if (!bwd_unit<VARLEN, true>(p, static_cast<int>(blockIdx.x), w)) return;
-    w.n = kv_tiles<CAUSAL>(w.r0 / kBlockM, w.nq, w.nk);
-    if (warp == 8) {
-        ptx::tmem_alloc(ptx::smem_u32(sm.tmem_slot()), 512);
-        ptx::tmem_relinquish();
-    }
-    if (warp == 9) bwd_init_barriers(sm, lane);
-    ptx::tc_fence_before_sync();
-    __syncthreads();
-    ptx::tc_fence_after_sync();
+    if (!bwd_begin(sm, warp, lane)) return;
     const uint32_t tmem = *sm.tmem_slot();
+    const BwdWait wait{sm.abort_flag(), p.wait_limit_ns};
+    auto range = [&](BwdUnit& w) { w.n = kv_tiles<CAUSAL>(w.r0 / kBlockM, w.nq, w.nk); };
+    auto unit = [&](int u) {
+        BwdUnit w;
+        bwd_unit<VARLEN, true>(p, u, w);
+        range(w);
+        return w;
+    };
+    uint32_t t = 0, full_units = 0;  // tiles and units with tiles before this one
 
-    if (warp == 9) {
-        // ---- loads
-        BwdLoader<D, VARLEN> load{sm, abort_flag, lim, lane};
+    if (warp == kBwdLoad) {
         const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
-        uint32_t a_cnt = 0, b_cnt = 0;
+        using Load = BwdLoader<Smem, VARLEN>;
+        bwd_load_role<VARLEN, true>(
+            sm, wait, p, lane, range,
+            [&](Load& load, const BwdUnit& w) {
+                return load.tile(tm_q, w, w.tq0, w.nq, w.r0, 0, sm.held_full(), once) &&
+                       load.tile(tm_do, w, w.tq0, w.nq, w.r0, Cfg::kTileBytes, sm.held_full(), once);
+            },
+            [&](Load& load, const BwdUnit& w, int j, uint32_t sa, uint32_t sb, int which) {
+                return which == 0
+                           ? load.tile(tm_k, w, w.tk0, w.nk, j * kBlockN, sm.a_off(sa), sm.a_full(sa), keep)
+                           : load.tile(tm_v, w, w.tk0, w.nk, j * kBlockN, sm.b_off(sb), sm.b_full(sb), keep);
+            });
+    } else if (warp == kBwdScore) {
+        // ---- S and dP, as soon as the elementwise warps have read those of the tile before
         bool ok = true;
-        if (w.n > 0)
-            ok = load.tile(tm_q, w, w.tq0, w.nq, w.r0, Cfg::kOffHeld, sm.held_full(), once) &&
-                 load.tile(tm_do, w, w.tq0, w.nq, w.r0, Cfg::kOffHeld + Cfg::kTileBytes, sm.held_full(), once);
-        for (int j = 0; j < w.n && ok; ++j) {
-            const int sa = j % Cfg::kStagesA, sb = j % Cfg::kStagesB;
-            ok = wait_phase_warp(sm.a_free(sa), ((j / Cfg::kStagesA) & 1) ^ 1, abort_flag, kStatusTimeoutFree, lim);
-            if (!ok) break;
-            ok = load.tile(tm_k, w, w.tk0, w.nk, j * kBlockN, sm.a_off(sa), sm.a_full(sa), keep);
-            if (!ok) break;
-            ++a_cnt;
-            ok = wait_phase_warp(sm.b_free(sb), ((j / Cfg::kStagesB) & 1) ^ 1, abort_flag, kStatusTimeoutFree, lim);
-            if (!ok) break;
-            ok = load.tile(tm_v, w, w.tk0, w.nk, j * kBlockN, sm.b_off(sb), sm.b_full(sb), keep);
-            if (ok) ++b_cnt;
-        }
-        if (!ok) bwd_drain_loads(sm, a_cnt, b_cnt);
-    } else if (warp == 8) {
-        // ---- MMAs: S(j+1) and dP(j+1) as soon as the elementwise warps have read those of j, then dQ += dS(j)·K(j)
-        bool ok = w.n == 0 || wait_phase_warp(sm.held_full(), 0, abort_flag, kStatusTimeoutLoad, lim);
-        auto scores = [&](int j) {
-            const int sa = j % Cfg::kStagesA, sb = j % Cfg::kStagesB;
-            if (!wait_phase_warp(sm.a_full(sa), (j / Cfg::kStagesA) & 1, abort_flag, kStatusTimeoutLoad, lim)) return false;
-            if (j > 0 && !wait_phase_warp(sm.s_free(), (j - 1) & 1, abort_flag, kStatusTimeoutSoftmax, lim)) return false;
-            ptx::tc_fence_after_sync();
-            bwd_score_mma<D>(tmem + Cfg::kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
-            ptx::mma_commit_elect(sm.s_full());
-            if (!wait_phase_warp(sm.b_full(sb), (j / Cfg::kStagesB) & 1, abort_flag, kStatusTimeoutLoad, lim)) return false;
-            if (j > 0 && !wait_phase_warp(sm.dp_free(), (j - 1) & 1, abort_flag, kStatusTimeoutSoftmax, lim)) return false;
-            ptx::tc_fence_after_sync();
-            bwd_score_mma<D>(tmem + Cfg::kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
-            ptx::mma_commit_elect(sm.dp_full());
-            ptx::mma_commit_elect(sm.b_free(sb));
-            return true;
-        };
-        if (ok && w.n > 0) ok = scores(0);
-        for (int j = 0; j < w.n && ok; ++j) {
-            if (j + 1 < w.n && !scores(j + 1)) break;
-            const int sa = j % Cfg::kStagesA;
-            ok = wait_phase_warp(sm.ds_full(), j & 1, abort_flag, kStatusTimeoutSoftmax, lim);
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            bwd_grad_mma<D>(tmem + kTmemDq, tmem + kTmemDs + (j & 1) * 64, 32, sm.sbase + sm.a_off(sa), j > 0);
-            ptx::mma_commit_elect(sm.ds_free(j & 1));
-            ptx::mma_commit_elect(sm.a_free(sa));
-        }
-        ptx::mma_commit_elect(sm.acc_full());
-        __syncwarp();
-        if (lane == 0) {
-            ptx::mma_commit(sm.fin());
-            wait_drain(sm.fin(), 0, 100000000ull);
-        }
-        __syncwarp();
-    } else if (warp < 8) {
-        // ---- elementwise: one query row per thread, 64 of a tile's keys
-        const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int q = w.r0 + row;
-        const bool have = q < w.nq;
-        const long long at = bwd_row<D, VARLEN>(p, w, w.tq0, have ? q : w.r0);
-        float delta = 0.f;
-        {
-            const uint4* o4 = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.o) + at + half * (D / 2));
-            const uint4* d4 = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + at + half * (D / 2));
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint4 x = o4[i], y = d4[i];
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sum = ptx::ffma2(ptx::unpack_bf16x2(xs[k]), ptx::unpack_bf16x2(ys[k]), sum);
-            }
-            sm.stat(0, half)[row] = sum.x + sum.y;
-            ptx::named_bar_sync(kBwdBarPair, 256);
-            delta = sm.stat(0, 0)[row] + sm.stat(0, 1)[row];
-        }
-        float nlse = -INFINITY;  // (P = 0)
-        if (have) {
-            const long long si = bwd_stat<VARLEN>(p, w, q);
-            const float lse = p.lse[si];
-            if (lse != -INFINITY) nlse = -lse * 1.44269504088896341f;
-            if (p.dlse) delta -= p.dlse[si];
-            if (half == 0) p.delta[si] = delta;
-        }
-        const float2 nd = make_float2(-delta, -delta), nl = make_float2(nlse, nlse);
-        const float2 cc = make_float2(p.scale_log2, p.scale_log2);
-        bool ok = true;
-        for (int j = 0; j < w.n; ++j) {
-            ok = __all_sync(0xffffffffu, wait_phase(sm.s_full(), j & 1, abort_flag, kStatusTimeoutMma, lim));
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            float s[64];
-            load_row64(tmem + Cfg::kTmemS + lanes + half * 64, s);
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.s_free());
-            const int key0 = j * kBlockN + half * 64;
-            const int off = w.nk - w.nq;
-            if (key0 + 64 > w.nk || (CAUSAL && key0 + 63 > w.r0 + off)) {
-                int last = w.nk - 1 - key0;
-                if (CAUSAL) last = min(last, q + off - key0);
-#pragma unroll
-                for (int c = 0; c < 64; ++c) s[c] = c > last ? -INFINITY : s[c];
-            }
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                const float2 x = ptx::ffma2(make_float2(s[c], s[c + 1]), cc, nl);
-                s[c] = ptx::ex2_approx(x.x);
-                s[c + 1] = ptx::ex2_approx(x.y);
-            }
-            ok = __all_sync(0xffffffffu, wait_phase(sm.dp_full(), j & 1, abort_flag, kStatusTimeoutMma, lim));
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            uint32_t r[32];
-            bwd_ds(s, tmem + Cfg::kTmemDp + lanes + half * 64, r, [&](int) { return nd; });
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.dp_free());
-            // dQ += dS·K of two tiles before has read this buffer
-            if (j >= 2) {
-                ok = __all_sync(0xffffffffu, wait_phase(sm.ds_free(j & 1), ((j >> 1) - 1) & 1, abort_flag,
-                                                        kStatusTimeoutMma, lim));
+        for (uint32_t it = 0; ok; ++it) {
+            const int u = bwd_next(sm, wait, it, lane);
+            if (u < 0) break;
+            const BwdUnit w = unit(u);
+            if (w.n == 0) continue;
+            ok = wait(sm.held_full(), full_units++, kStatusTimeoutLoad);
+            for (int j = 0; j < w.n && ok; ++j, ++t) {
+                const uint32_t sa = t % Cfg::kStagesA, sb = t % Cfg::kStagesB;
+                ok = wait(sm.a_full(sa), t / Cfg::kStagesA, kStatusTimeoutLoad) &&
+                     (t == 0 || wait(sm.s_free(), t - 1, kStatusTimeoutSoftmax));
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
+                bwd_score_mma<D>(tmem + kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
+                ptx::mma_commit_elect(sm.s_full(0));
+                ok = wait(sm.b_full(sb), t / Cfg::kStagesB, kStatusTimeoutLoad) &&
+                     (t == 0 || wait(sm.dp_free(), t - 1, kStatusTimeoutSoftmax));
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                bwd_score_mma<D>(tmem + kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
+                ptx::mma_commit_elect(sm.dp_full());
+                ptx::mma_commit_elect(sm.b_free(sb));
+                if (j + 1 == w.n) ptx::mma_commit_elect(sm.held_free());
             }
-            ptx::tmem_st_32x32b_x32(tmem + kTmemDs + (j & 1) * 64 + lanes + half * 32, r);
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.ds_full());
         }
-        uint16_t* to = static_cast<uint16_t*>(p.dq) + at + half * (D / 2);
-        if (w.n == 0) {
-            if (have) bwd_store_zero<D / 2>(to);
-        } else if (ok && __all_sync(0xffffffffu, wait_phase(sm.acc_full(), 0, abort_flag, kStatusTimeoutMma, lim)) &&
-                   *abort_flag == 0) {
-            ptx::tc_fence_after_sync();
-            bwd_store<D / 2>(tmem + kTmemDq + lanes + half * (D / 2), p.scale, to, have);
-        }
-    }
-    ptx::tc_fence_before_sync();
-    __syncthreads();
-    if (warp == 8) {
-        ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc(tmem, 512);
-    }
-}
-
-// ---------------------------------------------------------------- dK, dV
-// TMEM, d = 128: Sᵀ [0, 128) with P over it, dPᵀ [128, 256) with dS over it (each warp group writes only columns
-// that it alone has read), dV, dK. The next Sᵀ waits for dV += P·dO to have read P, the next dPᵀ for dK += dS·Q.
-// d = 64: P [256, 320) and dS [320, 384) have columns of their own, dV [384, 448), dK [448, 512).
-template <int D, bool CAUSAL, bool VARLEN>
-__global__ void __launch_bounds__(384, 1)
-    fa_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-                      const BwdParams p) {
-    using Cfg = BwdCfg<D>;
-    constexpr bool kOver = D == 128;
-    constexpr uint32_t kTmemP = kOver ? Cfg::kTmemS : 256, kTmemDs = kOver ? Cfg::kTmemDp : 320;
-    constexpr uint32_t kSecond = kOver ? 64 : 32;  // columns from the first 64 queries' pairs to the others'
-    constexpr uint32_t kTmemDv = kOver ? 256 : 384, kTmemDk = kTmemDv + D;
-    const BwdSmem<D> sm;
-    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-    const unsigned long long lim = p.wait_limit_ns;
-    volatile int* abort_flag = sm.abort_flag();
-    ptx::griddep_launch_dependents();
-    if (!sm.fits) {
-        if (threadIdx.x == 0) atomicOr(&g_status, static_cast<unsigned>(kStatusTimeoutOther));
-        return;
-    }
-    ptx::griddep_wait();
-    BwdUnit w;
-    if (!bwd_unit<VARLEN, false>(p, static_cast<int>(blockIdx.x), w)) return;
-    const int off = w.nk - w.nq;
-    {
-        // the query tiles with a query that sees the block's first key
-        const int tiles = (w.nq + kBlockM - 1) / kBlockM;
-        w.first = CAUSAL ? min(max(w.r0 - off, 0) / kBlockM, tiles) : 0;
-        w.n = tiles - w.first;
-    }
-    if (warp == 8) {
-        ptx::tmem_alloc(ptx::smem_u32(sm.tmem_slot()), 512);
-        ptx::tmem_relinquish();
-    }
-    if (warp == 9) bwd_init_barriers(sm, lane);
-    ptx::tc_fence_before_sync();
-    __syncthreads();
-    ptx::tc_fence_after_sync();
-    const uint32_t tmem = *sm.tmem_slot();
-
-    if (warp == 9) {
-        // ---- loads
-        BwdLoader<D, VARLEN> load{sm, abort_flag, lim, lane};
-        const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
-        uint32_t a_cnt = 0, b_cnt = 0;
+        bwd_drain_mmas(sm, 0, lane);
+    } else if (warp == kBwdGrad) {
+        // ---- dQ += dS·K  (K is there: S was made of it, which dS follows)
         bool ok = true;
-        if (w.n > 0)
-            ok = load.tile(tm_k, w, w.tk0, w.nk, w.r0, Cfg::kOffHeld, sm.held_full(), once) &&
-                 load.tile(tm_v, w, w.tk0, w.nk, w.r0, Cfg::kOffHeld + Cfg::kTileBytes, sm.held_full(), once);
-        for (int i = 0; i < w.n && ok; ++i) {
-            const int sa = i % Cfg::kStagesA, sb = i % Cfg::kStagesB, row = (w.first + i) * kBlockM;
-            ok = wait_phase_warp(sm.a_free(sa), ((i / Cfg::kStagesA) & 1) ^ 1, abort_flag, kStatusTimeoutFree, lim);
-            if (!ok) break;
-            ok = load.tile(tm_q, w, w.tq0, w.nq, row, sm.a_off(sa), sm.a_full(sa), keep);
-            if (!ok) break;
-            ++a_cnt;
-            ok = wait_phase_warp(sm.b_free(sb), ((i / Cfg::kStagesB) & 1) ^ 1, abort_flag, kStatusTimeoutFree, lim);
-            if (!ok) break;
-            ok = load.tile(tm_do, w, w.tq0, w.nq, row, sm.b_off(sb), sm.b_full(sb), keep);
-            if (ok) ++b_cnt;
-        }
-        if (!ok) bwd_drain_loads(sm, a_cnt, b_cnt);
-    } else if (warp == 8) {
-        // ---- MMAs
-        bool ok = w.n == 0 || wait_phase_warp(sm.held_full(), 0, abort_flag, kStatusTimeoutLoad, lim);
-        auto issue_s = [&](int i) {  // Sᵀ(i) = K·Q(i)ᵀ
-            const int sa = i % Cfg::kStagesA;
-            if (!wait_phase_warp(sm.a_full(sa), (i / Cfg::kStagesA) & 1, abort_flag, kStatusTimeoutLoad, lim)) return false;
-            if (i > 0 && !wait_phase_warp(kOver ? sm.p_free() : sm.s_free(), (i - 1) & 1, abort_flag,
-                                          kStatusTimeoutSoftmax, lim))
-                return false;
-            ptx::tc_fence_after_sync();
-            bwd_score_mma<D>(tmem + Cfg::kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
-            ptx::mma_commit_elect(sm.s_full());
-            return true;
-        };
-        auto issue_dp = [&](int i) {  // dPᵀ(i) = V·dO(i)ᵀ
-            const int sb = i % Cfg::kStagesB;
-            if (!wait_phase_warp(sm.b_full(sb), (i / Cfg::kStagesB) & 1, abort_flag, kStatusTimeoutLoad, lim)) return false;
-            if (i > 0 && !wait_phase_warp(kOver ? sm.ds_free(0) : sm.dp_free(), (i - 1) & 1, abort_flag,
-                                          kStatusTimeoutSoftmax, lim))
-                return false;
-            ptx::tc_fence_after_sync();
-            bwd_score_mma<D>(tmem + Cfg::kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
-            ptx::mma_commit_elect(sm.dp_full());
-            return true;
-        };
-        if (ok && w.n > 0) ok = issue_s(0) && issue_dp(0);
-        for (int i = 0; i < w.n && ok; ++i) {
-            const int sa = i % Cfg::kStagesA, sb = i % Cfg::kStagesB;
-            if (!kOver && i + 1 < w.n && !(ok = issue_s(i + 1))) break;
-            ok = wait_phase_warp(sm.p_full(), i & 1, abort_flag, kStatusTimeoutSoftmax, lim);
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            bwd_grad_mma<D>(tmem + kTmemDv, tmem + kTmemP, kSecond, sm.sbase + sm.b_off(sb), i > 0);
-            ptx::mma_commit_elect(sm.p_free());
-            ptx::mma_commit_elect(sm.b_free(sb));
-            if (i + 1 < w.n && !(ok = kOver ? issue_s(i + 1) : issue_dp(i + 1))) break;
-            ok = wait_phase_warp(sm.ds_full(), i & 1, abort_flag, kStatusTimeoutSoftmax, lim);
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            bwd_grad_mma<D>(tmem + kTmemDk, tmem + kTmemDs, kSecond, sm.sbase + sm.a_off(sa), i > 0);
-            ptx::mma_commit_elect(sm.ds_free(0));
-            ptx::mma_commit_elect(sm.a_free(sa));
-            if (kOver && i + 1 < w.n && !(ok = issue_dp(i + 1))) break;
-        }
-        ptx::mma_commit_elect(sm.acc_full());
-        __syncwarp();
-        if (lane == 0) {
-            ptx::mma_commit(sm.fin());
-            wait_drain(sm.fin(), 0, 100000000ull);
-        }
-        __syncwarp();
-    } else if (warp == 10) {
-        // ---- each query tile's -LSE·log2 e and -δ; queries past the end (and without keys) get P = 0
-        for (int i = 0; i < w.n; ++i) {
-            const int slot = i % Cfg::kStatSlots, q0 = (w.first + i) * kBlockM;
-            float l[4], d[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int q = q0 + k * 32 + lane;
-                l[k] = -INFINITY, d[k] = 0.f;
-                if (q < w.nq) {
-                    const long long si = bwd_stat<VARLEN>(p, w, q);
-                    const float lse = p.lse[si];
-                    if (lse != -INFINITY) l[k] = -lse * 1.44269504088896341f;
-                    d[k] = -p.delta[si];
-                }
+        for (uint32_t it = 0; ok; ++it) {
+            const int u = bwd_next(sm, wait, it, lane);
+            if (u < 0) break;
+            const BwdUnit w = unit(u);
+            if (w.n == 0) continue;
+            ok = full_units == 0 || wait(sm.acc_free(), full_units - 1, kStatusTimeoutSoftmax);
+            ++full_units;
+            for (int j = 0; j < w.n && ok; ++j, ++t) {
+                const uint32_t sa = t % Cfg::kStagesA, buf = t & 1;
+                ok = wait(sm.ds_full(buf), t >> 1, kStatusTimeoutSoftmax);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                bwd_grad_mma<D>(tmem + kTmemDq, tmem + kTmemDs + buf * 64, 16, sm.sbase + sm.a_off(sa), j > 0);
+                ptx::mma_commit_elect(sm.ds_free(buf));
+                ptx::mma_commit_elect(sm.a_free(sa));
             }
-            if (!wait_phase_warp(sm.stat_free(slot), ((i / Cfg::kStatSlots) & 1) ^ 1, abort_flag, kStatusTimeoutFree, lim))
-                break;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                sm.stat(slot, 0)[k * 32 + lane] = l[k];
-                sm.stat(slot, 1)[k * 32 + lane] = d[k];
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.stat_full(slot));
+            if (ok) ptx::mma_commit_elect(sm.acc_full());
         }
-    } else if (warp < 8) {
-        // ---- elementwise: one key per thread, 64 of a tile's queries
-        const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+        bwd_drain_mmas(sm, 1, lane);
+    } else if (warp < kBwdWarps) {
+        // ---- elementwise: one query row per thread, 32 of a tile's keys
+        const int part = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int key = w.r0 + row;
         const float2 cc = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
-        for (int i = 0; i < w.n; ++i) {
-            const int slot = i % Cfg::kStatSlots;
-            ok = __all_sync(0xffffffffu, wait_phase(sm.stat_full(slot), (i / Cfg::kStatSlots) & 1, abort_flag,
-                                                    kStatusTimeoutOther, lim) &&
-                                             wait_phase(sm.s_full(), i & 1, abort_flag, kStatusTimeoutMma, lim));
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            float s[64];
-            load_row64(tmem + Cfg::kTmemS + lanes + half * 64, s);
-            if (!kOver) {
+        BwdRow<D, VARLEN> mine;
+        int u = bwd_next(sm, wait, 0, lane);
+        BwdUnit w{};
+        if (u >= 0) {
+            w = unit(u);
+            mine.load(p, w, part, row);
+        }
+        ok = u >= 0;
+        for (uint32_t it = 0;; ++it) {
+            // -LSE·log2 e (such that P = 0 without keys) and -δ of the unit that `mine` was loaded for (0 where no key is
+            // seen). The warps agree on going on: one that gave up ends all.
+            if (ok && w.n > 0) {
+                ok = wait(sm.held_full(), full_units, kStatusTimeoutLoad);
+                if (ok) sm.stat(0, 0)[part * kBlockM + row] = mine.dot(sm.base + Cfg::kTileBytes, part, row);
+                __syncwarp();
+                if (ok && lane == 0) ptx::mbar_arrive(sm.held_free());
+            }
+            if (named_bar_or(kBwdBarPair, kBwdWarps * 32, !ok)) break;
+            float delta = -mine.dlse;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) delta += sm.stat(0, 0)[i * kBlockM + row];
+            const float nlse = mine.have && mine.lse != -INFINITY ? -mine.lse * 1.44269504088896341f : -INFINITY;
+            if (!mine.have || w.n == 0) delta = 0.f;
+            const float2 nl = make_float2(nlse, nlse), nd = make_float2(-delta, -delta);
+            if (mine.have && part == 0) p.delta[mine.stat] = delta;
+            // of the unit, the walk needs only where keys begin to be hidden: from the block's first query, from this one
+            const int n = w.n, off = w.nk - w.nq;
+            const int seen_all = CAUSAL ? min(w.nk - 1, w.r0 + off) : w.nk - 1;
+            const int seen = CAUSAL ? min(w.nk - 1, w.r0 + row + off) : w.nk - 1;
+            const bool have = mine.have;
+            const long long out = bwd_row<D, VARLEN>(p, w, w.tq0, have ? w.r0 + row : w.r0) + part * (D / 4);
+            for (int j = 0; j < n; ++j, ++t) {
+                ok = wait(sm.s_full(0), t, kStatusTimeoutMma);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                uint32_t x[32];
+                float s[32];
+                ptx::tmem_ld_32x32b_x32(tmem + kTmemS + lanes + part * 32, x);
+                ptx::tmem_wait_ld(x);
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(sm.s_free());
-            }
-            const int q0 = (w.first + i) * kBlockM + half * 64;
-            if (CAUSAL && w.r0 + kBlockN - 1 > q0 + off) {
-                const int first = key - off - q0;  // first column that sees the key
 #pragma unroll
-                for (int c = 0; c < 64; ++c) s[c] = c < first ? -INFINITY : s[c];
-            }
-            const float4* nl = reinterpret_cast<const float4*>(sm.stat(slot, 0) + half * 64);
+                for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(x[c]);
+                const int key0 = j * kBlockN + part * 32;
+                if (key0 + 31 > seen_all) {
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                const float4 l = nl[c / 4];
-                const float2 x = ptx::ffma2(make_float2(s[c], s[c + 1]), cc, make_float2(l.x, l.y));
-                const float2 y = ptx::ffma2(make_float2(s[c + 2], s[c + 3]), cc, make_float2(l.z, l.w));
-                s[c] = ptx::ex2_approx(x.x);
-                s[c + 1] = ptx::ex2_approx(x.y);
-                s[c + 2] = ptx::ex2_approx(y.x);
-                s[c + 3] = ptx::ex2_approx(y.y);
-            }
-            uint32_t r[32];
+                    for (int c = 0; c < 32; ++c) s[c] = c > seen - key0 ? -INFINITY : s[c];
+                }
 #pragma unroll
-            for (int c = 0; c < 32; ++c) r[c] = ptx::pack_bf16x2(s[2 * c], s[2 * c + 1]);
-            if (!kOver && i > 0) {  // dV += P·dO of the tile before has read P
-                ok = __all_sync(0xffffffffu, wait_phase(sm.p_free(), (i - 1) & 1, abort_flag, kStatusTimeoutMma, lim));
+                for (int c = 0; c < 32; c += 2) {
+                    const float2 e = ptx::ffma2(make_float2(s[c], s[c + 1]), cc, nl);
+                    s[c] = ptx::ex2_approx(e.x);
+                    s[c + 1] = ptx::ex2_approx(e.y);
+                }
+                ok = wait(sm.dp_full(), t, kStatusTimeoutMma);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
-            }
-            ptx::tmem_st_32x32b_x32(tmem + kTmemP + lanes + half * kSecond, r);
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.p_full());
-
-            ok = __all_sync(0xffffffffu, wait_phase(sm.dp_full(), i & 1, abort_flag, kStatusTimeoutMma, lim));
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            const float2* nd = reinterpret_cast<const float2*>(sm.stat(slot, 1) + half * 64);
-            bwd_ds(s, tmem + Cfg::kTmemDp + lanes + half * 64, r, [&](int c) { return nd[c / 2]; });
-            if (!kOver) {
+                ptx::tmem_ld_32x32b_x32(tmem + kTmemDp + lanes + part * 32, x);
+                ptx::tmem_wait_ld(x);
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(sm.dp_free());
-                if (i > 0) {  // dK += dS·Q of the tile before has read dS
-                    ok = __all_sync(0xffffffffu, wait_phase(sm.ds_free(0), (i - 1) & 1, abort_flag, kStatusTimeoutMma, lim));
+                uint32_t r[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float2 e = ptx::fadd2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), nd);
+                    const float2 ds = ptx::fmul2(make_float2(s[c], s[c + 1]), e);
+                    r[c / 2] = ptx::pack_bf16x2(ds.x, ds.y);
+                }
+                const uint32_t buf = t & 1;
+                if (t >= 2) {  // dQ += dS·K has read what was there
+                    ok = wait(sm.ds_free(buf), (t >> 1) - 1, kStatusTimeoutMma);
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
                 }
+                ptx::tmem_st_32x32b_x16(tmem + kTmemDs + buf * 64 + lanes + part * 16, r);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sm.ds_full(buf));
             }
-            ptx::tmem_st_32x32b_x32(tmem + kTmemDs + lanes + half * kSecond, r);
-            ptx::tmem_wait_st();
+            // the next unit's rows, behind this one's last products
+            uint16_t* to = static_cast<uint16_t*>(p.dq) + out;
+            u = ok ? bwd_next(sm, wait, it + 1, lane) : -2;
+            if (u >= 0) {
+                w = unit(u);
+                mine.load(p, w, part, row);
+            }
+            if (ok && n == 0) {
+                if (have) bwd_store_zero<D / 4>(to);
+            } else if (ok) {
+                ok = wait(sm.acc_full(), full_units++, kStatusTimeoutMma);
+                if (ok) {
+                    ptx::tc_fence_after_sync();
+                    bwd_store<D / 4>(tmem + kTmemDq + lanes + part * (D / 4), p.scale, to, have);
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(sm.acc_free());
+                }
+            }
+            ok = ok && u >= 0;
+        }
+    }
+    bwd_end(tmem, warp);
+}
+
+// ---------------------------------------------------------------- dK, dV
+// TMEM, d = 128: Sᵀ [0, 128) with P over it, dPᵀ [128, 256) with dS over it (a warp writes only lanes and columns that
+// it alone has read), dV [256, 384), dK [384, 512). The next Sᵀ waits for dV += P·dO to have read P, the next dPᵀ for
+// dK += dS·Q to have read dS. d = 64: P [256, 320) and dS [320, 384) have columns of their own, dV [384, 448), dK
+// [448, 512): the elementwise warps wait for the product before, which is long done, and the scores for them alone
+// (16384 x 16384 x 8 heads 860 us; with dS over dPᵀ and two buffers of P 950).
+template <int D, bool CAUSAL, bool VARLEN>
+__global__ void __launch_bounds__(kBwdDkvThreads, 1)
+    fa_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                      const BwdParams p) {
+    using Smem = BwdSmem<D, false>;
+    using Cfg = typename Smem::Cfg;
+    constexpr bool kOver = D == 128;               // P and dS lie over Sᵀ and dPᵀ
+    constexpr uint32_t kPitch = kOver ? 32 : 16;   // columns from one 32 queries' pairs to the next's
+    constexpr uint32_t kTmemS = 0, kTmemDp = 128, kTmemP = kOver ? kTmemS : 256, kTmemDs = kOver ? kTmemDp : 320;
+    constexpr uint32_t kTmemDv = kOver ? 256 : 384, kTmemDk = kTmemDv + D;
+    const Smem sm;
+    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+    if (!bwd_begin(sm, warp, lane)) return;
+    const uint32_t tmem = *sm.tmem_slot();
+    const BwdWait wait{sm.abort_flag(), p.wait_limit_ns};
+    auto range = [&](BwdUnit& w) {
+        // the query tiles with a query that sees the block's first key
+        const int tiles = (w.nq + kBlockM - 1) / kBlockM;
+        w.first = CAUSAL ? min(max(w.r0 - (w.nk - w.nq), 0) / kBlockM, tiles) : 0;
+        w.n = tiles - w.first;
+    };
+    auto unit = [&](int u) {
+        BwdUnit w;
+        bwd_unit<VARLEN, false>(p, u, w);
+        range(w);
+        return w;
+    };
+    uint32_t t = 0, full_units = 0;  // tiles and units with tiles before this one
+
+    if (warp == kBwdLoad) {
+        const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
+        using Load = BwdLoader<Smem, VARLEN>;
+        bwd_load_role<VARLEN, false>(
+            sm, wait, p, lane, range,
+            [&](Load& load, const BwdUnit& w) {
+                return load.tile(tm_k, w, w.tk0, w.nk, w.r0, 0, sm.held_full(), once) &&
+                       load.tile(tm_v, w, w.tk0, w.nk, w.r0, Cfg::kTileBytes, sm.held_full(), once);
+            },
+            [&](Load& load, const BwdUnit& w, int i, uint32_t sa, uint32_t sb, int which) {
+                const int row = (w.first + i) * kBlockM;
+                return which == 0 ? load.tile(tm_q, w, w.tq0, w.nq, row, sm.a_off(sa), sm.a_full(sa), keep)
+                                  : load.tile(tm_do, w, w.tq0, w.nq, row, sm.b_off(sb), sm.b_full(sb), keep);
+            });
+    } else if (warp == kBwdScore) {
+        // ---- Sᵀ = K·Qᵀ and dPᵀ = V·dOᵀ, as soon as their columns are free
+        bool ok = true;
+        for (uint32_t it = 0; ok; ++it) {
+            const int u = bwd_next(sm, wait, it, lane);
+            if (u < 0) break;
+            const BwdUnit w = unit(u);
+            if (w.n == 0) continue;
+            ok = wait(sm.held_full(), full_units++, kStatusTimeoutLoad);
+            for (int i = 0; i < w.n && ok; ++i, ++t) {
+                const uint32_t sa = t % Cfg::kStagesA, sb = t % Cfg::kStagesB;
+                ok = wait(sm.a_full(sa), t / Cfg::kStagesA, kStatusTimeoutLoad) &&
+                     wait(sm.stat_full(t & 1), t >> 1, kStatusTimeoutOther) &&
+                     (t == 0 || wait(kOver ? sm.p_free(0) : sm.s_free(), t - 1, kStatusTimeoutSoftmax));
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                bwd_score_mma<D>(tmem + kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
+                if (lane == 0) {  // (before the commit, which may wait for room in the queue)
+                    ptx::mbar_arrive(sm.s_issued());
+                    ptx::mbar_arrive(sm.s_full(0));
+                }
+                __syncwarp();
+                ptx::mma_commit_elect(sm.s_full(0));
+                ok = wait(sm.b_full(sb), t / Cfg::kStagesB, kStatusTimeoutLoad) &&
+                     (t == 0 || wait(kOver ? sm.ds_free(0) : sm.dp_free(), t - 1, kStatusTimeoutSoftmax));
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                bwd_score_mma<D>(tmem + kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
+                ptx::mma_commit_elect(sm.dp_full());
+                ptx::mma_commit_elect(sm.b_free(sb));
+                if (i + 1 == w.n) ptx::mma_commit_elect(sm.held_free());
+            }
+        }
+        bwd_drain_mmas(sm, 0, lane);
+    } else if (warp == kBwdGrad) {
+        // ---- dV += P·dO, dK += dS·Q. dO may still be on its way when P is there; Q is not.
+        bool ok = true;
+        for (uint32_t it = 0; ok; ++it) {
+            const int u = bwd_next(sm, wait, it, lane);
+            if (u < 0) break;
+            const BwdUnit w = unit(u);
+            if (w.n == 0) continue;
+            ok = full_units == 0 || wait(sm.acc_free(), full_units - 1, kStatusTimeoutSoftmax);
+            ++full_units;
+            for (int i = 0; i < w.n && ok; ++i, ++t) {
+                const uint32_t sa = t % Cfg::kStagesA, sb = t % Cfg::kStagesB;
+                ok = wait(sm.b_full(sb), t / Cfg::kStagesB, kStatusTimeoutLoad) &&
+                     wait(sm.p_full(0), t, kStatusTimeoutSoftmax);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                bwd_grad_mma<D>(tmem + kTmemDv, tmem + kTmemP, kPitch, sm.sbase + sm.b_off(sb), i > 0);
+                ptx::mma_commit_elect(sm.p_free(0));
+                ptx::mma_commit_elect(sm.b_free(sb));
+                // d = 128: the next Sᵀ, which the next P waits for, goes to the tensor core before dK, which
+                // nothing waits for but the next dPᵀ.
+                ok = (!kOver || i + 1 == w.n || wait(sm.s_issued(), t + 1, kStatusTimeoutOther)) &&
+                     wait(sm.ds_full(0), t, kStatusTimeoutSoftmax);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                bwd_grad_mma<D>(tmem + kTmemDk, tmem + kTmemDs, kPitch, sm.sbase + sm.a_off(sa), i > 0);
+                ptx::mma_commit_elect(sm.ds_free(0));
+                ptx::mma_commit_elect(sm.a_free(sa));
+            }
+            if (ok) ptx::mma_commit_elect(sm.acc_full());
+        }
+        bwd_drain_mmas(sm, 1, lane);
+    } else if (warp == kBwdStat) {
+        // ---- each query tile's -LSE·log2 e and -δ; queries past the end (and without keys) get P = 0
+        bool ok = true;
+        for (uint32_t it = 0; ok; ++it) {
+            const int u = bwd_next(sm, wait, it, lane);
+            if (u < 0) break;
+            const BwdUnit w = unit(u);
+            for (int i = 0; i < w.n; ++i, ++t) {
+                const int slot = t & 1, q0 = (w.first + i) * kBlockM;
+                float l[4], d[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int q = q0 + k * 32 + lane;
+                    l[k] = -INFINITY, d[k] = 0.f;
+                    if (q < w.nq) {
+                        const long long si = bwd_stat<VARLEN>(p, w, q);
+                        const float lse = p.lse[si];
+                        if (lse != -INFINITY) l[k] = -lse * 1.44269504088896341f;
+                        d[k] = -p.delta[si];
+                    }
+                }
+                ok = t < 2 || wait(sm.stat_free(slot), (t >> 1) - 1, kStatusTimeoutFree);
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    sm.stat(slot, 0)[k * 32 + lane] = l[k];
+                    sm.stat(slot, 1)[k * 32 + lane] = d[k];
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sm.stat_full(slot));
+            }
+        }
+    } else {
+        // ---- elementwise: 32 keys by 32 of a tile's queries per warp, as two blocks of 16 keys in the accumulator
+        // layout of warp-level matrix instructions: a thread has 8 queries of 4 keys, so that LSE and δ, which go by
+        // the query, are 8 loads of 8 bytes (as 24 loads of 16 bytes, the same for all lanes, with a row of 32 queries
+        // to a thread, they took shared memory as much time as the matrix operands)
+        const int part = warp >> 2, row = (warp & 3) * 32, g = lane >> 2, t4 = lane & 3;
+        const uint32_t lanes = static_cast<uint32_t>(row) << 16;
+        const float2 cc = make_float2(p.scale_log2, p.scale_log2);
+        bool ok = true;
+        for (uint32_t it = 0; ok; ++it) {
+            const int u = bwd_next(sm, wait, it, lane);
+            if (u < 0) break;
+            const BwdUnit w = unit(u);
+            const int off = w.nk - w.nq;
+            for (int i = 0; i < w.n; ++i, ++t) {
+                const int slot = t & 1;
+                const uint32_t at_s = tmem + kTmemS + lanes + part * 32;
+                ok = wait(sm.s_full(0), t, kStatusTimeoutMma);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                uint32_t x[2][16];
+                float s[2][16];
+                ptx::tmem_ld_16x256b_x4(at_s, x[0]);
+                ptx::tmem_ld_16x256b_x4(at_s + (16u << 16), x[1]);
+                float2 nl[4], nd[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    nl[n] = *reinterpret_cast<const float2*>(sm.stat(slot, 0) + part * 32 + n * 8 + t4 * 2);
+                    nd[n] = *reinterpret_cast<const float2*>(sm.stat(slot, 1) + part * 32 + n * 8 + t4 * 2);
+                }
+                ptx::tmem_wait_ld(x[0]);
+                ptx::reg_fence(x[1]);
+                if (!kOver) {
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(sm.s_free());
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) s[h][c] = __uint_as_float(x[h][c]);
+                const int q0 = (w.first + i) * kBlockM + part * 32;
+                if (CAUSAL && w.r0 + row + 31 - off > q0) {
+                    // query q0 + c sees the key in row r when c >= r0 + r - off - q0
+                    const int first = w.r0 + row + g - off - q0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if ((c >> 2) * 8 + t4 * 2 + (c & 1) < first + h * 16 + (c & 2) * 4) s[h][c] = -INFINITY;
+                }
+                uint32_t r[2][8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        const float2 e = ptx::ffma2(make_float2(s[h][c], s[h][c + 1]), cc, nl[c >> 2]);
+                        s[h][c] = ptx::ex2_approx(e.x);
+                        s[h][c + 1] = ptx::ex2_approx(e.y);
+                        r[h][c / 2] = ptx::pack_bf16x2(s[h][c], s[h][c + 1]);
+                    }
+                if (!kOver && t > 0) {  // dV += P·dO of the tile before has read P
+                    ok = wait(sm.p_free(0), t - 1, kStatusTimeoutMma);
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                }
+                const uint32_t at_p = tmem + kTmemP + lanes + part * kPitch;
+                ptx::tmem_st_16x128b_x4(at_p, r[0]);
+                ptx::tmem_st_16x128b_x4(at_p + (16u << 16), r[1]);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(sm.p_full(0));
+                    ptx::mbar_arrive(sm.stat_free(slot));
+                }
+
+                const uint32_t at_dp = tmem + kTmemDp + lanes + part * 32;
+                ok = wait(sm.dp_full(), t, kStatusTimeoutMma);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                ptx::tmem_ld_16x256b_x4(at_dp, x[0]);
+                ptx::tmem_ld_16x256b_x4(at_dp + (16u << 16), x[1]);
+                ptx::tmem_wait_ld(x[0]);
+                ptx::reg_fence(x[1]);
+                if (!kOver) {
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(sm.dp_free());
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        const float2 e = ptx::fadd2(make_float2(__uint_as_float(x[h][c]), __uint_as_float(x[h][c + 1])),
+                                                    nd[c >> 2]);
+                        const float2 ds = ptx::fmul2(make_float2(s[h][c], s[h][c + 1]), e);
+                        r[h][c / 2] = ptx::pack_bf16x2(ds.x, ds.y);
+                    }
+                if (!kOver && t > 0) {  // dK += dS·Q of the tile before has read dS
+                    ok = wait(sm.ds_free(0), t - 1, kStatusTimeoutMma);
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                }
+                const uint32_t at_ds = tmem + kTmemDs + lanes + part * kPitch;
+                ptx::tmem_st_16x128b_x4(at_ds, r[0]);
+                ptx::tmem_st_16x128b_x4(at_ds + (16u << 16), r[1]);
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(sm.ds_full(0));
+            }
+            if (!ok) break;
+            // ---- one key per thread: dV by warps 0-7, dK by warps 8-15, half a row each
+            const int key = w.r0 + row + lane, half = part & 1;
+            const bool have = key < w.nk, is_dv = part < 2;
+            uint16_t* to = static_cast<uint16_t*>(is_dv ? p.dv : p.dk) +
+                           bwd_row<D, VARLEN>(p, w, w.tk0, have ? key : w.r0) + half * (D / 2);
+            if (w.n == 0) {
+                if (have) bwd_store_zero<D / 2>(to);
+                continue;
+            }
+            ok = wait(sm.acc_full(), full_units++, kStatusTimeoutMma);
+            if (!ok) break;
+            ptx::tc_fence_after_sync();
+            bwd_store<D / 2>(tmem + (is_dv ? kTmemDv : kTmemDk) + lanes + half * (D / 2), is_dv ? 1.f : p.scale, to, have);
             ptx::tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(sm.ds_full());
-                ptx::mbar_arrive(sm.stat_free(slot));
-            }
-        }
-        // ---- dV by warps 0-3, dK by warps 4-7
-        const bool have = key < w.nk;
-        uint16_t* to = static_cast<uint16_t*>(half == 0 ? p.dv : p.dk) +
-                       bwd_row<D, VARLEN>(p, w, w.tk0, have ? key : w.r0);
-        if (w.n == 0) {
-            if (have) bwd_store_zero<D>(to);
-        } else if (ok && __all_sync(0xffffffffu, wait_phase(sm.acc_full(), 0, abort_flag, kStatusTimeoutMma, lim)) &&
-                   *abort_flag == 0) {
-            ptx::tc_fence_after_sync();
-            bwd_store<D>(tmem + (half == 0 ? kTmemDv : kTmemDk) + lanes, half == 0 ? 1.f : p.scale, to, have);
+            if (lane == 0) ptx::mbar_arrive(sm.acc_free());
         }
     }
-    ptx::tc_fence_before_sync();
-    __syncthreads();
-    if (warp == 8) {
-        ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc(tmem, 512);
-    }
+    bwd_end(tmem, warp);
 }
 
 }  // namespace fa

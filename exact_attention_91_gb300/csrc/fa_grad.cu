@@ -26,11 +26,10 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 template <int D, bool CAUSAL, bool VARLEN>
 bool set_pair() {
-    constexpr int bytes = fa::BwdCfg<D>::kSmemBytes;
     return cudaFuncSetAttribute(fa::fa_bwd_dq_kernel<D, CAUSAL, VARLEN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                bytes) == cudaSuccess &&
+                                fa::BwdCfg<D, true>::kSmemBytes) == cudaSuccess &&
            cudaFuncSetAttribute(fa::fa_bwd_dkv_kernel<D, CAUSAL, VARLEN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                bytes) == cudaSuccess;
+                                fa::BwdCfg<D, false>::kSmemBytes) == cudaSuccess;
 }
 
 // The kernels' shared-memory sizes, set on the device by its first call that is not being captured; a captured call
@@ -57,12 +56,12 @@ struct Maps {
 // Both kernels are launched with programmatic stream serialization and wait for their predecessors before they touch
 // memory, as the serving kernels do.
 template <typename Kernel>
-int launch(Kernel kernel, long long blocks, int smem, cudaStream_t stream, const Maps& m, const fa::BwdParams& p) {
+int launch(Kernel kernel, int blocks, int threads, int smem, cudaStream_t stream, const Maps& m, const fa::BwdParams& p) {
     if (blocks == 0) return FA_OK;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(384);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -74,21 +73,28 @@ int launch(Kernel kernel, long long blocks, int smem, cudaStream_t stream, const
     return FA_ERR_LAUNCH;
 }
 
+// As many blocks as SMs, which take the units from the counters at p.next, or, where the SMs hold all units at once,
+// a block for each unit.
 template <int D, bool CAUSAL, bool VARLEN>
-int launch_pair(long long q_blocks, long long k_blocks, cudaStream_t s, const Maps& m, const fa::BwdParams& p) {
-    constexpr int bytes = fa::BwdCfg<D>::kSmemBytes;
-    const int rc = launch(fa::fa_bwd_dq_kernel<D, CAUSAL, VARLEN>, q_blocks, bytes, s, m, p);
-    return rc != FA_OK ? rc : launch(fa::fa_bwd_dkv_kernel<D, CAUSAL, VARLEN>, k_blocks, bytes, s, m, p);
+int launch_pair(int sms, cudaStream_t s, const Maps& m, fa::BwdParams p) {
+    if (p.q_units <= sms && p.k_units <= sms) {
+        p.next = nullptr;
+    } else if (cudaMemsetAsync(p.next, 0, 2 * sizeof(unsigned), s) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_LAUNCH;
+    }
+    const int rc = launch(fa::fa_bwd_dq_kernel<D, CAUSAL, VARLEN>, std::min(p.q_units, sms),
+                          fa::kBwdDqThreads, fa::BwdCfg<D, true>::kSmemBytes, s, m, p);
+    if (rc != FA_OK) return rc;
+    return launch(fa::fa_bwd_dkv_kernel<D, CAUSAL, VARLEN>, std::min(p.k_units, sms), fa::kBwdDkvThreads,
+                  fa::BwdCfg<D, false>::kSmemBytes, s, m, p);
 }
 
 template <bool VARLEN>
-int launch_any(int d, bool causal, long long q_blocks, long long k_blocks, cudaStream_t s, const Maps& m,
-               const fa::BwdParams& p) {
+int launch_any(int d, bool causal, int sms, cudaStream_t s, const Maps& m, const fa::BwdParams& p) {
     if (d == 64)
-        return causal ? launch_pair<64, true, VARLEN>(q_blocks, k_blocks, s, m, p)
-                      : launch_pair<64, false, VARLEN>(q_blocks, k_blocks, s, m, p);
-    return causal ? launch_pair<128, true, VARLEN>(q_blocks, k_blocks, s, m, p)
-                  : launch_pair<128, false, VARLEN>(q_blocks, k_blocks, s, m, p);
+        return causal ? launch_pair<64, true, VARLEN>(sms, s, m, p) : launch_pair<64, false, VARLEN>(sms, s, m, p);
+    return causal ? launch_pair<128, true, VARLEN>(sms, s, m, p) : launch_pair<128, false, VARLEN>(sms, s, m, p);
 }
 
 struct Range {
@@ -130,7 +136,7 @@ extern "C" {
 
 long long fa_bwd_workspace(long long queries, int H) {
     if (queries < 0 || H < 1 || queries > (1LL << 40) / H) return FA_ERR_BAD_SHAPE;
-    return (queries * H * 4 + 15) / 16 * 16;
+    return (queries * H * 4 + 15) / 16 * 16 + 16;  // δ, and the units' counters
 }
 
 int fa_bwd(const void* dout, const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -151,8 +157,8 @@ int fa_bwd(const void* dout, const void* q, const void* k, const void* v, const 
                          {dlse, dlse ? stat : 0}};
     const Range out[4] = {{dq, bytes}, {dk, bytes}, {dv, bytes}, {workspace, workspace ? workspace_bytes : 0}};
     if (any_alias(in, 7, out, 4)) return FA_ERR_ALIAS;
-    if (!workspace || workspace_bytes < static_cast<size_t>(fa_bwd_workspace(static_cast<long long>(B) * N, H)))
-        return FA_ERR_WORKSPACE;
+    const size_t need = static_cast<size_t>(fa_bwd_workspace(static_cast<long long>(B) * N, H));
+    if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
     int dev = 0, sms = 0;
     const int rc = fa::host_probe(&dev, &sms);
     if (rc != FA_OK) return rc;
@@ -165,8 +171,9 @@ int fa_bwd(const void* dout, const void* q, const void* k, const void* v, const 
         fa::host_map_rows(&m.v, v, bh, N, d) != FA_OK || fa::host_map_rows(&m.dout, dout, bh, N, d) != FA_OK)
         return FA_ERR_LAUNCH;
     fa::BwdParams p{};
-    p.o = o, p.dout = dout, p.lse = lse, p.dlse = dlse;
+    p.q = q, p.o = o, p.dout = dout, p.lse = lse, p.dlse = dlse;
     p.delta = static_cast<float*>(workspace);
+    p.next = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + need - 16);
     p.dq = dq, p.dk = dk, p.dv = dv;
     p.scale = scale;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
@@ -174,7 +181,8 @@ int fa_bwd(const void* dout, const void* q, const void* k, const void* v, const 
     p.num_heads_total = bh;
     p.N = N;
     p.q_tiles = p.k_tiles = static_cast<int>(blocks);
-    return launch_any<false>(d, causal != 0, BH * blocks, BH * blocks, s, m, p);
+    p.q_units = p.k_units = static_cast<int>(BH * blocks);
+    return launch_any<false>(d, causal != 0, sms, s, m, p);
 }
 
 int fa_bwd_varlen(const void* dout, const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -214,7 +222,7 @@ int fa_bwd_varlen(const void* dout, const void* q, const void* k, const void* v,
     const Range out[4] = {{dq, q_bytes}, {dk, k_bytes}, {dv, k_bytes}, {workspace, workspace ? workspace_bytes : 0}};
     if (any_alias(in, 9, out, 4)) return FA_ERR_ALIAS;
     const size_t need = static_cast<size_t>(fa_bwd_workspace(total_q, H));
-    if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
     int dev = 0, sms = 0;
     const int rc = fa::host_probe(&dev, &sms);
     if (rc != FA_OK) return rc;
@@ -232,8 +240,9 @@ int fa_bwd_varlen(const void* dout, const void* q, const void* k, const void* v,
         fa::host_map_tokens(&m.v, total_k ? v : q, total_k ? total_k : 1, H, d) != FA_OK)
         return FA_ERR_LAUNCH;
     fa::BwdParams p{};
-    p.o = o, p.dout = dout, p.lse = lse, p.dlse = dlse;
+    p.q = q, p.o = o, p.dout = dout, p.lse = lse, p.dlse = dlse;
     p.delta = static_cast<float*>(workspace);
+    p.next = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + need - 16);
     p.dq = dq, p.dk = dk, p.dv = dv;
     p.scale = scale;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
@@ -245,7 +254,8 @@ int fa_bwd_varlen(const void* dout, const void* q, const void* k, const void* v,
     p.q_tiles = static_cast<int>(packed & 1 ? all[0] : blocks_of(max_seqlen_q));
     p.k_tiles = static_cast<int>(packed & 2 ? all[1] : blocks_of(max_seqlen_k));
     p.packed = packed;
-    return launch_any<true>(d, causal != 0, blocks[0], blocks[1], s, m, p);
+    p.q_units = static_cast<int>(blocks[0]), p.k_units = static_cast<int>(blocks[1]);
+    return launch_any<true>(d, causal != 0, sms, s, m, p);
 }
 
 }  // extern "C"

@@ -238,7 +238,7 @@ int fa_bwd_varlen(const void* dout, const void* q, const void* k, const void* v,
 
 /*
  * fa_bwd_workspace — host-only: workspace bytes of a backward pass over this many queries (fa_bwd: B*N,
- * fa_bwd_varlen: total_q) of H heads: 4 for each, or FA_ERR_BAD_SHAPE.
+ * fa_bwd_varlen: total_q) of H heads: 4 for each and 16, to a multiple of 16, or FA_ERR_BAD_SHAPE.
  */
 long long fa_bwd_workspace(long long queries, int H);
 

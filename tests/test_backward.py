@@ -57,7 +57,7 @@ def test_oracle_matches_differences(nq, nk, causal):
 
 
 def bwd(dout=P, q=2 * P, k=3 * P, v=4 * P, o=5 * P, lse=6 * P, dlse=7 * P, dq=8 * P, dk=9 * P, dv=10 * P, B=2, H=2,
-        N=100, d=64, scale=0.125, ws=11 * P, ws_bytes=2 * 2 * 100 * 4):
+        N=100, d=64, scale=0.125, ws=11 * P, ws_bytes=2 * 2 * 100 * 4 + 16):
     return fa.fa_bwd(dout, q, k, v, o, lse, dlse, dq, dk, dv, B, H, N, d, scale, True, ws, ws_bytes, None)
 
 
@@ -68,7 +68,7 @@ COMMON = [
     (dict(q=2 * P + 8), -4), (dict(dout=P + 2), -4), (dict(dq=8 * P + 4), -4), (dict(dv=10 * P + 8), -4),
     (dict(lse=6 * P + 2), -4), (dict(dlse=7 * P + 1), -4), (dict(ws=11 * P + 8), -4),
     (dict(dq=2 * P), -10), (dict(dk=8 * P), -10), (dict(dv=5 * P + 16), -10), (dict(dq=P), -10), (dict(ws=6 * P), -10),
-    (dict(ws=9 * P + 16), -10), (dict(dk=7 * P), -10), (dict(ws=0), -11), (dict(ws_bytes=100), -11),
+    (dict(ws=9 * P + 16), -10), (dict(dk=7 * P), -10), (dict(ws=0), -11), (dict(ws_bytes=800), -11),
 ]
 
 
@@ -85,7 +85,7 @@ def test_a_call_without_a_device_or_a_gradient_of_lse():
 
 def bwd_varlen(dout=P, q=2 * P, k=3 * P, v=4 * P, o=5 * P, lse=6 * P, dlse=7 * P, dq=8 * P, dk=9 * P, dv=10 * P,
                cu_q=12 * P, cu_k=13 * P, B=2, H=2, total_q=100, total_k=120, max_q=60, max_k=120, d=64, scale=0.125,
-               ws=11 * P, ws_bytes=2 * 100 * 4):
+               ws=11 * P, ws_bytes=2 * 100 * 4 + 16):
     return fa.fa_bwd_varlen(dout, q, k, v, o, lse, dlse, dq, dk, dv, cu_q, cu_k, B, H, total_q, total_k, max_q, max_k, d,
                             scale, True, ws, ws_bytes, None)
 
@@ -101,9 +101,9 @@ def test_bad_packed_calls_are_rejected(kw, code):
 
 
 def test_workspace_sizes():
-    assert fa.fa_bwd_workspace(1000, 3) == 12000
-    assert fa.fa_bwd_workspace(1, 1) == 16
-    assert fa.fa_bwd_workspace(0, 4) == 0
+    assert fa.fa_bwd_workspace(1000, 3) == 12016
+    assert fa.fa_bwd_workspace(1, 1) == 32
+    assert fa.fa_bwd_workspace(0, 4) == 16
     for bad in ((-1, 1), (1, 0), (1 << 41, 1)):
         assert fa.fa_bwd_workspace(*bad) == -2
 
