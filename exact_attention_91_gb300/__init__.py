@@ -28,13 +28,13 @@ __all__ = ["FaError", "load_library", "fa_fwd", "fa_fwd_noalloc", "fa_strerror",
            "FaPagedCache", "fa_decode_paged", "fa_decode_paged_workspace", "fa_rotary", "fa_cache_append",
            "fa_page_maps", "attention_decode_paged", "rotary", "rotary_inv_freq", "cache_append", "page_maps",
            "PageMaps", "load_binding", "fa_bwd", "fa_bwd_varlen", "fa_bwd_workspace", "attention_backward",
-           "attention_backward_varlen"]
+           "attention_backward_varlen", "fa_decode_shared", "fa_decode_shared_workspace", "attention_decode_shared"]
 
 EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_noalloc", "fa_fwd_varlen", "fa_strerror", "fa_device_status",
                     "fa_set_wait_limit_ns", "fa_abi_version", "fa_selftest_wait_timeout", "fa_varlen_num_splits",
                     "fa_selftest_exp2", "fa_selftest_ex2_rate", "fa_decode_paged", "fa_decode_paged_workspace",
                     "fa_rotary", "fa_cache_append", "fa_page_maps", "fa_bwd",
-                    "fa_bwd_varlen", "fa_bwd_workspace")
+                    "fa_bwd_varlen", "fa_bwd_workspace", "fa_decode_shared", "fa_decode_shared_workspace")
 
 FA_OK = 0
 FA_ERR_DEVICE_TIMEOUT = -8
@@ -110,6 +110,10 @@ def load_library(path: str | None = None):
     lib.fa_bwd.restype = i
     lib.fa_bwd_varlen.argtypes = [vp] * 12 + [i] * 7 + [f, i, vp, ctypes.c_size_t, vp]
     lib.fa_bwd_varlen.restype = i
+    lib.fa_decode_shared.argtypes = [vp] * 7 + [i, i, i, i, ll, f, vp, ctypes.c_size_t, vp]
+    lib.fa_decode_shared.restype = i
+    lib.fa_decode_shared_workspace.argtypes = [i] * 6
+    lib.fa_decode_shared_workspace.restype = ll
     lib.fa_bwd_workspace.argtypes = [ll, i]
     lib.fa_bwd_workspace.restype = ll
     if path is None:
@@ -209,6 +213,21 @@ def fa_decode_paged_workspace(B: int, Hq: int, Hkv: int, d: int, cache_type: int
     """The C ``fa_decode_paged_workspace`` (host only): workspace bytes of
     ``fa_decode_paged`` for these sizes, or a negative status."""
     return load_library().fa_decode_paged_workspace(B, Hq, Hkv, d, cache_type, page_size, table_width, sm_count)
+
+
+def fa_decode_shared(q: int, cache: FaPagedCache, block_table: int, seq_lens: int, prefix_lens: int, o: int,
+                     lse: int | None, B: int, Hq: int, groups: int, table_width: int, table_stride: int, scale: float,
+                     workspace: int, workspace_bytes: int, stream: int | None) -> int:
+    """The C ``fa_decode_shared``: device pointers as ints, returns the status code."""
+    return load_library().fa_decode_shared(q, ctypes.byref(cache), block_table, seq_lens, prefix_lens, o, lse or None, B,
+                                           Hq, groups, table_width, table_stride, scale, workspace or None,
+                                           workspace_bytes, stream or None)
+
+
+def fa_decode_shared_workspace(B: int, Hq: int, Hkv: int, d: int, groups: int, sm_count: int) -> int:
+    """The C ``fa_decode_shared_workspace`` (host only): workspace bytes of
+    ``fa_decode_shared`` for these sizes, or a negative status."""
+    return load_library().fa_decode_shared_workspace(B, Hq, Hkv, d, groups, sm_count)
 
 
 def fa_bwd(dout: int, q: int, k: int, v: int, o: int, lse: int, dlse: int | None, dq: int, dk: int, dv: int, B: int,
@@ -474,6 +493,24 @@ def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: fl
                       workspace)
     return _on_stream(stream, q.device, decode, q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale,
                       out, lse, return_lse, workspace)
+
+
+def attention_decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, scale: float | None = None,
+                            k_scale=None, v_scale=None, out=None, lse=None, return_lse: bool = True, workspace=None,
+                            stream=None):
+    """``attention_decode_paged`` for requests that share the pages of a prefix,
+    whose keys and values are read once for all that share them (several answers
+    to one question, one system prompt, the beams of a search). The B requests
+    come in groups of B / G neighbours; ``prefix_lens`` (int32 [G]) holds the
+    groups' shared tokens: in a group's rows of ``block_table`` the first
+    ``prefix_lens[g] // page_size`` entries are the same (they are read in its
+    first row). The result is that of ``attention_decode_paged`` on the same
+    arguments, but for the rounding of the shared keys' weights to bf16. The
+    workspace is ``fa_decode_shared_workspace`` bytes."""
+    decode = (_bind or load_binding()).decode_shared
+    args = (q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse, return_lse, workspace,
+            prefix_lens)
+    return decode(*args) if stream is None else _on_stream(stream, q.device, decode, *args)
 
 
 def attention_backward(dout, q, k, v, out, lse, causal: bool = False, scale: float | None = None, dlse=None, dq=None,

@@ -1,8 +1,9 @@
 """Builds libfa.so in-tree with nvcc for sm_103a.
 
-The library is three translation units that include their kernels, compiled at
+The library is four translation units that include their kernels, compiled at
 once: ``csrc/fa_api.cu`` (attention forward), ``csrc/fa_grad.cu`` (its backward
-pass) and ``csrc/fa_serve.cu`` (paged cache and rotary positions). It links the CUDA runtime statically and resolves
+pass), ``csrc/fa_serve.cu`` (paged cache and rotary positions) and
+``csrc/fa_shared.cu`` (decode behind shared prefixes). It links the CUDA runtime statically and resolves
 the driver's tensor-map encoder at run time, so it needs no libcuda at link
 time.
 
@@ -60,9 +61,9 @@ def sources() -> list[str]:
 
 def nvcc_cmd(out_path: str, extra: list[str] | None = None) -> list[str]:
     return [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
-            "-Xcompiler", "-fPIC", "-shared", "--threads", "3", "-I", INCLUDE, "-I", CSRC,
+            "-Xcompiler", "-fPIC", "-shared", "--threads", "4", "-I", INCLUDE, "-I", CSRC,
             *(extra or []), os.path.join(CSRC, "fa_api.cu"), os.path.join(CSRC, "fa_serve.cu"), os.path.join(CSRC, "fa_grad.cu"),
-            "-o", out_path]
+            os.path.join(CSRC, "fa_shared.cu"), "-o", out_path]
 
 
 def bind_cmds(obj: str, out_path: str) -> tuple[list[str], list[str]]:

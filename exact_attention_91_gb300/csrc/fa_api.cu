@@ -525,15 +525,15 @@ int fa_device_status(void* stream, unsigned* bits) {
         cudaGetLastError();
         return FA_ERR_NO_DEVICE;
     }
-    unsigned word = 0, grad = 0;
+    unsigned word = 0, grad = 0, shared = 0;
     const unsigned zero = 0;
     if (cudaMemcpyFromSymbol(&word, fa::g_status, sizeof(word)) != cudaSuccess ||
         cudaMemcpyToSymbol(fa::g_status, &zero, sizeof(zero)) != cudaSuccess) {
         cudaGetLastError();
         return FA_ERR_LAUNCH;
     }
-    if (fa::grad_status(&grad) != FA_OK) return FA_ERR_LAUNCH;
-    word |= grad;
+    if (fa::grad_status(&grad) != FA_OK || fa::shared_status(&shared) != FA_OK) return FA_ERR_LAUNCH;
+    word |= grad | shared;
     if (bits) *bits = word;
     return word ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
 }

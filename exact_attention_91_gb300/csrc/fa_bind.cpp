@@ -174,10 +174,10 @@ PyObject* pair(Tensor a, Tensor b) {
 }
 
 // q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse,
-// return_lse, workspace
-PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    HANDLE_TH_ERRORS
-    arguments(n, 12);
+// return_lse, workspace, and for groups that share a prefix prefix_lens
+PyObject* decode_any(PyObject* const* a, PyObject* prefix_lens) {
+    static const Tensor none;
+    const Tensor& prefix = prefix_lens ? tensor(prefix_lens, "prefix_lens") : none;
     const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_cache"), &v = tensor(a[2], "v_cache");
     const Tensor &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seq_lens");
     const Tensor &ks = tensor_or_none(a[6], "k_scale"), &vs = tensor_or_none(a[7], "v_scale");
@@ -187,6 +187,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_TYPE(q.scalar_type() == at::kBFloat16, "q must be bf16");
     int32(table, "block_table");
     int32(lens, "seq_lens");
+    if (prefix_lens) int32(prefix, "prefix_lens");
     TORCH_CHECK_VALUE(q.dim() == 3 && table.dim() == 2 && table.size(0) == q.size(0) && is(lens, {q.size(0)}),
                       "q must be [B, Hq, d], block_table [B, width] and seq_lens [B]");
     TORCH_CHECK_VALUE(q.is_contiguous() && lens.is_contiguous() && dense_last(table),
@@ -200,10 +201,13 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       "lse must be a contiguous fp32 tensor [B, Hq]");
     TORCH_CHECK_VALUE(!ws.defined() || (ws.scalar_type() == at::kByte && ws.is_contiguous()),
                       "workspace must be a contiguous uint8 tensor");
+    const int64_t groups = prefix_lens && prefix.dim() == 1 ? prefix.numel() : 0;
+    TORCH_CHECK_VALUE(!prefix_lens || (groups > 0 && B % groups == 0 && prefix.is_contiguous()),
+                      "prefix_lens must be [groups], contiguous, and B a multiple of groups");
     const c10::Device device = q.device();
     const fa_paged_cache cache = paged_cache(k, v, ks, vs, device);
     cuda(q);
-    for (const Tensor* t : {&table, &lens, static_cast<const Tensor*>(&out), static_cast<const Tensor*>(&lse),
+    for (const Tensor* t : {&table, &lens, &prefix, static_cast<const Tensor*>(&out), static_cast<const Tensor*>(&lse),
                             static_cast<const Tensor*>(&ws)})
         on(*t, device);
     const long long rc = [&]() -> long long {
@@ -215,22 +219,42 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
             int dev = 0, sms = 0;
             const int probed = fa::host_probe(&dev, &sms);
             if (probed != FA_OK) return probed;
-            const long long room = fa_decode_paged_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, cache.type,
-                                                             cache.page_size, to_int(width), sms);
+            const long long room =
+                prefix_lens ? fa_decode_shared_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, to_int(groups), sms)
+                            : fa_decode_paged_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, cache.type,
+                                                        cache.page_size, to_int(width), sms);
             if (room < 0) return room;
             if (room > 0) ws = make({room}, at::kByte, q);
         }
-        return fa_decode_paged(q.data_ptr(), &cache, static_cast<const int*>(table.data_ptr()),
-                               static_cast<const int*>(lens.data_ptr()), out.data_ptr(), static_cast<float*>(ptr(lse)),
-                               to_int(B), to_int(Hq), to_int(width), table.stride(0), scale, ptr(ws),
-                               ws.defined() ? static_cast<size_t>(ws.numel()) : 0,
-                               c10::cuda::getCurrentCUDAStream(device.index()).stream());
+        void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+        const size_t room = ws.defined() ? static_cast<size_t>(ws.numel()) : 0;
+        const int *tables = static_cast<const int*>(table.data_ptr()), *keys = static_cast<const int*>(lens.data_ptr());
+        float* l = static_cast<float*>(ptr(lse));
+        if (prefix_lens)
+            return fa_decode_shared(q.data_ptr(), &cache, tables, keys, static_cast<const int*>(prefix.data_ptr()),
+                                    out.data_ptr(), l, to_int(B), to_int(Hq), to_int(groups), to_int(width),
+                                    table.stride(0), scale, ptr(ws), room, stream);
+        return fa_decode_paged(q.data_ptr(), &cache, tables, keys, out.data_ptr(), l, to_int(B), to_int(Hq),
+                               to_int(width), table.stride(0), scale, ptr(ws), room, stream);
     }();
-    if (rc != FA_OK) return failed(rc, "fa_decode_paged");
+    if (rc != FA_OK) return failed(rc, prefix_lens ? "fa_decode_shared" : "fa_decode_paged");
     wrote(out);
     wrote(lse);
     wrote(ws);
     return return_lse ? pair(std::move(out), std::move(lse)) : THPVariable_Wrap(std::move(out));
+}
+
+PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments(n, 12);
+    return decode_any(a, nullptr);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arguments(n, 13);
+    return decode_any(a, a[12]);
     END_HANDLE_TH_ERRORS
 }
 
@@ -516,6 +540,7 @@ PyObject* maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define FA_FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
 PyMethodDef kMethods[] = {{"setup", FA_FAST(setup), METH_FASTCALL, nullptr},
                           {"decode", FA_FAST(decode), METH_FASTCALL, nullptr},
+                          {"decode_shared", FA_FAST(decode_shared), METH_FASTCALL, nullptr},
                           {"backward", FA_FAST(backward), METH_FASTCALL, nullptr},
                           {"backward_varlen", FA_FAST(backward_varlen), METH_FASTCALL, nullptr},
                           {"rotary", FA_FAST(rotary), METH_FASTCALL, nullptr},

@@ -58,6 +58,8 @@
 // 10.8 us, 0.9 are the third part of P (9.8 with two, which lose 2^-18 of it).
 #pragma once
 
+#include <type_traits>
+
 #include "fa_common.cuh"
 #include "serve_ptx.cuh"
 
@@ -268,10 +270,10 @@ __device__ __forceinline__ uint32_t decode_load(const DecodeParams& p, const Dec
 // The page of this lane's 16-key group of tile t (lanes 0 .. kGroups-1; -1
 // past the end of the keys: never read).
 template <int D, bool E4M3, bool WIDE>
-__device__ __forceinline__ int decode_page(const DecodeParams& p, const DecodeSeg& s, int t, int lane) {
+__device__ __forceinline__ int decode_page(const DecodeParams& p, const DecodeSeg& s, int t, int lane, int page0 = 0) {
     using C = DecodeCfg<D, E4M3, WIDE>;
     const int key = t * C::kKeys + (lane % C::kGroups) * 16;
-    return key < s.len ? p.table[s.b * p.table_stride + (key >> p.page_shift)] : -1;
+    return key < s.len ? p.table[s.b * p.table_stride + page0 + (key >> p.page_shift)] : -1;
 }
 
 // The largest bf16 below each of w (zero for zero); returns what is left: exact,
@@ -285,8 +287,18 @@ __device__ __forceinline__ float2 cut_bf16x2(float2 w, uint32_t& half) {
 // CLUSTER: the small form. Block r of a cluster of p.cluster takes the r-th
 // share of one unit's tiles; the blocks' results are added up through
 // distributed shared memory.
-template <int D, bool E4M3, bool WIDE, bool CLUSTER>
-__global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p) {
+// SHARED (small form): the keys behind a prefix that the requests of a group share, and its partial results, which the
+// kernel before leaves. That one lets this one start once all before both is done (see fa_prefix_kernel): a request's own
+// keys are read at once, and only what it left is waited for.
+struct SharedParams;
+struct SharedAt;
+template <int D>
+__device__ __forceinline__ void shared_add(const SharedParams& p, const SharedAt& a, int i, int c4, float& m, float& l,
+                                           float4& o);
+template <int D, bool E4M3, bool WIDE, bool CLUSTER, bool SHARED = false>
+__global__ void __launch_bounds__(128, 2)
+    fa_decode_kernel(const std::conditional_t<SHARED, SharedParams, DecodeParams> p) {
+    static_assert(CLUSTER || !SHARED);
     using C = DecodeCfg<D, E4M3, WIDE>;
     constexpr int NT = C::kKeys / 8;  // score columns, 8 keys each
     constexpr int ND = D / 8;         // output columns, 8 values each
@@ -304,13 +316,19 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     uint64_t policy = ptx::policy_evict_normal();
     const int worker = blockIdx.x;
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
+    if constexpr (!SHARED) ptx::griddep_wait();
+    int page0 = 0;
     if constexpr (CLUSTER) {
         const int unit = worker / p.cluster, rank = worker - unit * p.cluster;
         if (p.once) policy = ptx::policy_evict_first();
         seg.b = unit / HH;
         seg.u = unit - seg.b * HH;
         seg.len = decode_len(p, seg.b);
+        if constexpr (SHARED) {
+            const int start = shared_start(p, seg.b, seg.len);
+            seg.len -= start;
+            page0 = start >> p.page_shift;
+        }
         seg.nt = decode_tiles<C::kKeys>(seg.len);
         seg.t0 = seg.nt * rank / p.cluster;
         seg.t1 = seg.nt * (rank + 1) / p.cluster;
@@ -410,9 +428,9 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
     };
     seek();
     // (the first two tiles' pages are looked up together, later ones a tile ahead)
-    int entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
+    int entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane, page0) : -1;
     const bool two = more && at + way.step < ahead.t1;
-    const int second = two ? decode_page<D, E4M3, WIDE>(p, ahead, at + way.step, lane) : -1;
+    const int second = two ? decode_page<D, E4M3, WIDE>(p, ahead, at + way.step, lane, page0) : -1;
     uint32_t slot_in = 0, slot_out = 0, ok_bits = 0;
     auto load = [&](bool first) {
         if (more) {
@@ -424,7 +442,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                 entry = second;
             } else {
                 seek();
-                entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
+                entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane, page0) : -1;
             }
         }
         slot_in = slot_in + 1 == C::kStages ? 0 : slot_in + 1;
@@ -788,6 +806,14 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
             continue;
         }
 
+        auto prefix = [&]() {
+            if constexpr (SHARED) {
+                ptx::griddep_wait();
+                return shared_at(p, seg.b, h);
+            } else {
+                return 0;
+            }
+        }();
         // ---- the warps' results of one unit, added up: 8 rows at a time
         float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat);
         float4* merge = reinterpret_cast<float4*>(smem + C::kOffMerge);
@@ -834,6 +860,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                     o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
                 }
                 if (whole) {
+                    if constexpr (SHARED) shared_add<D>(p, prefix, rg * C::kRows + row + 8 * r, c4, mm, l, o);
                     const float inv = l == 0.f ? 0.f : vs / l;
                     const long long out = row0 + row + 8 * r;
                     reinterpret_cast<uint2*>(p.o)[out * (D / 4) + c4] =
@@ -887,6 +914,7 @@ __global__ void __launch_bounds__(128, 2) fa_decode_kernel(const DecodeParams p)
                     l += each[w].y * f;
                     o.x += x[w].x * f, o.y += x[w].y * f, o.z += x[w].z * f, o.w += x[w].w * f;
                 }
+                if constexpr (SHARED) shared_add<D>(p, prefix, rg * C::kRows + row, i % (D / 4), mm, l, o);
                 const float inv = l == 0.f ? 0.f : vs / l;
                 done[k] = make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
                 done_lse[k] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;

@@ -22,8 +22,10 @@ int host_map_tokens(CUtensorMap* map, const void* ptr, int total, int H, int d);
 // How long a kernel waits on one mbarrier phase (fa_set_wait_limit_ns).
 unsigned long long host_wait_limit_ns();
 
-// Reads and clears the status word of the backward kernels' translation unit on the current device.
+// Read and clear the status words of the backward kernels' and the shared-prefix decode's translation units on the
+// current device.
 int grad_status(unsigned* word);
+int shared_status(unsigned* word);
 
 constexpr int kHostMaxDevices = 64;
 

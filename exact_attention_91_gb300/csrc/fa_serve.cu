@@ -14,7 +14,9 @@
 #include "fa_decode_kernel.cuh"
 #include "fa_host.h"
 #include "fa_maps_kernel.cuh"
+#include "fa_prefix_kernel.cuh"
 #include "fa_rotary_kernel.cuh"
+#include "fa_shared.h"
 
 namespace {
 
@@ -256,6 +258,90 @@ int check_decode_sizes(long long B, long long Hq, long long Hkv, int d, int page
     return FA_OK;
 }
 
+// The checks of a decode call, with prefixes of `groups` groups or (0) without.
+int check_decode(const void* q, const fa_paged_cache* cache, const Cache& c, const int* block_table, const int* seq_lens,
+                 const int* prefix_lens, int groups, const void* o, const float* lse, int B, int Hq, int table_width,
+                 long long table_stride, float scale, const void* workspace, size_t workspace_bytes) {
+    const int Hkv = cache->heads, d = cache->d;
+    const int rc = check_decode_sizes(B, Hq, Hkv, d, cache->page_size, table_width);
+    if (rc != FA_OK) return rc;
+    if (table_stride < table_width && B > 1) return FA_ERR_BAD_SHAPE;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_BAD_SCALE;
+    if (B == 0) return FA_OK;
+    if (!q || !o || !block_table || !seq_lens || (groups > 0 && !prefix_lens)) return FA_ERR_NULL_PTR;
+    if (misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4) || misaligned(block_table, 4) ||
+        misaligned(seq_lens, 4) || misaligned(prefix_lens, 4) || misaligned(workspace, 16))
+        return FA_ERR_MISALIGNED;
+    const size_t q_bytes = static_cast<size_t>(B) * Hq * d * 2, lse_bytes = lse ? static_cast<size_t>(B) * Hq * 4 : 0;
+    const size_t table_bytes = (static_cast<size_t>(B - 1) * (B > 1 ? table_stride : 0) + table_width) * 4;
+    const void* outs[3] = {o, lse, workspace};
+    const size_t out_bytes[3] = {q_bytes, lse_bytes, workspace_bytes};
+    for (int i = 0; i < 3; ++i) {
+        if (overlap(outs[i], out_bytes[i], q, q_bytes) || overlap(outs[i], out_bytes[i], cache->k, c.k_bytes) ||
+            overlap(outs[i], out_bytes[i], cache->v, c.v_bytes) ||
+            overlap(outs[i], out_bytes[i], block_table, table_bytes) ||
+            overlap(outs[i], out_bytes[i], seq_lens, static_cast<size_t>(B) * 4) ||
+            overlap(outs[i], out_bytes[i], prefix_lens, static_cast<size_t>(groups) * 4) ||
+            overlap(outs[i], out_bytes[i], cache->k_scale, cache->k_scale ? static_cast<size_t>(Hkv) * 4 : 0) ||
+            overlap(outs[i], out_bytes[i], cache->v_scale, cache->v_scale ? static_cast<size_t>(Hkv) * 4 : 0))
+            return FA_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], out_bytes[i], outs[j], out_bytes[j])) return FA_ERR_ALIAS;
+    }
+    return FA_OK;
+}
+
+void fill_decode(fa::DecodeParams& p, const void* q, const fa_paged_cache* cache, const Cache& c, const int* block_table,
+                 const int* seq_lens, void* o, float* lse, int B, int Hq, int table_width, long long table_stride,
+                 float scale) {
+    p.q = q;
+    p.k = static_cast<const uint8_t*>(cache->k);
+    p.v = static_cast<const uint8_t*>(cache->v);
+    p.o = o;
+    p.lse = lse;
+    p.table = block_table;
+    p.lens = seq_lens;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.k_block = c.k_block, p.k_token = c.k_token, p.k_head = c.k_head;
+    p.v_block = c.v_block, p.v_token = c.v_token, p.v_head = c.v_head;
+    p.table_stride = B > 1 ? table_stride : 0;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    p.B = B;
+    p.Hkv = cache->heads;
+    p.G = Hq / cache->heads;
+    p.row_groups = (p.G + 15) / 16;
+    p.num_blocks = cache->num_blocks;
+    p.page_shift = c.shift;
+    p.width = table_width;
+}
+
+// ---------------------------------------------------------------- decode behind shared prefixes
+
+// How a launch is laid out, from what the host knows.
+struct SharedPlan {
+    int each, rows, row_blocks, slot_rows, chains, workers;
+    long long units;
+    size_t ml, bytes;
+};
+// false: past the limits of an index
+bool shared_plan(long long B, long long Hq, long long Hkv, int d, long long groups, int sms, SharedPlan* out) {
+    SharedPlan& s = *out;
+    s.each = static_cast<int>(B / groups);
+    const long long rows = s.each * (Hq / Hkv);
+    s.rows = static_cast<int>(rows);
+    s.row_blocks = static_cast<int>((rows + 255) / 256);
+    s.slot_rows = static_cast<int>(std::min<long long>(rows, 256));
+    s.chains = rows <= 128 ? 2 : 1;
+    s.workers = sms;
+    s.units = groups * Hkv * s.row_blocks;
+    if (s.units > 0x7fffffffLL) return false;
+    const size_t lines = static_cast<size_t>(s.units + 2LL * s.workers) * s.chains * s.slot_rows;
+    s.ml = (lines * 8 + 15) / 16 * 16;
+    s.bytes = s.ml + lines * d * 4;
+    return true;
+}
+
 template <int D, bool E4M3, bool WIDE>
 int launch_decode(const fa::DecodeParams& p, unsigned blocks, cudaStream_t s) {
     using C = fa::DecodeCfg<D, E4M3, WIDE>;
@@ -328,30 +414,9 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
     int rc = check_cache(cache, &c);
     if (rc != FA_OK) return rc;
     const int Hkv = cache->heads, d = cache->d;
-    rc = check_decode_sizes(B, Hq, Hkv, d, cache->page_size, table_width);
-    if (rc != FA_OK) return rc;
-    if (table_stride < table_width && B > 1) return FA_ERR_BAD_SHAPE;
-    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_BAD_SCALE;
-    if (B == 0) return FA_OK;
-    if (!q || !o || !block_table || !seq_lens) return FA_ERR_NULL_PTR;
-    if (misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4) || misaligned(block_table, 4) ||
-        misaligned(seq_lens, 4) || misaligned(workspace, 16))
-        return FA_ERR_MISALIGNED;
-    const size_t q_bytes = static_cast<size_t>(B) * Hq * d * 2, lse_bytes = lse ? static_cast<size_t>(B) * Hq * 4 : 0;
-    const size_t table_bytes = (static_cast<size_t>(B - 1) * (B > 1 ? table_stride : 0) + table_width) * 4;
-    const void* outs[3] = {o, lse, workspace};
-    const size_t out_bytes[3] = {q_bytes, lse_bytes, workspace_bytes};
-    for (int i = 0; i < 3; ++i) {
-        if (overlap(outs[i], out_bytes[i], q, q_bytes) || overlap(outs[i], out_bytes[i], cache->k, c.k_bytes) ||
-            overlap(outs[i], out_bytes[i], cache->v, c.v_bytes) ||
-            overlap(outs[i], out_bytes[i], block_table, table_bytes) ||
-            overlap(outs[i], out_bytes[i], seq_lens, static_cast<size_t>(B) * 4) ||
-            overlap(outs[i], out_bytes[i], cache->k_scale, cache->k_scale ? static_cast<size_t>(Hkv) * 4 : 0) ||
-            overlap(outs[i], out_bytes[i], cache->v_scale, cache->v_scale ? static_cast<size_t>(Hkv) * 4 : 0))
-            return FA_ERR_ALIAS;
-        for (int j = 0; j < i; ++j)
-            if (overlap(outs[i], out_bytes[i], outs[j], out_bytes[j])) return FA_ERR_ALIAS;
-    }
+    rc = check_decode(q, cache, c, block_table, seq_lens, nullptr, 0, o, lse, B, Hq, table_width, table_stride, scale,
+                      workspace, workspace_bytes);
+    if (rc != FA_OK || B == 0) return rc;
     int dev = 0, sms = 0;
     rc = fa::host_probe(&dev, &sms);
     if (rc != FA_OK) return rc;
@@ -364,38 +429,69 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
     if (ready(dev, s) != FA_OK) return FA_ERR_LAUNCH;
 
     fa::DecodeParams p{};
-    p.q = q;
-    p.k = static_cast<const uint8_t*>(cache->k);
-    p.v = static_cast<const uint8_t*>(cache->v);
-    p.o = o;
-    p.lse = lse;
-    p.table = block_table;
-    p.lens = seq_lens;
-    p.k_scale = cache->k_scale;
-    p.v_scale = cache->v_scale;
+    fill_decode(p, q, cache, c, block_table, seq_lens, o, lse, B, Hq, table_width, table_stride, scale);
     if (sp.bytes > 0) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.meta = reinterpret_cast<int4*>(ws + sp.meta);
         p.part_ml = reinterpret_cast<float2*>(ws + sp.ml);
         p.part_o = reinterpret_cast<float*>(ws + sp.o);
     }
-    p.k_block = c.k_block, p.k_token = c.k_token, p.k_head = c.k_head;
-    p.v_block = c.v_block, p.v_token = c.v_token, p.v_head = c.v_head;
-    p.table_stride = B > 1 ? table_stride : 0;
-    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-    p.B = B;
-    p.Hkv = Hkv;
-    p.G = Hq / Hkv;
-    p.row_groups = (p.G + 15) / 16;
-    p.num_blocks = cache->num_blocks;
-    p.page_shift = c.shift;
-    p.width = table_width;
     p.cluster = plan.cluster;
     p.once = plan.tiles >= 2 * fa::kOnceTiles;  // (ragged lengths fill about half of the bound)
     p.fours = decode_fours(Hq, Hkv) ? 1 : 0;
     const long long units = static_cast<long long>(B) * Hkv * p.row_groups;
     const unsigned w = static_cast<unsigned>(plan.cluster > 0 ? units * plan.cluster : plan.workers);
     return d == 64 ? launch_decode_any<64>(c.e4m3, wide, p, w, s) : launch_decode_any<128>(c.e4m3, wide, p, w, s);
+}
+
+long long fa_decode_shared_workspace(int B, int Hq, int Hkv, int d, int groups, int sm_count) {
+    const int rc = check_decode_sizes(B, Hq, Hkv, d, kMinPage, 1);
+    if (rc != FA_OK) return rc;
+    if (sm_count < 1 || groups < 1 || B % groups != 0) return FA_ERR_BAD_SHAPE;
+    if (B == 0) return 0;
+    SharedPlan plan;
+    if (!shared_plan(B, Hq, Hkv, d, groups, sm_count, &plan)) return FA_ERR_BAD_SHAPE;
+    return static_cast<long long>(plan.bytes);
+}
+
+int fa_decode_shared(const void* q, const fa_paged_cache* cache, const int* block_table, const int* seq_lens,
+                     const int* prefix_lens, void* o, float* lse, int B, int Hq, int groups, int table_width,
+                     long long table_stride, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    Cache c;
+    int rc = check_cache(cache, &c);
+    if (rc != FA_OK) return rc;
+    const int Hkv = cache->heads, d = cache->d;
+    if (groups < 1 || B % groups != 0) return FA_ERR_BAD_SHAPE;
+    rc = check_decode(q, cache, c, block_table, seq_lens, prefix_lens, groups, o, lse, B, Hq, table_width, table_stride,
+                      scale, workspace, workspace_bytes);
+    if (rc != FA_OK || B == 0) return rc;
+    const long long units = static_cast<long long>(B) * Hkv * ((Hq / Hkv + 15) / 16);
+    SharedPlan plan;
+    if (units > 0x7fffffffLL / fa::kDecodeCluster) return FA_ERR_BAD_SHAPE;
+    int dev = 0, sms = 0;
+    rc = fa::host_probe(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    if (!shared_plan(B, Hq, Hkv, d, groups, sms, &plan)) return FA_ERR_BAD_SHAPE;
+    if (!workspace || workspace_bytes < plan.bytes) return FA_ERR_WORKSPACE;
+
+    fa::SharedParams p{};
+    fill_decode(p, q, cache, c, block_table, seq_lens, o, lse, B, Hq, table_width, table_stride, scale);
+    // a cluster for each (request, key head)'s own keys, as large as one wave holds: how many they are only the GPU knows
+    p.cluster = 1;
+    while (p.cluster < fa::kDecodeCluster && 2 * p.cluster * units <= static_cast<long long>(kWorkersPerSm) * sms)
+        p.cluster *= 2;
+    p.prefix_lens = prefix_lens;
+    p.groups = groups;
+    p.each = plan.each;
+    p.rows = plan.rows;
+    p.row_blocks = plan.row_blocks;
+    p.slot_rows = plan.slot_rows;
+    p.chains = plan.chains;
+    p.prefix_workers = plan.workers;
+    p.shared_ml = static_cast<float2*>(workspace);
+    p.shared_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.ml);
+    p.wait_limit_ns = fa::host_wait_limit_ns();
+    return fa::shared_launch(dev, d, c.e4m3, p, static_cast<cudaStream_t>(stream));
 }
 
 int fa_rotary(const void* x, void* y, const int* positions, const double* inv_freq, int B, int H, int N, int d,

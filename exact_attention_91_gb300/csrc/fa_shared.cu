@@ -1,0 +1,105 @@
+// Launches of the shared-prefix decode: the kernel of the shared part, and the decode kernel that adds it to each
+// request's own keys. (Argument checks: fa_serve.cu.)
+#include <atomic>
+#include <mutex>
+
+#include <cuda_runtime.h>
+
+#include "fa.h"
+#include "fa_host.h"
+#include "fa_prefix_kernel.cuh"
+#include "fa_shared.h"
+
+namespace {
+
+std::mutex g_ready_mu;
+std::atomic<bool> g_ready[fa::kHostMaxDevices];
+
+template <typename Kernel>
+bool set_smem(Kernel kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess;
+}
+
+template <int D, bool E4M3>
+bool set_pair() {
+    return set_smem(fa::fa_prefix_kernel<D, E4M3>, fa::PrefixCfg<D, E4M3>::kSmemBytes) &&
+           set_smem(fa::fa_decode_kernel<D, E4M3, false, true, true>, fa::DecodeCfg<D, E4M3, false>::kSmemBytes) &&
+           set_smem(fa::fa_decode_kernel<D, E4M3, true, true, true>, fa::DecodeCfg<D, E4M3, true>::kSmemBytes);
+}
+
+// The kernels' shared-memory sizes, set on the device by its first call that is not being captured; a captured call
+// needs them set already.
+int ready(int dev, cudaStream_t stream) {
+    if (g_ready[dev].load(std::memory_order_acquire)) return FA_OK;
+    if (fa::host_capturing(stream) != 0) return FA_ERR_LAUNCH;
+    std::lock_guard<std::mutex> lock(g_ready_mu);
+    if (!(set_pair<64, false>() && set_pair<64, true>() && set_pair<128, false>() && set_pair<128, true>())) {
+        cudaGetLastError();
+        return FA_ERR_LAUNCH;
+    }
+    g_ready[dev].store(true, std::memory_order_release);
+    return FA_OK;
+}
+
+int launch(void (*kernel)(fa::SharedParams), unsigned blocks, int threads, int smem, cudaStream_t stream,
+           const fa::SharedParams& p, int cluster) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return FA_OK;
+    cudaGetLastError();
+    return FA_ERR_LAUNCH;
+}
+
+template <int D, bool E4M3, bool WIDE>
+int launch_both(const fa::SharedParams& p, cudaStream_t s) {
+    using C = fa::PrefixCfg<D, E4M3>;
+    using Own = fa::DecodeCfg<D, E4M3, WIDE>;
+    const int rc = launch(fa::fa_prefix_kernel<D, E4M3>, static_cast<unsigned>(p.prefix_workers), C::kThreads,
+                          C::kSmemBytes, s, p, 1);
+    if (rc != FA_OK) return rc;
+    return launch(fa::fa_decode_kernel<D, E4M3, WIDE, true, true>,
+                  static_cast<unsigned>(p.B * p.Hkv * p.row_groups * p.cluster), Own::kThreads, Own::kSmemBytes, s, p,
+                  p.cluster);
+}
+
+template <int D>
+int launch_any(bool e4m3, bool wide, const fa::SharedParams& p, cudaStream_t s) {
+    if (e4m3) return wide ? launch_both<D, true, true>(p, s) : launch_both<D, true, false>(p, s);
+    return wide ? launch_both<D, false, true>(p, s) : launch_both<D, false, false>(p, s);
+}
+
+}  // namespace
+
+namespace fa {
+
+int shared_launch(int dev, int d, bool e4m3, const SharedParams& p, cudaStream_t s) {
+    if (ready(dev, s) != FA_OK) return FA_ERR_LAUNCH;
+    const bool wide = p.G > 8;
+    return d == 64 ? launch_any<64>(e4m3, wide, p, s) : launch_any<128>(e4m3, wide, p, s);
+}
+
+int shared_status(unsigned* word) {
+    const unsigned zero = 0;
+    if (cudaMemcpyFromSymbol(word, g_status, sizeof(*word)) == cudaSuccess &&
+        cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) == cudaSuccess)
+        return FA_OK;
+    cudaGetLastError();
+    return FA_ERR_LAUNCH;
+}
+
+}  // namespace fa

@@ -1,0 +1,13 @@
+// The shared-prefix decode's launches, for the translation unit that checks its arguments.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace fa {
+
+struct SharedParams;
+
+// Launches both kernels on the current device `dev`.
+int shared_launch(int dev, int d, bool e4m3, const SharedParams& p, cudaStream_t s);
+
+}  // namespace fa

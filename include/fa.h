@@ -341,6 +341,34 @@ long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_typ
                                     int sm_count);
 
 /*
+ * fa_decode_shared — fa_decode_paged for requests that share the pages of a prefix (several answers
+ * to one question, a system prompt, the beams of a search), whose keys and values are then read once for
+ * all of them. The requests come in `groups` groups of B / groups neighbours.
+ *
+ *   prefix_lens  int32 [groups], device: the first prefix_lens[g] / page_size (rounded down) entries of
+ *                block_table are the same in all rows of group g; they are read in the group's first row
+ *                (padding requests' rows too: the first row holds the prefix's pages whatever its own
+ *                length is). 0 or less: nothing is shared. Clamped to the table's width.
+ *   B            a multiple of groups
+ *   workspace    device, 16-byte aligned, at least fa_decode_shared_workspace() bytes, as fa_decode_paged's
+ *
+ * Everything else is as for fa_decode_paged, and so is the result: attention over the first seq_lens[b] keys of
+ * each request, its hidden pages and scales likewise, but that weights of the shared keys are rounded to
+ * bf16 (2^-9 relative, each before it meets its value) as fa_fwd's are. A request that is shorter than its
+ * group's prefix is read by itself.
+ * Two kernels; the second one starts on the requests' own keys while the first is at the prefixes.
+ */
+int fa_decode_shared(const void* q, const fa_paged_cache* cache, const int* block_table, const int* seq_lens,
+                     const int* prefix_lens, void* o, float* lse, int B, int Hq, int groups, int table_width,
+                     long long table_stride, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_decode_shared_workspace — host-only: workspace bytes of fa_decode_shared for these sizes on a GPU with
+ * sm_count SMs, or a negative status under the call's own rules.
+ */
+long long fa_decode_shared_workspace(int B, int Hq, int Hkv, int d, int groups, int sm_count);
+
+/*
  * fa_rotary — rotary positions of x [B, H, N, d] (bf16, device), into y.
  * Pair i < rotary_dim/2 of each head is turned by a = position · inv_freq[i]:
  *   (y1, y2) = factor · (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
