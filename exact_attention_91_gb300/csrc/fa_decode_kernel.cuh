@@ -808,8 +808,9 @@ __global__ void __launch_bounds__(128, 2)
 
         auto prefix = [&]() {
             if constexpr (SHARED) {
+                const auto at = shared_at(p, seg.b, h);
                 ptx::griddep_wait();
-                return shared_at(p, seg.b, h);
+                return at;
             } else {
                 return 0;
             }

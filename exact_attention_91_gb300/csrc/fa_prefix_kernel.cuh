@@ -24,6 +24,7 @@
 namespace fa {
 
 constexpr int kPrefixWorkersMinRun = 2;  // least key tiles of a block's run
+constexpr int kStagger = 2;              // tiles of a chain from which on the chains start one after the other
 
 struct SharedParams : DecodeParams {
     const int* prefix_lens;  // [groups] tokens; whole pages of it are shared
@@ -46,22 +47,16 @@ __device__ __forceinline__ int prefix_tokens(const SharedParams& p, int g) {
 }
 __device__ __forceinline__ int prefix_tiles(int tokens) { return tokens / kBlockN + (tokens % kBlockN != 0); }
 
-// Tiles of one (key head, row block) of groups before g, and of all groups; by a whole warp.
+// Tiles of one (key head, row block) of groups before g, and of all groups; by a whole warp. (A group's fit in 24 bits.)
 __device__ __forceinline__ void prefix_sums(const SharedParams& p, int g, long long& before, long long& total) {
     const int lane = static_cast<int>(threadIdx.x & 31);
-    long long b = 0, t = 0;
-    for (int i = lane; i < p.groups; i += 32) {
-        const int n = prefix_tiles(prefix_tokens(p, i));
-        t += n;
-        if (i < g) b += n;
+    before = total = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+        const int i = g0 + lane;
+        const unsigned n = i < p.groups ? static_cast<unsigned>(prefix_tiles(prefix_tokens(p, i))) : 0u;
+        total += __reduce_add_sync(0xffffffffu, n);
+        if (g0 < g) before += __reduce_add_sync(0xffffffffu, i < g ? n : 0u);
     }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-        b += __shfl_xor_sync(0xffffffffu, b, m);
-        t += __shfl_xor_sync(0xffffffffu, t, m);
-    }
-    before = b;
-    total = t;
 }
 
 // Blocks that a total of key tiles is cut for.
@@ -95,26 +90,26 @@ __device__ __forceinline__ bool prefix_first(const SharedParams& p, int worker, 
     s.rem = decode_start(total, workers, worker + 1) - at;
     if (s.rem <= 0) return false;
     for (int g0 = 0;; g0 += 32) {
-        const int n = g0 + lane < p.groups ? prefix_tiles(prefix_tokens(p, g0 + lane)) : 0;
-        long long sum = n;
+        const int tokens = g0 + lane < p.groups ? prefix_tokens(p, g0 + lane) : 0, n = prefix_tiles(tokens);
+        int sum = n;
 #pragma unroll
         for (int i = 1; i < 32; i <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, sum, i);
+            const int x = __shfl_up_sync(0xffffffffu, sum, i);
             if (lane >= i) sum += x;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, at < sum * per);
+        const unsigned past = __ballot_sync(0xffffffffu, at < static_cast<long long>(sum) * per);
         if (past != 0) {
             const int l = __ffs(past) - 1;
             s.g = g0 + l;
             s.T = __shfl_sync(0xffffffffu, n, l);
-            at -= __shfl_sync(0xffffffffu, sum - n, l) * per;
+            s.tokens = __shfl_sync(0xffffffffu, tokens, l);
+            at -= static_cast<long long>(__shfl_sync(0xffffffffu, sum - n, l)) * per;
             break;
         }
-        at -= __shfl_sync(0xffffffffu, sum, 31) * per;
+        at -= static_cast<long long>(__shfl_sync(0xffffffffu, sum, 31)) * per;
         if (g0 + 32 >= p.groups) return false;  // (only if the lengths changed under the launch)
     }
-    s.tokens = prefix_tokens(p, s.g);
-    const int unit = static_cast<int>(at / s.T);
+    const int unit = static_cast<int>(at <= 0xffffffffLL ? static_cast<unsigned>(at) / static_cast<unsigned>(s.T) : at / s.T);
     s.t0 = static_cast<int>(at - static_cast<long long>(unit) * s.T);
     s.h = min(unit / p.row_blocks, p.Hkv - 1);
     s.rb = unit % p.row_blocks;
@@ -151,25 +146,35 @@ __device__ __forceinline__ long long prefix_slot(const SharedParams& p, long lon
 
 template <int D, bool E4M3>
 struct PrefixCfg {
-    static constexpr int kThreads = 14 * 32;
+    static constexpr int kThreads = 512;  // warpgroups: softmax of the two chains, loads, products (two of its warps)
     static constexpr int kTileBytes = D * kBlockM * 2;
-    static constexpr int kStages = D == 128 ? 5 : 8;  // K and V in turn
-    static constexpr int kLag = 2;                    // copies in flight behind the newest
+    static constexpr int kStages = D == 128 ? (E4M3 ? 3 : 5) : (E4M3 ? 6 : 8);  // K and V in turn
+    static constexpr int kLag = 2;                    // bf16: copies in flight behind the newest
+    static constexpr int kRaw = E4M3 ? (D == 128 ? 4 : 8) : 0;  // e4m3: tiles as the cache holds them, on their way
+    static constexpr int kRawBytes = D * kBlockN;
     static constexpr int kOffRing = 2 * kTileBytes;   // (Q tiles first)
-    static constexpr int kOffSeen = kOffRing + kStages * kTileBytes;  // [slot][4] words: keys whose page is in the cache
-    static constexpr int kOffBar = kOffSeen + kStages * 16;
-    static constexpr int kNumBars = 2 * kStages + 5 * 2;
+    static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
+    // [tile of the run % 8][4] words: keys whose page is in the cache. (The ring holds 4 tiles at most, and a tile's K is
+    // taken only when the softmax of the one before is done: 8 are more than are ever between the loads and the softmax.)
+    static constexpr int kOffSeen = kOffRaw + kRaw * kRawBytes;
+    static constexpr int kOffRawSeen = kOffSeen + 8 * 16;
+    static constexpr int kOffBar = kOffRawSeen + kRaw * 16;
+    static constexpr int kNumBars = 2 * kStages + 5 * 2 + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr int kSmemBytes = kOffMisc + 8 + 1024;
+    static constexpr int kOffSeg = kOffMisc + 16;  // (behind TMEM slot, abort flag, tiles that chain 0 has done)
+    static constexpr int kSmemBytes = kOffSeg + 48 + 1024;
     static_assert(kSmemBytes <= 227 * 1024);
     static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
     static constexpr int kRowLanes = kRowBytes / 16;      // lanes that copy one row
     static constexpr int kRowsPerCopy = 32 / kRowLanes;
     static constexpr int kCopies = 32 / kRowsPerCopy;     // of a warp's 32 rows
+    // 512 threads launch with 128 registers each, all that an SM has; the softmax keeps a row of 128 scores.
+    static constexpr uint32_t kRegsSoftmax = 184, kRegsOther = 72;
+    static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * 128, "register split");
 };
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(448, 1) fa_prefix_kernel(const SharedParams p) {
+__global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p) {
     using C = PrefixCfg<D, E4M3>;
     constexpr uint32_t kTmemS = 0, kTmemO = 256;  // S of chain c at 128 c (P over its first 64 columns), O at 256 + D c
     extern __shared__ uint8_t smem_raw[];
@@ -184,8 +189,10 @@ __global__ void __launch_bounds__(448, 1) fa_prefix_kernel(const SharedParams p)
     auto p_full = [&](int c) { return bar(2 * C::kStages + 4 + c); };
     auto pv_done = [&](int c) { return bar(2 * C::kStages + 6 + c); };
     auto fin = [&](int c) { return bar(2 * C::kStages + 8 + c); };
+    const uint32_t seg_full = bar(2 * C::kStages + 10);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::kOffMisc + 4);
+    volatile uint32_t* chain0 = reinterpret_cast<uint32_t*>(base + C::kOffMisc + 8);
     const unsigned long long lim = p.wait_limit_ns;
     // A whole warp waits for the n-th phase of a barrier.
     auto wait = [&](uint32_t b, uint32_t n, unsigned site) {
@@ -204,111 +211,168 @@ __global__ void __launch_bounds__(448, 1) fa_prefix_kernel(const SharedParams p)
             if (b == q_full(0) || b == q_full(1) || b == p_full(0) || b == p_full(1)) count = 4;
             ptx::mbar_init(b, count);
         }
-        if (lane == 0) *abort_flag = 0;
+        if (lane == 0) {
+            *abort_flag = 0;
+            *chain0 = 0u;
+        }
         ptx::fence_mbar_init();
     }
-    ptx::griddep_wait();
-    // From here on what precedes this launch is done and visible: so it is to the kernel behind it, which reads its own
-    // keys at once and waits for this one only for the partial results.
-    ptx::griddep_launch_dependents();
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
     const int worker = static_cast<int>(blockIdx.x);
     const bool half = p.chains == 2;  // the chains take the even and the odd key tiles of the same rows
-    PrefixSeg s;
-    bool more = prefix_first(p, worker, s);
+    PrefixSeg s{};  // (set in each role, behind its register split)
+    bool more = false;
+    PrefixSeg* first_seg = reinterpret_cast<PrefixSeg*>(base + C::kOffSeg);
+    static_assert(sizeof(PrefixSeg) <= 48);
+    auto take_first = [&]() {  // the first segment, as a loading warp found it
+        if (!wait(seg_full, 0, kStatusTimeoutOther)) return false;
+        s = *first_seg;
+        return s.T > 0;
+    };
     // whether chain c uses tile t of the segment; rows of chain c
     auto rows_of = [&](int c) { return half ? p.rows : min(max(p.rows - s.rb * 256 - c * 128, 0), 128); };
     auto uses = [&](int c, int t) { return half ? ((t - s.t0) & 1) == c : rows_of(c) > 0; };
 
     if (warp >= 8 && warp < 12) {
         // ---- loads: each warp 32 rows of every tile
+        ptx::regs_dec<C::kRegsOther>();
+        ptx::griddep_wait();
+        more = prefix_first(p, worker, s);
+        if (warp == 8 && lane == 0) {  // for the other roles
+            *first_seg = s;
+            if (!more) first_seg->T = 0;
+            ptx::mbar_arrive(seg_full);
+        }
         const int lw = warp - 8, lr = lane / C::kRowLanes, lc = lane % C::kRowLanes;
-        uint32_t cnt = 0;
-        bool ok = true;
-        uint32_t done = 0;  // tiles handed over
         const uint64_t policy = ptx::policy_evict_normal();
-        auto hand_over = [&](uint32_t upto) {
-            for (; done < upto; ++done) {
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(full(done));
-            }
+        uint32_t cnt = 0;  // tiles copied (K and V in turn)
+        bool ok = true;
+        // the cursor of the copies: tile `t` of segment s, the page of this lane's key in it and in the next one
+        int t = s.t0, page = -1;
+        long long k_at = 0, v_at = 0;
+        unsigned seen = 0;
+        auto page_of = [&](int tile) {
+            const int key = tile * kBlockN + lw * 32 + lane;
+            return key < s.tokens && tile < s.t1
+                       ? p.table[static_cast<long long>(s.g) * p.each * p.table_stride + (key >> p.page_shift)]  // first row
+                       : -1;
         };
-        for (; more && ok; more = prefix_next(p, s)) {
-            const int* table = p.table + static_cast<long long>(s.g) * p.each * p.table_stride;  // the first request's row
-            for (int t = s.t0; t < s.t1 && ok; ++t) {
-                const int key0 = t * kBlockN + lw * 32, mine = key0 + lane;
-                const int page = mine < s.tokens ? table[mine >> p.page_shift] : -1;
-                const bool in = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
-                const unsigned seen = __ballot_sync(0xffffffffu, in);
-                const int tok = mine & ((1 << p.page_shift) - 1);
-                const long long k_at = (in ? page : 0) * p.k_block + tok * p.k_token + s.h * p.k_head;
-                const long long v_at = (in ? page : 0) * p.v_block + tok * p.v_token + s.h * p.v_head;
-                // both slots of the tile: the softmax looks at `seen` behind V's, which is not taken before P is there
-                ok = (cnt < C::kStages || wait(free_(cnt), cnt / C::kStages - 1, kStatusTimeoutFree)) &&
-                     (cnt + 1 < C::kStages || wait(free_(cnt + 1), (cnt + 1) / C::kStages - 1, kStatusTimeoutFree));
-                if (!ok) break;
-                if (lane == 0) reinterpret_cast<unsigned*>(base + C::kOffSeen)[(cnt + 1) % C::kStages * 4 + lw] = seen;
+        if (more) page = page_of(t);
+        auto enter = [&]() {  // where this lane's key of tile t is; on to the page of the tile behind it
+            const bool in = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_blocks);
+            seen = __ballot_sync(0xffffffffu, in);
+            const long long block = in ? page : 0;
+            const int tok = (t * kBlockN + lw * 32 + lane) & ((1 << p.page_shift) - 1);
+            k_at = block * p.k_block + tok * p.k_token + s.h * p.k_head;
+            v_at = block * p.v_block + tok * p.v_token + s.h * p.v_head;
+            page = page_of(t + 1);
+        };
+        auto advance = [&]() {
+            if (++t < s.t1) return;
+            more = prefix_next(p, s);
+            if (!more) return;
+            t = s.t0;
+            page = page_of(t);
+        };
+        auto copy = [&](const uint8_t* from, long long at, auto&& to) {
+#pragma unroll
+            for (int i = 0; i < C::kCopies; ++i) {
+                const int r = i * C::kRowsPerCopy + lr;
+                const long long src = __shfl_sync(0xffffffffu, at, r);
+                ptx::cp_async16(to(i, lw * 32 + r), from + src + lc * 16, seen >> r & 1 ? 16u : 0u, policy);
+            }
+            ptx::cp_async_commit();
+        };
+        auto take_slot = [&](uint32_t at, unsigned words) {
+            ok = at < C::kStages || wait(free_(at), at / C::kStages - 1, kStatusTimeoutFree);
+            if ((at & 1) == 0 && lane == 0) reinterpret_cast<unsigned*>(base + C::kOffSeen)[(at / 2 & 7) * 4 + lw] = words;
+        };
+        auto hand_over = [&](uint32_t at) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(full(at));
+        };
+        if constexpr (!E4M3) {
+            for (; more && ok; advance()) {
+                enter();
 #pragma unroll
                 for (int which = 0; which < 2; ++which, ++cnt) {
-                    const uint32_t slot = cnt % C::kStages, to = sbase + C::kOffRing + slot * C::kTileBytes;
-                    const uint8_t* from = which == 0 ? p.k : p.v;
-                    const long long at = which == 0 ? k_at : v_at;
-                    if constexpr (!E4M3) {
-#pragma unroll
-                        for (int i = 0; i < C::kCopies; ++i) {
-                            const int r = i * C::kRowsPerCopy + lr, row = lw * 32 + r;
-                            const long long src = __shfl_sync(0xffffffffu, at, r);
-                            ptx::cp_async16(to + (lc >> 3) * kBoxBytes + sw128_offset(row, lc & 7), from + src + lc * 16,
-                                            seen >> r & 1 ? 16u : 0u, policy);
-                        }
-                        ptx::cp_async_commit();
-                        ptx::cp_async_wait<C::kLag>();
-                        if (cnt >= C::kLag) hand_over(cnt - C::kLag + 1);
-                    } else {
-                        uint4 x[C::kCopies];
-#pragma unroll
-                        for (int i = 0; i < C::kCopies; ++i) {
-                            const int r = i * C::kRowsPerCopy + lr;
-                            const long long src = __shfl_sync(0xffffffffu, at, r);
-                            x[i] = make_uint4(0, 0, 0, 0);
-                            if (seen >> r & 1) x[i] = *reinterpret_cast<const uint4*>(from + src + lc * 16);
-                        }
-#pragma unroll
-                        for (int i = 0; i < C::kCopies; ++i) {
-                            const int row = lw * 32 + i * C::kRowsPerCopy + lr;
-                            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                            uint32_t b[8];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float2 f = ptx::unpack_f16x2(
-                                        ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(e ? w[k] >> 16 : w[k])));
-                                    b[2 * k + e] = ptx::pack_bf16x2(f.x, f.y);
-                                }
-                            const int c = lc * 2;  // 16-byte chunk of the bf16 row
-                            uint8_t* box = base + C::kOffRing + slot * C::kTileBytes + (c >> 3) * kBoxBytes;
-                            *reinterpret_cast<uint4*>(box + sw128_offset(row, c & 7)) = make_uint4(b[0], b[1], b[2], b[3]);
-                            *reinterpret_cast<uint4*>(box + sw128_offset(row, (c & 7) + 1)) = make_uint4(b[4], b[5], b[6], b[7]);
-                        }
-                        hand_over(cnt + 1);
-                    }
+                    take_slot(cnt, seen);
+                    if (!ok) break;
+                    const uint32_t to = sbase + C::kOffRing + cnt % C::kStages * C::kTileBytes;
+                    copy(which ? p.v : p.k, which ? v_at : k_at,
+                         [&](int, int row) { return to + (lc >> 3) * kBoxBytes + sw128_offset(row, lc & 7); });
+                    ptx::cp_async_wait<C::kLag>();
+                    if (cnt >= C::kLag) hand_over(cnt - C::kLag);
                 }
             }
+            ptx::cp_async_wait<0>();
+            for (uint32_t at = cnt < C::kLag ? 0 : cnt - C::kLag; ok && at < cnt; ++at) hand_over(at);
+        } else {
+            // a thread widens the 16-byte pieces that it copied itself
+            const uint32_t raw = sbase + C::kOffRaw + (lw * C::kCopies * 32 + lane) * 16;
+            unsigned* raw_seen = reinterpret_cast<unsigned*>(base + C::kOffRawSeen) + lw;
+            bool second = false;  // whether V of the cursor's tile is next
+            auto issue = [&]() {
+                if (more) {
+                    const uint32_t slot = cnt % C::kRaw;
+                    if (!second) enter();
+                    if (lane == 0) raw_seen[slot * 4] = seen;
+                    copy(second ? p.v : p.k, second ? v_at : k_at,
+                         [&](int i, int) { return raw + slot * C::kRawBytes + i * 512; });
+                    ++cnt;
+                    if (second) advance();
+                    second = !second;
+                } else {
+                    ptx::cp_async_commit();
+                }
+            };
+#pragma unroll 1
+            for (int i = 0; i < C::kRaw - 1; ++i) issue();
+#pragma unroll 1
+            for (uint32_t at = 0; at < cnt && ok; ++at) {
+                issue();
+                ptx::cp_async_wait<C::kRaw - 1>();
+                take_slot(at, lane == 0 ? raw_seen[at % C::kRaw * 4] : 0u);
+                if (!ok) break;
+                uint8_t* to = base + C::kOffRing + at % C::kStages * C::kTileBytes;
+#pragma unroll
+                for (int i = 0; i < C::kCopies; ++i) {
+                    const int row = lw * 32 + i * C::kRowsPerCopy + lr, chunk = lc * 2;  // (16 bytes of the bf16 row)
+                    const uint4 x = ptx::lds128(raw + at % C::kRaw * C::kRawBytes + i * 512);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t b[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 f =
+                                ptx::unpack_f16x2(ptx::e4m3x2_to_f16x2(static_cast<uint16_t>(e ? w[k] >> 16 : w[k])));
+                            b[2 * k + e] = ptx::pack_bf16x2(f.x, f.y);
+                        }
+                    uint8_t* box = to + (chunk >> 3) * kBoxBytes;
+                    *reinterpret_cast<uint4*>(box + sw128_offset(row, chunk & 7)) = make_uint4(b[0], b[1], b[2], b[3]);
+                    *reinterpret_cast<uint4*>(box + sw128_offset(row, (chunk & 7) + 1)) = make_uint4(b[4], b[5], b[6], b[7]);
+                }
+                hand_over(at);
+            }
+            ptx::cp_async_wait<0>();
         }
-        ptx::cp_async_wait<0>();
-        if (ok) hand_over(cnt);
     } else if (warp >= 12) {
         // ---- the products of chain c
+        ptx::regs_dec<C::kRegsOther>();
         const int c = warp - 12;
+        const uint32_t tmem = *tmem_slot;
+        ptx::griddep_wait();
+        more = take_first();
+        if (c >= 2) more = false;
         constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, kBlockN, false, false);
         constexpr uint32_t kIdescPv = ptx::idesc_bf16_f32(128, D, false, true);
         const uint32_t tS = tmem + kTmemS + c * 128, tO = tmem + kTmemO + c * D;
         uint32_t cnt = 0, done = 0, units = 0;  // ring position, tiles of this chain, segments that it took part in
+        uint32_t others = 0;                    // tiles of chain 0
         bool ok = true;
         for (; more && ok; more = prefix_next(p, s)) {
             bool started = false;
@@ -323,7 +387,13 @@ __global__ void __launch_bounds__(448, 1) fa_prefix_kernel(const SharedParams p)
                     }
                     continue;
                 }
-                if (!started) ok = wait(q_full(c), units++, kStatusTimeoutOther);
+                if (!started) {
+                    ok = wait(q_full(c), units++, kStatusTimeoutOther);
+                    // chain 1 starts half a step behind, so that the softmax of one chain meets the products
+                    // of the other (a preference only: it guards no data)
+                    if (c == 1 && (s.t1 - s.t0) / (half ? 2 : 1) >= kStagger)
+                        for (int spin = 0; spin < 100 && *chain0 <= others; ++spin) __nanosleep(32);
+                }
                 // (S is written over the P that the product before reads)
                 if (ok && done > 0) ok = wait(pv_done(c), done - 1, kStatusTimeoutMma);
                 if (!ok) break;
@@ -351,50 +421,82 @@ __global__ void __launch_bounds__(448, 1) fa_prefix_kernel(const SharedParams p)
                 started = true;
                 ++done;
             }
+            others += static_cast<uint32_t>(half ? (s.t1 - s.t0 + 1) / 2 : s.t1 - s.t0);
         }
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && c < 2) {
             ptx::mma_commit(fin(c));
             wait_drain(fin(c), 0, 100000000ull);
         }
         __syncwarp();
     } else {
         // ---- softmax of chain c, one row per thread
+        ptx::regs_inc<C::kRegsSoftmax>();
+        const uint32_t tmem = *tmem_slot;
         const int c = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + kTmemS + c * 128 + lanes, tO = tmem + kTmemO + c * D + lanes;
-        uint32_t done = 0, cnt = 0, tiles = 0;  // of this chain; ring position of the segment; its tiles
+        const int step = half ? 2 : 1;
+        uint32_t done = 0, cnt = 0;  // tiles of this chain; ring position of the segment
         bool ok = true;
         constexpr float kLazy = 8.f;  // O and the sum are rescaled only when the row maximum rises by more
-        for (; more && ok; more = prefix_next(p, s)) {
-            cnt += 2 * tiles;
-            tiles = static_cast<uint32_t>(s.t1 - s.t0);
-            const int first = half ? s.t0 + c : s.t0, step = half ? 2 : 1;
-            const int rows = rows_of(c);
-            const long long unit = (static_cast<long long>(s.g) * p.Hkv + s.h) * p.row_blocks + s.rb;
-            const long long slot = prefix_slot(p, unit, worker, s.t0 == 0, s.t1 == s.T);
-            const long long out = half ? (slot * 2 + c) * p.slot_rows : slot * p.slot_rows + c * 128;  // first row
-            const bool have = row < rows;
-            if (rows == 0) continue;
-            if (first >= s.t1) {  // no key tile for this chain
-                if (have) p.shared_ml[out + row] = make_float2(-INFINITY, 0.f);
-                continue;
-            }
-            // the factor from q·k to base-2 scores, made positive: a negative one's sign goes to q (0: every score is next to it)
-            float cs = p.scale_log2 * (p.k_scale ? p.k_scale[s.h] : 1.f);
-            const uint32_t flip = cs < 0.f ? 0x80008000u : 0u;
-            cs = cs == 0.f ? 1.17549435e-38f : fabsf(cs);
-            // ---- this row of q into shared memory; the products of the segment before have read theirs
-            const int r = (half ? 0 : s.rb * 256 + c * 128) + (have ? row : 0);
-            const int b = s.g * p.each + r / p.G;
-            {
-                const uint4* from = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(p.q) + ((static_cast<long long>(b) * p.Hkv + s.h) * p.G + r % p.G) * D);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    uint4 x = have ? from[i] : make_uint4(0, 0, 0, 0);
-                    x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-                    *reinterpret_cast<uint4*>(base + c * C::kTileBytes + (i >> 3) * kBoxBytes + sw128_offset(row, i & 7)) = x;
+        // The first time round is dry: a segment of one tile and no row, on whatever TMEM holds, for nothing but its
+        // instructions, before the wait for what precedes this launch. Their first use takes about 10000 cycles, which
+        // otherwise come when the first scores are there.
+        for (bool dry = true;; dry = false) {
+            int first = 0, end = 1, rows = 0, b = 0;
+            long long out = 0;
+            bool have = false, idle = false;
+            float cs = 1.f;
+            uint32_t flip = 0;
+            if (!dry) {
+                if (!more || !ok) break;
+                first = half ? s.t0 + c : s.t0;
+                end = s.t1;
+                rows = rows_of(c);
+                const long long unit = (static_cast<long long>(s.g) * p.Hkv + s.h) * p.row_blocks + s.rb;
+                const long long slot = prefix_slot(p, unit, worker, s.t0 == 0, s.t1 == s.T);
+                out = half ? (slot * 2 + c) * p.slot_rows : slot * p.slot_rows + c * 128;  // first row
+                have = row < rows;
+                idle = (warp & 3) * 32 >= rows;  // none of this warp's rows
+                if (rows == 0 || first >= end) {  // nothing for this chain
+                    if (have) p.shared_ml[out + row] = make_float2(-INFINITY, 0.f);
+                    cnt += 2 * static_cast<uint32_t>(end - s.t0);
+                    more = prefix_next(p, s);
+                    continue;
+                }
+                // the warp's rows of q into shared memory (the products of the segment before have read theirs), ahead of
+                // what the loading warps ask for: behind it they took 12000 cycles
+                constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes that copy one row
+                const int r = (half ? 0 : s.rb * 256 + c * 128) + (have ? row : 0);
+                b = s.g * p.each + r / p.G;
+                const long long mine = ((static_cast<long long>(b) * p.Hkv + s.h) * p.G + r % p.G) * D;
+                const unsigned rows_here = __ballot_sync(0xffffffffu, have);
+                const uint64_t policy = ptx::policy_evict_normal();
+                const int chunk = lane % kLanes;
+#pragma unroll 4
+                for (int i = 0; i < kLanes; ++i) {
+                    const int which = i * kRows + lane / kLanes;
+                    const long long src = __shfl_sync(0xffffffffu, mine, which);
+                    ptx::cp_async16(sbase + c * C::kTileBytes + (chunk >> 3) * kBoxBytes +
+                                        sw128_offset((warp & 3) * 32 + which, chunk & 7),
+                                    static_cast<const uint16_t*>(p.q) + src + chunk * 8, rows_here >> which & 1 ? 16u : 0u,
+                                    policy);
+                }
+                ptx::cp_async_commit();
+                // the factor from q·k to base-2 scores, made positive: a negative one's sign goes to q (0: all scores next to 0)
+                cs = p.scale_log2 * (p.k_scale ? p.k_scale[s.h] : 1.f);
+                flip = cs < 0.f ? 0x80008000u : 0u;
+                cs = cs == 0.f ? 1.17549435e-38f : fabsf(cs);
+                ptx::cp_async_wait<0>();
+                __syncwarp();
+                if (flip != 0) {
+#pragma unroll 1
+                    for (int i = 0; i < D / 8; ++i) {
+                        uint4* at = reinterpret_cast<uint4*>(base + c * C::kTileBytes + (i >> 3) * kBoxBytes +
+                                                             sw128_offset(row, i & 7));
+                        *at = make_uint4(at->x ^ flip, at->y ^ flip, at->z ^ flip, at->w ^ flip);
+                    }
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
@@ -402,35 +504,55 @@ __global__ void __launch_bounds__(448, 1) fa_prefix_kernel(const SharedParams p)
             }
             const bool sees = have && shared_start(p, b, decode_len(p, b)) > 0;
             float m_ref = -INFINITY, l = 0.f;
-            for (int t = first; t < s.t1; t += step) {
+            if (idle) {  // (whatever is in its rows of P, their O is not looked at)
+                for (int t = first; t < end && ok; t += step, ++done) {
+                    ok = wait(s_full(c), done, kStatusTimeoutMma);
+                    ptx::tc_fence_before_sync();
+                    if (ok && lane == 0) ptx::mbar_arrive(p_full(c));
+                }
+            }
+            for (int t = first; !idle && t < end; t += step) {
                 const uint32_t v_cnt = cnt + 2u * static_cast<uint32_t>(t - s.t0) + 1u;
-                ok = wait(s_full(c), done, kStatusTimeoutMma) && wait(full(v_cnt), v_cnt / C::kStages, kStatusTimeoutLoad);
-                if (!ok) break;
+                if (!dry) {
+                    ok = wait(s_full(c), done, kStatusTimeoutMma) && wait(full(v_cnt), v_cnt / C::kStages, kStatusTimeoutLoad);
+                    if (!ok) break;
+                }
                 ptx::tc_fence_after_sync();
-                const uint4 words = *reinterpret_cast<const uint4*>(base + C::kOffSeen + v_cnt % C::kStages * 16);
+                const uint4 words = *reinterpret_cast<const uint4*>(base + C::kOffSeen + (v_cnt / 2 & 7) * 16);
                 const unsigned seen[4] = {words.x, words.y, words.z, words.w};
                 const bool ragged = (words.x & words.y & words.z & words.w) != 0xffffffffu;  // (the same for all)
-                auto load = [&](int k, float(&f)[32]) {
-                    uint32_t x[32];
-                    ptx::tmem_ld_32x32b_x32(tS + k * 32, x);
-                    ptx::tmem_wait_ld(x);
+                float x[kBlockN];  // the row: all loads in flight at once
+                {
+                    uint32_t r0[32], r1[32], r2[32], r3[32];
+                    ptx::tmem_ld_32x32b_x32(tS, r0);
+                    ptx::tmem_ld_32x32b_x32(tS + 32, r1);
+                    ptx::tmem_ld_32x32b_x32(tS + 64, r2);
+                    ptx::tmem_ld_32x32b_x32(tS + 96, r3);
+                    ptx::tmem_wait_ld(r0);
+                    ptx::reg_fence(r1);
+                    ptx::reg_fence(r2);
+                    ptx::reg_fence(r3);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(x[i]);
-                    if (ragged) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!(seen[k] >> i & 1)) f[i] = -INFINITY;
+                    for (int i = 0; i < 32; ++i) {
+                        x[i] = __uint_as_float(r0[i]);
+                        x[32 + i] = __uint_as_float(r1[i]);
+                        x[64 + i] = __uint_as_float(r2[i]);
+                        x[96 + i] = __uint_as_float(r3[i]);
                     }
-                };
-                float top = -INFINITY;
+                }
+                if (ragged) {
+#pragma unroll
+                    for (int i = 0; i < kBlockN; ++i)
+                        if (!(seen[i >> 5] >> (i & 31) & 1)) x[i] = -INFINITY;
+                }
+                float tops[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float f[32];
-                    load(k, f);
+                    tops[k] = fmaxf(x[2 * k], x[2 * k + 1]);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) top = ptx::fmax3(top, f[i], f[i + 1]);
+                    for (int i = 8 + 2 * k; i < kBlockN; i += 8) tops[k] = ptx::fmax3(tops[k], x[i], x[i + 1]);
                 }
-                top = sees ? top * cs : -INFINITY;
+                const float top = sees ? fmaxf(ptx::fmax3(tops[0], tops[1], tops[2]), tops[3]) * cs : -INFINITY;
                 const bool move = top > m_ref + kLazy;
                 if (__any_sync(0xffffffffu, move)) {
                     float alpha = 1.f;
@@ -442,70 +564,93 @@ __global__ void __launch_bounds__(448, 1) fa_prefix_kernel(const SharedParams p)
                     if (t > first) {  // (the product before has been added: S was made after it)
 #pragma unroll 1
                         for (int i = 0; i < D / 8; ++i) {
-                            uint32_t x[8];
-                            ptx::tmem_ld_32x32b_x8(tO + i * 8, x);
-                            ptx::tmem_wait_ld(x);
+                            uint32_t y[8];
+                            ptx::tmem_ld_32x32b_x8(tO + i * 8, y);
+                            ptx::tmem_wait_ld(y);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-                            ptx::tmem_st_32x32b_x8(tO + i * 8, x);
+                            for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+                            ptx::tmem_st_32x32b_x8(tO + i * 8, y);
                         }
                     }
                 }
-                const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                const float2 cc = make_float2(cs, cs), mm = make_float2(-m_use, -m_use);
-                float2 sum = make_float2(0.f, 0.f);
+                // (rows that see nothing of the prefix: every weight is 2^-inf = 0)
+                const float minus = !sees ? -INFINITY : m_ref == -INFINITY ? 0.f : -m_ref;
+                const float2 cc = make_float2(cs, cs), mm = make_float2(minus, minus);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float f[32];
-                    load(k, f);
-                    uint32_t x[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 e = ptx::ffma2(make_float2(f[i], f[i + 1]), cc, mm);
-                        const float2 w = sees ? make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y)) : make_float2(0.f, 0.f);
-                        sum = ptx::fadd2(sum, w);
-                        x[i / 2] = ptx::pack_bf16x2(w.x, w.y);
-                    }
-                    ptx::tmem_st_32x32b_x16(tS + k * 16, x);  // over columns of S that have been read
+                for (int i = 0; i < kBlockN; i += 2) {
+                    const float2 e = ptx::ffma2(make_float2(x[i], x[i + 1]), cc, mm);
+                    x[i] = ptx::ex2_approx(e.x);
+                    x[i + 1] = ptx::ex2_approx(e.y);
                 }
+                float2 sums[4] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float2 w = make_float2(x[h * 64 + 2 * i], x[h * 64 + 2 * i + 1]);
+                        sums[i & 3] = ptx::fadd2(sums[i & 3], w);
+                        r[i] = ptx::pack_bf16x2(w.x, w.y);
+                    }
+                    ptx::tmem_st_32x32b_x32(tS + h * 32, r);  // over the scores
+                }
+                const float2 sum = ptx::fadd2(ptx::fadd2(sums[0], sums[1]), ptx::fadd2(sums[2], sums[3]));
                 l += sum.x + sum.y;
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before_sync();
                 __syncwarp();
+                if (dry) break;
                 if (lane == 0) ptx::mbar_arrive(p_full(c));
                 ++done;
+                if (warp == 0 && lane == 0) *chain0 = done;
             }
-            if (ok) ok = wait(pv_done(c), done - 1, kStatusTimeoutMma);
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            if (have) p.shared_ml[out + row] = make_float2(l == 0.f ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref, l);
+            if (!dry) {
+                if (ok) ok = wait(pv_done(c), done - 1, kStatusTimeoutMma);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                // (a sum of zero: no key; NaN is no zero and is passed on)
+                if (have) p.shared_ml[out + row] = make_float2(l == 0.f ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref, l);
+            }
             // O as in warp-level accumulators, so that four lanes write 32 bytes side by side
             const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
+            for (int hh = idle ? 2 : 0; hh < 2; ++hh) {
                 const int r0 = (warp & 3) * 32 + hh * 16 + g;
+                float* to = p.shared_o + (out + r0) * D + 2 * t4;
+#pragma unroll 1
+                for (int col = 0; col < D; col += 32, to += 32) {
+                    uint32_t y[16];
+                    ptx::tmem_ld_16x256b_x4(tO + (static_cast<uint32_t>(hh * 16) << 16) + col, y);
+                    ptx::tmem_wait_ld(y);
 #pragma unroll
-                for (int col = 0; col < D; col += 32) {
-                    uint32_t x[16];
-                    ptx::tmem_ld_16x256b_x4(tO + (static_cast<uint32_t>(hh * 16) << 16) + col, x);
-                    ptx::tmem_wait_ld(x);
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (r0 + 8 * e < rows)
-                                *reinterpret_cast<float2*>(p.shared_o + (out + r0 + 8 * e) * D + col + 8 * n + 2 * t4) =
-                                    make_float2(__uint_as_float(x[4 * n + 2 * e]), __uint_as_float(x[4 * n + 2 * e + 1]));
+                    for (int n = 0; n < 4; ++n) {
+                        if (r0 < rows)
+                            *reinterpret_cast<float2*>(to + 8 * n) =
+                                make_float2(__uint_as_float(y[4 * n]), __uint_as_float(y[4 * n + 1]));
+                        if (r0 + 8 < rows)
+                            *reinterpret_cast<float2*>(to + 8 * D + 8 * n) =
+                                make_float2(__uint_as_float(y[4 * n + 2]), __uint_as_float(y[4 * n + 3]));
+                    }
                 }
             }
             ptx::tc_fence_before_sync();
+            if (dry) {
+                ptx::griddep_wait();
+                // From here on what precedes this launch is done and visible: so it is to the kernel behind it, which
+                // reads its own keys at once and waits for this one only for the partial results.
+                if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+                more = take_first();
+            } else {
+                cnt += 2 * static_cast<uint32_t>(end - s.t0);
+                more = prefix_next(p, s);
+            }
         }
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
     if (warp == 12) {
         ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc(*tmem_slot, 512);
     }
 }
 
@@ -542,7 +687,7 @@ template <int D>
 __device__ __forceinline__ void shared_add(const SharedParams& p, const SharedAt& a, int i, int c4, float& m, float& l,
                                            float4& o) {
     if (!a.any) return;
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 8;
     const int r = a.row + i, rb = r >> 8, in = p.chains == 2 ? r : r & 255;
     const long long begin = a.first + static_cast<long long>(rb) * a.T;
     const int c0 = decode_worker_of(a.total, a.workers, begin), c1 = decode_worker_of(a.total, a.workers, begin + a.T - 1);
