@@ -112,7 +112,7 @@ def load_library(path: str | None = None):
     lib.fa_bwd_varlen.restype = i
     lib.fa_decode_shared.argtypes = [vp] * 7 + [i, i, i, i, ll, f, vp, ctypes.c_size_t, vp]
     lib.fa_decode_shared.restype = i
-    lib.fa_decode_shared_workspace.argtypes = [i] * 6
+    lib.fa_decode_shared_workspace.argtypes = [i] * 9
     lib.fa_decode_shared_workspace.restype = ll
     lib.fa_bwd_workspace.argtypes = [ll, i]
     lib.fa_bwd_workspace.restype = ll
@@ -224,10 +224,11 @@ def fa_decode_shared(q: int, cache: FaPagedCache, block_table: int, seq_lens: in
                                            workspace_bytes, stream or None)
 
 
-def fa_decode_shared_workspace(B: int, Hq: int, Hkv: int, d: int, groups: int, sm_count: int) -> int:
+def fa_decode_shared_workspace(B: int, Hq: int, Hkv: int, d: int, cache_type: int, page_size: int, table_width: int,
+                               groups: int, sm_count: int) -> int:
     """The C ``fa_decode_shared_workspace`` (host only): workspace bytes of
     ``fa_decode_shared`` for these sizes, or a negative status."""
-    return load_library().fa_decode_shared_workspace(B, Hq, Hkv, d, groups, sm_count)
+    return load_library().fa_decode_shared_workspace(B, Hq, Hkv, d, cache_type, page_size, table_width, groups, sm_count)
 
 
 def fa_bwd(dout: int, q: int, k: int, v: int, o: int, lse: int, dlse: int | None, dq: int, dk: int, dv: int, B: int,

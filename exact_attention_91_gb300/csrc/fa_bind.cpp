@@ -220,7 +220,8 @@ PyObject* decode_any(PyObject* const* a, PyObject* prefix_lens) {
             const int probed = fa::host_probe(&dev, &sms);
             if (probed != FA_OK) return probed;
             const long long room =
-                prefix_lens ? fa_decode_shared_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, to_int(groups), sms)
+                prefix_lens ? fa_decode_shared_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, cache.type,
+                                                         cache.page_size, to_int(width), to_int(groups), sms)
                             : fa_decode_paged_workspace(to_int(B), to_int(Hq), cache.heads, cache.d, cache.type,
                                                         cache.page_size, to_int(width), sms);
             if (room < 0) return room;

@@ -154,6 +154,7 @@ constexpr int kDecodeCluster = 8;
 // more counted tiles of the run.
 struct DecodeSeg {
     int b, u, t0, t1, nt, len;
+    int page0;  // the table's entry of key 0 (behind a shared prefix; else 0)
     long long rem;
 };
 
@@ -161,6 +162,12 @@ __device__ __forceinline__ int decode_len(const DecodeParams& p, int b) {
     const long long cap = static_cast<long long>(p.width) << p.page_shift;
     const int n = max(p.lens[b], 0);
     return n > cap ? static_cast<int>(cap) : n;
+}
+
+// The request's own keys and the page that they begin at. (Behind a shared prefix: another overload.)
+__device__ __forceinline__ int decode_own(const DecodeParams& p, int b, int& page0) {
+    page0 = 0;
+    return decode_len(p, b);
 }
 
 template <int KEYS>
@@ -179,14 +186,14 @@ __device__ __forceinline__ void decode_take(DecodeSeg& s, int x, int cost) {
 }
 
 // On to the next unit with a tile in the run; false at the run's end.
-template <int KEYS>
-__device__ __forceinline__ bool decode_next(DecodeSeg& s, const DecodeParams& p, const DecodeWay& way) {
+template <int KEYS, class Params>
+__device__ __forceinline__ bool decode_next(DecodeSeg& s, const Params& p, const DecodeWay& way) {
     do {
         if (s.rem <= 0) return false;
         if (++s.u >= way.units) {
             s.u = 0;
             if (++s.b >= p.B) return false;  // (only if the lengths changed under the launch)
-            s.len = decode_len(p, s.b);
+            s.len = decode_own(p, s.b, s.page0);
             s.nt = decode_tiles<KEYS>(s.len);
         }
         decode_take(s, 0, way.cost);
@@ -270,10 +277,10 @@ __device__ __forceinline__ uint32_t decode_load(const DecodeParams& p, const Dec
 // The page of this lane's 16-key group of tile t (lanes 0 .. kGroups-1; -1
 // past the end of the keys: never read).
 template <int D, bool E4M3, bool WIDE>
-__device__ __forceinline__ int decode_page(const DecodeParams& p, const DecodeSeg& s, int t, int lane, int page0 = 0) {
+__device__ __forceinline__ int decode_page(const DecodeParams& p, const DecodeSeg& s, int t, int lane) {
     using C = DecodeCfg<D, E4M3, WIDE>;
     const int key = t * C::kKeys + (lane % C::kGroups) * 16;
-    return key < s.len ? p.table[s.b * p.table_stride + page0 + (key >> p.page_shift)] : -1;
+    return key < s.len ? p.table[s.b * p.table_stride + s.page0 + (key >> p.page_shift)] : -1;
 }
 
 // The largest bf16 below each of w (zero for zero); returns what is left: exact,
@@ -287,9 +294,10 @@ __device__ __forceinline__ float2 cut_bf16x2(float2 w, uint32_t& half) {
 // CLUSTER: the small form. Block r of a cluster of p.cluster takes the r-th
 // share of one unit's tiles; the blocks' results are added up through
 // distributed shared memory.
-// SHARED (small form): the keys behind a prefix that the requests of a group share, and its partial results, which the
-// kernel before leaves. That one lets this one start once all before both is done (see fa_prefix_kernel): a request's own
-// keys are read at once, and only what it left is waited for.
+// SHARED: the keys behind a prefix that the requests of a group share. The small form comes behind the kernel of the shared
+// part, whose partial results it adds: that one lets this one start once all before both is done (see fa_prefix_kernel),
+// so a request's own keys are read at once, and only what it left is waited for. The other form comes before it and
+// leaves all its results as partial ones, those of a unit that one worker holds whole in a place of their own.
 struct SharedParams;
 struct SharedAt;
 template <int D>
@@ -298,7 +306,6 @@ __device__ __forceinline__ void shared_add(const SharedParams& p, const SharedAt
 template <int D, bool E4M3, bool WIDE, bool CLUSTER, bool SHARED = false>
 __global__ void __launch_bounds__(128, 2)
     fa_decode_kernel(const std::conditional_t<SHARED, SharedParams, DecodeParams> p) {
-    static_assert(CLUSTER || !SHARED);
     using C = DecodeCfg<D, E4M3, WIDE>;
     constexpr int NT = C::kKeys / 8;  // score columns, 8 keys each
     constexpr int ND = D / 8;         // output columns, 8 values each
@@ -315,20 +322,15 @@ __global__ void __launch_bounds__(128, 2)
     bool first_seg = true;
     uint64_t policy = ptx::policy_evict_normal();
     const int worker = blockIdx.x;
+    if constexpr (SHARED && !CLUSTER) ptx::griddep_wait();  // (what follows this kernel reads what it has waited for)
     ptx::griddep_launch_dependents();
     if constexpr (!SHARED) ptx::griddep_wait();
-    int page0 = 0;
     if constexpr (CLUSTER) {
         const int unit = worker / p.cluster, rank = worker - unit * p.cluster;
         if (p.once) policy = ptx::policy_evict_first();
         seg.b = unit / HH;
         seg.u = unit - seg.b * HH;
-        seg.len = decode_len(p, seg.b);
-        if constexpr (SHARED) {
-            const int start = shared_start(p, seg.b, seg.len);
-            seg.len -= start;
-            page0 = start >> p.page_shift;
-        }
+        seg.len = decode_own(p, seg.b, seg.page0);
         seg.nt = decode_tiles<C::kKeys>(seg.len);
         seg.t0 = seg.nt * rank / p.cluster;
         seg.t1 = seg.nt * (rank + 1) / p.cluster;
@@ -338,7 +340,8 @@ __global__ void __launch_bounds__(128, 2)
         const int per = (p.B + C::kThreads - 1) / C::kThreads;
         const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
         long long mine = 0;  // tiles of one key head of requests [b_lo, b_hi)
-        for (int b = b_lo; b < b_hi; ++b) mine += decode_tiles<C::kKeys>(decode_len(p, b));
+        int page0;
+        for (int b = b_lo; b < b_hi; ++b) mine += decode_tiles<C::kKeys>(decode_own(p, b, page0));
         long long incl = mine;
 #pragma unroll
         for (int i = 1; i < 32; i <<= 1) {
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(128, 2)
         const long long total = (tiles + static_cast<long long>(p.B) * way.cost) * way.units;
         const int workers = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kMinRun - 1) / kMinRun));
         if (worker >= workers) {
-            if (tid == 0) p.meta[worker] = make_int4(-1, 0, 0, 0);
+            if (!SHARED && tid == 0) p.meta[worker] = make_int4(-1, 0, 0, 0);
             return;
         }
         const long long begin = decode_start(total, workers, worker), end = decode_start(total, workers, worker + 1);
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(128, 2)
             if (begin >= at && begin < at + (mine + static_cast<long long>(b_hi - b_lo) * way.cost) * way.units) {
                 int b = b_lo, len = 0;
                 for (;; ++b) {
-                    len = decode_len(p, b);
+                    len = decode_own(p, b, page0);
                     const long long n = static_cast<long long>(decode_tiles<C::kKeys>(len) + way.cost) * way.units;
                     if (begin < at + n || b + 1 >= b_hi) break;
                     at += n;
@@ -385,6 +388,8 @@ __global__ void __launch_bounds__(128, 2)
         __syncthreads();
         seg.b = sh_b;
         seg.len = sh_len;
+        if constexpr (SHARED) seg.len = decode_own(p, seg.b, seg.page0);
+        else seg.page0 = 0;
         seg.nt = decode_tiles<C::kKeys>(seg.len);
         const unsigned long long in = static_cast<unsigned long long>(begin - sh_begin);
         const unsigned unit = static_cast<unsigned>(seg.nt + way.cost);
@@ -393,7 +398,7 @@ __global__ void __launch_bounds__(128, 2)
         const int x = static_cast<int>(in - static_cast<unsigned long long>(seg.u) * unit);
         seg.rem = end - begin;
         decode_take(seg, x, way.cost);
-        if (tid == C::kThreads - 1) {
+        if (!SHARED && tid == C::kThreads - 1) {
             // For the join of a cut unit: request, unit, the slot of its first part, its last worker. (Its tile 0
             // is in the first worker's run, and is the first part of that run if the run begins in the unit.)
             int4 m = make_int4(-1, 0, 0, 0);
@@ -428,9 +433,9 @@ __global__ void __launch_bounds__(128, 2)
     };
     seek();
     // (the first two tiles' pages are looked up together, later ones a tile ahead)
-    int entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane, page0) : -1;
+    int entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
     const bool two = more && at + way.step < ahead.t1;
-    const int second = two ? decode_page<D, E4M3, WIDE>(p, ahead, at + way.step, lane, page0) : -1;
+    const int second = two ? decode_page<D, E4M3, WIDE>(p, ahead, at + way.step, lane) : -1;
     uint32_t slot_in = 0, slot_out = 0, ok_bits = 0;
     auto load = [&](bool first) {
         if (more) {
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(128, 2)
                 entry = second;
             } else {
                 seek();
-                entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane, page0) : -1;
+                entry = more ? decode_page<D, E4M3, WIDE>(p, ahead, at, lane) : -1;
             }
         }
         slot_in = slot_in + 1 == C::kStages ? 0 : slot_in + 1;
@@ -758,6 +763,25 @@ __global__ void __launch_bounds__(128, 2)
         const bool whole = CLUSTER ? p.cluster == 1 : seg.t0 == 0 && seg.t1 == seg.nt;
         const long long slot = 2LL * worker + (first_seg ? 0 : 1);
         const float vs = p.v_scale ? p.v_scale[h] : 1.f;
+        if constexpr (SHARED && !CLUSTER) {  // where the unit's results are: its first slot (-1: whole) and last worker
+            if (way.heads > 1 ? lane == 0 : tid == 0) {
+                int2* info = p.own_info + static_cast<long long>(seg.b) * HH + hh;
+                if (seg.t0 == 0) info->x = whole ? -1 : static_cast<int>(slot);
+                if (seg.t1 == seg.nt) info->y = worker * 8 + way.heads;
+            }
+        }
+        // (SHARED: all results are partial ones, a whole unit's by rows)
+        const bool final_ = whole && !(SHARED && !CLUSTER);
+        auto part_at = [&](long long part, long long out, float*& o, float2*& at_ml) {
+            o = p.part_o, at_ml = p.part_ml;
+            if constexpr (SHARED && !CLUSTER) {
+                if (whole) {
+                    o = p.own_o, at_ml = p.own_ml;
+                    return out;
+                }
+            }
+            return part;
+        };
 
         if (!CLUSTER && way.heads > 1) {
             // ---- one head per warp: the output, or the partial result, straight from the fragments
@@ -765,11 +789,14 @@ __global__ void __launch_bounds__(128, 2)
             for (int r = 0; r < R; ++r) {
                 const int row = g + 8 * r;
                 if (row >= rows) continue;
-                const float f = whole ? (ml[r].y == 0.f ? 0.f : vs / ml[r].y) : 1.f;
-                const long long out = row0 + row, part = (slot * 4 + warp) * C::kRows + row;
+                const float f = final_ ? (ml[r].y == 0.f ? 0.f : vs / ml[r].y) : 1.f;
+                const long long out = row0 + row;
+                float* part_o;
+                float2* part_ml;
+                const long long part = part_at((slot * 4 + warp) * C::kRows + row, out, part_o, part_ml);
                 if (t4 == 0) {
-                    if (!whole)
-                        p.part_ml[part] = ml[r];
+                    if (!final_)
+                        part_ml[part] = ml[r];
                     else if (p.lse)
                         p.lse[out] = ml[r].y == 0.f ? -INFINITY : (ml[r].x + log2f(ml[r].y)) * 0.69314718055994531f;
                 }
@@ -782,21 +809,21 @@ __global__ void __launch_bounds__(128, 2)
                             const int c4 = ((2 * t4 + j) * ND + n) / 4;
                             const float x[4] = {of(acc[n][r], j) * f, of(acc[n + 1][r], j) * f,
                                                 of(acc[n + 2][r], j) * f, of(acc[n + 3][r], j) * f};
-                            if (whole)
+                            if (final_)
                                 reinterpret_cast<uint2*>(p.o)[out * (D / 4) + c4] =
                                     make_uint2(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]));
                             else
-                                reinterpret_cast<float4*>(p.part_o)[part * (D / 4) + c4] =
+                                reinterpret_cast<float4*>(part_o)[part * (D / 4) + c4] =
                                     make_float4(x[0], x[1], x[2], x[3]);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const int nn = n + 2 * j + i, c2 = nn * 4 + t4;
                                 const float x0 = acc[nn][r].x * f, x1 = acc[nn][r].y * f;
-                                if (whole)
+                                if (final_)
                                     reinterpret_cast<uint32_t*>(p.o)[out * (D / 2) + c2] = ptx::pack_bf16x2(x0, x1);
                                 else
-                                    reinterpret_cast<float2*>(p.part_o)[part * (D / 2) + c2] = make_float2(x0, x1);
+                                    reinterpret_cast<float2*>(part_o)[part * (D / 2) + c2] = make_float2(x0, x1);
                             }
                         }
                     }
@@ -807,7 +834,7 @@ __global__ void __launch_bounds__(128, 2)
         }
 
         auto prefix = [&]() {
-            if constexpr (SHARED) {
+            if constexpr (SHARED && CLUSTER) {
                 const auto at = shared_at(p, seg.b, h);
                 ptx::griddep_wait();
                 return at;
@@ -860,8 +887,8 @@ __global__ void __launch_bounds__(128, 2)
                     l += each[w].y * f;
                     o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
                 }
-                if (whole) {
-                    if constexpr (SHARED) shared_add<D>(p, prefix, rg * C::kRows + row + 8 * r, c4, mm, l, o);
+                if (final_) {
+                    if constexpr (SHARED && CLUSTER) shared_add<D>(p, prefix, rg * C::kRows + row + 8 * r, c4, mm, l, o);
                     const float inv = l == 0.f ? 0.f : vs / l;
                     const long long out = row0 + row + 8 * r;
                     reinterpret_cast<uint2*>(p.o)[out * (D / 4) + c4] =
@@ -872,8 +899,11 @@ __global__ void __launch_bounds__(128, 2)
                     reinterpret_cast<float4*>(smem)[(row + 8 * r) * (D / 4) + c4] = o;
                     if (c4 == 0) stat[C::kWarps * 16 + row + 8 * r] = make_float2(mm, l);
                 } else {
-                    reinterpret_cast<float4*>(p.part_o)[(slot * C::kRows + row + 8 * r) * (D / 4) + c4] = o;
-                    if (c4 == 0) p.part_ml[slot * C::kRows + row + 8 * r] = make_float2(mm, l);
+                    float* part_o;
+                    float2* part_ml;
+                    const long long part = part_at(slot * C::kRows + row + 8 * r, row0 + row + 8 * r, part_o, part_ml);
+                    reinterpret_cast<float4*>(part_o)[part * (D / 4) + c4] = o;
+                    if (c4 == 0) part_ml[part] = make_float2(mm, l);
                 }
             }
         }

@@ -37,6 +37,11 @@ struct SharedParams : DecodeParams {
     float* shared_o;         // [units + 2 * workers][chains][slot_rows][D]
     float2* shared_ml;       // [units + 2 * workers][chains][slot_rows]
     unsigned long long wait_limit_ns;
+    // Many requests: their own keys come first, cut into equal runs, and a third kernel adds all up.
+    int own_first, own_workers;
+    float* own_o;            // [B, Hq, D]: partial results of units that one worker holds whole
+    float2* own_ml;          // [B, Hq]
+    int2* own_info;          // [B][Hkv * row_groups]: first slot (-1: whole), last worker * 8 + heads of a unit
 };
 
 // Shared tokens of group g: whole pages.
@@ -70,6 +75,13 @@ __device__ __forceinline__ int prefix_blocks(const SharedParams& p, long long to
 __device__ __forceinline__ int shared_start(const SharedParams& p, int b, int len) {
     const int n = prefix_tokens(p, b / p.each);
     return len >= n ? n : 0;
+}
+
+// A request's own keys, those behind it.
+__device__ __forceinline__ int decode_own(const SharedParams& p, int b, int& page0) {
+    const int len = decode_len(p, b), start = shared_start(p, b, len);
+    page0 = start >> p.page_shift;
+    return len - start;
 }
 
 // The part [t0, t1) of a unit's T key tiles that a block holds, `rem` tiles of its run behind it.
@@ -238,7 +250,7 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
     if (warp >= 8 && warp < 12) {
         // ---- loads: each warp 32 rows of every tile
         ptx::regs_dec<C::kRegsOther>();
-        ptx::griddep_wait();
+        if (!p.own_first) ptx::griddep_wait();
         more = prefix_first(p, worker, s);
         if (warp == 8 && lane == 0) {  // for the other roles
             *first_seg = s;
@@ -365,7 +377,7 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
         ptx::regs_dec<C::kRegsOther>();
         const int c = warp - 12;
         const uint32_t tmem = *tmem_slot;
-        ptx::griddep_wait();
+        if (!p.own_first) ptx::griddep_wait();
         more = take_first();
         if (c >= 2) more = false;
         constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, kBlockN, false, false);
@@ -635,9 +647,10 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
             }
             ptx::tc_fence_before_sync();
             if (dry) {
-                ptx::griddep_wait();
                 // From here on what precedes this launch is done and visible: so it is to the kernel behind it, which
-                // reads its own keys at once and waits for this one only for the partial results.
+                // reads its own keys at once and waits for this one only for the partial results. (Behind the requests' own
+                // keys: what precedes those is, since their blocks have all waited for it, and they are not looked at.)
+                if (!p.own_first) ptx::griddep_wait();
                 if (threadIdx.x == 0) ptx::griddep_launch_dependents();
                 more = take_first();
             } else {
@@ -646,6 +659,7 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
             }
         }
     }
+    if (p.own_first) ptx::griddep_wait();  // (so that this kernel's end means that the one before has ended)
     ptx::tc_fence_before_sync();
     __syncthreads();
     if (warp == 12) {
@@ -682,39 +696,119 @@ __device__ __forceinline__ SharedAt shared_at(const SharedParams& p, int b, int 
     return a;
 }
 
-// Adds them to the row of query head i of the key head: the sums l and O (values 4 c4 ..) relative to 2^m.
+// Adds a partial result (its sums relative to 2^ml.x) to a row's: l and o, relative to 2^m.
+__device__ __forceinline__ void shared_join(float& m, float& l, float4& o, float2 ml, float4 x) {
+    if (ml.x == -INFINITY) return;  // (no key)
+    const float mm = fmaxf(m, ml.x);
+    const float fa_ = m == -INFINITY ? 0.f : ptx::ex2_approx(m - mm), fb = ptx::ex2_approx(ml.x - mm);
+    l = l * fa_ + ml.y * fb;
+    o.x = o.x * fa_ + x.x * fb, o.y = o.y * fa_ + x.y * fb;
+    o.z = o.z * fa_ + x.z * fb, o.w = o.w * fa_ + x.w * fb;
+    m = mm;
+}
+
+// The partial results of the prefix for the row of query head i of the key head, kBatch of them in flight.
 template <int D>
-__device__ __forceinline__ void shared_add(const SharedParams& p, const SharedAt& a, int i, int c4, float& m, float& l,
-                                           float4& o) {
-    if (!a.any) return;
-    constexpr int kBatch = 8;
-    const int r = a.row + i, rb = r >> 8, in = p.chains == 2 ? r : r & 255;
-    const long long begin = a.first + static_cast<long long>(rb) * a.T;
-    const int c0 = decode_worker_of(a.total, a.workers, begin), c1 = decode_worker_of(a.total, a.workers, begin + a.T - 1);
-    const long long unit = (static_cast<long long>(a.g) * p.Hkv + a.h) * p.row_blocks + rb;
-    const int n = (c1 - c0 + 1) * p.chains;
-    for (int k0 = 0; k0 < n; k0 += kBatch) {
-        float2 ml[kBatch];
-        float4 x[kBatch];
+struct SharedRow {
+    static constexpr int kBatch = 8;
+    const SharedParams& p;
+    long long unit;
+    int c0, c1, n, in;
+
+    __device__ __forceinline__ SharedRow(const SharedParams& params, const SharedAt& a, int i) : p(params) {
+        const int r = a.row + i, rb = r >> 8;
+        in = p.chains == 2 ? r : r & 255;
+        const long long begin = a.first + static_cast<long long>(rb) * a.T;
+        // (the bounds have no effect unless lengths change under the launch)
+        const int top = max(a.workers - 1, 0);
+        c0 = min(max(decode_worker_of(a.total, a.workers, begin), 0), top);
+        c1 = min(max(decode_worker_of(a.total, a.workers, begin + a.T - 1), c0), top);
+        unit = (static_cast<long long>(a.g) * p.Hkv + a.h) * p.row_blocks + rb;
+        n = a.any ? (c1 - c0 + 1) * p.chains : 0;
+    }
+    __device__ __forceinline__ void load(int k0, int c4, float2 (&ml)[kBatch], float4 (&x)[kBatch]) const {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int kk = min(k0 + k, n - 1), w = c0 + kk / p.chains;
+            const int kk = min(k0 + k, n - 1), two = p.chains - 1, w = c0 + (kk >> two);
             const long long slot = prefix_slot(p, unit, w, w == c0, w == c1);
-            const long long at = (slot * p.chains + kk % p.chains) * p.slot_rows + in;
+            const long long at = ((slot << two) + (kk & two)) * p.slot_rows + in;
             ml[k] = p.shared_ml[at];
             x[k] = reinterpret_cast<const float4*>(p.shared_o)[at * (D / 4) + c4];
         }
+    }
+    __device__ __forceinline__ void add(int k0, const float2 (&ml)[kBatch], const float4 (&x)[kBatch], float& m, float& l,
+                                        float4& o) const {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            if (k0 + k >= n || ml[k].x == -INFINITY) continue;
-            const float mm = fmaxf(m, ml[k].x);
-            const float fa_ = m == -INFINITY ? 0.f : ptx::ex2_approx(m - mm), fb = ptx::ex2_approx(ml[k].x - mm);
-            l = l * fa_ + ml[k].y * fb;
-            o.x = o.x * fa_ + x[k].x * fb, o.y = o.y * fa_ + x[k].y * fb;
-            o.z = o.z * fa_ + x[k].z * fb, o.w = o.w * fa_ + x[k].w * fb;
-            m = mm;
+        for (int k = 0; k < kBatch; ++k)
+            if (k0 + k < n) shared_join(m, l, o, ml[k], x[k]);
+    }
+};
+
+// Adds all of them.
+template <int D>
+__device__ __forceinline__ void shared_add(const SharedParams& p, const SharedAt& a, int i, int c4, float& m, float& l,
+                                           float4& o) {
+    const SharedRow<D> row(p, a, i);
+    for (int k0 = 0; k0 < row.n; k0 += row.kBatch) {
+        float2 ml[row.kBatch];
+        float4 x[row.kBatch];
+        row.load(k0, c4, ml, x);
+        row.add(k0, ml, x, m, l, o);
+    }
+}
+
+// Many requests: a row's own results and those of its prefix, added up. A warp per row (d = 64: two rows), so that many
+// rows' loads are in flight: their bytes are what bounds it.
+constexpr int kSharedJoinThreads = 256;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kSharedJoinThreads) fa_shared_join_kernel(const SharedParams p) {
+    constexpr int kLanes = D / 4, kPer = kSharedJoinThreads / kLanes;
+    ptx::griddep_launch_dependents();
+    const int c4 = threadIdx.x % kLanes, hq = p.Hkv * p.G;
+    const long long out = static_cast<long long>(blockIdx.x) * kPer + threadIdx.x / kLanes;
+    const bool have = out < static_cast<long long>(p.B) * hq;
+    const int b = have ? static_cast<int>(out / hq) : 0, i = have ? static_cast<int>(out % hq) : 0;
+    const int h = i / p.G, j = i % p.G, rg = j / ROWS, hh = h * p.row_groups + rg;
+    // (lengths are inputs: what precedes the first of these launches was done before this one could start)
+    // a warp's rows may be of two requests: the group's sums are made for each
+    SharedAt at = shared_at(p, __shfl_sync(0xffffffffu, b, 0), h);
+    if constexpr (kLanes < 32) {
+        const SharedAt other = shared_at(p, __shfl_sync(0xffffffffu, b, 16), h);
+        if ((threadIdx.x & 16) != 0) at = other;
+    }
+    const SharedRow<D> row(p, at, j);
+    const float vs = p.v_scale ? p.v_scale[h] : 1.f;
+    ptx::griddep_wait();
+    if (!have) return;
+    // all that does not wait for something else at once: where the own results are, those of a whole unit, the first
+    // ones of the prefix
+    float2 ml[row.kBatch];
+    float4 x[row.kBatch];
+    const int2 info = p.own_info[static_cast<long long>(b) * p.Hkv * p.row_groups + hh];
+    const float2 own = p.own_ml[out];
+    float4 o = reinterpret_cast<const float4*>(p.own_o)[out * kLanes + c4];
+    if (row.n > 0) row.load(0, c4, ml, x);
+    float m = own.x, l = own.y;
+    if (info.x >= 0) {
+        m = -INFINITY, l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        // (the bounds have no effect unless lengths change under the launch)
+        const int slot = min(info.x, 2 * p.own_workers - 1), first = slot >> 1;
+        const int last = min(info.y >> 3, p.own_workers - 1), heads = p.fours && (info.y & 7) == 4 ? 4 : 1;
+        for (int k = 0; k <= last - first; ++k) {
+            const long long part = ((k == 0 ? slot : 2LL * (first + k)) * heads + hh % heads) * ROWS + j % ROWS;
+            shared_join(m, l, o, p.part_ml[part], reinterpret_cast<const float4*>(p.part_o)[part * kLanes + c4]);
         }
     }
+    if (m == -INFINITY) l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < row.n; k0 += row.kBatch) {
+        row.add(k0, ml, x, m, l, o);
+        if (k0 + row.kBatch < row.n) row.load(k0 + row.kBatch, c4, ml, x);
+    }
+    const float inv = l == 0.f ? 0.f : vs / l;
+    reinterpret_cast<uint2*>(p.o)[out * kLanes + c4] =
+        make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
+    if (c4 == 0 && p.lse) p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace fa

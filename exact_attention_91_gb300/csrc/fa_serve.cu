@@ -318,27 +318,55 @@ void fill_decode(fa::DecodeParams& p, const void* q, const fa_paged_cache* cache
 
 // ---------------------------------------------------------------- decode behind shared prefixes
 
-// How a launch is laid out, from what the host knows.
+// How a launch is laid out, from what the host knows. The workspace: partial results of the shared part, and, with own
+// keys in equal runs, those of the runs, of whole units, and where each unit's are.
 struct SharedPlan {
-    int each, rows, row_blocks, slot_rows, chains, workers;
-    long long units;
-    size_t ml, bytes;
+    int each, rows, row_blocks, slot_rows, chains, workers, cluster;
+    long long units, own_units, own_workers;
+    size_t o, run_ml, run_o, own_ml, own_o, info, bytes;
 };
+// A batch whose tables could hold no more keys and values than kSharedLeast bytes is read as by fa_decode_paged: what it
+// reads twice comes from L2, and a shared part costs 10 to 15 us of launches and partial results. Measured (us, shared /
+// paged; bf16, 32/8 heads, d 128): 4 x 2040 keys, 34 MB, 19.3 / 8.4; 8 x 2040, 67 MB, 17.2 / 11.7; 16 x 2040, 134 MB,
+// 17.6 / 22.0; 32 x 2040, 268 MB, 17.5 / 33.9; but 2 x 16040, 131 MB, 30.0 / 23.1; 12/12 heads, d 64: 32 x 1100,
+// 109 MB, 20.4 / 19.6; 48 x 1800, 267 MB, 25.4 / 27.5.
+constexpr long long kSharedLeast = 1LL << 27;
+bool shared_small(long long B, long long Hkv, int d, int type, long long max_keys) {
+    return B * Hkv * d * (type == FA_CACHE_E4M3 ? 2 : 4) <= (kSharedLeast - 1) / max_keys;
+}
+
 // false: past the limits of an index
 bool shared_plan(long long B, long long Hq, long long Hkv, int d, long long groups, int sms, SharedPlan* out) {
     SharedPlan& s = *out;
     s.each = static_cast<int>(B / groups);
-    const long long rows = s.each * (Hq / Hkv);
+    const long long rows = s.each * (Hq / Hkv), row_groups = (Hq / Hkv + 15) / 16;
     s.rows = static_cast<int>(rows);
     s.row_blocks = static_cast<int>((rows + 255) / 256);
     s.slot_rows = static_cast<int>(std::min<long long>(rows, 256));
     s.chains = rows <= 128 ? 2 : 1;
     s.workers = sms;
     s.units = groups * Hkv * s.row_blocks;
-    if (s.units > 0x7fffffffLL) return false;
+    s.own_units = B * Hkv * row_groups;
+    if (s.units > 0x7fffffffLL || s.own_units > 0x7fffffffLL / fa::kDecodeCluster) return false;
+    // Own keys: the small form, a cluster for each unit (as large as one wave holds: how long they are only the GPU
+    // knows), if one wave holds them; else equal runs.
+    const long long resident = static_cast<long long>(kWorkersPerSm) * sms;
+    s.cluster = s.own_units <= resident ? 1 : 0;
+    while (s.cluster > 0 && s.cluster < fa::kDecodeCluster && 2 * s.cluster * s.own_units <= resident) s.cluster *= 2;
+    s.own_workers = s.cluster > 0 ? 0 : resident;
+    const auto aligned = [](size_t n) { return (n + 15) / 16 * 16; };
     const size_t lines = static_cast<size_t>(s.units + 2LL * s.workers) * s.chains * s.slot_rows;
-    s.ml = (lines * 8 + 15) / 16 * 16;
-    s.bytes = s.ml + lines * d * 4;
+    s.o = aligned(lines * 8);
+    s.run_ml = s.o + lines * d * 4;
+    s.bytes = s.run_ml;
+    if (s.own_workers == 0) return true;
+    const size_t run = static_cast<size_t>(2 * s.own_workers) * (Hq / Hkv > 8 ? 16 : 8) * (decode_fours(Hq, Hkv) ? 4 : 1);
+    const size_t all = static_cast<size_t>(B) * Hq;
+    s.run_o = s.run_ml + aligned(run * 8);
+    s.own_ml = s.run_o + run * d * 4;
+    s.own_o = s.own_ml + aligned(all * 8);
+    s.info = s.own_o + all * d * 4;
+    s.bytes = s.info + static_cast<size_t>(s.own_units) * 8;
     return true;
 }
 
@@ -444,11 +472,12 @@ int fa_decode_paged(const void* q, const fa_paged_cache* cache, const int* block
     return d == 64 ? launch_decode_any<64>(c.e4m3, wide, p, w, s) : launch_decode_any<128>(c.e4m3, wide, p, w, s);
 }
 
-long long fa_decode_shared_workspace(int B, int Hq, int Hkv, int d, int groups, int sm_count) {
-    const int rc = check_decode_sizes(B, Hq, Hkv, d, kMinPage, 1);
-    if (rc != FA_OK) return rc;
-    if (sm_count < 1 || groups < 1 || B % groups != 0) return FA_ERR_BAD_SHAPE;
-    if (B == 0) return 0;
+long long fa_decode_shared_workspace(int B, int Hq, int Hkv, int d, int cache_type, int page_size, int table_width,
+                                     int groups, int sm_count) {
+    const long long paged = fa_decode_paged_workspace(B, Hq, Hkv, d, cache_type, page_size, table_width, sm_count);
+    if (paged < 0) return paged;
+    if (groups < 1 || B % groups != 0) return FA_ERR_BAD_SHAPE;
+    if (B == 0 || shared_small(B, Hkv, d, cache_type, static_cast<long long>(table_width) * page_size)) return paged;
     SharedPlan plan;
     if (!shared_plan(B, Hq, Hkv, d, groups, sm_count, &plan)) return FA_ERR_BAD_SHAPE;
     return static_cast<long long>(plan.bytes);
@@ -465,9 +494,10 @@ int fa_decode_shared(const void* q, const fa_paged_cache* cache, const int* bloc
     rc = check_decode(q, cache, c, block_table, seq_lens, prefix_lens, groups, o, lse, B, Hq, table_width, table_stride,
                       scale, workspace, workspace_bytes);
     if (rc != FA_OK || B == 0) return rc;
-    const long long units = static_cast<long long>(B) * Hkv * ((Hq / Hkv + 15) / 16);
+    if (shared_small(B, Hkv, d, cache->type, static_cast<long long>(table_width) * cache->page_size))
+        return fa_decode_paged(q, cache, block_table, seq_lens, o, lse, B, Hq, table_width, table_stride, scale, workspace,
+                               workspace_bytes, stream);
     SharedPlan plan;
-    if (units > 0x7fffffffLL / fa::kDecodeCluster) return FA_ERR_BAD_SHAPE;
     int dev = 0, sms = 0;
     rc = fa::host_probe(&dev, &sms);
     if (rc != FA_OK) return rc;
@@ -476,10 +506,18 @@ int fa_decode_shared(const void* q, const fa_paged_cache* cache, const int* bloc
 
     fa::SharedParams p{};
     fill_decode(p, q, cache, c, block_table, seq_lens, o, lse, B, Hq, table_width, table_stride, scale);
-    // a cluster for each (request, key head)'s own keys, as large as one wave holds: how many they are only the GPU knows
-    p.cluster = 1;
-    while (p.cluster < fa::kDecodeCluster && 2 * p.cluster * units <= static_cast<long long>(kWorkersPerSm) * sms)
-        p.cluster *= 2;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.cluster = plan.cluster;
+    p.own_first = plan.own_workers > 0 ? 1 : 0;
+    if (p.own_first) {
+        p.own_workers = static_cast<int>(plan.own_workers);
+        p.fours = decode_fours(Hq, Hkv) ? 1 : 0;
+        p.part_ml = reinterpret_cast<float2*>(ws + plan.run_ml);
+        p.part_o = reinterpret_cast<float*>(ws + plan.run_o);
+        p.own_ml = reinterpret_cast<float2*>(ws + plan.own_ml);
+        p.own_o = reinterpret_cast<float*>(ws + plan.own_o);
+        p.own_info = reinterpret_cast<int2*>(ws + plan.info);
+    }
     p.prefix_lens = prefix_lens;
     p.groups = groups;
     p.each = plan.each;
@@ -488,10 +526,11 @@ int fa_decode_shared(const void* q, const fa_paged_cache* cache, const int* bloc
     p.slot_rows = plan.slot_rows;
     p.chains = plan.chains;
     p.prefix_workers = plan.workers;
-    p.shared_ml = static_cast<float2*>(workspace);
-    p.shared_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.ml);
+    p.shared_ml = reinterpret_cast<float2*>(ws);
+    p.shared_o = reinterpret_cast<float*>(ws + plan.o);
     p.wait_limit_ns = fa::host_wait_limit_ns();
-    return fa::shared_launch(dev, d, c.e4m3, p, static_cast<cudaStream_t>(stream));
+    const long long blocks = p.own_first ? plan.own_workers : plan.own_units * plan.cluster;
+    return fa::shared_launch(dev, d, c.e4m3, p, static_cast<unsigned>(blocks), static_cast<cudaStream_t>(stream));
 }
 
 int fa_rotary(const void* x, void* y, const int* positions, const double* inv_freq, int B, int H, int N, int d,

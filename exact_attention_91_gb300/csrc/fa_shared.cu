@@ -1,5 +1,6 @@
-// Launches of the shared-prefix decode: the kernel of the shared part, and the decode kernel that adds it to each
-// request's own keys. (Argument checks: fa_serve.cu.)
+// Launches of the shared-prefix decode. Few requests: the kernel of the shared part, then the decode kernel's small form,
+// which adds it to each request's own keys. Many: the decode kernel on the own keys, the shared part, and a kernel that adds
+// all up. (Argument checks: fa_serve.cu.)
 #include <atomic>
 #include <mutex>
 
@@ -25,7 +26,9 @@ template <int D, bool E4M3>
 bool set_pair() {
     return set_smem(fa::fa_prefix_kernel<D, E4M3>, fa::PrefixCfg<D, E4M3>::kSmemBytes) &&
            set_smem(fa::fa_decode_kernel<D, E4M3, false, true, true>, fa::DecodeCfg<D, E4M3, false>::kSmemBytes) &&
-           set_smem(fa::fa_decode_kernel<D, E4M3, true, true, true>, fa::DecodeCfg<D, E4M3, true>::kSmemBytes);
+           set_smem(fa::fa_decode_kernel<D, E4M3, true, true, true>, fa::DecodeCfg<D, E4M3, true>::kSmemBytes) &&
+           set_smem(fa::fa_decode_kernel<D, E4M3, false, false, true>, fa::DecodeCfg<D, E4M3, false>::kSmemBytes) &&
+           set_smem(fa::fa_decode_kernel<D, E4M3, true, false, true>, fa::DecodeCfg<D, E4M3, true>::kSmemBytes);
 }
 
 // The kernels' shared-memory sizes, set on the device by its first call that is not being captured; a captured call
@@ -66,31 +69,39 @@ int launch(void (*kernel)(fa::SharedParams), unsigned blocks, int threads, int s
 }
 
 template <int D, bool E4M3, bool WIDE>
-int launch_both(const fa::SharedParams& p, cudaStream_t s) {
+int launch_all(const fa::SharedParams& p, unsigned workers, cudaStream_t s) {
     using C = fa::PrefixCfg<D, E4M3>;
     using Own = fa::DecodeCfg<D, E4M3, WIDE>;
-    const int rc = launch(fa::fa_prefix_kernel<D, E4M3>, static_cast<unsigned>(p.prefix_workers), C::kThreads,
-                          C::kSmemBytes, s, p, 1);
+    int rc = FA_OK;
+    if (p.own_first)
+        rc = launch(fa::fa_decode_kernel<D, E4M3, WIDE, false, true>, workers, Own::kThreads, Own::kSmemBytes, s, p, 1);
+    if (rc == FA_OK)
+        rc = launch(fa::fa_prefix_kernel<D, E4M3>, static_cast<unsigned>(p.prefix_workers), C::kThreads, C::kSmemBytes, s, p,
+                    1);
     if (rc != FA_OK) return rc;
-    return launch(fa::fa_decode_kernel<D, E4M3, WIDE, true, true>,
-                  static_cast<unsigned>(p.B * p.Hkv * p.row_groups * p.cluster), Own::kThreads, Own::kSmemBytes, s, p,
-                  p.cluster);
+    if (p.own_first) {
+        constexpr int per = fa::kSharedJoinThreads / (D / 4);
+        const long long rows = static_cast<long long>(p.B) * p.Hkv * p.G;
+        return launch(fa::fa_shared_join_kernel<D, Own::kRows>, static_cast<unsigned>((rows + per - 1) / per),
+                      fa::kSharedJoinThreads, 0, s, p, 1);
+    }
+    return launch(fa::fa_decode_kernel<D, E4M3, WIDE, true, true>, workers, Own::kThreads, Own::kSmemBytes, s, p, p.cluster);
 }
 
 template <int D>
-int launch_any(bool e4m3, bool wide, const fa::SharedParams& p, cudaStream_t s) {
-    if (e4m3) return wide ? launch_both<D, true, true>(p, s) : launch_both<D, true, false>(p, s);
-    return wide ? launch_both<D, false, true>(p, s) : launch_both<D, false, false>(p, s);
+int launch_any(bool e4m3, bool wide, const fa::SharedParams& p, unsigned workers, cudaStream_t s) {
+    if (e4m3) return wide ? launch_all<D, true, true>(p, workers, s) : launch_all<D, true, false>(p, workers, s);
+    return wide ? launch_all<D, false, true>(p, workers, s) : launch_all<D, false, false>(p, workers, s);
 }
 
 }  // namespace
 
 namespace fa {
 
-int shared_launch(int dev, int d, bool e4m3, const SharedParams& p, cudaStream_t s) {
+int shared_launch(int dev, int d, bool e4m3, const SharedParams& p, unsigned workers, cudaStream_t s) {
     if (ready(dev, s) != FA_OK) return FA_ERR_LAUNCH;
     const bool wide = p.G > 8;
-    return d == 64 ? launch_any<64>(e4m3, wide, p, s) : launch_any<128>(e4m3, wide, p, s);
+    return d == 64 ? launch_any<64>(e4m3, wide, p, workers, s) : launch_any<128>(e4m3, wide, p, workers, s);
 }
 
 int shared_status(unsigned* word) {

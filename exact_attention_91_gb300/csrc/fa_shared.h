@@ -7,7 +7,7 @@ namespace fa {
 
 struct SharedParams;
 
-// Launches both kernels on the current device `dev`.
-int shared_launch(int dev, int d, bool e4m3, const SharedParams& p, cudaStream_t s);
+// Launches the kernels on the current device `dev`; `workers`: blocks of the decode kernel.
+int shared_launch(int dev, int d, bool e4m3, const SharedParams& p, unsigned workers, cudaStream_t s);
 
 }  // namespace fa

@@ -355,8 +355,8 @@ long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_typ
  * Everything else is as for fa_decode_paged, and so is the result: attention over the first seq_lens[b] keys of
  * each request, its hidden pages and scales likewise, but that weights of the shared keys are rounded to
  * bf16 (2^-9 relative, each before it meets its value) as fa_fwd's are. A request that is shorter than its
- * group's prefix is read by itself.
- * Two kernels; the second one starts on the requests' own keys while the first is at the prefixes.
+ * group's prefix is read by itself, and so is a batch whose table has no room for more than 128 MB of keys and
+ * values (those come from L2 sooner than they are shared out).
  */
 int fa_decode_shared(const void* q, const fa_paged_cache* cache, const int* block_table, const int* seq_lens,
                      const int* prefix_lens, void* o, float* lse, int B, int Hq, int groups, int table_width,
@@ -366,7 +366,8 @@ int fa_decode_shared(const void* q, const fa_paged_cache* cache, const int* bloc
  * fa_decode_shared_workspace — host-only: workspace bytes of fa_decode_shared for these sizes on a GPU with
  * sm_count SMs, or a negative status under the call's own rules.
  */
-long long fa_decode_shared_workspace(int B, int Hq, int Hkv, int d, int groups, int sm_count);
+long long fa_decode_shared_workspace(int B, int Hq, int Hkv, int d, int cache_type, int page_size, int table_width,
+                                     int groups, int sm_count);
 
 /*
  * fa_rotary — rotary positions of x [B, H, N, d] (bf16, device), into y.

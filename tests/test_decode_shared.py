@@ -60,11 +60,15 @@ def test_no_request_and_no_device():
 
 def test_workspace_sizes():
     f = fa.fa_decode_shared_workspace
-    small, large = f(4, 32, 8, 128, 1, 152), f(64, 32, 8, 128, 1, 152)
-    assert 0 < small < large < 64 << 20
-    assert f(0, 32, 8, 128, 1, 152) == 0
-    for bad, code in ((dict(B=5, groups=2), -2), (dict(groups=0), -2), (dict(Hq=9), -2), (dict(d=80), -3), (dict(sms=0), -2)):
-        kw = dict(B=4, Hq=8, Hkv=8, d=64, groups=2, sms=152) | bad
+    #                B  Hq  Hkv d  type page width groups SMs
+    small, large = f(4, 32, 8, 128, 0, 16, 4096, 1, 152), f(64, 32, 8, 128, 0, 16, 4096, 1, 152)
+    assert 0 < small < large < 128 << 20
+    assert f(64, 32, 8, 128, 0, 16, 10 ** 6, 1, 152) == large      # bounded by the requests and the GPU
+    assert f(4, 32, 8, 128, 0, 16, 64, 1, 152) == 0                 # read as fa_decode_paged reads it
+    assert f(0, 32, 8, 128, 0, 16, 64, 1, 152) == 0
+    for bad, code in ((dict(B=5, groups=2), -2), (dict(groups=0), -2), (dict(Hq=9), -2), (dict(d=80), -3), (dict(sms=0), -2),
+                      (dict(page=20), -2), (dict(width=0), -2), (dict(kind=3), -12)):
+        kw = dict(B=4, Hq=8, Hkv=8, d=64, kind=0, page=16, width=9, groups=2, sms=152) | bad
         assert f(*kw.values()) == code, bad
 
 
@@ -92,7 +96,9 @@ def make(prefixes, own, hq, hkv, d, page, e4m3=False, order="token", seed=0, wid
     del fresh
     blocks = len(pool) + 2
     perm = torch.randperm(blocks, generator=g).int()
-    width = width or max(1, max(len(r) for r in rows))
+    # (a table too small for 128 MB would be read as fa_decode_paged reads it)
+    room = (1 << 27) // (len(rows) * hkv * d * (2 if e4m3 else 4) * page) + 1
+    width = width or max(room, max(len(r) for r in rows))
     table = torch.full((len(rows), width), -1, dtype=torch.int32)
     for b, r in enumerate(rows):
         table[b, :len(r)] = perm[torch.tensor(r, dtype=torch.long)] if r else table[b, :0]
@@ -261,13 +267,33 @@ def test_many_groups_and_long_prefixes():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,lens", [
+    (8, 8, 64, "short"), (16, 8, 128, "short"), (16, 8, 128, "long"), (5, 5, 64, "long"), (30, 10, 128, "mixed"),
+    (80, 8, 64, "mixed"), (40, 1, 128, "none"),
+])
+def test_many_requests(hq, hkv, d, lens, e4m3):
+    """More units than one wave of clusters: own keys in equal runs, ahead of the prefixes."""
+    n = 40 if hkv >= 5 else 160
+    own = {"short": [i % 5 for i in range(n)], "long": [900 if i == 7 else 30 + i for i in range(n)],
+           "mixed": [(None, -3, 0, 1, 64, 257)[i % 6] for i in range(n)], "none": [0] * n}[lens]
+    x = make([208, 33], own, hq, hkv, d, 16, e4m3=e4m3, seed=hq + n)
+    got = call(x)
+    check(got, want(x))
+    for a, b in zip(call(x), got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_repeats_streams_buffers_and_agreement_with_paged_decode(e4m3):
     x = make([640, 1024], [50, 3, 200], 16, 4, 128, 16, e4m3=e4m3, seed=17)
     ref = call(x)
     check(ref, want(x))
     side = torch.cuda.Stream()
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    ws = torch.full((fa.fa_decode_shared_workspace(6, 16, 4, 128, 2, sms),), 255, dtype=torch.uint8, device="cuda")
+    room = fa.fa_decode_shared_workspace(6, 16, 4, 128, fa.CACHE_E4M3 if e4m3 else fa.CACHE_BF16, 16, x["table"].shape[1],
+                                         2, sms)
+    ws = torch.full((room,), 255, dtype=torch.uint8, device="cuda")
     out, lse = torch.full_like(ref[0], float("nan")), torch.full_like(ref[1], float("nan"))
     for kw in ({}, dict(stream=side), dict(out=out, lse=lse, workspace=ws)):
         got = call(x, **kw)
@@ -279,6 +305,14 @@ def test_repeats_streams_buffers_and_agreement_with_paged_decode(e4m3):
     # (both are within their bounds of the same value: LSE of fp32's rounding, O of two roundings to bf16 and P's)
     assert (l - ref[1]).abs().max() <= 2.0 ** -15
     assert (o.float() - ref[0].float()).abs().max() <= 2 * 2.0 ** -8 * o.float().abs().max() + 2.0 ** -8
+
+
+@pytest.mark.gpu
+def test_a_small_batch_is_read_as_by_paged_decode():
+    x = make([64, 64], [1, 20], 4, 2, 64, 16, seed=19, width=8)
+    want_o, want_l = fa.attention_decode_paged(x["q"], x["k"], x["v"], x["table"], x["lens"])
+    got = call(x)
+    assert torch.equal(got[0], want_o) and torch.equal(got[1], want_l)
 
 
 @pytest.mark.gpu
