@@ -173,7 +173,8 @@ int ready(int dev, cudaStream_t stream) {
                     set_decode<128, false, true>() && set_decode<128, true, false>() &&
                     set_decode<128, true, true>() &&
                     cudaFuncSetAttribute(fa::fa_page_maps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kMapsSmem) == cudaSuccess;
+                                         kMapsSmem) == cudaSuccess &&
+                    fa::shared_prepare();
     if (!ok) {
         cudaGetLastError();
         return FA_ERR_LAUNCH;
@@ -530,7 +531,9 @@ int fa_decode_shared(const void* q, const fa_paged_cache* cache, const int* bloc
     p.shared_o = reinterpret_cast<float*>(ws + plan.o);
     p.wait_limit_ns = fa::host_wait_limit_ns();
     const long long blocks = p.own_first ? plan.own_workers : plan.own_units * plan.cluster;
-    return fa::shared_launch(dev, d, c.e4m3, p, static_cast<unsigned>(blocks), static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (ready(dev, s) != FA_OK) return FA_ERR_LAUNCH;
+    return fa::shared_launch(d, c.e4m3, p, static_cast<unsigned>(blocks), s);
 }
 
 int fa_rotary(const void* x, void* y, const int* positions, const double* inv_freq, int B, int H, int N, int d,

@@ -1,9 +1,6 @@
 // Launches of the shared-prefix decode. Few requests: the kernel of the shared part, then the decode kernel's small form,
 // which adds it to each request's own keys. Many: the decode kernel on the own keys, the shared part, and a kernel that adds
 // all up. (Argument checks: fa_serve.cu.)
-#include <atomic>
-#include <mutex>
-
 #include <cuda_runtime.h>
 
 #include "fa.h"
@@ -12,9 +9,6 @@
 #include "fa_shared.h"
 
 namespace {
-
-std::mutex g_ready_mu;
-std::atomic<bool> g_ready[fa::kHostMaxDevices];
 
 template <typename Kernel>
 bool set_smem(Kernel kernel, int bytes) {
@@ -29,20 +23,6 @@ bool set_pair() {
            set_smem(fa::fa_decode_kernel<D, E4M3, true, true, true>, fa::DecodeCfg<D, E4M3, true>::kSmemBytes) &&
            set_smem(fa::fa_decode_kernel<D, E4M3, false, false, true>, fa::DecodeCfg<D, E4M3, false>::kSmemBytes) &&
            set_smem(fa::fa_decode_kernel<D, E4M3, true, false, true>, fa::DecodeCfg<D, E4M3, true>::kSmemBytes);
-}
-
-// The kernels' shared-memory sizes, set on the device by its first call that is not being captured; a captured call
-// needs them set already.
-int ready(int dev, cudaStream_t stream) {
-    if (g_ready[dev].load(std::memory_order_acquire)) return FA_OK;
-    if (fa::host_capturing(stream) != 0) return FA_ERR_LAUNCH;
-    std::lock_guard<std::mutex> lock(g_ready_mu);
-    if (!(set_pair<64, false>() && set_pair<64, true>() && set_pair<128, false>() && set_pair<128, true>())) {
-        cudaGetLastError();
-        return FA_ERR_LAUNCH;
-    }
-    g_ready[dev].store(true, std::memory_order_release);
-    return FA_OK;
 }
 
 int launch(void (*kernel)(fa::SharedParams), unsigned blocks, int threads, int smem, cudaStream_t stream,
@@ -98,8 +78,11 @@ int launch_any(bool e4m3, bool wide, const fa::SharedParams& p, unsigned workers
 
 namespace fa {
 
-int shared_launch(int dev, int d, bool e4m3, const SharedParams& p, unsigned workers, cudaStream_t s) {
-    if (ready(dev, s) != FA_OK) return FA_ERR_LAUNCH;
+bool shared_prepare() {
+    return set_pair<64, false>() && set_pair<64, true>() && set_pair<128, false>() && set_pair<128, true>();
+}
+
+int shared_launch(int d, bool e4m3, const SharedParams& p, unsigned workers, cudaStream_t s) {
     const bool wide = p.G > 8;
     return d == 64 ? launch_any<64>(e4m3, wide, p, workers, s) : launch_any<128>(e4m3, wide, p, workers, s);
 }

@@ -7,7 +7,10 @@ namespace fa {
 
 struct SharedParams;
 
-// Launches the kernels on the current device `dev`; `workers`: blocks of the decode kernel.
-int shared_launch(int dev, int d, bool e4m3, const SharedParams& p, unsigned workers, cudaStream_t s);
+// Sets the kernels' shared-memory sizes on the current device.
+bool shared_prepare();
+
+// Launches the kernels on the current device; `workers`: blocks of the decode kernel.
+int shared_launch(int d, bool e4m3, const SharedParams& p, unsigned workers, cudaStream_t s);
 
 }  // namespace fa

@@ -5,12 +5,17 @@
 (the same kernels as :func:`exact_attention_91_gb300.attention_forward`).
 ``torch.ops.fa91.attention_forward_varlen(q, k, v, cu_seqlens_q,
 cu_seqlens_k, max_seqlen_q, causal, scale)`` returns ``(O [total_q, H, d],
-LSE [H, total_q])`` for packed sequences, computed by ``fa_fwd_varlen``. The
-attention operators are forward-only: the attention backward pass is not part
-of this library. ``torch.ops.fa91.rotary`` (rotary positions) is
-differentiable. ``attention_decode_paged``, ``cache_append`` and ``page_maps``
-serve from a paged cache, as the functions of the same names do; the last two
-change their caches or block table in place. (``cache_append`` here has no
+LSE [H, total_q])`` for packed sequences, computed by ``fa_fwd_varlen``. Both
+are differentiable with respect to q, k and v (through O and LSE) by
+``attention_backward`` and ``attention_backward_varlen``, which are operators too
+(``fa_bwd``, ``fa_bwd_varlen``; not differentiable themselves), and so is
+``torch.ops.fa91.rotary`` (rotary positions). ``attention_decode_paged``,
+``attention_decode_shared``, ``cache_append`` and ``page_maps`` serve from a paged
+cache, as the functions of the same names do; the last two change their caches or
+block table in place. A training step may be captured into a CUDA graph after an
+ordinary one, under autograd's own rule: no graph made outside the capture may hold
+the leaves whose gradients it accumulates (drop what the ordinary steps returned, or
+take the gradients by ``torch.autograd.grad``). (``cache_append`` here has no
 ``k_out``: a prompt's own attention takes its keys from ``torch.ops.fa91.rotary``.)
 The fake (meta) implementations
 give output shapes and dtypes without a GPU, so the operators can be traced.
@@ -19,8 +24,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (PageMaps, attention_decode_paged, attention_forward, attention_forward_varlen, cache_append, page_maps,
-               rotary)
+from . import (PageMaps, attention_backward, attention_backward_varlen, attention_decode_paged, attention_decode_shared,
+               attention_forward, attention_forward_varlen, cache_append, page_maps, rotary)
 
 
 @torch.library.custom_op("fa91::attention_forward", mutates_args=())
@@ -55,6 +60,80 @@ def _attention_forward_varlen_fake(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seql
     return torch.empty_like(q), q.new_empty((H, total_q), dtype=torch.float32)
 
 
+@torch.library.custom_op("fa91::attention_backward", mutates_args=())
+def attention_backward_op(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                          lse: torch.Tensor, causal: bool = False, scale: float | None = None,
+                          dlse: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    return attention_backward(dout, q, k, v, out, lse, causal=causal, scale=scale, dlse=dlse)
+
+
+@attention_backward_op.register_fake
+def _attention_backward_fake(dout, q, k, v, out, lse, causal=False, scale=None, dlse=None):
+    if q.dim() != 4 or k.shape != q.shape or v.shape != q.shape or dout.shape != q.shape or out.shape != q.shape:
+        raise ValueError("dout, q, k, v, out must all be [B, H, N, d]")
+    return torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+
+
+@torch.library.custom_op("fa91::attention_backward_varlen", mutates_args=())
+def attention_backward_varlen_op(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                 out: torch.Tensor, lse: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                                 cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                                 causal: bool = False, scale: float | None = None, dlse: torch.Tensor | None = None
+                                 ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    # (rows behind the last sequence have no gradient: the kernels leave them as they are)
+    dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    return attention_backward_varlen(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                                     causal=causal, scale=scale, dlse=dlse, dq=dq, dk=dk, dv=dv)
+
+
+@attention_backward_varlen_op.register_fake
+def _attention_backward_varlen_fake(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                                    causal=False, scale=None, dlse=None):
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or dout.shape != q.shape or out.shape != q.shape:
+        raise ValueError("dout, q, out must be [total_q, H, d] and k, v [total_k, H, d]")
+    return torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+
+
+def _attention_setup(ctx, inputs, output):
+    ctx.set_materialize_grads(False)
+    ctx.rest = inputs[3:]
+    ctx.save_for_backward(*inputs[:3], *output)
+
+
+def _dense(grad, like=None):
+    """A gradient as the kernels take it (a reduction's is broadcast, a slice's has strides); zeros where there is none."""
+    return grad.contiguous() if grad is not None else None if like is None else torch.zeros_like(like)
+
+
+def _attention_backward(ctx, do, dlse):
+    q, k, v, o, lse = ctx.saved_tensors
+    causal, scale = ctx.rest
+    if do is None and dlse is None:
+        return None, None, None, None, None
+    grads = torch.ops.fa91.attention_backward(_dense(do, o), q, k, v, o, lse, causal, scale, _dense(dlse))
+    return *grads, None, None
+
+
+def _attention_varlen_setup(ctx, inputs, output):
+    ctx.set_materialize_grads(False)
+    ctx.rest = inputs[5:]
+    ctx.save_for_backward(*inputs[:5], *output)
+
+
+def _attention_varlen_backward(ctx, do, dlse):
+    q, k, v, cu_q, cu_k, o, lse = ctx.saved_tensors
+    max_q, causal, scale = ctx.rest
+    if do is None and dlse is None:
+        return None, None, None, None, None, None, None, None
+    grads = torch.ops.fa91.attention_backward_varlen(_dense(do, o), q, k, v, o, lse, cu_q, cu_k, max_q, k.shape[0],
+                                                     causal, scale, _dense(dlse))
+    return *grads, None, None, None, None, None
+
+
+attention_forward_op.register_autograd(_attention_backward, setup_context=_attention_setup)
+attention_forward_varlen_op.register_autograd(_attention_varlen_backward, setup_context=_attention_varlen_setup)
+
+
 @torch.library.custom_op("fa91::attention_decode_paged", mutates_args=())
 def attention_decode_paged_op(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                               block_table: torch.Tensor, seq_lens: torch.Tensor, scale: float | None = None,
@@ -71,6 +150,22 @@ def _attention_decode_paged_fake(q, k_cache, v_cache, block_table, seq_lens, sca
         raise ValueError("q must be [B, Hq, d] and the caches [num_blocks, page_size, heads, d]")
     B, Hq, _ = q.shape
     return torch.empty_like(q), q.new_empty((B, Hq), dtype=torch.float32)
+
+
+@torch.library.custom_op("fa91::attention_decode_shared", mutates_args=())
+def attention_decode_shared_op(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               block_table: torch.Tensor, seq_lens: torch.Tensor, prefix_lens: torch.Tensor,
+                               scale: float | None = None, k_scale: torch.Tensor | None = None,
+                               v_scale: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    o, lse = attention_decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, scale=scale,
+                                     k_scale=k_scale, v_scale=v_scale)
+    return o, lse
+
+
+@attention_decode_shared_op.register_fake
+def _attention_decode_shared_fake(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, scale=None, k_scale=None,
+                                  v_scale=None):
+    return _attention_decode_paged_fake(q, k_cache, v_cache, block_table, seq_lens)
 
 
 @torch.library.custom_op("fa91::rotary", mutates_args=())
