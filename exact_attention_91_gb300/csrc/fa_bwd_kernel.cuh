@@ -413,22 +413,43 @@ __device__ __forceinline__ void bwd_grad_mma(uint32_t d_tmem, uint32_t a_tmem, u
                           b0 + static_cast<uint32_t>(kk * (2048 >> 4)), kIdesc, accumulate || kk > 0 ? 1u : 0u);
 }
 
-// COLS columns of an accumulator, times f, to bf16 at `to`.
+// COLS columns of 32 rows of an accumulator, times f, to bf16: row i of a warp's 32 goes to `to` + i·pitch, if i < rows.
+// A lane has a row; before they are stored, groups of four lanes exchange their 16-byte pieces, so that a store's pieces
+// lie side by side, 64 bytes of 8 rows (as 16 bytes of 32 rows a unit's end took 2 us more: a 128-byte line a cycle).
 template <int COLS>
-__device__ __forceinline__ void bwd_store(uint32_t taddr, float f, void* to, bool have) {
+__device__ __forceinline__ void bwd_store(uint32_t taddr, float f, uint16_t* to, long long pitch, int rows, int lane) {
+    constexpr int kPieces = COLS >= 32 ? 4 : COLS / 8;
+    const int mine = lane & (kPieces - 1), row0 = lane - mine;
+    to += row0 * pitch + mine * 8;
 #pragma unroll
-    for (int c = 0; c < COLS; c += 16) {
-        uint32_t x[8], y[8];
-        ptx::tmem_ld_32x32b_x8(taddr + c, x);
-        ptx::tmem_ld_32x32b_x8(taddr + c + 8, y);
-        ptx::tmem_wait_ld(x);
-        ptx::tmem_wait_ld(y);
-        if (!have) continue;
-        auto two = [&](const uint32_t(&v)[8], int k) {
-            return ptx::pack_bf16x2(__uint_as_float(v[k]) * f, __uint_as_float(v[k + 1]) * f);
-        };
-        reinterpret_cast<uint4*>(to)[c / 8] = make_uint4(two(x, 0), two(x, 2), two(x, 4), two(x, 6));
-        reinterpret_cast<uint4*>(to)[c / 8 + 1] = make_uint4(two(y, 0), two(y, 2), two(y, 4), two(y, 6));
+    for (int c = 0; c < COLS; c += kPieces * 8) {
+        uint32_t x[kPieces][4];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            uint32_t v[8];
+            ptx::tmem_ld_32x32b_x8(taddr + c + i * 8, v);
+            ptx::tmem_wait_ld(v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                x[i][k] = ptx::pack_bf16x2(__uint_as_float(v[2 * k]) * f, __uint_as_float(v[2 * k + 1]) * f);
+        }
+#pragma unroll
+        for (int bit = 1; bit < kPieces; bit <<= 1)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                if (i & bit) continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool high = (lane & bit) != 0;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? x[i][k] : x[i | bit][k], bit);
+                    if (high) x[i][k] = got;
+                    else x[i | bit][k] = got;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            if (row0 + i < rows)
+                *reinterpret_cast<uint4*>(to + i * pitch + c) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
     }
 }
 
@@ -538,6 +559,7 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
         return w;
     };
     uint32_t t = 0, full_units = 0;  // tiles and units with tiles before this one
+    const long long pitch = VARLEN ? static_cast<long long>(p.heads) * D : D;  // of a head's rows in memory
 
     if (warp == kBwdLoad) {
         const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
@@ -638,8 +660,9 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
             const int n = w.n, off = w.nk - w.nq;
             const int seen_all = CAUSAL ? min(w.nk - 1, w.r0 + off) : w.nk - 1;
             const int seen = CAUSAL ? min(w.nk - 1, w.r0 + row + off) : w.nk - 1;
-            const bool have = mine.have;
-            const long long out = bwd_row<D, VARLEN>(p, w, w.tq0, have ? w.r0 + row : w.r0) + part * (D / 4);
+            // of the output: the warp's first row (the block's if it has none), and how many it has
+            const int rows = w.nq - w.r0 - (warp & 3) * 32;
+            const long long out = bwd_row<D, VARLEN>(p, w, w.tq0, rows > 0 ? w.r0 + (warp & 3) * 32 : w.r0) + part * (D / 4);
             for (int j = 0; j < n; ++j, ++t) {
                 ok = wait(sm.s_full(0), t, kStatusTimeoutMma);
                 if (!ok) break;
@@ -699,12 +722,12 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
                 mine.load(p, w, part, row);
             }
             if (ok && n == 0) {
-                if (have) bwd_store_zero<D / 4>(to);
+                if (lane < rows) bwd_store_zero<D / 4>(to + lane * pitch);
             } else if (ok) {
                 ok = wait(sm.acc_full(), full_units++, kStatusTimeoutMma);
                 if (ok) {
                     ptx::tc_fence_after_sync();
-                    bwd_store<D / 4>(tmem + kTmemDq + lanes + part * (D / 4), p.scale, to, have);
+                    bwd_store<D / 4>(tmem + kTmemDq + lanes + part * (D / 4), p.scale, to, pitch, rows, lane);
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(sm.acc_free());
@@ -751,6 +774,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
         return w;
     };
     uint32_t t = 0, full_units = 0;  // tiles and units with tiles before this one
+    const long long pitch = VARLEN ? static_cast<long long>(p.heads) * D : D;  // of a head's rows in memory
 
     if (warp == kBwdLoad) {
         const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
@@ -977,19 +1001,19 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(sm.ds_full(0));
             }
             if (!ok) break;
-            // ---- one key per thread: dV by warps 0-7, dK by warps 8-15, half a row each
-            const int key = w.r0 + row + lane, half = part & 1;
-            const bool have = key < w.nk, is_dv = part < 2;
+            // ---- a key per lane: dV by warps 0-7, dK by warps 8-15, half a row each
+            const int rows = w.nk - w.r0 - row, half = part & 1;
+            const bool is_dv = part < 2;
             uint16_t* to = static_cast<uint16_t*>(is_dv ? p.dv : p.dk) +
-                           bwd_row<D, VARLEN>(p, w, w.tk0, have ? key : w.r0) + half * (D / 2);
+                           bwd_row<D, VARLEN>(p, w, w.tk0, rows > 0 ? w.r0 + row : w.r0) + half * (D / 2);
             if (w.n == 0) {
-                if (have) bwd_store_zero<D / 2>(to);
+                if (lane < rows) bwd_store_zero<D / 2>(to + lane * pitch);
                 continue;
             }
             ok = wait(sm.acc_full(), full_units++, kStatusTimeoutMma);
             if (!ok) break;
             ptx::tc_fence_after_sync();
-            bwd_store<D / 2>(tmem + (is_dv ? kTmemDv : kTmemDk) + lanes + half * (D / 2), is_dv ? 1.f : p.scale, to, have);
+            bwd_store<D / 2>(tmem + (is_dv ? kTmemDv : kTmemDk) + lanes + half * (D / 2), is_dv ? 1.f : p.scale, to, pitch, rows, lane);
             ptx::tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(sm.acc_free());
