@@ -64,12 +64,12 @@ struct BwdParams {
 };
 
 // A unit: one head of one sequence, and a block of 128 of its queries (dq) or keys (dkv).
-struct BwdUnit {
-    int bh, head;   // b*H + h; h (variable length: the tensor maps' coordinate)
+struct alignas(16) BwdUnit {
+    int head;       // b*H + h, or (variable length) h
     int tq0, tk0;   // variable length: first query / key token of the sequence
     int nq, nk;
     int r0;         // first row of the block within the sequence
-    int first, n;   // tiles that it walks: [first, first + n)
+    int first, n;   // tiles that it walks: [first, first + n); n < 0: there is no unit
 };
 
 // The first row and the row count of sequence b in offsets `cu` of `total` rows.
@@ -101,18 +101,16 @@ __device__ __forceinline__ int2 bwd_find(const int* cu, int B, int total, int t)
 }
 
 // Unit u of the dq kernel (QUERIES) or the dkv kernel; false if it holds no row. Heads are taken in groups of 16, so
-// that those in flight share tiles in L2; equal length: a group's blocks in the order of the kernel's causal work,
-// the longest walks first.
+// that those in flight share tiles in L2; a group's blocks in the order of the kernel's causal work, the longest walks
+// first (packed: block by block from the end).
 template <bool VARLEN, bool QUERIES>
 __device__ __forceinline__ bool bwd_unit(const BwdParams& p, int u, BwdUnit& w) {
     const int tiles = QUERIES ? p.q_tiles : p.k_tiles;
-    w.first = w.n = 0;
     if constexpr (!VARLEN) {
         int block;
-        unit_coords(u, tiles, p.num_heads_total, w.bh, block);
+        unit_coords(u, tiles, p.num_heads_total, w.head, block);
         if (!QUERIES) block = tiles - 1 - block;
         w.r0 = block * kBlockM;
-        w.head = 0;
         w.tq0 = w.tk0 = 0;
         w.nq = w.nk = p.N;
         return true;
@@ -124,11 +122,12 @@ __device__ __forceinline__ bool bwd_unit(const BwdParams& p, int u, BwdUnit& w) 
             if (at.x >= p.B) return false;
             b = at.x, block = at.y;
         } else {
-            unit_coords(u, tiles, p.num_heads_total, w.bh, block);
-            b = w.bh / p.heads;
-            w.head = w.bh - b * p.heads;
+            int bh;
+            unit_coords(u, tiles, p.num_heads_total, bh, block);
+            if (!QUERIES) block = tiles - 1 - block;
+            b = bh / p.heads;
+            w.head = bh - b * p.heads;
         }
-        w.bh = b * p.heads + w.head;
         const int2 sq = bwd_seq(p.cu_q, b, p.total_q), sk = bwd_seq(p.cu_k, b, p.total_k);
         w.tq0 = sq.x, w.nq = sq.y, w.tk0 = sk.x, w.nk = sk.y;
         w.r0 = block * kBlockM;
@@ -140,14 +139,14 @@ __device__ __forceinline__ bool bwd_unit(const BwdParams& p, int u, BwdUnit& w) 
 template <int D, bool VARLEN>
 __device__ __forceinline__ long long bwd_row(const BwdParams& p, const BwdUnit& w, int t0, int row) {
     if constexpr (VARLEN) return (static_cast<long long>(t0 + row) * p.heads + w.head) * D;
-    return (static_cast<long long>(w.bh) * p.N + row) * D;
+    return (static_cast<long long>(w.head) * p.N + row) * D;
 }
 
 // Index of query `row` in lse, dlse and delta.
 template <bool VARLEN>
 __device__ __forceinline__ long long bwd_stat(const BwdParams& p, const BwdUnit& w, int row) {
     if constexpr (VARLEN) return static_cast<long long>(w.head) * p.total_q + w.tq0 + row;
-    return static_cast<long long>(w.bh) * p.N + row;
+    return static_cast<long long>(w.head) * p.N + row;
 }
 
 constexpr int kBwdWarps = 16;  // elementwise
@@ -174,7 +173,8 @@ struct BwdCfg {
     static constexpr int kOffBar = kOffStat + 2 * 2 * kBlockM * 4;
     static constexpr int kFixedBars = 29;
     static constexpr int kNumBars = kFixedBars + 2 * kStagesA + 2 * kStagesB;
-    static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM slot, abort flag, unit queue
+    static constexpr int kOffUnits = (kOffBar + kNumBars * 8 + 15) / 16 * 16;  // unit queue: two slots
+    static constexpr int kOffMisc = kOffUnits + 2 * 32;                        // TMEM slot, abort flag
     // A block's shared memory starts on a 1024-byte boundary in practice; kSlack would move it there from any
     // 512-byte one (the kernels look, and report instead of running past the end).
     static constexpr int kSlack = 512;
@@ -230,9 +230,7 @@ struct BwdSmem {
     __device__ __forceinline__ volatile int* abort_flag() const {
         return reinterpret_cast<volatile int*>(base + Cfg::kOffMisc + 4);
     }
-    __device__ __forceinline__ volatile int* unit_slot(int i) const {
-        return reinterpret_cast<volatile int*>(base + Cfg::kOffMisc + 8) + i;
-    }
+    __device__ __forceinline__ int4* unit_slot(int i) const { return reinterpret_cast<int4*>(base + Cfg::kOffUnits) + 2 * i; }
 };
 
 // What a role waits with.
@@ -266,14 +264,16 @@ __device__ __forceinline__ void bwd_init_barriers(const Smem& sm, int lane) {
     ptx::fence_mbar_init();
 }
 
-// The block's it-th unit; -1: no more, -2: the wait gave up.
+// The block's it-th unit; false: the wait gave up. (The loading warp alone works out which rows a unit has: the code of that
+// in every role cost the packed dkv kernel 25 us of 135 on 12 sequences of 1024, 16 heads.)
 template <class Smem>
-__device__ __forceinline__ int bwd_next(const Smem& sm, const BwdWait& wait, uint32_t it, int lane) {
-    if (!wait(sm.u_full(it & 1), it >> 1, kStatusTimeoutOther)) return -2;
-    const int u = *sm.unit_slot(it & 1);
+__device__ __forceinline__ bool bwd_next(const Smem& sm, const BwdWait& wait, uint32_t it, int lane, BwdUnit& w) {
+    if (!wait(sm.u_full(it & 1), it >> 1, kStatusTimeoutOther)) return false;
+    const int4 a = sm.unit_slot(it & 1)[0], b = sm.unit_slot(it & 1)[1];
+    w = BwdUnit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(sm.u_free(it & 1));
-    return u;
+    return true;
 }
 
 // Loads a tile of 128 rows, from row `row` of the sequence at token t0 with n rows, into `off`, completing `full`.
@@ -289,7 +289,7 @@ struct BwdLoader {
 
     __device__ __forceinline__ bool tile(const CUtensorMap& map, const BwdUnit& w, int t0, int n, int row, int off,
                                          uint32_t full, uint64_t policy) {
-        const int y = VARLEN ? w.head : row, z = VARLEN ? t0 + row : w.bh;
+        const int y = VARLEN ? w.head : row, z = VARLEN ? t0 + row : w.head;
         const bool ragged = VARLEN && row + kBlockM > n;
         const uint32_t bar = ragged ? sm.fix() : full;
         ptx::mbar_arrive_expect_tx_elect(bar, Smem::Cfg::kTileBytes);
@@ -324,40 +324,36 @@ __device__ __forceinline__ void bwd_load_role(const Smem& sm, const BwdWait& wai
     BwdLoader<Smem, VARLEN> load{sm, wait, lane};
     uint32_t cnt = 0, a_cnt = 0, b_cnt = 0, helds = 0;
     bool ok = true;
-    // the next unit with rows, from u on
-    auto settle = [&](int u, BwdUnit& w) {
-        while (u < units && !bwd_unit<VARLEN, QUERIES>(p, u, w)) {
-            if (p.next == nullptr) return units;
-            u = 0;
-            if (lane == 0) u = static_cast<int>(atomicAdd(p.next + (QUERIES ? 0 : 1), 1u) + gridDim.x);
-            u = __shfl_sync(0xffffffffu, u, 0);
+    // hands on the it-th unit: the block's own, or the next with rows that it can claim
+    BwdUnit ahead;
+    auto hand_on = [&](uint32_t it) {
+        ahead.n = -1;
+        for (bool have = it > 0;; have = true) {
+            int u = static_cast<int>(blockIdx.x);
+            if (have) {
+                if (p.next == nullptr) break;
+                if (lane == 0) u = static_cast<int>(atomicAdd(p.next + (QUERIES ? 0 : 1), 1u) + gridDim.x);
+                u = __shfl_sync(0xffffffffu, u, 0);
+            }
+            if (u >= units) break;
+            if (bwd_unit<VARLEN, QUERIES>(p, u, ahead)) {
+                range(ahead);
+                break;
+            }
         }
-        return min(u, units);
-    };
-    auto publish = [&](uint32_t it, int u) {
         if (it >= 2 && !wait(sm.u_free(it & 1), (it >> 1) - 1, kStatusTimeoutOther)) return false;
         if (lane == 0) {
-            *sm.unit_slot(it & 1) = u < units ? u : -1;
+            sm.unit_slot(it & 1)[0] = make_int4(ahead.head, ahead.tq0, ahead.tk0, ahead.nq);
+            sm.unit_slot(it & 1)[1] = make_int4(ahead.nk, ahead.r0, ahead.first, ahead.n);
             ptx::mbar_arrive(sm.u_full(it & 1));
         }
         __syncwarp();
         return true;
     };
-    BwdUnit w, ahead;
-    int u = settle(static_cast<int>(blockIdx.x), w);
-    ok = publish(0, u);
-    for (uint32_t it = 0; ok && u < units; ++it) {
-        range(w);
-        int next = units;
+    ok = hand_on(0);
+    for (uint32_t it = 0; ok && ahead.n >= 0; ++it) {
+        const BwdUnit w = ahead;
         bool handed = false;
-        auto hand_on = [&]() {
-            if (p.next != nullptr) {
-                if (lane == 0) next = static_cast<int>(atomicAdd(p.next + (QUERIES ? 0 : 1), 1u) + gridDim.x);
-                next = settle(__shfl_sync(0xffffffffu, next, 0), ahead);
-            }
-            handed = true;
-            return publish(it + 1, next);
-        };
         if (w.n > 0) {
             ok = helds == 0 || wait(sm.held_free(), helds - 1, kStatusTimeoutFree);
             if (ok) ok = held(load, w);
@@ -373,11 +369,12 @@ __device__ __forceinline__ void bwd_load_role(const Smem& sm, const BwdWait& wai
             if (ok) ok = pair(load, w, i, sa, sb, 1);
             if (!ok) break;
             ++b_cnt;
-            if (i == 1) ok = hand_on();  // (the claim's latency behind the first loads)
+            if (i == 1) {  // (the claim's latency behind the first loads)
+                ok = hand_on(it + 1);
+                handed = true;
+            }
         }
-        if (ok && !handed) ok = hand_on();
-        u = next;
-        w = ahead;
+        if (ok && !handed) ok = hand_on(it + 1);
     }
     if (ok) return;
     // a block that gave up on something exits only when its copies in flight have landed
@@ -551,13 +548,7 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
     if (!bwd_begin(sm, warp, lane)) return;
     const uint32_t tmem = *sm.tmem_slot();
     const BwdWait wait{sm.abort_flag(), p.wait_limit_ns};
-    auto range = [&](BwdUnit& w) { w.n = kv_tiles<CAUSAL>(w.r0 / kBlockM, w.nq, w.nk); };
-    auto unit = [&](int u) {
-        BwdUnit w;
-        bwd_unit<VARLEN, true>(p, u, w);
-        range(w);
-        return w;
-    };
+    auto range = [&](BwdUnit& w) { w.first = 0, w.n = kv_tiles<CAUSAL>(w.r0 / kBlockM, w.nq, w.nk); };
     uint32_t t = 0, full_units = 0;  // tiles and units with tiles before this one
     const long long pitch = VARLEN ? static_cast<long long>(p.heads) * D : D;  // of a head's rows in memory
 
@@ -579,9 +570,8 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
         // ---- S and dP, as soon as the elementwise warps have read those of the tile before
         bool ok = true;
         for (uint32_t it = 0; ok; ++it) {
-            const int u = bwd_next(sm, wait, it, lane);
-            if (u < 0) break;
-            const BwdUnit w = unit(u);
+            BwdUnit w;
+            if (!bwd_next(sm, wait, it, lane, w) || w.n < 0) break;
             if (w.n == 0) continue;
             ok = wait(sm.held_full(), full_units++, kStatusTimeoutLoad);
             for (int j = 0; j < w.n && ok; ++j, ++t) {
@@ -607,9 +597,8 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
         // ---- dQ += dS·K  (K is there: S was made of it, which dS follows)
         bool ok = true;
         for (uint32_t it = 0; ok; ++it) {
-            const int u = bwd_next(sm, wait, it, lane);
-            if (u < 0) break;
-            const BwdUnit w = unit(u);
+            BwdUnit w;
+            if (!bwd_next(sm, wait, it, lane, w) || w.n < 0) break;
             if (w.n == 0) continue;
             ok = full_units == 0 || wait(sm.acc_free(), full_units - 1, kStatusTimeoutSoftmax);
             ++full_units;
@@ -632,13 +621,10 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
         const float2 cc = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
         BwdRow<D, VARLEN> mine;
-        int u = bwd_next(sm, wait, 0, lane);
-        BwdUnit w{};
-        if (u >= 0) {
-            w = unit(u);
-            mine.load(p, w, part, row);
-        }
-        ok = u >= 0;
+        BwdUnit w;
+        bool more = bwd_next(sm, wait, 0, lane, w) && w.n >= 0;
+        if (more) mine.load(p, w, part, row);
+        ok = more;
         for (uint32_t it = 0;; ++it) {
             // -LSE·log2 e (such that P = 0 without keys) and -δ of the unit that `mine` was loaded for (0 where no key is
             // seen). The warps agree on going on: one that gave up ends all.
@@ -716,11 +702,8 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
             }
             // the next unit's rows, behind this one's last products
             uint16_t* to = static_cast<uint16_t*>(p.dq) + out;
-            u = ok ? bwd_next(sm, wait, it + 1, lane) : -2;
-            if (u >= 0) {
-                w = unit(u);
-                mine.load(p, w, part, row);
-            }
+            more = ok && bwd_next(sm, wait, it + 1, lane, w) && w.n >= 0;
+            if (more) mine.load(p, w, part, row);
             if (ok && n == 0) {
                 if (lane < rows) bwd_store_zero<D / 4>(to + lane * pitch);
             } else if (ok) {
@@ -733,7 +716,7 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
                     if (lane == 0) ptx::mbar_arrive(sm.acc_free());
                 }
             }
-            ok = ok && u >= 0;
+            ok = ok && more;
         }
     }
     bwd_end(tmem, warp);
@@ -767,12 +750,6 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
         w.first = CAUSAL ? min(max(w.r0 - (w.nk - w.nq), 0) / kBlockM, tiles) : 0;
         w.n = tiles - w.first;
     };
-    auto unit = [&](int u) {
-        BwdUnit w;
-        bwd_unit<VARLEN, false>(p, u, w);
-        range(w);
-        return w;
-    };
     uint32_t t = 0, full_units = 0;  // tiles and units with tiles before this one
     const long long pitch = VARLEN ? static_cast<long long>(p.heads) * D : D;  // of a head's rows in memory
 
@@ -794,9 +771,8 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
         // ---- Sᵀ = K·Qᵀ and dPᵀ = V·dOᵀ, as soon as their columns are free
         bool ok = true;
         for (uint32_t it = 0; ok; ++it) {
-            const int u = bwd_next(sm, wait, it, lane);
-            if (u < 0) break;
-            const BwdUnit w = unit(u);
+            BwdUnit w;
+            if (!bwd_next(sm, wait, it, lane, w) || w.n < 0) break;
             if (w.n == 0) continue;
             ok = wait(sm.held_full(), full_units++, kStatusTimeoutLoad);
             for (int i = 0; i < w.n && ok; ++i, ++t) {
@@ -828,9 +804,8 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
         // ---- dV += P·dO, dK += dS·Q. dO may still be on its way when P is there; Q is not.
         bool ok = true;
         for (uint32_t it = 0; ok; ++it) {
-            const int u = bwd_next(sm, wait, it, lane);
-            if (u < 0) break;
-            const BwdUnit w = unit(u);
+            BwdUnit w;
+            if (!bwd_next(sm, wait, it, lane, w) || w.n < 0) break;
             if (w.n == 0) continue;
             ok = full_units == 0 || wait(sm.acc_free(), full_units - 1, kStatusTimeoutSoftmax);
             ++full_units;
@@ -860,9 +835,8 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
         // ---- each query tile's -LSE·log2 e and -δ; queries past the end (and without keys) get P = 0
         bool ok = true;
         for (uint32_t it = 0; ok; ++it) {
-            const int u = bwd_next(sm, wait, it, lane);
-            if (u < 0) break;
-            const BwdUnit w = unit(u);
+            BwdUnit w;
+            if (!bwd_next(sm, wait, it, lane, w) || w.n < 0) break;
             for (int i = 0; i < w.n; ++i, ++t) {
                 const int slot = t & 1, q0 = (w.first + i) * kBlockM;
                 float l[4], d[4];
@@ -898,9 +872,8 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
         const float2 cc = make_float2(p.scale_log2, p.scale_log2);
         bool ok = true;
         for (uint32_t it = 0; ok; ++it) {
-            const int u = bwd_next(sm, wait, it, lane);
-            if (u < 0) break;
-            const BwdUnit w = unit(u);
+            BwdUnit w;
+            if (!bwd_next(sm, wait, it, lane, w) || w.n < 0) break;
             const int off = w.nk - w.nq;
             for (int i = 0; i < w.n; ++i, ++t) {
                 const int slot = t & 1;
