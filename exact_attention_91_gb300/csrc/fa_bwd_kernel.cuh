@@ -233,13 +233,24 @@ struct BwdSmem {
     __device__ __forceinline__ int4* unit_slot(int i) const { return reinterpret_cast<int4*>(base + Cfg::kOffUnits) + 2 * i; }
 };
 
+// (Not inlined: some forty waits of 2 KB each would be most of a kernel's code, and what its roles take of the instruction
+// cache shows at each unit's end.)
+__device__ __noinline__ bool bwd_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned site,
+                                           unsigned long long lim) {
+    return wait_slow(bar, parity, abort_flag, site, lim);
+}
+
+__device__ __noinline__ void bwd_wait_drain(uint32_t bar, uint32_t parity) { wait_drain(bar, parity, 100000000ull); }
+
 // What a role waits with.
 struct BwdWait {
     volatile int* abort_flag;
     unsigned long long lim;
-    // A whole warp waits for the n-th phase (0, 1, ..) of a barrier; false if the wait gave up.
+    // A whole warp waits for the n-th phase (0, 1, ..) of a barrier; false if the wait gave up. The phase before the first
+    // (n = -1, for what needs no waiting the first time) counts as done.
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t n, unsigned site) const {
-        return __all_sync(0xffffffffu, wait_phase(bar, n & 1, abort_flag, site, lim));
+        const bool ok = ptx::mbar_try_wait(bar, n & 1) || bwd_wait_slow(bar, n & 1, abort_flag, site, lim);
+        return __all_sync(0xffffffffu, ok);
     }
 };
 
@@ -301,8 +312,10 @@ struct BwdLoader {
             ++fixes;
             if (!ok) return false;
             // a box's rows are 128 bytes each, in order: the swizzle moves chunks within a row
+#pragma unroll 1
             for (int c = 0; c < D / kBoxCols; ++c) {
                 uint4* to = reinterpret_cast<uint4*>(sm.base + off + c * kBoxBytes);
+#pragma unroll 1
                 for (int i = max(0, n - row) * 8 + lane; i < kBlockM * 8; i += 32) to[i] = make_uint4(0, 0, 0, 0);
             }
             ptx::fence_proxy_async_smem();
@@ -314,12 +327,11 @@ struct BwdLoader {
 };
 
 // The loading role: claims units, hands them to the other roles one ahead, and loads their tiles. `range(w)` sets a
-// unit's walk; held(loader, w) loads its two held tiles, pair(loader, w, i, sa, sb, which) a tile of its walk.
+// unit's walk; held(loader, w, i) loads one of its two held tiles, pair(loader, w, i, sa, sb, which) a tile of its walk.
 template <bool VARLEN, bool QUERIES, class Smem, class Range, class Held, class Pair>
 __device__ __forceinline__ void bwd_load_role(const Smem& sm, const BwdWait& wait, const BwdParams& p, int lane,
                                               Range&& range, Held&& held, Pair&& pair) {
     using Cfg = typename Smem::Cfg;
-    constexpr unsigned long long kDrainNs = 100000000ull;
     const int units = QUERIES ? p.q_units : p.k_units;
     BwdLoader<Smem, VARLEN> load{sm, wait, lane};
     uint32_t cnt = 0, a_cnt = 0, b_cnt = 0, helds = 0;
@@ -341,7 +353,7 @@ __device__ __forceinline__ void bwd_load_role(const Smem& sm, const BwdWait& wai
                 break;
             }
         }
-        if (it >= 2 && !wait(sm.u_free(it & 1), (it >> 1) - 1, kStatusTimeoutOther)) return false;
+        if (!wait(sm.u_free(it & 1), (it >> 1) - 1, kStatusTimeoutOther)) return false;
         if (lane == 0) {
             sm.unit_slot(it & 1)[0] = make_int4(ahead.head, ahead.tq0, ahead.tk0, ahead.nq);
             sm.unit_slot(it & 1)[1] = make_int4(ahead.nk, ahead.r0, ahead.first, ahead.n);
@@ -350,39 +362,37 @@ __device__ __forceinline__ void bwd_load_role(const Smem& sm, const BwdWait& wai
         __syncwarp();
         return true;
     };
-    ok = hand_on(0);
-    for (uint32_t it = 0; ok && ahead.n >= 0; ++it) {
-        const BwdUnit w = ahead;
-        bool handed = false;
+    // (one place for each step: what the roles' code takes of the instruction cache shows in the unit's end)
+    BwdUnit w;
+    w.n = 0;  // (before the first unit)
+    for (uint32_t it = 0; ok; ++it) {
         if (w.n > 0) {
-            ok = helds == 0 || wait(sm.held_free(), helds - 1, kStatusTimeoutFree);
-            if (ok) ok = held(load, w);
+            ok = wait(sm.held_free(), helds - 1, kStatusTimeoutFree);
+#pragma unroll 1
+            for (int i = 0; i < 2 && ok; ++i) ok = held(load, w, i);
             ++helds;
         }
-        for (int i = 0; i < w.n && ok; ++i, ++cnt) {
+        for (int i = 0; ok; ++i, ++cnt) {
+            if (i == min(2, w.n)) ok = hand_on(it);  // (the claim's latency behind the first loads)
+            if (!ok || i == w.n) break;
             const uint32_t sa = cnt % Cfg::kStagesA, sb = cnt % Cfg::kStagesB;
-            ok = cnt < Cfg::kStagesA || wait(sm.a_free(sa), cnt / Cfg::kStagesA - 1, kStatusTimeoutFree);
-            if (ok) ok = pair(load, w, i, sa, sb, 0);
-            if (!ok) break;
-            ++a_cnt;
-            ok = cnt < Cfg::kStagesB || wait(sm.b_free(sb), cnt / Cfg::kStagesB - 1, kStatusTimeoutFree);
-            if (ok) ok = pair(load, w, i, sa, sb, 1);
-            if (!ok) break;
-            ++b_cnt;
-            if (i == 1) {  // (the claim's latency behind the first loads)
-                ok = hand_on(it + 1);
-                handed = true;
+#pragma unroll 1
+            for (int which = 0; which < 2 && ok; ++which) {
+                ok = wait(which == 0 ? sm.a_free(sa) : sm.b_free(sb), (which == 0 ? cnt / Cfg::kStagesA : cnt / Cfg::kStagesB) - 1, kStatusTimeoutFree);
+                if (ok) ok = pair(load, w, i, sa, sb, which);
+                if (ok) ++(which == 0 ? a_cnt : b_cnt);
             }
         }
-        if (ok && !handed) ok = hand_on(it + 1);
+        if (ahead.n < 0) break;
+        w = ahead;
     }
     if (ok) return;
     // a block that gave up on something exits only when its copies in flight have landed
-    if (helds > 0) wait_drain(sm.held_full(), (helds - 1) & 1, kDrainNs);
+    if (helds > 0) bwd_wait_drain(sm.held_full(), (helds - 1) & 1);
     for (uint32_t i = a_cnt > Cfg::kStagesA ? a_cnt - Cfg::kStagesA : 0; i < a_cnt; ++i)
-        wait_drain(sm.a_full(i % Cfg::kStagesA), (i / Cfg::kStagesA) & 1, kDrainNs);
+        bwd_wait_drain(sm.a_full(i % Cfg::kStagesA), (i / Cfg::kStagesA) & 1);
     for (uint32_t i = b_cnt > Cfg::kStagesB ? b_cnt - Cfg::kStagesB : 0; i < b_cnt; ++i)
-        wait_drain(sm.b_full(i % Cfg::kStagesB), (i / Cfg::kStagesB) & 1, kDrainNs);
+        bwd_wait_drain(sm.b_full(i % Cfg::kStagesB), (i / Cfg::kStagesB) & 1);
 }
 
 // D[128 x 128] = A·Bᵀ over D: both K-major tiles.
@@ -464,7 +474,7 @@ __device__ __forceinline__ void bwd_drain_mmas(const Smem& sm, int m, int lane) 
     __syncwarp();
     if (lane == 0) {
         ptx::mma_commit(sm.fin(m));
-        wait_drain(sm.fin(m), 0, 100000000ull);
+        bwd_wait_drain(sm.fin(m), 0);
     }
     __syncwarp();
 }
@@ -557,14 +567,12 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
         using Load = BwdLoader<Smem, VARLEN>;
         bwd_load_role<VARLEN, true>(
             sm, wait, p, lane, range,
-            [&](Load& load, const BwdUnit& w) {
-                return load.tile(tm_q, w, w.tq0, w.nq, w.r0, 0, sm.held_full(), once) &&
-                       load.tile(tm_do, w, w.tq0, w.nq, w.r0, Cfg::kTileBytes, sm.held_full(), once);
+            [&](Load& load, const BwdUnit& w, int i) {
+                return load.tile(i == 0 ? tm_q : tm_do, w, w.tq0, w.nq, w.r0, i * Cfg::kTileBytes, sm.held_full(), once);
             },
             [&](Load& load, const BwdUnit& w, int j, uint32_t sa, uint32_t sb, int which) {
-                return which == 0
-                           ? load.tile(tm_k, w, w.tk0, w.nk, j * kBlockN, sm.a_off(sa), sm.a_full(sa), keep)
-                           : load.tile(tm_v, w, w.tk0, w.nk, j * kBlockN, sm.b_off(sb), sm.b_full(sb), keep);
+                return load.tile(which == 0 ? tm_k : tm_v, w, w.tk0, w.nk, j * kBlockN,
+                                 which == 0 ? sm.a_off(sa) : sm.b_off(sb), which == 0 ? sm.a_full(sa) : sm.b_full(sb), keep);
             });
     } else if (warp == kBwdScore) {
         // ---- S and dP, as soon as the elementwise warps have read those of the tile before
@@ -577,13 +585,13 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
             for (int j = 0; j < w.n && ok; ++j, ++t) {
                 const uint32_t sa = t % Cfg::kStagesA, sb = t % Cfg::kStagesB;
                 ok = wait(sm.a_full(sa), t / Cfg::kStagesA, kStatusTimeoutLoad) &&
-                     (t == 0 || wait(sm.s_free(), t - 1, kStatusTimeoutSoftmax));
+                     wait(sm.s_free(), t - 1, kStatusTimeoutSoftmax);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
                 bwd_score_mma<D>(tmem + kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
                 ptx::mma_commit_elect(sm.s_full(0));
                 ok = wait(sm.b_full(sb), t / Cfg::kStagesB, kStatusTimeoutLoad) &&
-                     (t == 0 || wait(sm.dp_free(), t - 1, kStatusTimeoutSoftmax));
+                     wait(sm.dp_free(), t - 1, kStatusTimeoutSoftmax);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
                 bwd_score_mma<D>(tmem + kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
@@ -600,8 +608,7 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
             BwdUnit w;
             if (!bwd_next(sm, wait, it, lane, w) || w.n < 0) break;
             if (w.n == 0) continue;
-            ok = full_units == 0 || wait(sm.acc_free(), full_units - 1, kStatusTimeoutSoftmax);
-            ++full_units;
+            ok = wait(sm.acc_free(), full_units++ - 1, kStatusTimeoutSoftmax);
             for (int j = 0; j < w.n && ok; ++j, ++t) {
                 const uint32_t sa = t % Cfg::kStagesA, buf = t & 1;
                 ok = wait(sm.ds_full(buf), t >> 1, kStatusTimeoutSoftmax);
@@ -689,11 +696,9 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
                     r[c / 2] = ptx::pack_bf16x2(ds.x, ds.y);
                 }
                 const uint32_t buf = t & 1;
-                if (t >= 2) {  // dQ += dS·K has read what was there
-                    ok = wait(sm.ds_free(buf), (t >> 1) - 1, kStatusTimeoutMma);
-                    if (!ok) break;
-                    ptx::tc_fence_after_sync();
-                }
+                ok = wait(sm.ds_free(buf), (t >> 1) - 1, kStatusTimeoutMma);  // dQ += dS·K has read what was there
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
                 ptx::tmem_st_32x32b_x16(tmem + kTmemDs + buf * 64 + lanes + part * 16, r);
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before_sync();
@@ -758,14 +763,13 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
         using Load = BwdLoader<Smem, VARLEN>;
         bwd_load_role<VARLEN, false>(
             sm, wait, p, lane, range,
-            [&](Load& load, const BwdUnit& w) {
-                return load.tile(tm_k, w, w.tk0, w.nk, w.r0, 0, sm.held_full(), once) &&
-                       load.tile(tm_v, w, w.tk0, w.nk, w.r0, Cfg::kTileBytes, sm.held_full(), once);
+            [&](Load& load, const BwdUnit& w, int i) {
+                return load.tile(i == 0 ? tm_k : tm_v, w, w.tk0, w.nk, w.r0, i * Cfg::kTileBytes, sm.held_full(), once);
             },
             [&](Load& load, const BwdUnit& w, int i, uint32_t sa, uint32_t sb, int which) {
                 const int row = (w.first + i) * kBlockM;
-                return which == 0 ? load.tile(tm_q, w, w.tq0, w.nq, row, sm.a_off(sa), sm.a_full(sa), keep)
-                                  : load.tile(tm_do, w, w.tq0, w.nq, row, sm.b_off(sb), sm.b_full(sb), keep);
+                return load.tile(which == 0 ? tm_q : tm_do, w, w.tq0, w.nq, row, which == 0 ? sm.a_off(sa) : sm.b_off(sb),
+                                 which == 0 ? sm.a_full(sa) : sm.b_full(sb), keep);
             });
     } else if (warp == kBwdScore) {
         // ---- Sᵀ = K·Qᵀ and dPᵀ = V·dOᵀ, as soon as their columns are free
@@ -779,7 +783,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
                 const uint32_t sa = t % Cfg::kStagesA, sb = t % Cfg::kStagesB;
                 ok = wait(sm.a_full(sa), t / Cfg::kStagesA, kStatusTimeoutLoad) &&
                      wait(sm.stat_full(t & 1), t >> 1, kStatusTimeoutOther) &&
-                     (t == 0 || wait(kOver ? sm.p_free(0) : sm.s_free(), t - 1, kStatusTimeoutSoftmax));
+                     wait(kOver ? sm.p_free(0) : sm.s_free(), t - 1, kStatusTimeoutSoftmax);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
                 bwd_score_mma<D>(tmem + kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
@@ -790,7 +794,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
                 __syncwarp();
                 ptx::mma_commit_elect(sm.s_full(0));
                 ok = wait(sm.b_full(sb), t / Cfg::kStagesB, kStatusTimeoutLoad) &&
-                     (t == 0 || wait(kOver ? sm.ds_free(0) : sm.dp_free(), t - 1, kStatusTimeoutSoftmax));
+                     wait(kOver ? sm.ds_free(0) : sm.dp_free(), t - 1, kStatusTimeoutSoftmax);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
                 bwd_score_mma<D>(tmem + kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
@@ -807,8 +811,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
             BwdUnit w;
             if (!bwd_next(sm, wait, it, lane, w) || w.n < 0) break;
             if (w.n == 0) continue;
-            ok = full_units == 0 || wait(sm.acc_free(), full_units - 1, kStatusTimeoutSoftmax);
-            ++full_units;
+            ok = wait(sm.acc_free(), full_units++ - 1, kStatusTimeoutSoftmax);
             for (int i = 0; i < w.n && ok; ++i, ++t) {
                 const uint32_t sa = t % Cfg::kStagesA, sb = t % Cfg::kStagesB;
                 ok = wait(sm.b_full(sb), t / Cfg::kStagesB, kStatusTimeoutLoad) &&
@@ -851,7 +854,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
                         d[k] = -p.delta[si];
                     }
                 }
-                ok = t < 2 || wait(sm.stat_free(slot), (t >> 1) - 1, kStatusTimeoutFree);
+                ok = wait(sm.stat_free(slot), (t >> 1) - 1, kStatusTimeoutFree);
                 if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -922,7 +925,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
                         s[h][c + 1] = ptx::ex2_approx(e.y);
                         r[h][c / 2] = ptx::pack_bf16x2(s[h][c], s[h][c + 1]);
                     }
-                if (!kOver && t > 0) {  // dV += P·dO of the tile before has read P
+                if (!kOver) {  // dV += P·dO of the tile before has read P
                     ok = wait(sm.p_free(0), t - 1, kStatusTimeoutMma);
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
@@ -960,7 +963,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
                         const float2 ds = ptx::fmul2(make_float2(s[h][c], s[h][c + 1]), e);
                         r[h][c / 2] = ptx::pack_bf16x2(ds.x, ds.y);
                     }
-                if (!kOver && t > 0) {  // dK += dS·Q of the tile before has read dS
+                if (!kOver) {  // dK += dS·Q of the tile before has read dS
                     ok = wait(sm.ds_free(0), t - 1, kStatusTimeoutMma);
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
