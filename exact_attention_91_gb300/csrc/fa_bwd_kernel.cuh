@@ -149,6 +149,7 @@ __device__ __forceinline__ long long bwd_stat(const BwdParams& p, const BwdUnit&
     return static_cast<long long>(w.head) * p.N + row;
 }
 
+constexpr unsigned long long kBwdDrainNs = 100000000ull;
 constexpr int kBwdWarps = 16;  // elementwise
 constexpr int kBwdScore = 16, kBwdLoad = 17, kBwdGrad = 18, kBwdStat = 19;
 constexpr int kBwdDqThreads = 19 * 32, kBwdDkvThreads = 20 * 32;
@@ -233,24 +234,12 @@ struct BwdSmem {
     __device__ __forceinline__ int4* unit_slot(int i) const { return reinterpret_cast<int4*>(base + Cfg::kOffUnits) + 2 * i; }
 };
 
-// (Not inlined: some forty waits of 2 KB each would be most of a kernel's code, and what its roles take of the instruction
-// cache shows at each unit's end.)
-__device__ __noinline__ bool bwd_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned site,
-                                           unsigned long long lim) {
-    return wait_slow(bar, parity, abort_flag, site, lim);
-}
-
-__device__ __noinline__ void bwd_wait_drain(uint32_t bar, uint32_t parity) { wait_drain(bar, parity, 100000000ull); }
-
 // What a role waits with.
 struct BwdWait {
     volatile int* abort_flag;
     unsigned long long lim;
-    // A whole warp waits for the n-th phase (0, 1, ..) of a barrier; false if the wait gave up. The phase before the first
-    // (n = -1, for what needs no waiting the first time) counts as done.
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t n, unsigned site) const {
-        const bool ok = ptx::mbar_try_wait(bar, n & 1) || bwd_wait_slow(bar, n & 1, abort_flag, site, lim);
-        return __all_sync(0xffffffffu, ok);
+        return wait_nth(bar, n, abort_flag, site, lim);
     }
 };
 
@@ -388,23 +377,33 @@ __device__ __forceinline__ void bwd_load_role(const Smem& sm, const BwdWait& wai
     }
     if (ok) return;
     // a block that gave up on something exits only when its copies in flight have landed
-    if (helds > 0) bwd_wait_drain(sm.held_full(), (helds - 1) & 1);
+    if (helds > 0) wait_drain_call(sm.held_full(), (helds - 1) & 1, kBwdDrainNs);
     for (uint32_t i = a_cnt > Cfg::kStagesA ? a_cnt - Cfg::kStagesA : 0; i < a_cnt; ++i)
-        bwd_wait_drain(sm.a_full(i % Cfg::kStagesA), (i / Cfg::kStagesA) & 1);
+        wait_drain_call(sm.a_full(i % Cfg::kStagesA), (i / Cfg::kStagesA) & 1, kBwdDrainNs);
     for (uint32_t i = b_cnt > Cfg::kStagesB ? b_cnt - Cfg::kStagesB : 0; i < b_cnt; ++i)
-        bwd_wait_drain(sm.b_full(i % Cfg::kStagesB), (i / Cfg::kStagesB) & 1);
+        wait_drain_call(sm.b_full(i % Cfg::kStagesB), (i / Cfg::kStagesB) & 1, kBwdDrainNs);
 }
 
+// An elected lane issues all MMAs of a product behind one branch (a third of the code of an election for each), but not S and
+// dP of the dkv kernel at d = 128: there they then reach the tensor core ahead of dV (4x32x4096x128 causal: 700 us for 670;
+// dq 612 for 619; d = 64, 16384 x 16384 x 8 heads: both kernels 1305 for 1345).
+template <bool DQ, int D>
+constexpr bool kBwdOneBranch = DQ || D == 64;
+
 // D[128 x 128] = A·Bᵀ over D: both K-major tiles.
-template <int D>
+template <int D, bool ONE>
 __device__ __forceinline__ void bwd_score_mma(uint32_t d_tmem, uint32_t a, uint32_t b) {
     constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(128, 128, false, false);
     const uint64_t a0 = ptx::sdesc_sw128(a, 16, 1024), b0 = ptx::sdesc_sw128(b, 16, 1024);
+    if (!ONE || ptx::elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = static_cast<uint32_t>(((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4);
-        ptx::mma_ss_elect(d_tmem, a0 + off, b0 + off, kIdesc, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = static_cast<uint32_t>(((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4);
+            if constexpr (ONE) ptx::mma_ss(d_tmem, a0 + off, b0 + off, kIdesc, kk > 0 ? 1u : 0u);
+            else ptx::mma_ss_elect(d_tmem, a0 + off, b0 + off, kIdesc, kk > 0 ? 1u : 0u);
+        }
     }
+    __syncwarp();
 }
 
 // D[128 x D] (+)= A·B over 128: A in TMEM, 16 packed columns for each 32 values of a row, `pitch` columns apart; B an
@@ -414,10 +413,13 @@ __device__ __forceinline__ void bwd_grad_mma(uint32_t d_tmem, uint32_t a_tmem, u
                                              bool accumulate) {
     constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(128, D, false, true);
     const uint64_t b0 = ptx::sdesc_sw128(b, kBoxBytes, 1024);
+    if (ptx::elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < kBlockN / 16; ++kk)
-        ptx::mma_ts_elect(d_tmem, a_tmem + (kk >> 1) * pitch + (kk & 1) * 8,
-                          b0 + static_cast<uint32_t>(kk * (2048 >> 4)), kIdesc, accumulate || kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < kBlockN / 16; ++kk)
+            ptx::mma_ts(d_tmem, a_tmem + (kk >> 1) * pitch + (kk & 1) * 8,
+                        b0 + static_cast<uint32_t>(kk * (2048 >> 4)), kIdesc, accumulate || kk > 0 ? 1u : 0u);
+    }
+    __syncwarp();
 }
 
 // COLS columns of 32 rows of an accumulator, times f, to bf16: row i of a warp's 32 goes to `to` + i·pitch, if i < rows.
@@ -474,7 +476,7 @@ __device__ __forceinline__ void bwd_drain_mmas(const Smem& sm, int m, int lane) 
     __syncwarp();
     if (lane == 0) {
         ptx::mma_commit(sm.fin(m));
-        bwd_wait_drain(sm.fin(m), 0);
+        wait_drain_call(sm.fin(m), 0, kBwdDrainNs);
     }
     __syncwarp();
 }
@@ -588,13 +590,13 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
                      wait(sm.s_free(), t - 1, kStatusTimeoutSoftmax);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
-                bwd_score_mma<D>(tmem + kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
+                bwd_score_mma<D, kBwdOneBranch<true, D>>(tmem + kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
                 ptx::mma_commit_elect(sm.s_full(0));
                 ok = wait(sm.b_full(sb), t / Cfg::kStagesB, kStatusTimeoutLoad) &&
                      wait(sm.dp_free(), t - 1, kStatusTimeoutSoftmax);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
-                bwd_score_mma<D>(tmem + kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
+                bwd_score_mma<D, kBwdOneBranch<true, D>>(tmem + kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
                 ptx::mma_commit_elect(sm.dp_full());
                 ptx::mma_commit_elect(sm.b_free(sb));
                 if (j + 1 == w.n) ptx::mma_commit_elect(sm.held_free());
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
                      wait(kOver ? sm.p_free(0) : sm.s_free(), t - 1, kStatusTimeoutSoftmax);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
-                bwd_score_mma<D>(tmem + kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
+                bwd_score_mma<D, kBwdOneBranch<false, D>>(tmem + kTmemS, sm.held(0), sm.sbase + sm.a_off(sa));
                 if (lane == 0) {  // (before the commit, which may wait for room in the queue)
                     ptx::mbar_arrive(sm.s_issued());
                     ptx::mbar_arrive(sm.s_full(0));
@@ -797,7 +799,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
                      wait(kOver ? sm.ds_free(0) : sm.dp_free(), t - 1, kStatusTimeoutSoftmax);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
-                bwd_score_mma<D>(tmem + kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
+                bwd_score_mma<D, kBwdOneBranch<false, D>>(tmem + kTmemDp, sm.held(1), sm.sbase + sm.b_off(sb));
                 ptx::mma_commit_elect(sm.dp_full());
                 ptx::mma_commit_elect(sm.b_free(sb));
                 if (i + 1 == w.n) ptx::mma_commit_elect(sm.held_free());

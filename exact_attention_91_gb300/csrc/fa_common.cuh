@@ -90,6 +90,20 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     return wait_slow(bar, parity, cta_abort, site, limit_ns);
 }
 
+// A whole converged warp waits for the n-th phase (0, 1, ..) of a barrier; false if any lane gave up. The phase before the
+// first (n = -1, for what needs no waiting the first time) counts as done. Its slow path is not inlined: with many waits its
+// 2 KB each would be most of a kernel's code, and what the roles of a block take of the instruction cache shows at every
+// change of work (attention's backward pass: 12 sequences of 100 to 2048, 16 heads of 128: 325 us, now 295).
+static __device__ __noinline__ bool wait_slow_call(uint32_t bar, uint32_t parity, volatile int* cta_abort, unsigned site,
+                                                   unsigned long long limit_ns) {
+    return wait_slow(bar, parity, cta_abort, site, limit_ns);
+}
+__device__ __forceinline__ bool wait_nth(uint32_t bar, uint32_t n, volatile int* cta_abort, unsigned site,
+                                         unsigned long long limit_ns) {
+    const bool ok = ptx::mbar_try_wait(bar, n & 1) || wait_slow_call(bar, n & 1, cta_abort, site, limit_ns);
+    return __all_sync(0xffffffffu, ok);
+}
+
 // wait_phase for a whole converged warp: every lane polls, and the result is
 // made warp-uniform (false if any lane gave up).
 __device__ __forceinline__ bool wait_phase_warp(uint32_t bar, uint32_t parity, volatile int* cta_abort,
@@ -110,6 +124,9 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, unsign
             return false;
         }
     }
+}
+static __device__ __noinline__ bool wait_drain_call(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+    return wait_drain(bar, parity, limit_ns);
 }
 
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a box

@@ -206,9 +206,9 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::kOffMisc + 4);
     volatile uint32_t* chain0 = reinterpret_cast<uint32_t*>(base + C::kOffMisc + 8);
     const unsigned long long lim = p.wait_limit_ns;
-    // A whole warp waits for the n-th phase of a barrier.
-    auto wait = [&](uint32_t b, uint32_t n, unsigned site) {
-        return __all_sync(0xffffffffu, wait_phase(b, n & 1, abort_flag, site, lim));
+    auto wait = [&](uint32_t b, uint32_t n, unsigned site) { return wait_nth(b, n, abort_flag, site, lim); };
+    auto wait_inline = [&](uint32_t b, uint32_t n, unsigned site) {
+        return wait_phase_warp(b, n & 1, abort_flag, site, lim);
     };
     if (warp == 12) {
         ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
     PrefixSeg* first_seg = reinterpret_cast<PrefixSeg*>(base + C::kOffSeg);
     static_assert(sizeof(PrefixSeg) <= 48);
     auto take_first = [&]() {  // the first segment, as a loading warp found it
-        if (!wait(seg_full, 0, kStatusTimeoutOther)) return false;
+        if (!wait_inline(seg_full, 0, kStatusTimeoutOther)) return false;
         s = *first_seg;
         return s.T > 0;
     };
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
             ptx::cp_async_commit();
         };
         auto take_slot = [&](uint32_t at, unsigned words) {
-            ok = at < C::kStages || wait(free_(at), at / C::kStages - 1, kStatusTimeoutFree);
+            ok = wait(free_(at), at / C::kStages - 1, kStatusTimeoutFree);
             if ((at & 1) == 0 && lane == 0) reinterpret_cast<unsigned*>(base + C::kOffSeen)[(at / 2 & 7) * 4 + lw] = words;
         };
         auto hand_over = [&](uint32_t at) {
@@ -407,16 +407,19 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
                         for (int spin = 0; spin < 100 && *chain0 <= others; ++spin) __nanosleep(32);
                 }
                 // (S is written over the P that the product before reads)
-                if (ok && done > 0) ok = wait(pv_done(c), done - 1, kStatusTimeoutMma);
+                if (ok) ok = wait(pv_done(c), done - 1, kStatusTimeoutMma);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
                 const uint64_t a0 = ptx::sdesc_sw128(sbase + c * C::kTileBytes, 16, 1024);
                 const uint64_t k0 = ptx::sdesc_sw128(sbase + C::kOffRing + cnt % C::kStages * C::kTileBytes, 16, 1024);
+                if (ptx::elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = static_cast<uint32_t>(((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4);
-                    ptx::mma_ss_elect(tS, a0 + off, k0 + off, kIdescS, kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = static_cast<uint32_t>(((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4);
+                        ptx::mma_ss(tS, a0 + off, k0 + off, kIdescS, kk > 0 ? 1u : 0u);
+                    }
                 }
+                __syncwarp();
                 ptx::mma_commit_elect(s_full(c));
                 ptx::mma_commit_elect(free_(cnt));
                 ok = wait(full(cnt + 1), (cnt + 1) / C::kStages, kStatusTimeoutLoad) &&
@@ -424,10 +427,13 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
                 const uint64_t v0 = ptx::sdesc_sw128(sbase + C::kOffRing + (cnt + 1) % C::kStages * C::kTileBytes, kBoxBytes, 1024);
+                if (ptx::elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kBlockN / 16; ++kk)
-                    ptx::mma_ts_elect(tO, tS + kk * 8, v0 + static_cast<uint32_t>(kk * (2048 >> 4)), kIdescPv,
-                                      started || kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < kBlockN / 16; ++kk)
+                        ptx::mma_ts(tO, tS + kk * 8, v0 + static_cast<uint32_t>(kk * (2048 >> 4)), kIdescPv,
+                                    started || kk > 0 ? 1u : 0u);
+                }
+                __syncwarp();
                 ptx::mma_commit_elect(pv_done(c));
                 ptx::mma_commit_elect(free_(cnt + 1));
                 started = true;
@@ -438,7 +444,7 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
         __syncwarp();
         if (lane == 0 && c < 2) {
             ptx::mma_commit(fin(c));
-            wait_drain(fin(c), 0, 100000000ull);
+            wait_drain_call(fin(c), 0, 100000000ull);
         }
         __syncwarp();
     } else {
@@ -518,7 +524,7 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
             float m_ref = -INFINITY, l = 0.f;
             if (idle) {  // (whatever is in its rows of P, their O is not looked at)
                 for (int t = first; t < end && ok; t += step, ++done) {
-                    ok = wait(s_full(c), done, kStatusTimeoutMma);
+                    ok = wait_inline(s_full(c), done, kStatusTimeoutMma);
                     ptx::tc_fence_before_sync();
                     if (ok && lane == 0) ptx::mbar_arrive(p_full(c));
                 }
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
             for (int t = first; !idle && t < end; t += step) {
                 const uint32_t v_cnt = cnt + 2u * static_cast<uint32_t>(t - s.t0) + 1u;
                 if (!dry) {
-                    ok = wait(s_full(c), done, kStatusTimeoutMma) && wait(full(v_cnt), v_cnt / C::kStages, kStatusTimeoutLoad);
+                    ok = wait_inline(s_full(c), done, kStatusTimeoutMma) && wait_inline(full(v_cnt), v_cnt / C::kStages, kStatusTimeoutLoad);
                     if (!ok) break;
                 }
                 ptx::tc_fence_after_sync();
@@ -617,7 +623,7 @@ __global__ void __launch_bounds__(512, 1) fa_prefix_kernel(const SharedParams p)
                 if (warp == 0 && lane == 0) *chain0 = done;
             }
             if (!dry) {
-                if (ok) ok = wait(pv_done(c), done - 1, kStatusTimeoutMma);
+                if (ok) ok = wait_inline(pv_done(c), done - 1, kStatusTimeoutMma);
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
                 // (a sum of zero: no key; NaN is no zero and is passed on)

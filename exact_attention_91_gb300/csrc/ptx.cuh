@@ -272,6 +272,14 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 // tcgen05.mma moving operands to uniform registers, which starves the tensor
 // core of instructions.
 
+// Whether this lane is the one elected of a converged warp: a branch on it keeps an issuing loop short, with operands that
+// the whole warp has computed.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.b32 %0, 1, 0, e;\n}" : "=r"(e)::"memory");
+    return e != 0;
+}
+
 __device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
     asm volatile(
