@@ -714,9 +714,9 @@ __device__ __forceinline__ void shared_join(float& m, float& l, float4& o, float
 }
 
 // The partial results of the prefix for the row of query head i of the key head, kBatch of them in flight.
-template <int D>
+template <int D, int BATCH>
 struct SharedRow {
-    static constexpr int kBatch = 8;
+    static constexpr int kBatch = BATCH;
     const SharedParams& p;
     long long unit;
     int c0, c1, n, in;
@@ -754,7 +754,7 @@ struct SharedRow {
 template <int D>
 __device__ __forceinline__ void shared_add(const SharedParams& p, const SharedAt& a, int i, int c4, float& m, float& l,
                                            float4& o) {
-    const SharedRow<D> row(p, a, i);
+    const SharedRow<D, 8> row(p, a, i);
     for (int k0 = 0; k0 < row.n; k0 += row.kBatch) {
         float2 ml[row.kBatch];
         float4 x[row.kBatch];
@@ -763,11 +763,14 @@ __device__ __forceinline__ void shared_add(const SharedParams& p, const SharedAt
     }
 }
 
-// Many requests: a row's own results and those of its prefix, added up. A warp per row (d = 64: two rows), so that many
-// rows' loads are in flight: their bytes are what bounds it.
+// Many requests: a row's own results and those of its prefix, added up. A warp per row (d = 64: two rows); what bounds it
+// is how many loads are in flight. BATCH: partial results of the prefix that a row loads at once. 8 of them, two blocks
+// to an SM, where one wave of blocks holds all rows, else 4 and four blocks (us, 8 / 4: 2048 rows of 19 partial results
+// 7.1 / 9.4; 8192 of 6, 13.9 / 9.8).
 constexpr int kSharedJoinThreads = 256;
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kSharedJoinThreads) fa_shared_join_kernel(const SharedParams p) {
+template <int D, int ROWS, int BATCH>
+__global__ void __launch_bounds__(kSharedJoinThreads, BATCH == 4 ? 4 : 2) fa_shared_join_kernel(const SharedParams p) {
+    constexpr int kBatch = BATCH;
     constexpr int kLanes = D / 4, kPer = kSharedJoinThreads / kLanes;
     ptx::griddep_launch_dependents();
     const int c4 = threadIdx.x % kLanes, hq = p.Hkv * p.G;
@@ -782,34 +785,37 @@ __global__ void __launch_bounds__(kSharedJoinThreads) fa_shared_join_kernel(cons
         const SharedAt other = shared_at(p, __shfl_sync(0xffffffffu, b, 16), h);
         if ((threadIdx.x & 16) != 0) at = other;
     }
-    const SharedRow<D> row(p, at, j);
+    const SharedRow<D, kBatch> row(p, at, j);
     const float vs = p.v_scale ? p.v_scale[h] : 1.f;
     ptx::griddep_wait();
     if (!have) return;
     // all that does not wait for something else at once: where the own results are, those of a whole unit, the first
     // ones of the prefix
-    float2 ml[row.kBatch];
-    float4 x[row.kBatch];
     const int2 info = p.own_info[static_cast<long long>(b) * p.Hkv * p.row_groups + hh];
     const float2 own = p.own_ml[out];
     float4 o = reinterpret_cast<const float4*>(p.own_o)[out * kLanes + c4];
-    if (row.n > 0) row.load(0, c4, ml, x);
     float m = own.x, l = own.y;
-    if (info.x >= 0) {
-        m = -INFINITY, l = 0.f;
-        o = make_float4(0.f, 0.f, 0.f, 0.f);
-        // (the bounds have no effect unless lengths change under the launch)
-        const int slot = min(info.x, 2 * p.own_workers - 1), first = slot >> 1;
-        const int last = min(info.y >> 3, p.own_workers - 1), heads = p.fours && (info.y & 7) == 4 ? 4 : 1;
-        for (int k = 0; k <= last - first; ++k) {
-            const long long part = ((k == 0 ? slot : 2LL * (first + k)) * heads + hh % heads) * ROWS + j % ROWS;
-            shared_join(m, l, o, p.part_ml[part], reinterpret_cast<const float4*>(p.part_o)[part * kLanes + c4]);
+#pragma unroll 1
+    for (int k0 = 0; k0 == 0 || k0 < row.n; k0 += kBatch) {
+        float2 ml[kBatch];
+        float4 x[kBatch];
+        if (row.n > 0) row.load(k0, c4, ml, x);
+        if (k0 == 0) {
+            if (info.x >= 0) {
+                m = -INFINITY, l = 0.f;
+                o = make_float4(0.f, 0.f, 0.f, 0.f);
+                // (the bounds have no effect unless lengths change under the launch)
+                const int slot = min(info.x, 2 * p.own_workers - 1), first = slot >> 1;
+                const int last = min(info.y >> 3, p.own_workers - 1), heads = p.fours && (info.y & 7) == 4 ? 4 : 1;
+#pragma unroll 1
+                for (int k = 0; k <= last - first; ++k) {
+                    const long long part = ((k == 0 ? slot : 2LL * (first + k)) * heads + hh % heads) * ROWS + j % ROWS;
+                    shared_join(m, l, o, p.part_ml[part], reinterpret_cast<const float4*>(p.part_o)[part * kLanes + c4]);
+                }
+            }
+            if (m == -INFINITY) l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-    }
-    if (m == -INFINITY) l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < row.n; k0 += row.kBatch) {
         row.add(k0, ml, x, m, l, o);
-        if (k0 + row.kBatch < row.n) row.load(k0 + row.kBatch, c4, ml, x);
     }
     const float inv = l == 0.f ? 0.f : vs / l;
     reinterpret_cast<uint2*>(p.o)[out * kLanes + c4] =

@@ -61,9 +61,10 @@ int launch_all(const fa::SharedParams& p, unsigned workers, cudaStream_t s) {
     if (rc != FA_OK) return rc;
     if (p.own_first) {
         constexpr int per = fa::kSharedJoinThreads / (D / 4);
-        const long long rows = static_cast<long long>(p.B) * p.Hkv * p.G;
-        return launch(fa::fa_shared_join_kernel<D, Own::kRows>, static_cast<unsigned>((rows + per - 1) / per),
-                      fa::kSharedJoinThreads, 0, s, p, 1);
+        const long long rows = static_cast<long long>(p.B) * p.Hkv * p.G, blocks = (rows + per - 1) / per;
+        return launch(blocks <= 2 * p.prefix_workers ? fa::fa_shared_join_kernel<D, Own::kRows, 8>
+                                                     : fa::fa_shared_join_kernel<D, Own::kRows, 4>,
+                      static_cast<unsigned>(blocks), fa::kSharedJoinThreads, 0, s, p, 1);
     }
     return launch(fa::fa_decode_kernel<D, E4M3, WIDE, true, true>, workers, Own::kThreads, Own::kSmemBytes, s, p, p.cluster);
 }
