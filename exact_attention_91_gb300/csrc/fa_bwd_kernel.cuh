@@ -315,9 +315,15 @@ struct BwdLoader {
     }
 };
 
+// Whether the blocks of the dq kernel take every gridDim-th unit, its walks all alike, and zero the other kernel's counter:
+// setting both on the stream costs 3 to 4 us (1x24x1024x64: 40.6 us, without 37.0). With unequal walks the counter wins
+// (1x10x4096x128 causal: 134 us, without 146), in the dkv kernel with equal ones too (16x16x1024x128: 187 us, without 194).
+template <bool CAUSAL, bool VARLEN>
+constexpr bool kBwdStrided = !CAUSAL && !VARLEN;
+
 // The loading role: claims units, hands them to the other roles one ahead, and loads their tiles. `range(w)` sets a
 // unit's walk; held(loader, w, i) loads one of its two held tiles, pair(loader, w, i, sa, sb, which) a tile of its walk.
-template <bool VARLEN, bool QUERIES, class Smem, class Range, class Held, class Pair>
+template <bool VARLEN, bool QUERIES, bool STRIDED, class Smem, class Range, class Held, class Pair>
 __device__ __forceinline__ void bwd_load_role(const Smem& sm, const BwdWait& wait, const BwdParams& p, int lane,
                                               Range&& range, Held&& held, Pair&& pair) {
     using Cfg = typename Smem::Cfg;
@@ -327,14 +333,19 @@ __device__ __forceinline__ void bwd_load_role(const Smem& sm, const BwdWait& wai
     bool ok = true;
     // hands on the it-th unit: the block's own, or the next with rows that it can claim
     BwdUnit ahead;
+    if (STRIDED && p.next != nullptr && blockIdx.x == 0 && lane == 0) p.next[1] = 0u;  // (the dkv kernel's)
     auto hand_on = [&](uint32_t it) {
         ahead.n = -1;
         for (bool have = it > 0;; have = true) {
             int u = static_cast<int>(blockIdx.x);
             if (have) {
                 if (p.next == nullptr) break;
-                if (lane == 0) u = static_cast<int>(atomicAdd(p.next + (QUERIES ? 0 : 1), 1u) + gridDim.x);
-                u = __shfl_sync(0xffffffffu, u, 0);
+                if constexpr (STRIDED) {
+                    u = static_cast<int>(static_cast<unsigned>(blockIdx.x) + it * gridDim.x);
+                } else {
+                    if (lane == 0) u = static_cast<int>(atomicAdd(p.next + (QUERIES ? 0 : 1), 1u) + gridDim.x);
+                    u = __shfl_sync(0xffffffffu, u, 0);
+                }
             }
             if (u >= units) break;
             if (bwd_unit<VARLEN, QUERIES>(p, u, ahead)) {
@@ -567,7 +578,7 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
     if (warp == kBwdLoad) {
         const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
         using Load = BwdLoader<Smem, VARLEN>;
-        bwd_load_role<VARLEN, true>(
+        bwd_load_role<VARLEN, true, kBwdStrided<CAUSAL, VARLEN>>(
             sm, wait, p, lane, range,
             [&](Load& load, const BwdUnit& w, int i) {
                 return load.tile(i == 0 ? tm_q : tm_do, w, w.tq0, w.nq, w.r0, i * Cfg::kTileBytes, sm.held_full(), once);
@@ -763,7 +774,7 @@ __global__ void __launch_bounds__(kBwdDkvThreads, 1)
     if (warp == kBwdLoad) {
         const uint64_t keep = ptx::policy_evict_last(), once = ptx::policy_evict_first();
         using Load = BwdLoader<Smem, VARLEN>;
-        bwd_load_role<VARLEN, false>(
+        bwd_load_role<VARLEN, false, false>(
             sm, wait, p, lane, range,
             [&](Load& load, const BwdUnit& w, int i) {
                 return load.tile(i == 0 ? tm_k : tm_v, w, w.tk0, w.nk, w.r0, i * Cfg::kTileBytes, sm.held_full(), once);

@@ -79,7 +79,7 @@ template <int D, bool CAUSAL, bool VARLEN>
 int launch_pair(int sms, cudaStream_t s, const Maps& m, fa::BwdParams p) {
     if (p.q_units <= sms && p.k_units <= sms) {
         p.next = nullptr;
-    } else if (cudaMemsetAsync(p.next, 0, 2 * sizeof(unsigned), s) != cudaSuccess) {
+    } else if (!fa::kBwdStrided<CAUSAL, VARLEN> && cudaMemsetAsync(p.next, 0, 2 * sizeof(unsigned), s) != cudaSuccess) {
         cudaGetLastError();
         return FA_ERR_LAUNCH;
     }
