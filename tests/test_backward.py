@@ -263,6 +263,36 @@ def test_repeats_streams_and_given_buffers_give_the_same_bits(d, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,causal", [(64, False), (64, True), (128, False), (128, True)])
+def test_more_units_than_sms(d, causal):
+    """Units beyond the first of a block, in strides and by the counters; the workspace holds anything before a call."""
+    x = make(3, 60, 130, d, causal, 11, dlse=True)
+    ws = torch.full((fa.fa_bwd_workspace(3 * 130, 60),), 255, dtype=torch.uint8, device="cuda")
+    got = fa.attention_backward(**x, workspace=ws)
+    check(x, got)
+    ws.fill_(1)
+    for a, b in zip(fa.attention_backward(**x, workspace=ws), got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,causal", [(64, False), (64, True), (128, True)])
+def test_many_packed_sequences(d, causal):
+    """More sequences than a warp has lanes, numbered through all of them, some of them empty; more units than SMs."""
+    g = np.random.default_rng(d + causal)
+    counts = [(int(a), int(b)) for a, b in zip(g.integers(0, 400, 70), g.integers(0, 300, 70))]
+    counts[3], counts[40], counts[69] = (0, 0), (0, 90), (1, 1)
+    counts[50] = (1100, 1300)
+    x = make_varlen(counts, 4, d, causal, 12, dlse=True, pad=5)
+    ws = torch.full((fa.fa_bwd_workspace(x["q"].shape[0], 4),), 255, dtype=torch.uint8, device="cuda")
+    got = fa.attention_backward_varlen(**x, workspace=ws)
+    check_varlen(x, got)
+    for a, b in zip(fa.attention_backward_varlen(**x, workspace=ws), got):
+        n = a.shape[0] - 5
+        assert torch.equal(a[:n], b[:n])
+
+
+@pytest.mark.gpu
 def test_refusals_of_the_python_functions():
     x = make(1, 2, 64, 64, False, 3)
     with pytest.raises(TypeError):

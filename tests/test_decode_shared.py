@@ -284,6 +284,14 @@ def test_many_requests(hq, hkv, d, lens, e4m3):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d", [(40, 8, 128), (96, 12, 64)])
+def test_many_rows(hq, hkv, d):
+    """More rows than one wave of the joining kernel's blocks, own keys cut between runs, several groups."""
+    x = make([208, 0, 1009], [700 if i == 5 else (i * 37) % 90 for i in range(28)], hq, hkv, d, 16, seed=hq)
+    check(call(x), want(x))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_repeats_streams_buffers_and_agreement_with_paged_decode(e4m3):
     x = make([640, 1024], [50, 3, 200], 16, 4, 128, 16, e4m3=e4m3, seed=17)
