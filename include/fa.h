@@ -211,8 +211,9 @@ int fa_varlen_num_splits(int B, int H, int total_k, int max_seqlen_q, int sm_cou
  *          nothing after the call's kernels. Calls (or graph replays) that may overlap in time need
  *          workspaces of their own.
  *
- * Every sum is fp32; P and dS are rounded to bf16 for the tensor cores, as fa_fwd rounds P. No atomics:
- * the same call gives the same bits. Sizes, scale, errors, ownership and streams are as for fa_fwd, except
+ * Every sum is fp32; P and dS are rounded to bf16 for the tensor cores, as fa_fwd rounds P. No atomics in
+ * a sum: the same call gives the same bits. An infinity or NaN reaches rows of its head that the mask hides it
+ * from, too (zero times it). Sizes, scale, errors, ownership and streams are as for fa_fwd, except
  * that B*H*ceil(N/128) <= 2^31 - 65537. Two kernels, launched with programmatic stream serialization
  * (they wait for what precedes them on the stream before they read or write, and let their own successor
  * start early). May be captured into CUDA graphs once the device has had one ordinary call of fa_bwd or
@@ -354,7 +355,7 @@ long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_typ
  *
  * Everything else is as for fa_decode_paged, and so is the result: attention over the first seq_lens[b] keys of
  * each request, its hidden pages and scales likewise, but that weights of the shared keys are rounded to
- * bf16 (2^-9 relative, each before it meets its value) as fa_fwd's are. A request that is shorter than its
+ * bf16 (2^-8 relative, each before it meets its value) as fa_fwd's are. A request that is shorter than its
  * group's prefix is read by itself, and so is a batch whose table has no room for more than 128 MB of keys and
  * values (those come from L2 sooner than they are shared out).
  */
