@@ -206,7 +206,7 @@ int fa_bwd_varlen(const void* dout, const void* q, const void* k, const void* v,
     long long blocks[2];
     int packed = 0;
     for (int i = 0; i < 2; ++i) {
-        const bool through = 4 * all[i] < 3 * each[i];
+        const bool through = 4 * all[i] < 3 * each[i] && all[i] <= 1 << 26;  // (16 heads' blocks are an int)
         packed |= (through ? 1 : 0) << i;
         blocks[i] = through ? all[i] * H : each[i] * H;
         if (BH > 0x7fffffffLL || blocks[i] > kMaxBlocks) return FA_ERR_BAD_SHAPE;

@@ -381,3 +381,26 @@ def test_captures_before_any_ordinary_call_are_refused(fa):
     r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, env=env, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "first -7 -7" in r.stdout and "then 0 0" in r.stdout and "(0, 0)" in r.stdout, r.stdout
+
+
+def test_operators_hold_their_registrations(fa):
+    x = [rand(1, 2, 100, 64, seed=i) for i in range(3)]
+    y = [t.detach() for t in x]
+    o, lse = fa.attention_forward(*y, causal=True)
+    cu = torch.tensor([0, 40, 100], dtype=torch.int32, device="cuda")
+    p = [rand(100, 2, 64, seed=i) for i in range(3)]
+    po, pl = fa.attention_forward_varlen(*(t.detach() for t in p), cu, cu, 60, causal=True)
+    cache = rand(8, 16, 2, 64, seed=3, grad=False)
+    table = torch.zeros(4, 4, dtype=torch.int32, device="cuda")
+    lens, prefix = torch.full((4,), 20, dtype=torch.int32, device="cuda"), torch.full((2,), 16, dtype=torch.int32, device="cuda")
+    ops = torch.ops.fa91
+    for op, args in ((ops.attention_forward, (*x, True, None)),
+                     (ops.attention_forward_varlen, (*p, cu, cu, 60, True, None)),
+                     (ops.attention_backward, (y[0], *y, o, lse, True, None, lse.clone())),
+                     (ops.attention_backward_varlen, (po, *(t.detach() for t in p), po, pl, cu, cu, 60, 60, True, None, None)),
+                     (ops.attention_decode_shared, (rand(4, 4, 64, seed=4, grad=False), cache, cache, table, lens, prefix))):
+        torch.library.opcheck(op.default, args, test_utils=("test_schema", "test_autograd_registration", "test_faketensor"))
+    with pytest.raises(RuntimeError):  # (no second derivatives: an error, not zeros)
+        o, _ = ops.attention_forward(*x, True, None)
+        g, = torch.autograd.grad(o.float().square().sum(), x[0], create_graph=True)
+        g.float().sum().backward()
