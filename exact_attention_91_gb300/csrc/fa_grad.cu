@@ -77,6 +77,7 @@ int launch(Kernel kernel, int blocks, int threads, int smem, cudaStream_t stream
 // a block for each unit.
 template <int D, bool CAUSAL, bool VARLEN>
 int launch_pair(int sms, cudaStream_t s, const Maps& m, fa::BwdParams p) {
+    p.alone = p.q_units == 0 ? 1 : 0;
     if (p.q_units <= sms && p.k_units <= sms) {
         p.next = nullptr;
     } else if (!fa::kBwdStrided<CAUSAL, VARLEN> && cudaMemsetAsync(p.next, 0, 2 * sizeof(unsigned), s) != cudaSuccess) {
