@@ -527,7 +527,6 @@ __device__ __forceinline__ void pv_role(const FwdParams& p, int lane, int t) {
         if (u < 0) break;
         const Item w = item_coords<CAUSAL, VARLEN, HALF>(u, p);
         const int n_t = w.n(t);
-        if (n_t == 0) ptx::mma_commit_elect(sm.o_full(t));  // nothing to add: O is all zero
         for (int j = 0; j < w.n_load; ++j) {
             const uint32_t v = kv_cnt + 2u * j + 1u;  // ring position of V_j
             ok = wait_phase_warp(sm.kv_full(v % S), (v / S) & 1, abort_flag, kStatusTimeoutLoad, lim);
@@ -607,6 +606,7 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap& tm_o, const FwdP
     const float c_log2 = p.scale_log2;
     uint32_t s_cnt = 0;
     uint32_t p_made = 0, pv_seen = 0;  // P tiles written / P·V completions observed
+    uint32_t o_cnt = 0;                // items with a key so far
     bool failed = false;
     for (int it = 0;; ++it) {
         const int u = next_unit(sm, it, lane, p);
@@ -744,7 +744,10 @@ __device__ __forceinline__ void softmax_role(const CUtensorMap& tm_o, const FwdP
         }
 
         // ---- epilogue of tile t
-        bool ok = !failed && wait_phase(sm.o_full(t), it & 1, abort_flag, kStatusTimeoutMma, lim);
+        // (Without a key there is no P·V and nothing to wait for. Were such an item signalled too, the P·V warp, which waits
+        // for nothing of this one's in it, could be two phases ahead, and a wait by parity would miss both.)
+        bool ok = !failed && (n_t == 0 || wait_phase(sm.o_full(t), o_cnt & 1, abort_flag, kStatusTimeoutMma, lim));
+        o_cnt += n_t > 0 ? 1u : 0u;
         ok = __all_sync(0xffffffffu, ok);
         // (a half item and a cluster split involve both warpgroups: they agree
         // on going on together, so that neither waits at a barrier the other
