@@ -25,8 +25,8 @@
 // of the next unit run on behind those of the last, so a unit's end costs its last products
 // and its output, not a block's start.
 //
-// What bounds it: in long walks at d = 128 the tensor core, 1652 to 1726 TFLOP/s over the seven products (1 x 8 x 16384,
-// 2.23 to 2.33 ms; the sustained rate under the power limit is 1702); at d = 64 the elementwise warps' chain of a tile,
+// What bounds it: in long walks at d = 128 the tensor core, 1652 to 1744 TFLOP/s over the seven products (1 x 8 x 16384,
+// 2.21 to 2.33 ms; the sustained rate under the power limit is 1702); at d = 64 the elementwise warps' chain of a tile,
 // 1300 cycles to the products' 770 and 1020 (1 x 8 x 16384, 1.30 to 1.37 ms); in walks of few tiles a unit's start and
 // end, 2 to 3 us (16 x 16 x 1024 x 128, 8 tiles of 1.4 us, 368 to 385 us).
 //
