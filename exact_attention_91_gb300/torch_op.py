@@ -60,11 +60,19 @@ def _attention_forward_varlen_fake(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seql
     return torch.empty_like(q), q.new_empty((H, total_q), dtype=torch.float32)
 
 
+def _dense(grad):
+    """A gradient as the kernels take it, whatever autograd hands back: a reduction's is broadcast, a slice's has strides or
+    starts at any element. (Looked at when the operator runs: a compiled backward pass meets other ones than it was traced with.)"""
+    grad = grad.contiguous()
+    return grad.clone() if grad.data_ptr() % 16 else grad
+
+
 @torch.library.custom_op("fa91::attention_backward", mutates_args=())
 def attention_backward_op(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
                           lse: torch.Tensor, causal: bool = False, scale: float | None = None,
                           dlse: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    return attention_backward(dout, q, k, v, out, lse, causal=causal, scale=scale, dlse=dlse)
+    return attention_backward(_dense(dout), q, k, v, out, lse, causal=causal, scale=scale,
+                              dlse=None if dlse is None else _dense(dlse))
 
 
 @attention_backward_op.register_fake
@@ -82,8 +90,9 @@ def attention_backward_varlen_op(dout: torch.Tensor, q: torch.Tensor, k: torch.T
                                  ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     # (rows behind the last sequence have no gradient: the kernels leave them as they are)
     dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
-    return attention_backward_varlen(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
-                                     causal=causal, scale=scale, dlse=dlse, dq=dq, dk=dk, dv=dv)
+    return attention_backward_varlen(_dense(dout), q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                     max_seqlen_k, causal=causal, scale=scale, dlse=None if dlse is None else _dense(dlse),
+                                     dq=dq, dk=dk, dv=dv)
 
 
 @attention_backward_varlen_op.register_fake
@@ -100,17 +109,13 @@ def _attention_setup(ctx, inputs, output):
     ctx.save_for_backward(*inputs[:3], *output)
 
 
-def _dense(grad, like=None):
-    """A gradient as the kernels take it (a reduction's is broadcast, a slice's has strides); zeros where there is none."""
-    return grad.contiguous() if grad is not None else None if like is None else torch.zeros_like(like)
-
-
 def _attention_backward(ctx, do, dlse):
     q, k, v, o, lse = ctx.saved_tensors
     causal, scale = ctx.rest
     if do is None and dlse is None:
         return None, None, None, None, None
-    grads = torch.ops.fa91.attention_backward(_dense(do, o), q, k, v, o, lse, causal, scale, _dense(dlse))
+    do = torch.zeros_like(o) if do is None else do
+    grads = torch.ops.fa91.attention_backward(do, q, k, v, o, lse, causal, scale, dlse)
     return *grads, None, None
 
 
@@ -125,8 +130,9 @@ def _attention_varlen_backward(ctx, do, dlse):
     max_q, causal, scale = ctx.rest
     if do is None and dlse is None:
         return None, None, None, None, None, None, None, None
-    grads = torch.ops.fa91.attention_backward_varlen(_dense(do, o), q, k, v, o, lse, cu_q, cu_k, max_q, k.shape[0],
-                                                     causal, scale, _dense(dlse))
+    do = torch.zeros_like(o) if do is None else do
+    grads = torch.ops.fa91.attention_backward_varlen(do, q, k, v, o, lse, cu_q, cu_k, max_q, k.shape[0], causal, scale,
+                                                     dlse)
     return *grads, None, None, None, None, None
 
 
