@@ -658,8 +658,8 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
         if (more) mine.load(p, w, part, row);
         ok = more;
         for (uint32_t it = 0;; ++it) {
-            // -LSE·log2 e (such that P = 0 without keys) and -δ of the unit that `mine` was loaded for (0 where no key is
-            // seen). The warps agree on going on: one that gave up ends all.
+            // -LSE·log2 e (such that P = 0 without keys) and -δ of the unit that `mine` was loaded for (0 where the query
+            // sees no key, by its LSE: dLSE may be no number there). The warps agree on going on: one that gave up ends all.
             if (ok && w.n > 0) {
                 ok = wait(sm.held_full(), full_units, kStatusTimeoutLoad);
                 if (ok) sm.stat(0, 0)[part * kBlockM + row] = mine.dot(sm.base + Cfg::kTileBytes, part, row);
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kBwdDqThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) delta += sm.stat(0, 0)[i * kBlockM + row];
             const float nlse = mine.have && mine.lse != -INFINITY ? -mine.lse * 1.44269504088896341f : -INFINITY;
-            if (!mine.have || w.n == 0) delta = 0.f;
+            if (!mine.have || w.n == 0 || mine.lse == -INFINITY) delta = 0.f;
             const float2 nl = make_float2(nlse, nlse), nd = make_float2(-delta, -delta);
             if (mine.have && part == 0) p.delta[mine.stat] = delta;
             // of the unit, the walk needs only where keys begin to be hidden: from the block's first query, from this one

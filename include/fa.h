@@ -204,7 +204,7 @@ int fa_varlen_num_splits(int B, int H, int total_k, int max_seqlen_q, int sm_cou
  * dout, q, k, v, o  device, bf16, contiguous [B, H, N, d], 16-byte aligned; o and lse are what
  *          fa_fwd gave for q, k, v with the same scale and causal. Read only.
  * lse      device, fp32, contiguous [B, H, N]. A query with LSE = -inf saw no key: it adds nothing, and
- *          its dQ is 0.
+ *          its dQ is 0, whatever its dlse is (an infinity or NaN too; in its dout those are as below).
  * dlse     device, fp32, contiguous [B, H, N]: the loss's gradient with respect to LSE, or NULL for 0.
  * dq, dk, dv  device, bf16, contiguous [B, H, N, d], 16-byte aligned. Written, and overlap nothing else.
  * workspace  device, 16-byte aligned, at least fa_bwd_workspace() bytes: needs no initial value, holds
@@ -212,8 +212,8 @@ int fa_varlen_num_splits(int B, int H, int total_k, int max_seqlen_q, int sm_cou
  *          workspaces of their own.
  *
  * Every sum is fp32; P and dS are rounded to bf16 for the tensor cores, as fa_fwd rounds P. No atomics in
- * a sum: the same call gives the same bits. An infinity or NaN reaches rows of its head that the mask hides it
- * from, too (zero times it). Sizes, scale, errors, ownership and streams are as for fa_fwd, except
+ * a sum: the same call gives the same bits. An infinity or NaN in dout, q, k, v or o may reach rows of its head
+ * that the mask hides it from, too (zero times it). Sizes, scale, errors, ownership and streams are as for fa_fwd, except
  * that B*H*ceil(N/128) <= 2^31 - 65537. Two kernels, launched with programmatic stream serialization
  * (they wait for what precedes them on the stream before they read or write, and let their own successor
  * start early). May be captured into CUDA graphs once the device has had one ordinary call of fa_bwd or
