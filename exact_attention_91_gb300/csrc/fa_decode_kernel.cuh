@@ -204,12 +204,12 @@ __device__ __forceinline__ bool decode_next(DecodeSeg& s, const Params& p, const
 // Where the run of worker c begins when `total` counted tiles are cut for
 // `workers`; the worker of a counted tile. (64-bit divisions take about 150
 // cycles each, and nothing else can start before them.)
-__device__ __forceinline__ long long decode_start(long long total, int workers, int c) {
+__host__ __device__ __forceinline__ long long decode_start(long long total, int workers, int c) {
     if (total < (1 << 20))
         return static_cast<unsigned>(total) * static_cast<unsigned>(c) / static_cast<unsigned>(workers);
     return total * c / workers;
 }
-__device__ __forceinline__ int decode_worker_of(long long total, int workers, long long tile) {
+__host__ __device__ __forceinline__ int decode_worker_of(long long total, int workers, long long tile) {
     if (total < (1 << 20))
         return static_cast<int>((static_cast<unsigned>(tile + 1) * static_cast<unsigned>(workers) - 1u) /
                                 static_cast<unsigned>(total));

@@ -716,6 +716,15 @@ __device__ __forceinline__ void shared_join(float& m, float& l, float4& o, float
     m = mm;
 }
 
+// The first and last worker with a tile of [begin, begin + T) where `total` tiles are cut for `workers`. Without tiles (no
+// whole page is shared, which is an ordinary call) there is no such worker, and nothing to divide by: {0, 0}. (The bounds
+// have no effect unless lengths change under the launch.)
+__host__ __device__ __forceinline__ int2 shared_cut(long long total, int workers, long long begin, int T) {
+    if (total <= 0 || workers <= 0) return make_int2(0, 0);
+    const int c0 = min(max(decode_worker_of(total, workers, begin), 0), workers - 1);
+    return make_int2(c0, min(max(decode_worker_of(total, workers, begin + T - 1), c0), workers - 1));
+}
+
 // The partial results of the prefix for the row of query head i of the key head, kBatch of them in flight.
 template <int D, int BATCH>
 struct SharedRow {
@@ -727,11 +736,8 @@ struct SharedRow {
     __device__ __forceinline__ SharedRow(const SharedParams& params, const SharedAt& a, int i) : p(params) {
         const int r = a.row + i, rb = r >> 8;
         in = p.chains == 2 ? r : r & 255;
-        const long long begin = a.first + static_cast<long long>(rb) * a.T;
-        // (the bounds have no effect unless lengths change under the launch)
-        const int top = max(a.workers - 1, 0);
-        c0 = min(max(decode_worker_of(a.total, a.workers, begin), 0), top);
-        c1 = min(max(decode_worker_of(a.total, a.workers, begin + a.T - 1), c0), top);
+        const int2 cut = shared_cut(a.total, a.workers, a.first + static_cast<long long>(rb) * a.T, a.T);
+        c0 = cut.x, c1 = cut.y;
         unit = (static_cast<long long>(a.g) * p.Hkv + a.h) * p.row_blocks + rb;
         n = a.any ? (c1 - c0 + 1) * p.chains : 0;
     }
