@@ -21,14 +21,15 @@
 // P and dS are rounded to bf16 for the tensor core (relative 2^-8 each at most, averaged over the
 // keys or queries of a sum), as the forward pass rounds P; everything else is fp32.
 //
-// One block per SM takes units as it frees up, longest walks first (from a counter; the loading warp claims). The loads
-// of the next unit run on behind those of the last, so a unit's end costs its last products
-// and its output, not a block's start.
+// One block per SM takes units as it frees up (the loading warp claims): from a counter, in causal batches of equal
+// lengths longest walks first, in packed ones numbered through all sequences from the last block to the first; the dQ
+// kernel of equal lengths without a mask in strides. The loads of the next unit run on behind those of the last, so a
+// unit's end costs its last products and its output, not a block's start.
 //
-// What bounds it: in long walks at d = 128 the tensor core, 1652 to 1744 TFLOP/s over the seven products (1 x 8 x 16384,
+// What bounds it: in long walks at d = 128 the tensor core, 1650 to 1744 TFLOP/s over the seven products (1 x 8 x 16384,
 // 2.21 to 2.33 ms; the sustained rate under the power limit is 1702); at d = 64 the elementwise warps' chain of a tile,
-// 1300 cycles to the products' 770 and 1020 (1 x 8 x 16384, 1.30 to 1.37 ms); in walks of few tiles a unit's start and
-// end, 2 to 3 us (16 x 16 x 1024 x 128, 8 tiles of 1.4 us, 368 to 385 us).
+// 1300 cycles to the products' 770 and 1020 (1 x 8 x 16384, 1.35 to 1.40 ms); in walks of few tiles a unit's start and
+// end, 2 to 3 us (16 x 16 x 1024 x 128, 8 tiles of 1.4 us, 383 to 388 us). (Ranges: boxes, and the power limit.)
 //
 // Roles (19 and 20 warps): 0-15 elementwise (four warps for each 32 of a tile's 128 columns, each of
 // them 32 TMEM lanes), 16 issues the MMAs of S and dP and owns TMEM, 17 claims units and loads
@@ -213,7 +214,7 @@ struct BwdCfg {
     static constexpr int kOffB = kOffA + kStagesA * kTileBytes;
     static constexpr int kOffStat = kOffB + kStagesB * kTileBytes;  // fp32 [slot][2][128]: -LSE·log2 e and -δ
     static constexpr int kOffBar = kOffStat + 2 * 2 * kBlockM * 4;
-    static constexpr int kFixedBars = 29;
+    static constexpr int kFixedBars = 29;  // (one numbering for both kernels, neither of which waits on all)
     static constexpr int kNumBars = kFixedBars + 2 * kStagesA + 2 * kStagesB;
     static constexpr int kOffUnits = (kOffBar + kNumBars * 8 + 15) / 16 * 16;  // unit queue: two slots
     static constexpr int kOffMisc = kOffUnits + 2 * 32;                        // TMEM slot, abort flag

@@ -330,7 +330,8 @@ struct SharedPlan {
 // reads twice comes from L2, and a shared part costs 10 to 15 us of launches and partial results. Measured (us, shared /
 // paged; bf16, 32/8 heads, d 128): 4 x 2040 keys, 34 MB, 19.3 / 8.4; 8 x 2040, 67 MB, 17.2 / 11.7; 16 x 2040, 134 MB,
 // 17.6 / 22.0; 32 x 2040, 268 MB, 17.5 / 33.9; but 2 x 16040, 131 MB, 30.0 / 23.1; 12/12 heads, d 64: 32 x 1100,
-// 109 MB, 20.4 / 19.6; 48 x 1800, 267 MB, 25.4 / 27.5.
+// 109 MB, 20.4 / 19.6; 48 x 1800, 267 MB, 25.4 / 27.5. What the tables hold only the GPU knows: 4 x 2040 keys under tables
+// for 8192 tokens or more take 18.4 us (paged 11.8).
 constexpr long long kSharedLeast = 1LL << 27;
 bool shared_small(long long B, long long Hkv, int d, int type, long long max_keys) {
     return B * Hkv * d * (type == FA_CACHE_E4M3 ? 2 : 4) <= (kSharedLeast - 1) / max_keys;

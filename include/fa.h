@@ -357,7 +357,8 @@ long long fa_decode_paged_workspace(int B, int Hq, int Hkv, int d, int cache_typ
  * each request, its hidden pages and scales likewise, but that weights of the shared keys are rounded to
  * bf16 (2^-8 relative, each before it meets its value) as fa_fwd's are. A request that is shorter than its
  * group's prefix is read by itself, and so is a batch whose table has no room for more than 128 MB of keys and
- * values (those come from L2 sooner than they are shared out).
+ * values (those come from L2 sooner than they are shared out). The table's width decides, since only the GPU
+ * knows the lengths: a few short requests under a table for long ones are shared out all the same.
  */
 int fa_decode_shared(const void* q, const fa_paged_cache* cache, const int* block_table, const int* seq_lens,
                      const int* prefix_lens, void* o, float* lse, int B, int Hq, int groups, int table_width,
